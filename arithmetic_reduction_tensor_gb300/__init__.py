@@ -19,6 +19,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 from .build import LIB_PATH
 
@@ -32,10 +33,13 @@ __all__ = [
     "tcr_order_descriptor", "tcr_order_equivalent", "tcr_status_string", "tcr_device_faults",
     "FAULT_PIPELINE_WAIT", "tcr_gemm_desc", "tcr_gemm_descriptor", "tcr_gemm_splitk",
     "tcr_reduce_sum_noalloc", "tcr_read_probe",
+    "I8", "I32", "NormOut", "tcr_norm_args", "tcr_norm_back_args", "tcr_rmsnorm",
+    "tcr_rmsnorm_backward", "tcr_quantize_rows_i8", "tcr_dequantize_rows_i8", "tcr_gemm_i8",
 ]
 
 MMA_CHAIN, SHUFFLE_TREE, FIXED_ORDER, MMA_CHAIN_TMEM = 0, 1, 2, 3
 F16, BF16, F32 = 0, 1, 2
+I8, I32 = 3, 4                 # of the 8-bit calls only
 DTYPE_NAMES = {F16: "f16", BF16: "bf16", F32: "f32"}
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA = 0, 1, 2, 3
 ORDER_TENSOR_CORE, ORDER_GRID_STRIDE, ORDER_BALANCED_TREE, ORDER_BLOCKED_TREE = 0, 1, 2, 3
@@ -79,6 +83,26 @@ class tcr_gemm_desc(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class tcr_norm_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_size_t),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("h", ctypes.c_void_p), ("ldh", ctypes.c_size_t),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_size_t),
+                ("scale", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t), ("eps", ctypes.c_float),
+                ("dtype", ctypes.c_int), ("y_dtype", ctypes.c_int)]
+
+
+class tcr_norm_back_args(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("lddy", ctypes.c_size_t),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("dh", ctypes.c_void_p), ("lddh", ctypes.c_size_t),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_size_t),
+                ("dweight", ctypes.c_void_p), ("rows", ctypes.c_size_t),
+                ("cols", ctypes.c_size_t), ("dtype", ctypes.c_int)]
 
 
 def Mode(kind: int, R: int = 0, block_threads: int = 0, dtype: int = F16,
@@ -139,6 +163,16 @@ def c_api() -> ctypes.CDLL:
             lib.tcr_reduce_sum_noalloc.restype = ctypes.c_int
             lib.tcr_read_probe.argtypes = [vp, sz, vp, ctypes.c_int, ctypes.c_int, vp]
             lib.tcr_read_probe.restype = ctypes.c_int
+            lib.tcr_rmsnorm.argtypes = [ctypes.POINTER(tcr_norm_args), vp]
+            lib.tcr_rmsnorm.restype = ctypes.c_int
+            lib.tcr_rmsnorm_backward.argtypes = [ctypes.POINTER(tcr_norm_back_args), vp]
+            lib.tcr_rmsnorm_backward.restype = ctypes.c_int
+            lib.tcr_quantize_rows_i8.argtypes = [vp, sz, vp, sz, vp, sz, vp, sz, sz, ctypes.c_int, vp]
+            lib.tcr_quantize_rows_i8.restype = ctypes.c_int
+            lib.tcr_dequantize_rows_i8.argtypes = [vp, sz, vp, vp, sz, sz, sz, ctypes.c_int, vp]
+            lib.tcr_dequantize_rows_i8.restype = ctypes.c_int
+            lib.tcr_gemm_i8.argtypes = [vp, sz, vp, sz, vp, vp, vp, sz, sz, sz, sz, ctypes.c_int, vp]
+            lib.tcr_gemm_i8.restype = ctypes.c_int
             lib.tcr_status_string.argtypes = [ctypes.c_int]
             lib.tcr_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -378,4 +412,218 @@ def tcr_gemm_splitk(A, W, splits: int = 0, out=None, stream=None, dtype: int | N
                                      M, N, K, splits, dtype, _stream_handle(A.device, stream))
     if st != OK:
         raise TcrError(st, "tcr_gemm_splitk")
+    return out
+
+
+# ------------------------------------------------------------------ the 8-bit linear path
+
+class NormOut(NamedTuple):
+    """What ``tcr_rmsnorm`` returns; None where an output was not asked for."""
+    y: object               # the normalised rows, or their 8-bit codes
+    scale: object           # the codes' scale of each row
+    h: object               # x + residual, rounded to the inputs' type
+    rstd: object            # 1 / sqrt(mean square + eps) of each row
+
+
+def _float_code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return F16
+    if t.dtype == torch.float32:
+        return F32
+    raise TypeError(f"expected float16, bfloat16 or float32, got {t.dtype}")
+
+
+def _matrix(name, t, shape, dtype, device, out=False):
+    """(pointer, leading dimension) of a 2-D CUDA tensor with contiguous rows."""
+    if t.dim() != 2 or t.shape != shape:
+        raise ValueError(f"{name} must be 2-D of shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    rows, cols = shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride 1 along its columns)")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols and (out or ld != 0):
+        raise ValueError(f"{name} has overlapping rows")
+    return t.data_ptr(), ld
+
+
+def _vector(name, t, n, dtype, device):
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return t.data_ptr()
+
+
+def _call(name, device, stream, *args):
+    """Call a C entry point on ``device``, its last argument the stream."""
+    import torch
+    f = getattr(c_api(), name)
+    if torch.cuda.current_device() == device.index:
+        st = f(*args, _stream_handle(device, stream))
+    else:
+        with torch.cuda.device(device):
+            st = f(*args, _stream_handle(device, stream))
+    if st != OK:
+        raise TcrError(st, name)
+
+
+def _check_rows(name, x):
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    return x.shape, x.device
+
+
+def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, h=None, out=None,
+                scale=None, rstd=None, want_rstd: bool = False, stream=None) -> NormOut:
+    """RMS norm of the rows of ``x + residual`` (``tcr_rmsnorm``).
+
+    ``out_dtype`` is x's own type (the default) or ``torch.int8``: 8-bit
+    codes with ``scale``, one float32 a row; an ``out`` given sets it.  ``h``
+    (x + residual, the next layer's residual) is returned when there is a
+    residual or an ``h`` to write to (``h=residual`` updates it in place);
+    ``rstd``, which the gradient takes, when asked for.  Rows may be strided
+    (stride 1 along the columns); x and residual may also be expanded rows.
+    """
+    import torch
+    shape, device = _check_rows("x", x)
+    rows, cols = shape
+    dt = _float_code(x)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    i8 = out.dtype == torch.int8
+    a = tcr_norm_args()
+    a.x, a.ldx = _matrix("x", x, shape, x.dtype, device)
+    if residual is not None:
+        a.residual, a.ldr = _matrix("residual", residual, shape, x.dtype, device)
+        if h is None:
+            h = torch.empty(shape, dtype=x.dtype, device=device)
+    if weight is not None:
+        a.weight = _vector("weight", weight, cols, x.dtype, device)
+    if h is not None:
+        a.h, a.ldh = _matrix("h", h, shape, x.dtype, device, out=True)
+    a.y, a.ldy = _matrix("out", out, shape, torch.int8 if i8 else x.dtype, device, out=True)
+    if i8:
+        if scale is None:
+            scale = torch.empty(rows, dtype=torch.float32, device=device)
+        a.scale = _vector("scale", scale, rows, torch.float32, device)
+    else:
+        scale = None
+    if rstd is None and want_rstd:
+        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+    if rstd is not None:
+        a.rstd = _vector("rstd", rstd, rows, torch.float32, device)
+    a.rows, a.cols, a.eps, a.dtype, a.y_dtype = rows, cols, eps, dt, I8 if i8 else dt
+    _call("tcr_rmsnorm", device, stream, ctypes.byref(a))
+    return NormOut(out, scale, h, rstd)
+
+
+def tcr_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
+                         want_dweight: bool = True, stream=None):
+    """(dx, dweight) of ``tcr_rmsnorm`` (``tcr_rmsnorm_backward``).
+
+    ``h`` and ``rstd`` are the forward call's (x itself without a residual);
+    ``dh`` is the gradient that reaches h along the residual path.  dx is the
+    gradient of x and of the residual; dweight (float32) is None when there is
+    no weight or it is not wanted."""
+    import torch
+    shape, device = _check_rows("h", h)
+    rows, cols = shape
+    a = tcr_norm_back_args()
+    a.dtype = _float_code(h)
+    a.dy, a.lddy = _matrix("dy", dy, shape, h.dtype, device)
+    a.h, a.ldh = _matrix("h", h, shape, h.dtype, device)
+    a.rstd = _vector("rstd", rstd, rows, torch.float32, device)
+    if weight is not None:
+        a.weight = _vector("weight", weight, cols, h.dtype, device)
+    if dh is not None:
+        a.dh, a.lddh = _matrix("dh", dh, shape, h.dtype, device)
+    if dx is None:
+        dx = torch.empty(shape, dtype=h.dtype, device=device)
+    a.dx, a.lddx = _matrix("dx", dx, shape, h.dtype, device, out=True)
+    if dweight is None and weight is not None and want_dweight:
+        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+    if dweight is not None:
+        a.dweight = _vector("dweight", dweight, cols, torch.float32, device)
+    a.rows, a.cols = rows, cols
+    _call("tcr_rmsnorm_backward", device, stream, ctypes.byref(a))
+    return dx, dweight
+
+
+def tcr_quantize_rows_i8(x, gate=None, out=None, scale=None, stream=None):
+    """(codes, scale) of the rows of ``x``, or of ``silu(gate) * x``
+    (``tcr_quantize_rows_i8``).  A weight matrix's rows are its output
+    channels."""
+    import torch
+    shape, device = _check_rows("x", x)
+    rows, cols = shape
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int8, device=device)
+    if scale is None:
+        scale = torch.empty(rows, dtype=torch.float32, device=device)
+    dt = _float_code(x)
+    xp, ldx = _matrix("x", x, shape, x.dtype, device)
+    gp, ldg = (None, 0) if gate is None else _matrix("gate", gate, shape, x.dtype, device)
+    qp, ldq = _matrix("out", out, shape, torch.int8, device, out=True)
+    sp = _vector("scale", scale, rows, torch.float32, device)
+    _call("tcr_quantize_rows_i8", device, stream, xp, ldx, gp, ldg, qp, ldq, sp, rows, cols, dt)
+    return out, scale
+
+
+def tcr_dequantize_rows_i8(q, scale, dtype=None, out=None, stream=None):
+    """The values ``q * scale`` of rows of codes (``tcr_dequantize_rows_i8``),
+    float32 unless ``dtype`` or ``out`` says otherwise."""
+    import torch
+    shape, device = _check_rows("q", q)
+    rows, cols = shape
+    if out is None:
+        out = torch.empty(shape, dtype=dtype or torch.float32, device=device)
+    elif dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out is {out.dtype}, dtype {dtype}")
+    qp, ldq = _matrix("q", q, shape, torch.int8, device)
+    sp = _vector("scale", scale, rows, torch.float32, device)
+    yp, ldy = _matrix("out", out, shape, out.dtype, device, out=True)
+    _call("tcr_dequantize_rows_i8", device, stream, qp, ldq, sp, yp, ldy, rows, cols, _float_code(out))
+    return out
+
+
+def tcr_gemm_i8(A, W, scale_a=None, scale_w=None, out_dtype=None, out=None, stream=None):
+    """C = (A @ W.T) * scale_a[:, None] * scale_w[None, :] with 8-bit codes A
+    (tokens x K) and W (channels x K), the products summed exactly
+    (``tcr_gemm_i8``).  ``out_dtype``: float16, bfloat16 (the default),
+    float32, or int32 for the sums themselves (scales are then refused)."""
+    import torch
+    if not A.is_cuda or A.dim() != 2 or W.dim() != 2:
+        raise ValueError("A and W must be 2-D CUDA tensors")
+    M, K = A.shape
+    N = W.shape[0]
+    if W.shape[1] != K:
+        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} vs {tuple(W.shape)}")
+    device = A.device
+    if out is None:
+        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    if out.dtype == torch.int32:
+        if scale_a is not None or scale_w is not None:
+            raise ValueError("int32 sums take no scales")
+        dt = I32
+    else:
+        dt = _float_code(out)
+    ap, lda = _matrix("A", A, A.shape, torch.int8, device, out=True)
+    wp, ldw = _matrix("W", W, W.shape, torch.int8, device, out=True)
+    cp, ldc = _matrix("out", out, (M, N), out.dtype, device, out=True)
+    sa = None if scale_a is None else _vector("scale_a", scale_a, M, torch.float32, device)
+    sw = None if scale_w is None else _vector("scale_w", scale_w, N, torch.float32, device)
+    _call("tcr_gemm_i8", device, stream, ap, lda, wp, ldw, sa, sw, cp, ldc, M, N, K, dt)
     return out

@@ -191,6 +191,96 @@ int gemm_block_threads();
 cudaError_t launch_combine(const float *partials, size_t segments, size_t count, float *out,
                            cudaStream_t stream);
 
+// ---- row operators with an 8-bit output (k_norm.cu): one team of threads
+// per row, the row in registers (rowvec.cuh holds the declared order of
+// their sums).  Leading dimensions in elements; an input's may be 0 (one
+// row for all).  Columns of rows longer than kRowLongT * 32 are read once
+// per step.
+constexpr int kRowNorm = 0;      // y = (x + r) * rstd * w; r, w, h, rstd may be null
+constexpr int kRowQuant = 1;     // y = x, or silu(r) * x where r is given
+constexpr int kRowLongT = 512;
+struct RowArgs {
+    const void *x, *r, *w;
+    size_t ldx, ldr;
+    void *h, *y;                 // y: the input type, or 8-bit codes with scale
+    size_t ldh, ldy;
+    float *scale, *rstd;
+    float eps;
+    size_t rows, cols;
+    bool al_in, al_w, al_h, al_y;    // 16-byte aligned rows (codes: 8-byte)
+};
+cudaError_t launch_rows_op(int op, int dtype, bool out_i8, const RowArgs &a, cudaStream_t stream);
+// y = q * scale[row] in `dtype`.
+cudaError_t launch_dequant(int dtype, const int8_t *q, size_t ldq, const float *scale, void *y, size_t ldy,
+                           size_t rows, size_t cols, cudaStream_t stream);
+
+// ---- the norm's gradient (k_norm_back.cu): dx per row, dw as G partials
+// (norm_back_groups) in scratch and their declared sum.  Rows of more than
+// kBackMaxVecs vectors of 8 take one more launch and a float of scratch
+// each.
+constexpr size_t kBackMaxVecs = 2048;
+struct BackArgs {
+    const void *dy, *h, *w, *dh;     // w, dh may be null
+    const float *rstd;
+    size_t lddy, ldh, lddh;
+    void *dx;
+    size_t lddx;
+    float *partial;
+    size_t rows, cols;
+    bool al_dy, al_h, al_w, al_dh, al_dx;
+};
+int norm_back_groups(size_t rows, size_t cols);
+size_t norm_back_scratch(size_t rows, size_t cols);
+cudaError_t launch_norm_back(int dtype, const BackArgs &a, float *dw, cudaStream_t stream);
+
+// ---- matrix product in 8-bit integers with scales (k_gemm_i8.cu)
+constexpr int kI8GemvTokens = 8;     // up to so many tokens: the integer-unit kernel
+constexpr int kOutI32 = 4;           // c_dtype beside kF16, kBF16, kF32: the integer sums themselves
+struct I8Args {
+    const int8_t *A, *W;
+    size_t lda, ldw, M, N, K;
+    const float *sa, *sw;            // null: 1
+    void *C;
+    size_t ldc;
+    int c_dtype;
+    bool al_a, al_w;                 // 16-byte aligned rows
+};
+struct I8Prepare {
+    const int8_t *A, *W;
+    size_t lda, ldw, M, N, K;
+    uint16_t *Af;
+    size_t ldf;
+    int8_t *Wp;
+    size_t ldp;
+    int *zero;
+    size_t zero_words;
+    unsigned blocks_a, blocks_w;
+    int team_log2;
+    bool al_a;
+};
+struct I8Gemm {
+    const float *sa, *sw;
+    void *C;
+    size_t ldc, M, N;
+    int c_dtype, tn, tiles_c, tiles_t, steps, sps, splits, units;
+    int *ws;
+    uint32_t *count;
+    uint32_t inject_stall;
+};
+struct I8Plan {
+    int tensor;                      // 0: the integer-unit kernel
+    int tn, tiles_c, tiles_t;        // tokens per tile, tiles
+    int steps, sps, splits, units;   // steps of 128 k; per split; K splits; CTA-pair work units
+    size_t ldf;                      // row pitch of the prepared operands
+    int launches;
+};
+int gemm_i8_pairs();
+I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs);
+size_t gemm_i8_scratch(const I8Plan &p, size_t M, size_t N, bool repack_w);
+cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool repack_w, bool inject_stall,
+                           cudaStream_t stream);
+cudaError_t read_gemm_i8_faults(unsigned int *flags, bool clear);
+
 // Make the driver load every variant of a kernel family now (one
 // cudaFuncGetAttributes per variant), so that no later launch of them loads
 // code: the chunk kernels' sums (FIXED_ORDER plain tree; MMA_CHAIN at every

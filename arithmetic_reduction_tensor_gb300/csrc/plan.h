@@ -1,11 +1,12 @@
-// plan.h -- host-side planning shared by the entry points of tcr_api.cu and
-// tcr_noalloc.cu: argument checks, device queries and the work split of the
-// chunked sum kernels.  One definition of each, in tcr_api.cu, so that the
-// two entry points of the 1-D sum cut the same input into the same chunks
-// (and so return the same bits).
+// plan.h -- host-side planning shared by the entry points of tcr_api.cu,
+// tcr_noalloc.cu and tcr_i8.cu: argument checks, device queries, scratch and
+// the work split of the chunked sum kernels.  One definition of each, in
+// tcr_api.cu, so that the two entry points of the 1-D sum cut the same input
+// into the same chunks (and so return the same bits).
 #pragma once
 
 #include <cstddef>
+#include <cuda_runtime.h>
 
 #include "../../include/tcr.h"
 #include "config.cuh"
@@ -34,6 +35,13 @@ int sm_count(int dev);
 // (device, variant, block size), so only a variant's first use queries the
 // runtime.  At least 1.
 int occupancy(int dev, Family fam, bool rows, int dtype, int op, bool aligned, int R, int block);
+
+// The library's stream-ordered scratch pool on `dev`; null if it cannot be
+// made.
+cudaMemPool_t pool_for(int dev);
+// Whether the environment asks for a failure of this kind (tests of the
+// error paths): TCR_FAULT_INJECT = "alloc", "launch" or "stall".
+bool fault_injected(const char *what);
 
 int log2_exact(int v);
 size_t elem_bytes(int dtype);

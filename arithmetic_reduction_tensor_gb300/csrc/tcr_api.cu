@@ -222,6 +222,12 @@ ChunkSplit chunk_split(size_t segments, size_t seg_len, int dtype, int block, bo
     return c;
 }
 
+bool fault_injected(const char *what)
+{
+    const char *e = std::getenv("TCR_FAULT_INJECT");
+    return e && std::strcmp(e, what) == 0;
+}
+
 }  // namespace plan
 }  // namespace tcr
 
@@ -506,12 +512,6 @@ Plan make_plan(size_t segments, size_t seg_len, bool rows_call, const tcr_mode &
     }
     plan_chunked(p, m.kind == TCR_FIXED_ORDER || m.block_threads == 0);
     return p;
-}
-
-bool fault_injected(const char *what)
-{
-    const char *e = std::getenv("TCR_FAULT_INJECT");
-    return e && std::strcmp(e, what) == 0;
 }
 
 tcr_status run_plan(const Plan &p, const void *x, float *out, cudaStream_t s, int dev)
@@ -956,10 +956,11 @@ tcr_status tcr_device_faults(unsigned int *flags, int clear)
 {
     if (!flags) return TCR_ERR_INVALID_ARG;
     if (current_device() < 0) return TCR_ERR_CUDA;
-    unsigned int a = 0, g = 0;
-    if (read_device_faults(&a, clear != 0) != cudaSuccess || read_gemm_faults(&g, clear != 0) != cudaSuccess)
+    unsigned int a = 0, g = 0, i = 0;
+    if (read_device_faults(&a, clear != 0) != cudaSuccess || read_gemm_faults(&g, clear != 0) != cudaSuccess ||
+        read_gemm_i8_faults(&i, clear != 0) != cudaSuccess)
         return TCR_ERR_CUDA;
-    *flags = a | g;
+    *flags = a | g | i;
     return TCR_OK;
 }
 

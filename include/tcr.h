@@ -136,7 +136,10 @@ typedef enum {
 typedef enum {
     TCR_F16 = 0,    /* IEEE 754 binary16 */
     TCR_BF16 = 1,   /* bfloat16: the upper 16 bits of a binary32 */
-    TCR_F32 = 2     /* IEEE 754 binary32 */
+    TCR_F32 = 2,    /* IEEE 754 binary32 */
+    /* of the 8-bit calls only (no tcr_mode takes them): */
+    TCR_I8 = 3,     /* 8-bit two's complement codes */
+    TCR_I32 = 4     /* 32-bit two's complement sums */
 } tcr_dtype;
 
 /*
@@ -458,9 +461,148 @@ TCR_API tcr_status tcr_gemm_splitk(const void *A, const void *W, float *C, size_
                                    size_t K, int splits, int dtype, void *stream);
 
 /*
+ * ---- The 8-bit linear path: norm, row quantiser, integer product ----
+ *
+ * What a layer of a language model does between its matrix products, and the
+ * product itself with both operands in 8-bit integers: the cascaded
+ * reductions of the "RedFuser" title in the first page's list of work, with
+ * every order declared as "Taming Bitwise Behavior in GPU Kernels with
+ * Tensor Core" (arXiv 2609.11356), Abstract, asks.  A row (token) of codes q
+ * has one binary32 scale s; it stands for the values q * s.
+ *
+ * Rows.  Matrices are row-major with a leading dimension in elements (ld*,
+ * at least cols; an input's may also be 0: one row for all; with at most one
+ * row it is not looked at) and rows of any element alignment.  rows < 2^31,
+ * cols <= 2^27, rows * cols < 2^40, rows * ld < 2^48.  dtype is TCR_F16,
+ * TCR_BF16 or TCR_F32 and is that of every matrix of the call but the codes.
+ * 16-byte aligned rows (base and ld) are the fast case.
+ *
+ * Declared order of their row sums.  Vector v is elements 8v .. 8v+7 (absent
+ * ones +0.0) and has the value ((e0+e1)+(e2+e3))+((e4+e5)+(e6+e7)); the
+ * vector values, padded with +0.0 to a power of two P, are folded upper half
+ * onto lower half (a[v] += a[v+h], h = P/2, P/4, .., 1).  All arithmetic is
+ * binary32 with one rounding to nearest per operation, nothing fused, so a
+ * row's results depend on that row's inputs and cols only: not on the rows
+ * beside it, their number, the alignment, the launch or the GPU.
+ *
+ * Codes.  amax = the row's largest |y|, scale = amax / 127, code =
+ * rint(y * (127 / amax)), ties to even: always in -127 .. 127.  A row with a
+ * NaN or an infinity has scale NaN and codes 0 (all its values read back as
+ * NaN); a row whose scale would be below 2^-126 has scale 0 and codes 0.
+ *
+ * tcr_rmsnorm -- for every row
+ *   h_j = x_j + residual_j   (h = x without a residual),
+ *   rstd = 1 / sqrt(S / cols + eps), S the declared sum of fl(h_j * h_j),
+ *   y_j = (h_j * rstd) * weight_j   (without a weight: h_j * rstd).
+ * h is used as the binary32 sum; the stored copy (the next residual, and
+ * what the gradient takes) is rounded to dtype.
+ *   residual, weight   may be NULL.
+ *   h, rstd            outputs, NULL where not wanted.  h may be x or the
+ *                      residual itself (same pointer and ld); y may be too
+ *                      when it has their type and h is NULL or elsewhere.
+ *                      No other overlap.
+ *   y, y_dtype         dtype, or TCR_I8 with scale (rows floats; not looked
+ *                      at otherwise).
+ *   eps                finite, >= 0.
+ * cols == 0: scale 0, rstd NaN.
+ */
+typedef struct {
+    const void *x;
+    size_t ldx;
+    const void *residual;
+    size_t ldr;
+    const void *weight;
+    void *h;
+    size_t ldh;
+    void *y;
+    size_t ldy;
+    float *scale;
+    float *rstd;
+    size_t rows, cols;
+    float eps;
+    int dtype, y_dtype;
+} tcr_norm_args;
+TCR_API tcr_status tcr_rmsnorm(const tcr_norm_args *args, void *stream);
+
+/*
+ * tcr_rmsnorm_backward -- the gradient of tcr_rmsnorm.  With xh = h * rstd,
+ * g = dy * weight, c = S' / cols, S' the declared row sum of fl(g * xh):
+ *   dx = rstd * (g - xh * c) + dh,
+ *   dweight_j = sum over rows of fl(dy * xh).
+ * dx is the gradient of x and of the residual alike.
+ *   dy     gradient of y (of the values the codes stand for, if y was
+ *          TCR_I8: the rounding counts as the identity).
+ *   h      the stored h of the forward call (x itself without a residual),
+ *   rstd   its rstd (rows floats).
+ *   dh     gradient that reaches h by the residual path, or NULL.
+ *   dx     may be dy, h or dh itself (same pointer and ld).
+ *   dweight  cols floats, or NULL; overwritten.  Its order: with G =
+ *          min(rows, 304) (152 where cols > 4096), partial g adds rows g,
+ *          g + G, .. in order; 32 sums add the partials k, k + 32, .. in
+ *          order; those fold as the row sums' lanes do.  No atomics: the
+ *          bits depend on the inputs, rows and cols only.
+ * Takes G * cols floats of pool scratch (and rows more for cols > 16384).
+ * rows == 0 writes dweight = +0.0.
+ */
+typedef struct {
+    const void *dy;
+    size_t lddy;
+    const void *h;
+    size_t ldh;
+    const void *weight;
+    const float *rstd;
+    const void *dh;
+    size_t lddh;
+    void *dx;
+    size_t lddx;
+    float *dweight;
+    size_t rows, cols;
+    int dtype;
+} tcr_norm_back_args;
+TCR_API tcr_status tcr_rmsnorm_backward(const tcr_norm_back_args *args, void *stream);
+
+/*
+ * tcr_quantize_rows_i8 -- codes and scale of every row of y = x, or, with a
+ * gate (NULL: none), of y = (gate / (1 + exp(-gate))) * x, each step rounded
+ * to binary32 (exp as the CUDA library computes it).  q: rows x cols codes;
+ * scale: rows floats.  Weights are quantised the same way, a row being an
+ * output channel.
+ *
+ * tcr_dequantize_rows_i8 -- y = q * scale[row], rounded to dtype.
+ */
+TCR_API tcr_status tcr_quantize_rows_i8(const void *x, size_t ldx, const void *gate, size_t ldg, void *q,
+                                        size_t ldq, float *scale, size_t rows, size_t cols, int dtype,
+                                        void *stream);
+TCR_API tcr_status tcr_dequantize_rows_i8(const void *q, size_t ldq, const float *scale, void *y, size_t ldy,
+                                          size_t rows, size_t cols, int dtype, void *stream);
+
+/*
+ * tcr_gemm_i8 -- C[t][n] = (float(S) * scale_a[t]) * scale_w[n], rounded to
+ * c_dtype, S = sum over k of A[t][k] * W[n][k] exactly (32-bit integers).
+ *   A        M x K codes (tokens), W: N x K codes (channels), row-major,
+ *            leading dimensions lda, ldw >= K, any alignment.  All 256 code
+ *            values are served.
+ *   scale_a  M floats, scale_w N floats, or NULL (1).
+ *   C        M x N, ldc >= N, TCR_F16, TCR_BF16, TCR_F32, or TCR_I32: S
+ *            itself (the scales are not looked at).
+ * M, N < 2^31, M * N, M * K, N * K < 2^40; K <= 131071 (any S then fits 32
+ * bits), a larger K returns TCR_ERR_UNSUPPORTED.  K == 0 writes zeros.
+ * C's bits depend on the inputs only: integer sums have no order.  Up to 8
+ * tokens run on the integer units in one launch; more on tcgen05, as exact
+ * binary16 MMAs over pairs of SMs, in two launches, with pool scratch of 2
+ * bytes per code of A, N * K bytes more when W's rows are not 16-byte
+ * aligned, and 4 bytes per output when K is split.  TCR_ERR_UNSUPPORTED where
+ * the device cannot schedule a pair.  A kernel whose wait gave up leaves NaN
+ * (TCR_I32: the least integer) and sets the word of tcr_device_faults.
+ */
+TCR_API tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t ldw, const float *scale_a,
+                               const float *scale_w, void *C, size_t ldc, size_t M, size_t N, size_t K,
+                               int c_dtype, void *stream);
+
+/*
  * tcr_device_faults -- the fault word of the current device: bit 0
- * (TCR_FAULT_PIPELINE_WAIT) is set when a wait inside a TCR_MMA_CHAIN_TMEM
- * or split-K GEMM kernel gave up after its limit of about one second (the kernel then
+ * (TCR_FAULT_PIPELINE_WAIT) is set when a wait inside a TCR_MMA_CHAIN_TMEM,
+ * split-K GEMM or 8-bit GEMM kernel gave up after its limit of about one second (the kernel then
  * drained its own copies and tensor-core work, freed its tensor memory and
  * wrote NaN partials, so that call's result is NaN).  The word stays set
  * until cleared: clear != 0 resets it after reading.  Synchronous with
