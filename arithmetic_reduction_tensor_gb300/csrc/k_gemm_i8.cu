@@ -34,12 +34,12 @@
 // so the splits add into a zeroed 32-bit scratch with atomics and the last
 // to arrive scales the tile -- the same bits in any order.
 //
-// CTA roles (448 threads, one persistent CTA per SM, clusters of two):
+// CTA roles (768 threads, one persistent CTA per SM, clusters of two):
 //   warp 0        TMA producer: 128 weight rows x 128 codes, and 2 boxes of
-//                 64 columns x tile/2 tokens, into a 5-stage ring
-//   warp 1        TMEM allocation; the leader's lane 0 issues the MMAs
-//   warps 2..5    conversion, two TMEM stages of 128 k ahead of the MMA
-//   warps 6..13   epilogue: two 192-column accumulators, so a chunk's
+//                 64 columns x tile/2 tokens, into a 7-stage ring
+//   warp 1        TMEM allocation; the leader's issues the MMAs
+//   warps 4..15   conversion, four TMEM stages of 128 k ahead of the MMA
+//   warps 16..23  epilogue: two 128-column accumulators, so a chunk's
 //                 readout runs beside the next chunk's MMAs
 // Every wait gives up after about a second as in the split-K GEMM.
 #include <cstring>
@@ -184,22 +184,30 @@ __global__ void __launch_bounds__(256) i8_prepare_kernel(const I8Prepare p)
 // ---------------------------------------------------------------- the tensor-core kernel
 
 constexpr int kI8BM = 256;                     // channels of a tile (128 per CTA)
-constexpr int kI8MaxTn = 192;                  // tokens of a tile, at most
+constexpr int kI8MaxTn = 160;                  // tokens of a tile, at most
 constexpr int kI8BK = 128;                     // k per stage
 constexpr int kI8ChunkSteps = 8;               // 1024 k per exact accumulation
 constexpr int kI8WBytes = 128 * kI8BK;         // 16 KiB of codes
 constexpr int kI8TBoxBytes = kI8MaxTn / 2 * 128;    // 64 binary16 columns of half the tokens
 constexpr int kI8StageBytes = kI8WBytes + 2 * kI8TBoxBytes;
-constexpr int kI8Stages = 5;
-constexpr int kI8AStages = 2;                  // TMEM stages of the widened weights
-constexpr int kI8DCols = kI8MaxTn;             // accumulators at columns 0 and 192
-constexpr int kI8ACol = 2 * kI8DCols;          // 384: 64 columns per A stage
-constexpr int kI8Threads = 448;
+constexpr int kI8Stages = 6;
+constexpr int kI8AStages = 3;                  // TMEM stages of the widened weights
+constexpr int kI8DCols = kI8MaxTn;             // accumulators at columns 0 and 160
+constexpr int kI8ACol = 2 * kI8DCols;          // 320: 64 columns per A stage
+constexpr int kI8ConvGroups = 3;               // warpgroups that take the steps in turn
 constexpr int kI8EpiWarps = 8;
+constexpr int kI8EpiWarp0 = 4 + 4 * kI8ConvGroups;
+constexpr int kI8Threads = 32 * (kI8EpiWarp0 + kI8EpiWarps);
+// Registers a thread by role (setmaxnreg); their sum over the warpgroups is
+// within what the launch holds: 768 threads of 80.
+constexpr int kI8RegsLaunch = 80, kI8RegsIssue = 48, kI8RegsConv = 64, kI8RegsEpi = 120;
+static_assert(kI8RegsIssue + kI8ConvGroups * kI8RegsConv + kI8EpiWarps / 4 * kI8RegsEpi <=
+                  kI8Threads / 128 * kI8RegsLaunch,
+              "registers of the launch");
 constexpr int kI8OffBars = kI8Stages * kI8StageBytes;
-// barriers: wfull[S], tfull[S] (leader's), empty[S], afull[A] (leader's),
-// aempty[A], dfull[2], dempty[2] (leader's), drain
-constexpr int kI8NumBars = 3 * kI8Stages + 2 * kI8AStages + 4 + 1;
+// barriers: wfull[S] (this CTA's codes), full[S] (leader's: both CTAs' tokens
+// and converted weights), empty[S], dfull[2], dempty[2] (leader's), drain
+constexpr int kI8NumBars = 3 * kI8Stages + 4 + 1;
 constexpr int kI8OffMisc = kI8OffBars + 8 * kI8NumBars;
 constexpr int kI8SmemBytes = kI8OffMisc + 64 + 1024;
 static_assert(kI8SmemBytes <= 232448, "one SM's 227 KiB");
@@ -219,23 +227,45 @@ __device__ __forceinline__ uint32_t i8_map_leader(uint32_t addr)
     return r;
 }
 
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool i8_elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void i8_cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// What is handed over is tensor memory, ordered by the tcgen05 fences on both
+// sides; no generic memory needs the (slow) release.
 __device__ __forceinline__ void i8_arrive_leader(uint32_t cluster_bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
-__device__ __forceinline__ void i8_load_tokens(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+// Two blocks of 64 k (block, block + 1) of the tile's tokens from `row` on,
+// one after the other in shared memory.
+__device__ __forceinline__ void i8_load_tokens(uint32_t dst, const CUtensorMap *map, int row, int block, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-        "[%0], [%1, {%2, %3}], [%4];"
-        ::"r"(dst), "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+        "[%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"((uint64_t)map), "r"(0), "r"(row), "r"(block), "r"(bar)
         : "memory");
 }
 
@@ -327,12 +357,10 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     const uint32_t bars = ring + kI8OffBars;
     auto bar = [&](int i) { return bars + 8u * (uint32_t)i; };
     auto wfull = [&](int s) { return bar(s); };
-    auto tfull = [&](int s) { return bar(kI8Stages + s); };
+    auto full = [&](int s) { return bar(kI8Stages + s); };
     auto empty = [&](int s) { return bar(2 * kI8Stages + s); };
-    auto afull = [&](int s) { return bar(3 * kI8Stages + s); };
-    auto aempty = [&](int s) { return bar(3 * kI8Stages + kI8AStages + s); };
-    auto dfull = [&](int s) { return bar(3 * kI8Stages + 2 * kI8AStages + s); };
-    auto dempty = [&](int s) { return bar(3 * kI8Stages + 2 * kI8AStages + 2 + s); };
+    auto dfull = [&](int s) { return bar(3 * kI8Stages + s); };
+    auto dempty = [&](int s) { return bar(3 * kI8Stages + 2 + s); };
     const uint32_t drain = bar(kI8NumBars - 1);
     uint32_t *misc = (uint32_t *)(smem + kI8OffMisc);
     volatile uint32_t *tmem_holder = misc;
@@ -348,12 +376,9 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < kI8Stages; s++) {
             mbar_init(wfull(s), 1);
-            mbar_init(tfull(s), 1);
+            // the tokens' expect and a conversion warpgroup in each CTA
+            mbar_init(full(s), 1 + 2 * 4);
             mbar_init(empty(s), 1);
-        }
-        for (int s = 0; s < kI8AStages; s++) {
-            mbar_init(afull(s), 8);              // four conversion warps in each CTA
-            mbar_init(aempty(s), 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(dfull(b), 1);
@@ -382,9 +407,12 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     auto split_steps = [&](int s) { return min(g.sps, g.steps - s * g.sps); };
     const int half = g.tn / 2;
 
-    if (warp == 0) {
-        // ---------------- producer
-        if (lane == 0) {
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kI8RegsIssue));
+        if (warp == 0) {
+            // ---------------- producer (a converged warp, one lane issuing)
+            const uint32_t leader_full = i8_map_leader(full(0));
+            const uint32_t token_bytes = (uint32_t)(4 * 128 * half);
             int st = 0;
             uint32_t phase = 0;
             uint32_t armed = 0, armed_phase = 0;
@@ -392,20 +420,19 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             for (int u = pair; u < g.units && ok; u += pairs) {
                 const I8Unit c = i8_decode(g, u);
                 const int nb = split_steps(c.split);
+                const int s0 = c.split * g.sps;
+                const int row_w = c.tc * kI8BM + 128 * (int)rank, row_t = c.tt * g.tn + half * (int)rank;
                 for (int j = 0; j < nb; j++) {
-                    if (*abort || !wait(empty(st), phase ^ 1u)) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(kFull, wait(empty(st), phase ^ 1u));
+                    if (!ok) break;
                     const uint32_t dst = ring + (uint32_t)st * kI8StageBytes;
-                    const int k = (c.split * g.sps + j) * kI8BK;
-                    mbar_arrive_expect_tx(wfull(st), kI8WBytes);
-                    tma_load_2d(dst, &map_w, k, c.tc * kI8BM + 128 * (int)rank, wfull(st));
-                    const uint32_t tf = i8_map_leader(tfull(st));
-                    if (leader) mbar_arrive_expect_tx(tfull(st), (uint32_t)(4 * 128 * half));
-                    const int t0 = c.tt * g.tn + half * (int)rank;
-                    i8_load_tokens(dst + kI8WBytes, &map_t, k, t0, tf);
-                    i8_load_tokens(dst + kI8WBytes + kI8TBoxBytes, &map_t, k + 64, t0, tf);
+                    if (i8_elect()) {
+                        mbar_arrive_expect_tx(wfull(st), kI8WBytes);
+                        tma_load_2d(dst, &map_w, (s0 + j) * kI8BK, row_w, wfull(st));
+                        if (leader) mbar_arrive_expect_tx(full(st), token_bytes);
+                        i8_load_tokens(dst + kI8WBytes, &map_t, row_t, 2 * (s0 + j), leader_full + 8u * (uint32_t)st);
+                    }
+                    __syncwarp();
                     armed |= 1u << st;
                     armed_phase = (armed_phase & ~(1u << st)) | (phase << st);
                     if (++st == kI8Stages) {
@@ -415,118 +442,116 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 }
             }
             if (*abort) {
-                // let the copies in flight land (the leader's token barriers
-                // count both CTAs' copies)
-                for (int i = 0; i < kI8Stages; i++) {
-                    if (!((armed >> i) & 1u)) continue;
-                    (void)mbar_wait_limited(wfull(i), (armed_phase >> i) & 1u);
-                    if (leader) (void)mbar_wait_limited(tfull(i), (armed_phase >> i) & 1u);
+                // let the copies in flight land; the tokens' share a barrier
+                // with conversions that may never come, so those get the time
+                // of a whole wait
+                for (int i = 0; i < kI8Stages; i++)
+                    if ((armed >> i) & 1u) (void)mbar_wait_limited(wfull(i), (armed_phase >> i) & 1u);
+                const uint64_t t0 = global_ns();
+                while (global_ns() - t0 < 10000000ull) {
                 }
             }
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // ---------------- MMA issuer
-        if (leader && lane == 0) {
+        } else if (warp == 1 && leader) {
+            // ---------------- MMA issuer: the whole warp walks the steps, so
+            // that the operands stay in uniform registers; one lane issues
             // kind::f16, D binary32, A and B binary16, M = 256, N = tn
             const uint32_t idesc = (1u << 4) | ((uint32_t)(g.tn >> 3) << 17) | ((uint32_t)(kI8BM >> 4) << 24);
             const uint64_t t_desc0 = smem_desc_sw128(ring + kI8WBytes);
             int st = 0, ta = 0, b = 0;
-            uint32_t phase = 0, aphase = 0, dphase = 0;
+            uint32_t phase = 0, dphase = 0;
             bool ok = true, withhold = g.inject_stall != 0u;
             for (int u = pair; u < g.units && ok; u += pairs) {
                 const I8Unit c = i8_decode(g, u);
                 const int nb = split_steps(c.split);
+                int in_chunk = 0;
                 for (int j = 0; j < nb && ok; j++) {
-                    const int in_chunk = j % kI8ChunkSteps;
-                    if (in_chunk == 0) {
-                        ok = !*abort && wait(dempty(b), ((dphase >> b) & 1u) ^ 1u);
-                        if (!ok) break;
-                    }
-                    ok = wait(tfull(st), phase) && wait(afull(ta), aphase);
+                    bool ready = true;
+                    if (in_chunk == 0) ready = !*abort && wait(dempty(b), ((dphase >> b) & 1u) ^ 1u);
+                    ready = ready && wait(full(st), phase);
+                    ok = __all_sync(kFull, ready);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(b * kI8DCols);
                     const uint32_t a = tmem + (uint32_t)(kI8ACol + 64 * ta);
                     const uint64_t t_desc = t_desc0 + (uint64_t)st * (kI8StageBytes >> 4);
+                    const bool end = in_chunk == kI8ChunkSteps - 1 || j == nb - 1;
+                    if (i8_elect()) {
+                        i8_mma(d, a, t_desc, idesc, in_chunk > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        i8_mma(d, a + 8u * (uint32_t)k,
-                               t_desc + (uint64_t)((k >> 2) * (kI8TBoxBytes >> 4) + (k & 3) * 2), idesc,
-                               (in_chunk > 0 || k > 0) ? 1u : 0u);
-                    i8_commit(empty(st));
-                    i8_commit(aempty(ta));
+                        for (int k = 1; k < 8; k++)
+                            i8_mma(d, a + 8u * (uint32_t)k,
+                                   t_desc + (uint64_t)((k >> 2) * (half << 3) + (k & 3) * 2), idesc, 1u);
+                        i8_commit(empty(st));
+                        if (end && !withhold) i8_commit(dfull(b));
+                    }
+                    __syncwarp();
                     if (++st == kI8Stages) {
                         st = 0;
                         phase ^= 1u;
                     }
-                    if (++ta == kI8AStages) {
-                        ta = 0;
-                        aphase ^= 1u;
-                    }
-                    if (in_chunk == kI8ChunkSteps - 1 || j == nb - 1) {
-                        if (withhold)
-                            withhold = false;
-                        else
-                            i8_commit(dfull(b));
+                    ta = (ta + 1) % kI8AStages;
+                    in_chunk++;
+                    if (end) {
+                        withhold = false;
+                        in_chunk = 0;
                         dphase ^= 1u << b;
                         b ^= 1;
                     }
                 }
             }
-            i8_commit_local(drain);
+            if (i8_elect()) i8_commit_local(drain);
+            __syncwarp();
             (void)mbar_wait_limited(drain, 0u);
         }
-        __syncwarp();
-    } else if (warp < 6) {
-        // ---------------- conversion: thread m widens weight row m of the box
+    } else if (warp < kI8EpiWarp0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kI8RegsConv));
+        // ---------------- conversion: thread m of a warpgroup widens weight row m
+        // of the box; the warpgroups take the steps in turn, so that a step's
+        // fixed costs (two waits, the handover) are spread over a whole box
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int m = 32 * (warp & 3) + lane;
         const uint32_t sw = (uint32_t)(m & 7);         // 128-byte swizzle of the box
-        int st = 0, ta = 0;
-        uint32_t phase = 0, aphase = 0;
+        int total = 0;                                 // steps of all units
+        for (int u = pair; u < g.units; u += pairs) total += split_steps(i8_decode(g, u).split);
         bool ok = true;
-        for (int u = pair; u < g.units && ok; u += pairs) {
-            const I8Unit c = i8_decode(g, u);
-            const int nb = split_steps(c.split);
-            for (int j = 0; j < nb; j++) {
-                const bool ready = !*abort && wait(wfull(st), phase) && wait(aempty(ta), aphase ^ 1u);
-                ok = __all_sync(kFull, ready);
-                if (!ok) break;
-                tc_fence_after();
-                const uint8_t *row = smem + (size_t)st * kI8StageBytes + m * kI8BK;
+        for (int i = (warp - 4) >> 2; i < total; i += kI8ConvGroups) {
+            const int st = i % kI8Stages;
+            ok = __all_sync(kFull, wait(wfull(st), (uint32_t)(i / kI8Stages) & 1u));
+            if (!ok) break;
+            const uint32_t row = ring + (uint32_t)(st * kI8StageBytes + m * kI8BK);
+            const uint32_t dst = tmem + lane_base + (uint32_t)(kI8ACol + 64 * (i % kI8AStages));
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    uint32_t o[32];
+            for (int h = 0; h < 2; h++) {
+                uint32_t o[32];
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
-                        const uint4 w = ld16(row + 16u * ((uint32_t)(4 * h + q) ^ sw));
-                        widen4(w.x, o[8 * q], o[8 * q + 1]);
-                        widen4(w.y, o[8 * q + 2], o[8 * q + 3]);
-                        widen4(w.z, o[8 * q + 4], o[8 * q + 5]);
-                        widen4(w.w, o[8 * q + 6], o[8 * q + 7]);
-                    }
-                    i8_st32(tmem + lane_base + (uint32_t)(kI8ACol + 64 * ta + 32 * h), o);
+                for (int q = 0; q < 4; q++) {
+                    const uint4 w = lds16(row + 16u * ((uint32_t)(4 * h + q) ^ sw));
+                    widen4(w.x, o[8 * q], o[8 * q + 1]);
+                    widen4(w.y, o[8 * q + 2], o[8 * q + 3]);
+                    widen4(w.z, o[8 * q + 4], o[8 * q + 5]);
+                    widen4(w.w, o[8 * q + 6], o[8 * q + 7]);
                 }
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) i8_arrive_leader(i8_map_leader(afull(ta)));
-                if (++st == kI8Stages) {
-                    st = 0;
-                    phase ^= 1u;
+                if (h == 0 && i >= kI8AStages) {
+                    // the MMAs that read this TMEM stage last are done
+                    const int e = i - kI8AStages;
+                    ok = __all_sync(kFull, wait(empty(e % kI8Stages), (uint32_t)(e / kI8Stages) & 1u));
+                    if (!ok) break;
+                    tc_fence_after();
                 }
-                if (++ta == kI8AStages) {
-                    ta = 0;
-                    aphase ^= 1u;
-                }
+                i8_st32(dst + 32u * (uint32_t)h, o);
             }
+            if (!ok) break;
+            asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) i8_arrive_leader(i8_map_leader(full(st)));
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kI8RegsEpi));
         // ---------------- epilogue: a thread holds one channel, half of the tile's tokens
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int m = 32 * (warp & 3) + lane;
-        const int col0 = warp < 10 ? 0 : half;
+        const int col0 = warp < kI8EpiWarp0 + 4 ? 0 : half;
         const int nblk = half / 16;
         int b = 0;
         uint32_t dphase = 0;
@@ -560,20 +585,20 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             }
             const size_t n = (size_t)c.tc * kI8BM + 128u * rank + (size_t)m;
             const size_t t0 = (size_t)c.tt * (size_t)g.tn + (size_t)col0;
+            // the tokens of this thread that exist
+            const int nt = n >= g.N || t0 >= g.M ? 0 : (int)min((size_t)half, g.M - t0);
             bool write = true;
             if (g.splits > 1 && live) {
                 // this split's share of the tile, then the last split scales it
+                int *ws = g.ws + t0 * g.N + n;
 #pragma unroll
-                for (int q = 0; q < kI8MaxTn / 32; q++)
-                    if (q < nblk)
-#pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const size_t t = t0 + 16 * q + i;
-                            if (n < g.N && t < g.M) atomicAdd(g.ws + t * g.N + n, acc[16 * q + i]);
-                        }
+                for (int i = 0; i < kI8MaxTn / 2; i++) {
+                    if (i < nt) atomicAdd(ws, acc[i]);
+                    ws += g.N;
+                }
                 __threadfence();
                 named_sync(1, 32 * kI8EpiWarps);
-                if (threadIdx.x == 192) {
+                if (threadIdx.x == 32 * kI8EpiWarp0) {
                     uint32_t *count = g.count + 2 * (c.tt * g.tiles_c + c.tc) + rank;
                     *last = !*abort && atomicAdd(count, 1u) == (uint32_t)(g.splits - 1);
                 }
@@ -584,33 +609,29 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     write = true;
                 } else if (write) {
                     __threadfence();
+                    ws = g.ws + t0 * g.N + n;
 #pragma unroll
-                    for (int q = 0; q < kI8MaxTn / 32; q++)
-                        if (q < nblk)
-#pragma unroll
-                            for (int i = 0; i < 16; i++) {
-                                const size_t t = t0 + 16 * q + i;
-                                if (n < g.N && t < g.M) acc[16 * q + i] = __ldcg(g.ws + t * g.N + n);
-                            }
+                    for (int i = 0; i < kI8MaxTn / 2; i++) {
+                        if (i < nt) acc[i] = __ldcg(ws);
+                        ws += g.N;
+                    }
                 }
             } else if (g.splits > 1) {
                 named_sync(1, 32 * kI8EpiWarps);
-                if (threadIdx.x == 192) *last = 0u;
+                if (threadIdx.x == 32 * kI8EpiWarp0) *last = 0u;
                 named_sync(1, 32 * kI8EpiWarps);
             }
-            if (write && n < g.N) {
+            if (write && nt > 0) {
                 // a wait that gave up leaves NaN (or the least integer)
                 const float sw = !live ? __int_as_float(0x7fc00000) : g.sw ? g.sw[n] : 1.0f;
+                size_t at = t0 * g.ldc + n;
 #pragma unroll
-                for (int q = 0; q < kI8MaxTn / 32; q++)
-                    if (q < nblk)
-#pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const size_t t = t0 + 16 * q + i;
-                            if (t < g.M)
-                                store_out(g.C, g.c_dtype, t * g.ldc + n, live ? acc[16 * q + i] : (int)0x80000000,
-                                          g.sa ? g.sa[t] : 1.0f, sw);
-                        }
+                for (int i = 0; i < kI8MaxTn / 2; i++) {
+                    if (i < nt)
+                        store_out(g.C, g.c_dtype, at, live ? acc[i] : (int)0x80000000, g.sa ? g.sa[t0 + i] : 1.0f,
+                                  sw);
+                    at += g.ldc;
+                }
             }
         }
     }
@@ -693,7 +714,7 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
     p.sps = p.steps ? (p.steps + (int)s - 1) / (int)s : 1;
     p.splits = p.steps ? (p.steps + p.sps - 1) / p.sps : 1;
     p.units = (int)(tiles * (size_t)p.splits);
-    p.ldf = (K + 15) / 16 * 16;
+    p.ldf = (K + 63) / 64 * 64;
     return p;
 }
 
@@ -767,13 +788,15 @@ cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool
     const cuuint64_t dw[2] = {(cuuint64_t)(repack_w ? p.ldf : a.K), (cuuint64_t)a.N};
     const cuuint64_t sw[1] = {(cuuint64_t)ldw};
     const cuuint32_t bw[2] = {kI8BK, 128};
-    const cuuint64_t dt[2] = {(cuuint64_t)p.ldf, (cuuint64_t)a.M};
-    const cuuint64_t stt[1] = {(cuuint64_t)p.ldf * 2};
-    const cuuint32_t bt[2] = {64, (cuuint32_t)(p.tn / 2)};
+    // the tokens as (64 k, token, block of 64 k)
+    const cuuint32_t estride3[3] = {1, 1, 1};
+    const cuuint64_t dt[3] = {64, (cuuint64_t)a.M, (cuuint64_t)(p.ldf / 64)};
+    const cuuint64_t stt[2] = {(cuuint64_t)p.ldf * 2, 128};
+    const cuuint32_t bt[3] = {64, (cuuint32_t)(p.tn / 2), 2};
     if (encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, (void *)w, dw, sw, bw, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
-        encode(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (void *)q.Af, dt, stt, bt, estride,
+        encode(&mt, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, (void *)q.Af, dt, stt, bt, estride3,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
