@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import NamedTuple
 
@@ -163,9 +164,9 @@ def c_api() -> ctypes.CDLL:
             lib.tcr_reduce_sum_noalloc.restype = ctypes.c_int
             lib.tcr_read_probe.argtypes = [vp, sz, vp, ctypes.c_int, ctypes.c_int, vp]
             lib.tcr_read_probe.restype = ctypes.c_int
-            lib.tcr_rmsnorm.argtypes = [ctypes.POINTER(tcr_norm_args), vp]
+            lib.tcr_rmsnorm.argtypes = [vp, vp]
             lib.tcr_rmsnorm.restype = ctypes.c_int
-            lib.tcr_rmsnorm_backward.argtypes = [ctypes.POINTER(tcr_norm_back_args), vp]
+            lib.tcr_rmsnorm_backward.argtypes = [vp, vp]
             lib.tcr_rmsnorm_backward.restype = ctypes.c_int
             lib.tcr_quantize_rows_i8.argtypes = [vp, sz, vp, sz, vp, sz, vp, sz, sz, ctypes.c_int, vp]
             lib.tcr_quantize_rows_i8.restype = ctypes.c_int
@@ -427,51 +428,64 @@ class NormOut(NamedTuple):
 
 def _float_code(t) -> int:
     import torch
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return BF16
-    if t.dtype == torch.float16:
+    if dt is torch.float16:
         return F16
-    if t.dtype == torch.float32:
+    if dt is torch.float32:
         return F32
-    raise TypeError(f"expected float16, bfloat16 or float32, got {t.dtype}")
+    raise TypeError(f"expected float16, bfloat16 or float32, got {dt}")
 
 
-def _matrix(name, t, shape, dtype, device, out=False):
+# A decoding step's calls are short beside what Python takes for them, so
+# these checks read as few properties of a tensor as they can.
+
+def _matrix(name, t, shape, dtype, dev, out=False):
     """(pointer, leading dimension) of a 2-D CUDA tensor with contiguous rows."""
-    if t.dim() != 2 or t.shape != shape:
-        raise ValueError(f"{name} must be 2-D of shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _mismatch(name, t, shape, dtype, dev)
     rows, cols = shape
-    if cols > 1 and t.stride(1) != 1:
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows (stride 1 along its columns)")
-    ld = t.stride(0) if rows > 1 else cols
-    if ld < cols and (out or ld != 0):
+    if rows <= 1:
+        ld = cols
+    elif ld < cols and (out or ld != 0):
         raise ValueError(f"{name} has overlapping rows")
     return t.data_ptr(), ld
 
 
-def _vector(name, t, n, dtype, device):
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+def _vector(name, t, n, dtype, dev):
+    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev:
+        _mismatch(name, t, (n,), dtype, dev)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _call(name, device, stream, *args):
-    """Call a C entry point on ``device``, its last argument the stream."""
+def _mismatch(name, t, shape, dtype, dev):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+
+
+def _call(name, dev, stream, *args):
+    """Call a C entry point on CUDA device ``dev``, its last argument the
+    stream (the current one if None)."""
     import torch
-    f = getattr(c_api(), name)
-    if torch.cuda.current_device() == device.index:
-        st = f(*args, _stream_handle(device, stream))
+    f = getattr(_lib or c_api(), name)
+    # the current stream's handle, without the Stream object around it
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(dev, stream)
+    if torch.cuda.current_device() == dev:
+        st = f(*args, s)
     else:
-        with torch.cuda.device(device):
-            st = f(*args, _stream_handle(device, stream))
+        with torch.cuda.device(dev):
+            st = f(*args, s)
     if st != OK:
         raise TcrError(st, name)
 
@@ -479,7 +493,13 @@ def _call(name, device, stream, *args):
 def _check_rows(name, x):
     if not x.is_cuda or x.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return x.shape, x.device
+    return x.shape, x.get_device()
+
+
+# tcr_norm_args and tcr_norm_back_args packed in one step (the same layout,
+# native alignment)
+_NORM_ARGS = struct.Struct("@PNPNPPNPNPPNNfii0P")
+_NORM_BACK_ARGS = struct.Struct("@PNPNPPPNPNPNNi0P")
 
 
 def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, h=None, out=None,
@@ -494,37 +514,37 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
     (stride 1 along the columns); x and residual may also be expanded rows.
     """
     import torch
-    shape, device = _check_rows("x", x)
+    shape, dev = _check_rows("x", x)
     rows, cols = shape
-    dt = _float_code(x)
+    dt, xt = _float_code(x), x.dtype
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or x.dtype, device=device)
+        out = torch.empty(shape, dtype=out_dtype or xt, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    i8 = out.dtype == torch.int8
-    a = tcr_norm_args()
-    a.x, a.ldx = _matrix("x", x, shape, x.dtype, device)
+    i8 = out.dtype is torch.int8
+    xp, ldx = _matrix("x", x, shape, xt, dev)
+    yp, ldy = _matrix("out", out, shape, torch.int8 if i8 else xt, dev, True)
+    rp = ldr = wp = hp = ldh = sp = tp = 0
     if residual is not None:
-        a.residual, a.ldr = _matrix("residual", residual, shape, x.dtype, device)
+        rp, ldr = _matrix("residual", residual, shape, xt, dev)
         if h is None:
-            h = torch.empty(shape, dtype=x.dtype, device=device)
+            h = torch.empty(shape, dtype=xt, device=x.device)
     if weight is not None:
-        a.weight = _vector("weight", weight, cols, x.dtype, device)
+        wp = _vector("weight", weight, cols, xt, dev)
     if h is not None:
-        a.h, a.ldh = _matrix("h", h, shape, x.dtype, device, out=True)
-    a.y, a.ldy = _matrix("out", out, shape, torch.int8 if i8 else x.dtype, device, out=True)
+        hp, ldh = _matrix("h", h, shape, xt, dev, True)
     if i8:
         if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=device)
-        a.scale = _vector("scale", scale, rows, torch.float32, device)
+            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        sp = _vector("scale", scale, rows, torch.float32, dev)
     else:
         scale = None
     if rstd is None and want_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=device)
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
     if rstd is not None:
-        a.rstd = _vector("rstd", rstd, rows, torch.float32, device)
-    a.rows, a.cols, a.eps, a.dtype, a.y_dtype = rows, cols, eps, dt, I8 if i8 else dt
-    _call("tcr_rmsnorm", device, stream, ctypes.byref(a))
+        tp = _vector("rstd", rstd, rows, torch.float32, dev)
+    _call("tcr_rmsnorm", dev, stream,
+          _NORM_ARGS.pack(xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, tp, rows, cols, eps, dt, I8 if i8 else dt))
     return NormOut(out, scale, h, rstd)
 
 
@@ -537,26 +557,26 @@ def tcr_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
     gradient of x and of the residual; dweight (float32) is None when there is
     no weight or it is not wanted."""
     import torch
-    shape, device = _check_rows("h", h)
+    shape, dev = _check_rows("h", h)
     rows, cols = shape
-    a = tcr_norm_back_args()
-    a.dtype = _float_code(h)
-    a.dy, a.lddy = _matrix("dy", dy, shape, h.dtype, device)
-    a.h, a.ldh = _matrix("h", h, shape, h.dtype, device)
-    a.rstd = _vector("rstd", rstd, rows, torch.float32, device)
+    dt, ht = _float_code(h), h.dtype
+    gp, ldg = _matrix("dy", dy, shape, ht, dev)
+    hp, ldh = _matrix("h", h, shape, ht, dev)
+    tp = _vector("rstd", rstd, rows, torch.float32, dev)
+    wp = dhp = lddh = dwp = 0
     if weight is not None:
-        a.weight = _vector("weight", weight, cols, h.dtype, device)
+        wp = _vector("weight", weight, cols, ht, dev)
     if dh is not None:
-        a.dh, a.lddh = _matrix("dh", dh, shape, h.dtype, device)
+        dhp, lddh = _matrix("dh", dh, shape, ht, dev)
     if dx is None:
-        dx = torch.empty(shape, dtype=h.dtype, device=device)
-    a.dx, a.lddx = _matrix("dx", dx, shape, h.dtype, device, out=True)
+        dx = torch.empty(shape, dtype=ht, device=h.device)
+    dxp, lddx = _matrix("dx", dx, shape, ht, dev, True)
     if dweight is None and weight is not None and want_dweight:
-        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+        dweight = torch.empty(cols, dtype=torch.float32, device=h.device)
     if dweight is not None:
-        a.dweight = _vector("dweight", dweight, cols, torch.float32, device)
-    a.rows, a.cols = rows, cols
-    _call("tcr_rmsnorm_backward", device, stream, ctypes.byref(a))
+        dwp = _vector("dweight", dweight, cols, torch.float32, dev)
+    _call("tcr_rmsnorm_backward", dev, stream,
+          _NORM_BACK_ARGS.pack(gp, ldg, hp, ldh, wp, tp, dhp, lddh, dxp, lddx, dwp, rows, cols, dt))
     return dx, dweight
 
 
@@ -565,18 +585,18 @@ def tcr_quantize_rows_i8(x, gate=None, out=None, scale=None, stream=None):
     (``tcr_quantize_rows_i8``).  A weight matrix's rows are its output
     channels."""
     import torch
-    shape, device = _check_rows("x", x)
+    shape, dev = _check_rows("x", x)
     rows, cols = shape
     if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=device)
+        out = torch.empty(shape, dtype=torch.int8, device=x.device)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=device)
+        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
     dt = _float_code(x)
-    xp, ldx = _matrix("x", x, shape, x.dtype, device)
-    gp, ldg = (None, 0) if gate is None else _matrix("gate", gate, shape, x.dtype, device)
-    qp, ldq = _matrix("out", out, shape, torch.int8, device, out=True)
-    sp = _vector("scale", scale, rows, torch.float32, device)
-    _call("tcr_quantize_rows_i8", device, stream, xp, ldx, gp, ldg, qp, ldq, sp, rows, cols, dt)
+    xp, ldx = _matrix("x", x, shape, x.dtype, dev)
+    gp, ldg = (None, 0) if gate is None else _matrix("gate", gate, shape, x.dtype, dev)
+    qp, ldq = _matrix("out", out, shape, torch.int8, dev, True)
+    sp = _vector("scale", scale, rows, torch.float32, dev)
+    _call("tcr_quantize_rows_i8", dev, stream, xp, ldx, gp, ldg, qp, ldq, sp, rows, cols, dt)
     return out, scale
 
 
@@ -584,16 +604,16 @@ def tcr_dequantize_rows_i8(q, scale, dtype=None, out=None, stream=None):
     """The values ``q * scale`` of rows of codes (``tcr_dequantize_rows_i8``),
     float32 unless ``dtype`` or ``out`` says otherwise."""
     import torch
-    shape, device = _check_rows("q", q)
+    shape, dev = _check_rows("q", q)
     rows, cols = shape
     if out is None:
-        out = torch.empty(shape, dtype=dtype or torch.float32, device=device)
+        out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype {dtype}")
-    qp, ldq = _matrix("q", q, shape, torch.int8, device)
-    sp = _vector("scale", scale, rows, torch.float32, device)
-    yp, ldy = _matrix("out", out, shape, out.dtype, device, out=True)
-    _call("tcr_dequantize_rows_i8", device, stream, qp, ldq, sp, yp, ldy, rows, cols, _float_code(out))
+    qp, ldq = _matrix("q", q, shape, torch.int8, dev)
+    sp = _vector("scale", scale, rows, torch.float32, dev)
+    yp, ldy = _matrix("out", out, shape, out.dtype, dev, True)
+    _call("tcr_dequantize_rows_i8", dev, stream, qp, ldq, sp, yp, ldy, rows, cols, _float_code(out))
     return out
 
 
@@ -609,21 +629,21 @@ def tcr_gemm_i8(A, W, scale_a=None, scale_w=None, out_dtype=None, out=None, stre
     N = W.shape[0]
     if W.shape[1] != K:
         raise ValueError(f"inner dimensions differ: {tuple(A.shape)} vs {tuple(W.shape)}")
-    device = A.device
+    dev = A.get_device()
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=device)
+        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=A.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    if out.dtype == torch.int32:
+    if out.dtype is torch.int32:
         if scale_a is not None or scale_w is not None:
             raise ValueError("int32 sums take no scales")
         dt = I32
     else:
         dt = _float_code(out)
-    ap, lda = _matrix("A", A, A.shape, torch.int8, device, out=True)
-    wp, ldw = _matrix("W", W, W.shape, torch.int8, device, out=True)
-    cp, ldc = _matrix("out", out, (M, N), out.dtype, device, out=True)
-    sa = None if scale_a is None else _vector("scale_a", scale_a, M, torch.float32, device)
-    sw = None if scale_w is None else _vector("scale_w", scale_w, N, torch.float32, device)
-    _call("tcr_gemm_i8", device, stream, ap, lda, wp, ldw, sa, sw, cp, ldc, M, N, K, dt)
+    ap, lda = _matrix("A", A, A.shape, torch.int8, dev, True)
+    wp, ldw = _matrix("W", W, W.shape, torch.int8, dev, True)
+    cp, ldc = _matrix("out", out, (M, N), out.dtype, dev, True)
+    sa = None if scale_a is None else _vector("scale_a", scale_a, M, torch.float32, dev)
+    sw = None if scale_w is None else _vector("scale_w", scale_w, N, torch.float32, dev)
+    _call("tcr_gemm_i8", dev, stream, ap, lda, wp, ldw, sa, sw, cp, ldc, M, N, K, dt)
     return out

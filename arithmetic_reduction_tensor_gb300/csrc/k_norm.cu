@@ -18,25 +18,43 @@ namespace tcr {
 
 constexpr int kOutSame = 0, kOutI8 = 1;
 
-template <int DT, int OP>
-__device__ __forceinline__ void row_value(const RowArgs &a, size_t r, size_t v, bool al, float (&y)[kRv])
-{
+// The rows of one call that a team works on.
+template <int DT>
+struct RowPtrs {
     using E = typename Elem<DT>::T;
-    unpack<DT>(load_raw<DT>((const E *)a.x + r * a.ldx, a.cols, v, al), y);
-    if constexpr (OP == kRowNorm) {
-        if (a.r) {
-            float b[kRv];
-            unpack<DT>(load_raw<DT>((const E *)a.r + r * a.ldr, a.cols, v, al), b);
-#pragma unroll
-            for (int k = 0; k < kRv; k++) y[k] = __fadd_rn(y[k], b[k]);
-        }
-    } else if (a.r) {
-        float g[kRv];
-        unpack<DT>(load_raw<DT>((const E *)a.r + r * a.ldr, a.cols, v, al), g);
-#pragma unroll
-        for (int k = 0; k < kRv; k++)
-            y[k] = __fmul_rn(__fdiv_rn(g[k], __fadd_rn(1.0f, expf(-g[k]))), y[k]);
+    const E *x, *r;
+    E *h;
+    void *y;
+    __device__ __forceinline__ RowPtrs(const RowArgs &a, size_t row, size_t y_bytes)
+    {
+        x = (const E *)a.x + row * a.ldx;
+        r = a.r ? (const E *)a.r + row * a.ldr : nullptr;
+        h = a.h ? (E *)a.h + row * a.ldh : nullptr;
+        y = (char *)a.y + row * a.ldy * y_bytes;
     }
+};
+
+// The values of a vector from its inputs as loaded.
+template <int DT, int OP>
+__device__ __forceinline__ void row_value(const RawVec<DT> &x, const RawVec<DT> &r, bool has_r, float (&y)[kRv])
+{
+    unpack<DT>(x, y);
+    if (!has_r) return;
+    float b[kRv];
+    unpack<DT>(r, b);
+#pragma unroll
+    for (int k = 0; k < kRv; k++)
+        y[k] = OP == kRowNorm ? __fadd_rn(y[k], b[k])
+                              : __fmul_rn(__fdividef(b[k], __fadd_rn(1.0f, __expf(-b[k]))), y[k]);
+}
+
+template <int DT, int OP>
+__device__ __forceinline__ void row_value(const RowArgs &a, const RowPtrs<DT> &p, uint32_t cols, uint32_t v,
+                                          float (&y)[kRv])
+{
+    const RawVec<DT> x = load_raw<DT>(p.x, cols, v, a.al_x);
+    const RawVec<DT> r = p.r ? load_raw<DT>(p.r, cols, v, a.al_r) : RawVec<DT>();
+    row_value<DT, OP>(x, r, p.r != nullptr, y);
 }
 
 __device__ __forceinline__ float squares8(const float (&h)[kRv])
@@ -47,50 +65,100 @@ __device__ __forceinline__ float squares8(const float (&h)[kRv])
     return tree8(e);
 }
 
-__device__ __forceinline__ float rstd_of(float s, size_t cols, float eps)
+__device__ __forceinline__ float rstd_of(float s, uint32_t cols, float eps)
 {
     return __frsqrt_rn(__fadd_rn(__fdiv_rn(s, (float)cols), eps));
 }
 
 template <int DT>
-__device__ __forceinline__ void apply_norm(const RowArgs &a, size_t v, float rstd, float (&h)[kRv])
+__device__ __forceinline__ RawVec<DT> load_weight(const RowArgs &a, uint32_t cols, uint32_t v)
+{
+    return a.w ? load_raw<DT>((const typename Elem<DT>::T *)a.w, cols, v, a.al_w) : RawVec<DT>();
+}
+
+template <int DT>
+__device__ __forceinline__ void apply_norm(const RawVec<DT> &wr, bool has_w, float rstd, float (&h)[kRv])
 {
     float w[kRv];
-    if (a.w) unpack<DT>(load_raw<DT>((const typename Elem<DT>::T *)a.w, a.cols, v, a.al_w), w);
+    if (has_w) unpack<DT>(wr, w);
 #pragma unroll
     for (int k = 0; k < kRv; k++) {
         h[k] = __fmul_rn(h[k], rstd);
-        if (a.w) h[k] = __fmul_rn(h[k], w[k]);
+        if (has_w) h[k] = __fmul_rn(h[k], w[k]);
     }
 }
 
-__device__ __forceinline__ uint32_t amax8(const float (&y)[kRv], uint32_t m)
+// Rows of at most 8 T columns, one vector a thread: teams of T threads
+// (T = 32: eight to a CTA; else the CTA, of 32 ceil(vectors / 32) <= T
+// threads) walk the rows, each loading its next row before it finishes the
+// current one, so that loads stay in flight across the row's barriers.
+template <int DT, int OP, int OUT, int T>
+__global__ void __launch_bounds__(T == 32 ? 256 : T, T == 32 ? 4 : 1024 / T)
+row_stream_kernel(const RowArgs a)
 {
-#pragma unroll
-    for (int k = 0; k < kRv; k++) m = max(m, __float_as_uint(y[k]) & 0x7fffffffu);
-    return m;
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    __shared__ float red[2][team_floats<T>()];
+    __shared__ uint32_t redm[2][32];
+    using E = typename Elem<DT>::T;
+    constexpr size_t y_bytes = OUT == kOutI8 ? 1 : sizeof(E);
+    const uint32_t v = T == 32 ? threadIdx.x & 31 : threadIdx.x, cols = (uint32_t)a.cols;
+    const uint32_t threads = T == 32 ? 32 : blockDim.x;
+    const size_t team = T == 32 ? (size_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    const size_t teams = T == 32 ? (size_t)gridDim.x * 8 : gridDim.x;
+    const bool has_r = a.r != nullptr, has_w = a.w != nullptr;
+    const RawVec<DT> w = OP == kRowNorm ? load_weight<DT>(a, cols, v) : RawVec<DT>();
+    RawVec<DT> x = {}, b = {};
+    auto load = [&](size_t r) {
+        x = load_raw<DT>((const E *)a.x + r * a.ldx, cols, v, a.al_x);
+        if (has_r) b = load_raw<DT>((const E *)a.r + r * a.ldr, cols, v, a.al_r);
+    };
+    if (team < a.rows) load(team);
+    int buf = 0;
+    for (size_t r = team; r < a.rows; r += teams, buf ^= 1) {
+        float y[kRv];
+        row_value<DT, OP>(x, b, has_r, y);
+        if (r + teams < a.rows) load(r + teams);
+        // two buffers each: a thread reaches the next row's write of one only
+        // after every thread has passed a barrier of the row between
+        if constexpr (OP == kRowNorm) {
+            const float rstd = rstd_of(team_sum<T>(squares8(y), red[buf], threads), cols, a.eps);
+            if (a.rstd && v == 0) a.rstd[r] = rstd;
+            if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, cols, v, a.al_h, y);
+            apply_norm<DT>(w, has_w, rstd, y);
+        }
+        char *out = (char *)a.y + r * a.ldy * y_bytes;
+        if constexpr (OUT == kOutSame) {
+            store_vec<DT>((E *)out, cols, v, a.al_y, y);
+        } else {
+            float scale, per;
+            const float m = kRv * v < cols ? amax8(y, 0.0f) : 0.0f;
+            i8_scale(team_max<T>(__float_as_uint(m), redm[buf], threads), scale, per);
+            if (v == 0) a.scale[r] = scale;
+            store_codes((int8_t *)out, cols, v, a.al_y, y, per);
+        }
+    }
 }
 
-// Rows of at most 8 T NV columns, one team of T threads each (T = 32: four
-// to a CTA).
+// Rows of at most 8 T NV columns, one CTA a row, NV vectors a thread.
 template <int DT, int OP, int OUT, int T, int NV>
-__global__ void __launch_bounds__(T == 32 ? 128 : T)
+__global__ void __launch_bounds__(T)
 row_kernel(const RowArgs a)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
-    __shared__ float red[T == 32 ? 1 : T];
+    __shared__ float red[team_floats<T>()];
     __shared__ uint32_t redm[32];
     using E = typename Elem<DT>::T;
-    const size_t r = T == 32 ? (size_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
-    if (r >= a.rows) return;               // T = 32 only: whole warps leave
-    const int t = T == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const size_t r = blockIdx.x;
+    const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
+    const RowPtrs<DT> p(a, r, OUT == kOutI8 ? 1 : sizeof(E));
     float y[NV][kRv];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const size_t v = (size_t)t + (size_t)i * T;
-        if (kRv * v < a.cols) {
-            row_value<DT, OP>(a, r, v, a.al_in, y[i]);
+        const uint32_t v = t + (uint32_t)(i * T);
+        if (kRv * v < cols) {
+            row_value<DT, OP>(a, p, cols, v, y[i]);
         } else {
 #pragma unroll
             for (int k = 0; k < kRv; k++) y[i][k] = 0.0f;
@@ -101,31 +169,31 @@ row_kernel(const RowArgs a)
         float s[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++) s[i] = squares8(y[i]);
-        rstd = rstd_of(team_sum<T>(halving<NV>(s), red), a.cols, a.eps);
+        rstd = rstd_of(team_sum<T>(halving<NV>(s), red), cols, a.eps);
         if (a.rstd && t == 0) a.rstd[r] = rstd;
     }
-    uint32_t m = 0u;
+    float m = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; i++) {
-        const size_t v = (size_t)t + (size_t)i * T;
-        if (kRv * v >= a.cols) continue;
+        const uint32_t v = t + (uint32_t)(i * T);
+        if (kRv * (v & ~31u) >= cols) continue;         // whole warps: stores are warp-wide
         if constexpr (OP == kRowNorm) {
-            if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, a.cols, v, a.al_h, y[i]);
-            apply_norm<DT>(a, v, rstd, y[i]);
+            if (p.h) store_vec<DT>(p.h, cols, v, a.al_h, y[i]);
+            apply_norm<DT>(load_weight<DT>(a, cols, v), a.w != nullptr, rstd, y[i]);
         }
         if constexpr (OUT == kOutSame)
-            store_vec<DT>((E *)a.y + r * a.ldy, a.cols, v, a.al_y, y[i]);
+            store_vec<DT>((E *)p.y, cols, v, a.al_y, y[i]);
         else
             m = amax8(y[i], m);
     }
     if constexpr (OUT == kOutI8) {
         float scale, per;
-        i8_scale(team_max<T>(m, redm), scale, per);
+        i8_scale(team_max<T>(__float_as_uint(m), redm), scale, per);
         if (t == 0) a.scale[r] = scale;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const size_t v = (size_t)t + (size_t)i * T;
-            if (kRv * v < a.cols) store_codes((int8_t *)a.y + r * a.ldy, a.cols, v, a.al_y, y[i], per);
+            const uint32_t v = t + (uint32_t)(i * T);
+            if (kRv * (v & ~31u) < cols) store_codes((int8_t *)p.y, cols, v, a.al_y, y[i], per);
         }
     }
 }
@@ -137,66 +205,79 @@ template <int DT, int OP, int OUT>
 __global__ void __launch_bounds__(kRowLongT)
 row_long_kernel(const RowArgs a)
 {
-    constexpr int T = kRowLongT;
+    constexpr uint32_t T = kRowLongT;
     pdl_launch_dependents();
     pdl_wait_primary();
-    __shared__ float red[T];
+    __shared__ float red[team_floats<(int)T>()];
     __shared__ uint32_t redm[32];
     using E = typename Elem<DT>::T;
     const size_t r = blockIdx.x;
-    const int t = threadIdx.x;
-    const size_t nvec = (a.cols + kRv - 1) / kRv;
-    const uint32_t steps = (uint32_t)((nvec + T - 1) / T);
+    const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
+    const RowPtrs<DT> p(a, r, OUT == kOutI8 ? 1 : sizeof(E));
+    const uint32_t nvec = (cols + kRv - 1) / kRv;
+    const uint32_t steps = (nvec + T - 1) / T;
     const int bits = ceil_log2_sz(steps);
     float rstd = 0.0f;
     float y[kRv];
     if constexpr (OP == kRowNorm) {
-        TreeCounter<32> tc;
+        TreeCounter<16> tc;
         for (uint32_t j = 0; j < (1u << bits); j++) {
-            const size_t v = (size_t)t + (size_t)bit_reverse(j, bits) * T;
+            const uint32_t v = t + bit_reverse(j, bits) * T;
             float s = 0.0f;
             if (v < nvec) {
-                row_value<DT, OP>(a, r, v, a.al_in, y);
+                row_value<DT, OP>(a, p, cols, v, y);
                 s = squares8(y);
             }
             tc.push(s);
         }
-        rstd = rstd_of(team_sum<T>(tc.finish(), red), a.cols, a.eps);
+        rstd = rstd_of(team_sum<T>(tc.finish(), red), cols, a.eps);
         if (a.rstd && t == 0) a.rstd[r] = rstd;
     }
     float per = 0.0f;
     if constexpr (OUT == kOutI8) {
-        uint32_t m = 0u;
-        for (size_t v = t; v < nvec; v += T) {
-            row_value<DT, OP>(a, r, v, a.al_in, y);
-            if constexpr (OP == kRowNorm) apply_norm<DT>(a, v, rstd, y);
+        float m = 0.0f;
+        for (uint32_t v = t; v < nvec; v += T) {
+            row_value<DT, OP>(a, p, cols, v, y);
+            if constexpr (OP == kRowNorm) apply_norm<DT>(load_weight<DT>(a, cols, v), a.w != nullptr, rstd, y);
             m = amax8(y, m);
         }
         float scale;
-        i8_scale(team_max<T>(m, redm), scale, per);
+        i8_scale(team_max<T>(__float_as_uint(m), redm), scale, per);
         if (t == 0) a.scale[r] = scale;
     }
-    for (size_t v = t; v < nvec; v += T) {
-        row_value<DT, OP>(a, r, v, a.al_in, y);
+    for (uint32_t i = 0; i < steps; i++) {              // whole warps: stores are warp-wide
+        const uint32_t v = t + i * T;
+        row_value<DT, OP>(a, p, cols, v, y);
         if constexpr (OP == kRowNorm) {
-            if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, a.cols, v, a.al_h, y);
-            apply_norm<DT>(a, v, rstd, y);
+            if (p.h) store_vec<DT>(p.h, cols, v, a.al_h, y);
+            apply_norm<DT>(load_weight<DT>(a, cols, v), a.w != nullptr, rstd, y);
         }
         if constexpr (OUT == kOutSame)
-            store_vec<DT>((E *)a.y + r * a.ldy, a.cols, v, a.al_y, y);
+            store_vec<DT>((E *)p.y, cols, v, a.al_y, y);
         else
-            store_codes((int8_t *)a.y + r * a.ldy, a.cols, v, a.al_y, y, per);
+            store_codes((int8_t *)p.y, cols, v, a.al_y, y, per);
     }
 }
 
 // ---------------------------------------------------------------- codes read back
 
-// y = q * scale[row], 16 codes a thread; a team of `team` threads (a power
-// of two, at most 256) walks each row.
+// Four codes as binary32: with its sign bit flipped a code is q + 128, as
+// the low byte of 2^23's pattern 2^23 + q + 128, and one subtraction leaves q.
+__device__ __forceinline__ void codes4(uint32_t w, float *f)
+{
+    const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        f[k] = __fsub_rn(__uint_as_float(__byte_perm(u, 0x4b000000u, 0x7650u | (uint32_t)k)), 8388736.0f);
+}
+
+// y = q * scale[row], 8 codes a thread and step; a team of 2^team_log2
+// threads walks each row, a warp at least (short rows leave lanes idle
+// rather than split a warp between rows, whose stores are warp-wide).
 template <int DT>
 __global__ void __launch_bounds__(256)
 dequant_kernel(const int8_t *q, size_t ldq, const float *scale, typename Elem<DT>::T *y, size_t ldy,
-               size_t rows, size_t cols, int team_log2, bool al_q, bool al_y)
+               size_t rows, uint32_t cols, int team_log2, bool al_q, bool al_y)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -204,22 +285,36 @@ dequant_kernel(const int8_t *q, size_t ldq, const float *scale, typename Elem<DT
     if (r >= rows) return;
     const float s = scale[r];
     const int8_t *row = q + r * ldq;
-    const size_t step = (size_t)16 << team_log2;
-    for (size_t c = (size_t)(threadIdx.x & ((1 << team_log2) - 1)) * 16; c < cols; c += step) {
-        float f[2][kRv];
-        if (al_q && c + 16 <= cols) {
-            const uint4 u = ld16(row + c);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-                f[k / 8][k % 8] = __fmul_rn((float)(int8_t)(w[k / 4] >> (8 * (k % 4))), s);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; k++)
-                f[k / 8][k % 8] = c + k < cols ? __fmul_rn((float)row[c + k], s) : 0.0f;
+    typename Elem<DT>::T *out = y + r * ldy;
+    const uint32_t team = 1u << team_log2;
+    for (uint32_t v = threadIdx.x & (team - 1); kRv * (v & ~31u) < cols; v += team) {
+        const uint32_t left = vec_left(cols, v);
+        uint32_t w[2] = {0u, 0u};
+        const int8_t *p = row + kRv * v;
+        if (al_q && left == kRv) {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x;
+            w[1] = u.y;
+        } else if (left) {
+            // the 8-byte granules that the codes touch
+            const uint32_t m = (uint32_t)(uintptr_t)p & 7u;
+            uint32_t g[6] = {0u, 0u, 0u, 0u, 0u, 0u};
+            const uint2 lo = *reinterpret_cast<const uint2 *>(p - m);
+            g[0] = lo.x;
+            g[1] = lo.y;
+            if (m + left > 8) {
+                const uint2 hi = *reinterpret_cast<const uint2 *>(p - m + 8);
+                g[2] = hi.x;
+                g[3] = hi.y;
+            }
+            shift_words<2>(g, m, w);
         }
-        store_vec<DT>(y + r * ldy, cols, c / kRv, al_y, f[0]);
-        if (c + kRv < cols) store_vec<DT>(y + r * ldy, cols, c / kRv + 1, al_y, f[1]);
+        float f[kRv];
+        codes4(w[0], f);
+        codes4(w[1], f + 4);
+#pragma unroll
+        for (int k = 0; k < kRv; k++) f[k] = __fmul_rn(f[k], s);
+        store_vec<DT>(out, cols, v, al_y, f);
     }
 }
 
@@ -227,31 +322,40 @@ dequant_kernel(const int8_t *q, size_t ldq, const float *scale, typename Elem<DT
 
 namespace {
 
+// One vector a thread up to 1024 vectors, as many teams as fill 152 SMs with
+// 1024 threads each (fewer rows: one team a row); then four vectors a
+// thread, one CTA a row; then the row is read once per step.
 template <int DT, int OP, int OUT>
 const void *pick(size_t nvec, size_t rows, int &threads, size_t &grid)
 {
+    if (nvec <= 1024) {
+        size_t teams_per_cta = 1, ctas;
+        if (nvec <= 32) {
+            threads = 256;
+            teams_per_cta = 8;
+            ctas = 152 * 4;
+        } else {
+            threads = (int)((nvec + 31) / 32 * 32);
+            ctas = 152 * (size_t)(1024 / threads);
+        }
+        const size_t need = (rows + teams_per_cta - 1) / teams_per_cta;
+        grid = need < ctas ? need : ctas;
+        return nvec <= 32    ? (const void *)row_stream_kernel<DT, OP, OUT, 32>
+               : nvec <= 64  ? (const void *)row_stream_kernel<DT, OP, OUT, 64>
+               : nvec <= 128 ? (const void *)row_stream_kernel<DT, OP, OUT, 128>
+               : nvec <= 256 ? (const void *)row_stream_kernel<DT, OP, OUT, 256>
+               : nvec <= 512 ? (const void *)row_stream_kernel<DT, OP, OUT, 512>
+                             : (const void *)row_stream_kernel<DT, OP, OUT, 1024>;
+    }
     grid = rows;
-    // few rows: more threads to a row, fewer values to a thread (the same bits)
-    const bool few = rows <= 304;
-#define TCR_ROW(T_, NV_) (threads = T_, (const void *)row_kernel<DT, OP, OUT, T_, NV_>)
-    if (nvec <= 128 && !(few && nvec > 32)) {
-        threads = 128;
-        grid = (rows + 3) / 4;
-        if (nvec <= 32) return (const void *)row_kernel<DT, OP, OUT, 32, 1>;
-        if (nvec <= 64) return (const void *)row_kernel<DT, OP, OUT, 32, 2>;
-        return (const void *)row_kernel<DT, OP, OUT, 32, 4>;
+    if (nvec <= 2048) {
+        threads = 512;
+        return (const void *)row_kernel<DT, OP, OUT, 512, 4>;
     }
-    if (few) {
-        if (nvec <= 128) return TCR_ROW(128, 1);
-        if (nvec <= 256) return TCR_ROW(256, 1);
-        if (nvec <= 512) return TCR_ROW(512, 1);
+    if (nvec <= 4096) {
+        threads = 1024;
+        return (const void *)row_kernel<DT, OP, OUT, 1024, 4>;
     }
-    if (nvec <= 256) return TCR_ROW(128, 2);
-    if (nvec <= 512) return TCR_ROW(128, 4);
-    if (nvec <= 1024) return few ? TCR_ROW(512, 2) : TCR_ROW(256, 4);
-    if (nvec <= 2048) return TCR_ROW(512, 4);
-    if (nvec <= 4096) return TCR_ROW(1024, 4);
-#undef TCR_ROW
     threads = kRowLongT;
     return (const void *)row_long_kernel<DT, OP, OUT>;
 }
@@ -282,17 +386,18 @@ cudaError_t launch_rows_op(int op, int dtype, bool out_i8, const RowArgs &a, cud
 cudaError_t launch_dequant(int dtype, const int8_t *q, size_t ldq, const float *scale, void *y, size_t ldy,
                            size_t rows, size_t cols, cudaStream_t stream)
 {
-    int team_log2 = 0;
-    while (team_log2 < 8 && ((size_t)16 << team_log2) < cols) team_log2++;
+    int team_log2 = 5;
+    while (team_log2 < 8 && ((size_t)kRv << team_log2) < cols) team_log2++;
+    uint32_t ncols = (uint32_t)cols;
     const size_t grid = (rows + ((size_t)256 >> team_log2) - 1) / ((size_t)256 >> team_log2);
     const size_t es = dtype == kF32 ? 4 : 2;
-    bool al_q = ((uintptr_t)q & 15u) == 0 && (rows == 1 || ldq % 16 == 0);
+    bool al_q = ((uintptr_t)q & 7u) == 0 && (rows == 1 || ldq % 8 == 0);
     bool al_y = ((uintptr_t)y & 15u) == 0 && (rows == 1 || (ldy * es) % 16 == 0);
     const void *k = dtype == kF16    ? (const void *)dequant_kernel<kF16>
                     : dtype == kBF16 ? (const void *)dequant_kernel<kBF16>
                                      : (const void *)dequant_kernel<kF32>;
     void *args[] = {(void *)&q,    (void *)&ldq,  (void *)&scale,     (void *)&y,    (void *)&ldy,
-                    (void *)&rows, (void *)&cols, (void *)&team_log2, (void *)&al_q, (void *)&al_y};
+                    (void *)&rows, (void *)&ncols, (void *)&team_log2, (void *)&al_q, (void *)&al_y};
     return launch_first(k, dim3((unsigned)grid), dim3(256), args, 0, stream);
 }
 

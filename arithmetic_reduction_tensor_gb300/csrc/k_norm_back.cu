@@ -16,134 +16,144 @@
 namespace tcr {
 
 template <int DT>
-__device__ __forceinline__ void back_products(const float (&dy)[kRv], const float (&h)[kRv],
-                                              const float (&w)[kRv], float rstd, float (&xh)[kRv],
-                                              float (&g)[kRv])
-{
-#pragma unroll
-    for (int k = 0; k < kRv; k++) {
-        xh[k] = __fmul_rn(h[k], rstd);
-        g[k] = __fmul_rn(dy[k], w[k]);
-    }
-}
+struct BackRow {
+    RawVec<DT> dy, h, dh;
+};
 
 template <int DT>
-__device__ __forceinline__ void load_weight(const BackArgs &a, size_t v, float (&w)[kRv])
-{
-    if (a.w) {
-        unpack<DT>(load_raw<DT>((const typename Elem<DT>::T *)a.w, a.cols, v, a.al_w), w);
-    } else {
-#pragma unroll
-        for (int k = 0; k < kRv; k++) w[k] = 1.0f;
-    }
-}
-
-template <int DT>
-__device__ __forceinline__ void store_dx(const BackArgs &a, size_t r, size_t v, float rstd, float c,
-                                         const float (&xh)[kRv], const float (&g)[kRv])
+__device__ __forceinline__ void load_row(const BackArgs &a, size_t r, uint32_t v, BackRow<DT> &b)
 {
     using E = typename Elem<DT>::T;
+    const uint32_t cols = (uint32_t)a.cols;
+    b.dy = load_raw<DT>((const E *)a.dy + r * a.lddy, cols, v, a.al_dy);
+    b.h = load_raw<DT>((const E *)a.h + r * a.ldh, cols, v, a.al_h);
+    if (a.dh) b.dh = load_raw<DT>((const E *)a.dh + r * a.lddh, cols, v, a.al_dh);
+}
+
+template <int DT>
+__device__ __forceinline__ RawVec<DT> load_weight(const BackArgs &a, uint32_t v)
+{
+    return load_raw<DT>((const typename Elem<DT>::T *)a.w, (uint32_t)a.cols, v, a.al_w);
+}
+
+// xh and g of a vector; returns the tree over g * xh and, where `acc` is
+// given, adds dy * xh to it.
+template <int DT>
+__device__ __forceinline__ float back_products(const BackArgs &a, const BackRow<DT> &b, const RawVec<DT> &wr,
+                                               float rstd, float (&xh)[kRv], float (&g)[kRv], float *acc)
+{
+    float w[kRv], e[kRv];
+    unpack<DT>(b.h, xh);
+    unpack<DT>(b.dy, g);
+    if (a.w) unpack<DT>(wr, w);
+#pragma unroll
+    for (int k = 0; k < kRv; k++) {
+        xh[k] = __fmul_rn(xh[k], rstd);
+        if (acc) acc[k] = __fadd_rn(acc[k], __fmul_rn(g[k], xh[k]));
+        if (a.w) g[k] = __fmul_rn(g[k], w[k]);
+        e[k] = __fmul_rn(g[k], xh[k]);
+    }
+    return tree8(e);
+}
+
+template <int DT>
+__device__ __forceinline__ void store_dx(const BackArgs &a, size_t r, uint32_t v, const BackRow<DT> &b, float rstd,
+                                         float c, const float (&xh)[kRv], const float (&g)[kRv])
+{
     float dx[kRv];
 #pragma unroll
     for (int k = 0; k < kRv; k++) dx[k] = __fmul_rn(rstd, __fsub_rn(g[k], __fmul_rn(xh[k], c)));
     if (a.dh) {
         float d[kRv];
-        unpack<DT>(load_raw<DT>((const E *)a.dh + r * a.lddh, a.cols, v, a.al_dh), d);
+        unpack<DT>(b.dh, d);
 #pragma unroll
         for (int k = 0; k < kRv; k++) dx[k] = __fadd_rn(dx[k], d[k]);
     }
-    store_vec<DT>((E *)a.dx + r * a.lddx, a.cols, v, a.al_dx, dx);
+    store_vec<DT>((typename Elem<DT>::T *)a.dx + r * a.lddx, (uint32_t)a.cols, v, a.al_dx, dx);
 }
 
 // partial[b * cols + j]: CTA b's sum of column j
-__device__ __forceinline__ void store_partial(const BackArgs &a, size_t v, const float (&acc)[kRv])
+__device__ __forceinline__ void store_partial(const BackArgs &a, uint32_t v, const float (&acc)[kRv])
 {
     float *p = a.partial + (size_t)blockIdx.x * a.cols + kRv * v;
+    const uint32_t left = vec_left((uint32_t)a.cols, v);
+    if (left == kRv && (a.cols & 3) == 0) {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        return;
+    }
 #pragma unroll
-    for (int k = 0; k < kRv; k++)
-        if (kRv * v + k < a.cols) p[k] = acc[k];
+    for (uint32_t k = 0; k < kRv; k++)
+        if (k < left) p[k] = acc[k];
 }
 
-// Rows of at most 8 T NV columns.
-template <int DT, int T, int NV>
-__global__ void __launch_bounds__(T)
+// Rows of at most 8 T vectors, one a thread; a CTA of 32 ceil(vectors / 32)
+// <= T threads.  The next row's inputs are loaded before the current row's
+// sum is waited for, so that loads stay in flight across the barrier (16384
+// rows of 4096 bfloat16: 165 us without, one vector a thread either way).
+template <int DT, int T>
+__global__ void __launch_bounds__(T, DT == kF32 ? 1 : 1024 / T)
 back_kernel(const BackArgs a)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
-    __shared__ float red[2][T];
-    using E = typename Elem<DT>::T;
-    const int t = threadIdx.x;
-    float acc[NV][kRv];
+    __shared__ float red[2][team_floats<T>()];
+    const uint32_t v = threadIdx.x;
+    // lanes past the row take part in the row's sum with zeros
+    const RawVec<DT> w = a.w ? load_weight<DT>(a, v) : RawVec<DT>();
+    float acc[kRv];
 #pragma unroll
-    for (int i = 0; i < NV; i++)
-#pragma unroll
-        for (int k = 0; k < kRv; k++) acc[i][k] = 0.0f;
+    for (int k = 0; k < kRv; k++) acc[k] = 0.0f;
+    BackRow<DT> cur;
+    load_row<DT>(a, blockIdx.x, v, cur);
+    float rstd = a.rstd[blockIdx.x];
     int buf = 0;
     for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x, buf ^= 1) {
-        const float rstd = a.rstd[r];
-        float xh[NV][kRv], g[NV][kRv], s[NV];
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const size_t v = (size_t)t + (size_t)i * T;
-            s[i] = 0.0f;
-            if (kRv * v >= a.cols) continue;
-            float dy[kRv], h[kRv], w[kRv], e[kRv];
-            unpack<DT>(load_raw<DT>((const E *)a.dy + r * a.lddy, a.cols, v, a.al_dy), dy);
-            unpack<DT>(load_raw<DT>((const E *)a.h + r * a.ldh, a.cols, v, a.al_h), h);
-            load_weight<DT>(a, v, w);
-            back_products<DT>(dy, h, w, rstd, xh[i], g[i]);
-#pragma unroll
-            for (int k = 0; k < kRv; k++) {
-                e[k] = __fmul_rn(g[i][k], xh[i][k]);
-                acc[i][k] = __fadd_rn(acc[i][k], __fmul_rn(dy[k], xh[i][k]));
-            }
-            s[i] = tree8(e);
+        float xh[kRv], g[kRv];
+        const float s = back_products<DT>(a, cur, w, rstd, xh, g, acc);
+        const size_t next = r + gridDim.x;
+        BackRow<DT> ahead = {};
+        float rstd_ahead = 0.0f;
+        if (next < a.rows) {
+            load_row<DT>(a, next, v, ahead);
+            rstd_ahead = a.rstd[next];
         }
         // two buffers: a thread reaches the next row's write of this one only
         // after every thread has passed the barrier of the row between
-        const float c = __fdiv_rn(team_sum<T>(halving<NV>(s), red[buf]), (float)a.cols);
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const size_t v = (size_t)t + (size_t)i * T;
-            if (kRv * v < a.cols) store_dx<DT>(a, r, v, rstd, c, xh[i], g[i]);
-        }
+        const float c = __fdiv_rn(team_sum<T>(s, red[buf], blockDim.x), (float)a.cols);
+        store_dx<DT>(a, r, v, cur, rstd, c, xh, g);
+        cur = ahead;
+        rstd = rstd_ahead;
     }
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const size_t v = (size_t)t + (size_t)i * T;
-        if (kRv * v < a.cols) store_partial(a, v, acc[i]);
-    }
+    store_partial(a, v, acc);
 }
 
-// Longer rows: the row sums first (c[r]), then blocks of 8 T columns.
+// Longer rows: the row sums first (c[r]), then blocks of 8 * 256 columns.
 template <int DT>
 __global__ void __launch_bounds__(kRowLongT)
 back_long_sum_kernel(const BackArgs a, float *c_out)
 {
-    constexpr int T = kRowLongT;
+    constexpr uint32_t T = kRowLongT;
     pdl_launch_dependents();
     pdl_wait_primary();
-    __shared__ float red[T];
-    using E = typename Elem<DT>::T;
+    __shared__ float red[team_floats<T>()];
     const size_t r = blockIdx.x;
-    const size_t nvec = (a.cols + kRv - 1) / kRv;
-    const uint32_t steps = (uint32_t)((nvec + T - 1) / T);
+    const uint32_t nvec = (uint32_t)((a.cols + kRv - 1) / kRv);
+    const uint32_t steps = (nvec + T - 1) / T;
     const int bits = ceil_log2_sz(steps);
     const float rstd = a.rstd[r];
-    TreeCounter<32> tc;
+    BackArgs b = a;
+    b.dh = nullptr;
+    TreeCounter<16> tc;
     for (uint32_t j = 0; j < (1u << bits); j++) {
-        const size_t v = (size_t)threadIdx.x + (size_t)bit_reverse(j, bits) * T;
+        const uint32_t v = threadIdx.x + bit_reverse(j, bits) * T;
         float s = 0.0f;
         if (v < nvec) {
-            float dy[kRv], h[kRv], w[kRv], xh[kRv], g[kRv], e[kRv];
-            unpack<DT>(load_raw<DT>((const E *)a.dy + r * a.lddy, a.cols, v, a.al_dy), dy);
-            unpack<DT>(load_raw<DT>((const E *)a.h + r * a.ldh, a.cols, v, a.al_h), h);
-            load_weight<DT>(a, v, w);
-            back_products<DT>(dy, h, w, rstd, xh, g);
-#pragma unroll
-            for (int k = 0; k < kRv; k++) e[k] = __fmul_rn(g[k], xh[k]);
-            s = tree8(e);
+            BackRow<DT> row;
+            float xh[kRv], g[kRv];
+            load_row<DT>(b, r, v, row);
+            const RawVec<DT> w = a.w ? load_weight<DT>(a, v) : RawVec<DT>();
+            s = back_products<DT>(a, row, w, rstd, xh, g, nullptr);
         }
         tc.push(s);
     }
@@ -157,22 +167,18 @@ back_long_kernel(const BackArgs a, const float *c_in)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
-    using E = typename Elem<DT>::T;
-    const size_t v = (size_t)blockIdx.y * 256 + threadIdx.x;
-    if (kRv * v >= a.cols) return;
-    float acc[kRv], w[kRv];
-    load_weight<DT>(a, v, w);
+    const uint32_t v = blockIdx.y * 256 + threadIdx.x;
+    const RawVec<DT> w = a.w ? load_weight<DT>(a, v) : RawVec<DT>();
+    float acc[kRv];
 #pragma unroll
     for (int k = 0; k < kRv; k++) acc[k] = 0.0f;
     for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const float rstd = a.rstd[r];
-        float dy[kRv], h[kRv], xh[kRv], g[kRv];
-        unpack<DT>(load_raw<DT>((const E *)a.dy + r * a.lddy, a.cols, v, a.al_dy), dy);
-        unpack<DT>(load_raw<DT>((const E *)a.h + r * a.ldh, a.cols, v, a.al_h), h);
-        back_products<DT>(dy, h, w, rstd, xh, g);
-#pragma unroll
-        for (int k = 0; k < kRv; k++) acc[k] = __fadd_rn(acc[k], __fmul_rn(dy[k], xh[k]));
-        store_dx<DT>(a, r, v, rstd, c_in[r], xh, g);
+        BackRow<DT> row;
+        float xh[kRv], g[kRv];
+        load_row<DT>(a, r, v, row);
+        (void)back_products<DT>(a, row, w, rstd, xh, g, acc);
+        store_dx<DT>(a, r, v, row, rstd, c_in[r], xh, g);
     }
     store_partial(a, v, acc);
 }
@@ -185,8 +191,10 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *partial, siz
     __shared__ float s[32][33];
     const size_t j = (size_t)blockIdx.x * 32 + threadIdx.x;
     float acc = 0.0f;
-    if (j < cols)
+    if (j < cols) {
+#pragma unroll 8
         for (int g = threadIdx.y; g < G; g += 32) acc = __fadd_rn(acc, partial[(size_t)g * cols + j]);
+    }
     s[threadIdx.y][threadIdx.x] = acc;
     __syncthreads();
     // warp y folds column y of the 32
@@ -197,10 +205,23 @@ __global__ void __launch_bounds__(1024) dweight_kernel(const float *partial, siz
 
 // ---------------------------------------------------------------- host
 
+namespace {
+
+uint32_t team_of(size_t cols)
+{
+    const size_t nvec = (cols + kRv - 1) / kRv;
+    return nvec > kBackMaxVecs ? 1024u : (uint32_t)((nvec + 31) / 32 * 32);
+}
+
+}  // namespace
+
+// Enough CTAs for 1024 threads on each of 152 SMs, but (above one an SM) no
+// more than a quarter of the rows: a partial costs as much traffic as a row.
 int norm_back_groups(size_t rows, size_t cols)
 {
-    // about two CTAs on each of 152 SMs; fewer, larger CTAs for long rows
-    const size_t g = cols > 4096 ? 152 : 304;
+    const size_t full = (size_t)152 * (1024 / team_of(cols));
+    const size_t quarter = (rows + 3) / 4 > 152 ? (rows + 3) / 4 : 152;
+    size_t g = full < quarter ? full : quarter;
     return (int)(rows < g ? rows : g);
 }
 
@@ -216,23 +237,22 @@ template <int DT>
 cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
 {
     const size_t nvec = (a.cols + kRv - 1) / kRv;
-    void *args[] = {(void *)&a};
-    const dim3 grid((unsigned)G);
-#define TCR_BACK(T_, NV_) launch_first((const void *)back_kernel<DT, T_, NV_>, grid, dim3(T_), args, 0, stream)
-    if (nvec <= 64) return TCR_BACK(64, 1);
-    if (nvec <= 128) return TCR_BACK(128, 1);
-    if (nvec <= 256) return TCR_BACK(256, 1);
-    if (nvec <= 512) return TCR_BACK(256, 2);
-    if (nvec <= 1024) return TCR_BACK(512, 2);
-    if (nvec <= kBackMaxVecs) return TCR_BACK(1024, 2);
-#undef TCR_BACK
+    if (nvec <= kBackMaxVecs) {
+        void *args[] = {(void *)&a};
+        const void *k = nvec <= 64    ? (const void *)back_kernel<DT, 64>
+                        : nvec <= 128 ? (const void *)back_kernel<DT, 128>
+                        : nvec <= 256 ? (const void *)back_kernel<DT, 256>
+                        : nvec <= 512 ? (const void *)back_kernel<DT, 512>
+                                      : (const void *)back_kernel<DT, 1024>;
+        return launch_first(k, dim3((unsigned)G), dim3(team_of(a.cols)), args, 0, stream);
+    }
     float *c = a.partial + (size_t)G * a.cols;
-    void *args1[] = {(void *)&a, (void *)&c};
+    void *args[] = {(void *)&a, (void *)&c};
     cudaError_t e = launch_first((const void *)back_long_sum_kernel<DT>, dim3((unsigned)a.rows), dim3(kRowLongT),
-                                 args1, 0, stream);
+                                 args, 0, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid2((unsigned)G, (unsigned)((nvec + 255) / 256));
-    return launch_first((const void *)back_long_kernel<DT>, grid2, dim3(256), args1, 0, stream);
+    const dim3 grid((unsigned)G, (unsigned)((nvec + 255) / 256));
+    return launch_first((const void *)back_long_kernel<DT>, grid, dim3(256), args, 0, stream);
 }
 
 }  // namespace

@@ -207,7 +207,7 @@ struct RowArgs {
     float *scale, *rstd;
     float eps;
     size_t rows, cols;
-    bool al_in, al_w, al_h, al_y;    // 16-byte aligned rows (codes: 8-byte)
+    bool al_x, al_r, al_w, al_h, al_y;   // 16-byte aligned rows (codes: 8-byte)
 };
 cudaError_t launch_rows_op(int op, int dtype, bool out_i8, const RowArgs &a, cudaStream_t stream);
 // y = q * scale[row] in `dtype`.
@@ -218,7 +218,7 @@ cudaError_t launch_dequant(int dtype, const int8_t *q, size_t ldq, const float *
 // (norm_back_groups) in scratch and their declared sum.  Rows of more than
 // kBackMaxVecs vectors of 8 take one more launch and a float of scratch
 // each.
-constexpr size_t kBackMaxVecs = 2048;
+constexpr size_t kBackMaxVecs = 1024;
 struct BackArgs {
     const void *dy, *h, *w, *dh;     // w, dh may be null
     const float *rstd;

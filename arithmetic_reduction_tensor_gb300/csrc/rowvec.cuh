@@ -68,33 +68,70 @@ struct RawVec {
     uint4 q[DT == kF32 ? 2 : 1];
 };
 
-// Vector v (8 v < cols) of a row at any element alignment.  A whole vector
-// of a 16-byte aligned row is one 16-byte load (two of binary32), anything
-// else is read element by element.
+// Bytes sh .. sh + 4 N - 1 of the words w[0 .. N + 3] (0 <= sh < 16; the
+// same sh in every lane that runs together, so the selects are uniform).
+template <int N>
+__device__ __forceinline__ void shift_words(const uint32_t (&w)[N + 4], uint32_t sh, uint32_t (&o)[N])
+{
+    uint32_t a[N + 2], b[N + 1];
+#pragma unroll
+    for (int k = 0; k < N + 2; k++) a[k] = (sh & 8u) ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < N + 1; k++) b[k] = (sh & 4u) ? a[k + 1] : a[k];
+#pragma unroll
+    for (int k = 0; k < N; k++) o[k] = __funnelshift_r(b[k], b[k + 1], 8u * (sh & 3u));
+}
+
+// The elements of vector v that the row has.
+__device__ __forceinline__ uint32_t vec_left(uint32_t cols, uint32_t v)
+{
+    return kRv * v >= cols ? 0u : min(cols - kRv * v, (uint32_t)kRv);
+}
+
+// Vector v of a row at any element alignment; elements past cols read as 0.
+// A whole vector of a 16-byte aligned row is one 16-byte load (two of
+// binary32).  Otherwise the 16-byte granules that its elements touch are
+// read and shifted in registers: up to 15 bytes before the row's first or
+// after its last element, in a granule that holds one of them.  (Element by
+// element, rows of 5001 bfloat16 took 2.5 times as long.)
 template <int DT>
 __device__ __forceinline__ RawVec<DT> load_raw(const typename Elem<DT>::T *row, size_t cols, size_t v,
                                                bool aligned)
 {
+    constexpr int es = DT == kF32 ? 4 : 2, NW = 2 * es;      // words of a vector
     RawVec<DT> r;
-    const typename Elem<DT>::T *p = row + kRv * v;
+    const char *p = (const char *)(row + kRv * v);
     if (aligned && kRv * v + kRv <= cols) {
 #pragma unroll
-        for (int k = 0; k < (DT == kF32 ? 2 : 1); k++) r.q[k] = ld16((const char *)p + 16 * k);
+        for (int k = 0; k < NW / 4; k++) r.q[k] = ld16(p + 16 * k);
         return r;
     }
-    const size_t left = kRv * v < cols ? cols - kRv * v : 0;
-    if constexpr (DT == kF32) {
-        uint32_t e[8];
+    const uint32_t left = vec_left(cols, v);
+    const uint32_t m = (uint32_t)(uintptr_t)p & 15u;
+    const uint32_t end = left ? m + left * es : 0u;          // bytes of the granules in use
+    p -= m;
+    uint32_t w[NW + 4], o[NW];
 #pragma unroll
-        for (int k = 0; k < 8; k++) e[k] = (size_t)k < left ? p[k] : 0u;
-        r.q[0] = make_uint4(e[0], e[1], e[2], e[3]);
-        r.q[1] = make_uint4(e[4], e[5], e[6], e[7]);
-    } else {
-        uint16_t e[8];
-#pragma unroll
-        for (int k = 0; k < 8; k++) e[k] = (size_t)k < left ? p[k] : (uint16_t)0;
-        r.q[0] = make_uint4(pack2(e[0], e[1]), pack2(e[2], e[3]), pack2(e[4], e[5]), pack2(e[6], e[7]));
+    for (int k = 0; k < NW / 4 + 1; k++) {
+        uint4 g = make_uint4(0u, 0u, 0u, 0u);
+        if (16u * k < end) g = ld16(p + 16 * k);
+        w[4 * k] = g.x;
+        w[4 * k + 1] = g.y;
+        w[4 * k + 2] = g.z;
+        w[4 * k + 3] = g.w;
     }
+    shift_words<NW>(w, m, o);
+    if (left < kRv) {
+#pragma unroll
+        for (int k = 0; k < NW; k++) {
+            if constexpr (es == 4)
+                o[k] = (uint32_t)k < left ? o[k] : 0u;
+            else
+                o[k] = 2u * k + 1u < left ? o[k] : 2u * k < left ? o[k] & 0xffffu : 0u;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < NW / 4; k++) r.q[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
     return r;
 }
 
@@ -115,26 +152,99 @@ __device__ __forceinline__ void unpack(const RawVec<DT> &r, float (&f)[kRv])
     }
 }
 
-template <int DT>
-__device__ __forceinline__ void store_vec(typename Elem<DT>::T *row, size_t cols, size_t v, bool aligned,
-                                          const float (&f)[kRv])
+// Store a vector of NW words (the elements es bytes each, `left` of them, 0
+// for a lane without a vector) where rows are not aligned: the lanes of a
+// warp hold consecutive vectors, and between them cover whole 16-byte
+// granules, so a lane stores the granules that begin in the vector before
+// its own (taken over by a shuffle) or in its own.  What has no partner (a
+// warp's first and last vectors, a row's last) goes element by element.
+// Every lane of the warp calls this.
+template <int NW, int es>
+__device__ __forceinline__ void store_shifted(char *p, uint32_t left, const uint32_t (&o)[NW])
 {
-    typename Elem<DT>::T *p = row + kRv * v;
-    if (aligned && kRv * v + kRv <= cols) {
-        if constexpr (DT == kF32) {
-            reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            *reinterpret_cast<uint4 *>(p) =
-                make_uint4(float2_to_word<DT>(f[0], f[1]), float2_to_word<DT>(f[2], f[3]),
-                           float2_to_word<DT>(f[4], f[5]), float2_to_word<DT>(f[6], f[7]));
-        }
+    constexpr uint32_t bytes = 4 * NW;                  // of a vector
+    constexpr uint32_t G = bytes < 16 ? bytes : 16;     // granule
+    constexpr uint32_t n = bytes / es;
+    const uint32_t m = (uint32_t)(uintptr_t)p & (G - 1);
+    const int lane = threadIdx.x & 31;
+    uint32_t prev[G / 4];                               // the last granule of the vector before
+#pragma unroll
+    for (uint32_t k = 0; k < G / 4; k++) prev[k] = __shfl_up_sync(kFull, o[NW - G / 4 + k], 1);
+    const bool joins = left == n && lane > 0 && m != 0u;        // (the vector before a vector is whole)
+    const bool next_joins = __shfl_down_sync(kFull, (int)joins, 1) && lane < 31;
+    if (left == n && m == 0u) {
+#pragma unroll
+        for (uint32_t k = 0; k < bytes / G; k++)
+            if constexpr (G == 16)
+                *reinterpret_cast<uint4 *>(p + 16 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            else
+                *reinterpret_cast<uint2 *>(p) = make_uint2(o[0], o[1]);
         return;
     }
-    const size_t left = kRv * v < cols ? cols - kRv * v : 0;
+    uint32_t w[NW + 4 + (G < 16 ? 2 : 0)], g[NW];
 #pragma unroll
-    for (int k = 0; k < kRv; k++)
-        if ((size_t)k < left) p[k] = float_to_elem<DT>(f[k]);
+    for (uint32_t k = 0; k < sizeof w / 4; k++) w[k] = 0u;
+#pragma unroll
+    for (uint32_t k = 0; k < G / 4; k++) w[k] = prev[k];
+#pragma unroll
+    for (uint32_t k = 0; k < NW; k++) w[G / 4 + k] = o[k];
+    uint32_t ww[NW + 4];
+#pragma unroll
+    for (int k = 0; k < NW + 4; k++) ww[k] = w[k];
+    shift_words<NW>(ww, G - m, g);                      // granules from p - m on
+    uint32_t from = 0, to = left;                       // own elements not covered by granules
+    if (joins) {
+#pragma unroll
+        for (uint32_t k = 0; k < bytes / G; k++)
+            if constexpr (G == 16)
+                *reinterpret_cast<uint4 *>(p - m + 16 * k) =
+                    make_uint4(g[4 * k], g[4 * k + 1], g[4 * k + 2], g[4 * k + 3]);
+            else
+                *reinterpret_cast<uint2 *>(p - m) = make_uint2(g[0], g[1]);
+        from = (bytes - m) / es;
+    }
+    if (next_joins) to = min(to, (bytes - m) / es);
+#pragma unroll
+    for (uint32_t k = 0; k < n; k++) {
+        if (k < from || k >= to) continue;
+        if constexpr (es == 4)
+            *reinterpret_cast<uint32_t *>(p + 4 * k) = o[k];
+        else if constexpr (es == 2)
+            *reinterpret_cast<uint16_t *>(p + 2 * k) = (uint16_t)(o[k / 2] >> (16 * (k % 2)));
+        else
+            *reinterpret_cast<uint8_t *>(p + k) = (uint8_t)(o[k / 4] >> (8 * (k % 4)));
+    }
+}
+
+// Vector v of a row, rounded to the type.  `aligned` (uniform): the rows are
+// 16-byte aligned.  Every lane of the warp calls it, with the vectors of
+// consecutive lanes consecutive; lanes past the row store nothing.
+template <int DT>
+__device__ __forceinline__ void store_vec(typename Elem<DT>::T *row, uint32_t cols, uint32_t v, bool aligned,
+                                          const float (&f)[kRv])
+{
+    constexpr int es = DT == kF32 ? 4 : 2, NW = 2 * es;
+    uint32_t o[NW];
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int k = 0; k < 8; k++) o[k] = __float_as_uint(f[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; k++) o[k] = float2_to_word<DT>(f[2 * k], f[2 * k + 1]);
+    }
+    char *p = (char *)(row + kRv * v);
+    if (aligned && kRv * v + kRv <= cols) {
+#pragma unroll
+        for (int k = 0; k < NW / 4; k++)
+            *reinterpret_cast<uint4 *>(p + 16 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    } else if (!aligned) {
+        store_shifted<NW, es>(p, vec_left(cols, v), o);
+    } else {
+        const uint32_t left = vec_left(cols, v);
+#pragma unroll
+        for (uint32_t k = 0; k < kRv; k++)
+            if (k < left) row[kRv * v + k] = (typename Elem<DT>::T)(es == 4 ? o[k] : o[k / 2] >> (16 * (k % 2)));
+    }
 }
 
 // The tree over the 8 values of a vector.
@@ -166,17 +276,39 @@ __device__ __forceinline__ float halving_lanes(float v)
 
 // The fold over a team of T threads (a warp, or the whole CTA) of values
 // already folded within each thread; every thread gets the result.  `red`:
-// T floats of shared memory, not in use by an earlier call that some thread
-// may still be reading.
+// team_floats<T>() floats of shared memory, not in use by an earlier call
+// that some thread may still be reading.  A CTA may have fewer than T
+// `threads` (whole warps); the absent ones count as +0.0.  Small teams:
+// every warp folds over the warps itself, one barrier.  From 16 warps on
+// that is more shared-memory reads than a second barrier costs: each warp
+// folds over the warps for some of the lanes and passes the results on.
 template <int T>
-__device__ __forceinline__ float team_sum(float v, float *red)
+__host__ __device__ constexpr int team_floats()
 {
-    if constexpr (T > 32) {
+    return T <= 32 ? 1 : T < 512 ? T : T / 32 * 33 + 32;
+}
+
+template <int T>
+__device__ __forceinline__ float team_sum(float v, float *red, uint32_t threads = T)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if constexpr (T >= 512) {
+        float *tot = red + T / 32 * 33;
+        const uint32_t warp = threadIdx.x >> 5, warps = threads >> 5;
+        red[warp * 33 + lane] = v;
+        __syncthreads();
+        for (uint32_t c = warp; c < 32; c += warps) {
+            const float a = halving_lanes(lane < warps ? red[lane * 33 + c] : 0.0f);
+            if (lane == 0) tot[c] = a;
+        }
+        __syncthreads();
+        v = tot[lane];
+    } else if constexpr (T > 32) {
         red[threadIdx.x] = v;
         __syncthreads();
         float a[T / 32];
 #pragma unroll
-        for (int w = 0; w < T / 32; w++) a[w] = red[32 * w + (threadIdx.x & 31)];
+        for (int w = 0; w < T / 32; w++) a[w] = 32u * w < threads ? red[32 * w + lane] : 0.0f;
         v = halving<T / 32>(a);
     }
     return halving_lanes(v);
@@ -186,13 +318,13 @@ __device__ __forceinline__ float team_sum(float v, float *red)
 // non-negative binary32 (their order as integers is the values', with NaN
 // above infinity, so a NaN is never lost).
 template <int T>
-__device__ __forceinline__ uint32_t team_max(uint32_t bits, uint32_t *red)
+__device__ __forceinline__ uint32_t team_max(uint32_t bits, uint32_t *red, uint32_t threads = T)
 {
     bits = __reduce_max_sync(kFull, bits);
     if constexpr (T > 32) {
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = bits;
         __syncthreads();
-        bits = __reduce_max_sync(kFull, (threadIdx.x & 31) < T / 32 ? red[threadIdx.x & 31] : 0u);
+        bits = __reduce_max_sync(kFull, (threadIdx.x & 31) < threads / 32 ? red[threadIdx.x & 31] : 0u);
     }
     return bits;
 }
@@ -217,29 +349,44 @@ __device__ __forceinline__ void i8_scale(uint32_t amax_bits, float &scale, float
         per = __fdiv_rn(127.0f, amax);
 }
 
-// rint(y * per) as an 8-bit code, ties to even; 0 where per is 0 (y may
-// then be NaN or infinite).
-__device__ __forceinline__ uint32_t i8_code(float y, float per)
-{
-    return per == 0.0f ? 0u : (uint32_t)__float2int_rn(__fmul_rn(y, per)) & 0xffu;
-}
-
-__device__ __forceinline__ void store_codes(int8_t *row, size_t cols, size_t v, bool aligned8,
+// The codes of a vector: rint(y * per), ties to even, the product not
+// rounded; 0 where per is 0 (y may then be NaN or infinite).  Adding
+// 1.5 * 2^23 in the same operation leaves the integer in the low bits (a
+// conversion instruction per value runs at an eighth of the rate).  Called
+// like store_vec; `aligned8`: the rows are 8-byte aligned.
+__device__ __forceinline__ void store_codes(int8_t *row, uint32_t cols, uint32_t v, bool aligned8,
                                             const float (&y)[kRv], float per)
 {
-    uint32_t c[kRv];
+    uint32_t o[2] = {0u, 0u};
+    if (per != 0.0f) {
 #pragma unroll
-    for (int k = 0; k < kRv; k++) c[k] = i8_code(y[k], per);
-    int8_t *p = row + kRv * v;
-    if (aligned8 && kRv * v + kRv <= cols) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                                                   c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
-        return;
+        for (int k = 0; k < 2; k++) {
+            uint32_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) c[i] = __float_as_uint(__fmaf_rn(y[4 * k + i], per, 12582912.0f));
+            o[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        }
     }
-    const size_t left = kRv * v < cols ? cols - kRv * v : 0;
+    char *p = (char *)(row + kRv * v);
+    if (aligned8 && kRv * v + kRv <= cols) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(o[0], o[1]);
+    } else if (!aligned8) {
+        store_shifted<2, 1>(p, vec_left(cols, v), o);
+    } else {
+        const uint32_t left = vec_left(cols, v);
 #pragma unroll
-    for (int k = 0; k < kRv; k++)
-        if ((size_t)k < left) p[k] = (int8_t)c[k];
+        for (uint32_t k = 0; k < kRv; k++)
+            if (k < left) row[kRv * v + k] = (int8_t)(o[k / 4] >> (8 * (k % 4)));
+    }
+}
+
+// The largest magnitude of m and a vector's values; NaN if one is NaN.
+__device__ __forceinline__ float amax8(const float (&y)[kRv], float m)
+{
+#pragma unroll
+    for (int k = 0; k < kRv; k += 2)
+        asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(y[k]), "f"(y[k + 1]));
+    return m;
 }
 
 // i with its `bits` low bits in reverse order: visiting a thread's vectors

@@ -128,7 +128,8 @@ tcr_status tcr_rmsnorm(const tcr_norm_args *args, void *stream)
     r.eps = a.eps;
     r.rows = a.rows;
     r.cols = a.cols;
-    r.al_in = rows_aligned(a.x, a.ldx, a.rows, eb) && (!a.residual || rows_aligned(a.residual, a.ldr, a.rows, eb));
+    r.al_x = rows_aligned(a.x, a.ldx, a.rows, eb);
+    r.al_r = rows_aligned(a.residual, a.ldr, a.rows, eb);
     r.al_w = is_aligned(a.weight, 16);
     r.al_h = rows_aligned(a.h, a.ldh, a.rows, eb);
     r.al_y = a.y_dtype == TCR_I8 ? rows_aligned(a.y, a.ldy, a.rows, 1, 8) : rows_aligned(a.y, a.ldy, a.rows, eb);
@@ -208,7 +209,8 @@ tcr_status tcr_quantize_rows_i8(const void *x, size_t ldx, const void *gate, siz
     r.scale = scale;
     r.rows = rows;
     r.cols = cols;
-    r.al_in = rows_aligned(x, ldx, rows, eb) && (!gate || rows_aligned(gate, ldg, rows, eb));
+    r.al_x = rows_aligned(x, ldx, rows, eb);
+    r.al_r = rows_aligned(gate, ldg, rows, eb);
     r.al_y = rows_aligned(q, ldq, rows, 1, 8);
     return of(launch_rows_op(kRowQuant, dtype, true, r, (cudaStream_t)stream));
 }

@@ -475,7 +475,10 @@ TCR_API tcr_status tcr_gemm_splitk(const void *A, const void *W, float *C, size_
  * row it is not looked at) and rows of any element alignment.  rows < 2^31,
  * cols <= 2^27, rows * cols < 2^40, rows * ld < 2^48.  dtype is TCR_F16,
  * TCR_BF16 or TCR_F32 and is that of every matrix of the call but the codes.
- * 16-byte aligned rows (base and ld) are the fast case.
+ * 16-byte aligned rows (base and ld) are the fast case; other rows are read
+ * as the 16-byte granules that hold their elements, so up to 15 bytes before
+ * the first or after the last element of a row, never outside a granule that
+ * the row touches.
  *
  * Declared order of their row sums.  Vector v is elements 8v .. 8v+7 (absent
  * ones +0.0) and has the value ((e0+e1)+(e2+e3))+((e4+e5)+(e6+e7)); the
@@ -486,7 +489,8 @@ TCR_API tcr_status tcr_gemm_splitk(const void *A, const void *W, float *C, size_
  * beside it, their number, the alignment, the launch or the GPU.
  *
  * Codes.  amax = the row's largest |y|, scale = amax / 127, code =
- * rint(y * (127 / amax)), ties to even: always in -127 .. 127.  A row with a
+ * rint(y * (127 / amax)), that product not rounded, ties to even: always in
+ * -127 .. 127.  A row with a
  * NaN or an infinity has scale NaN and codes 0 (all its values read back as
  * NaN); a row whose scale would be below 2^-126 has scale 0 and codes 0.
  *
@@ -536,12 +540,13 @@ TCR_API tcr_status tcr_rmsnorm(const tcr_norm_args *args, void *stream);
  *   rstd   its rstd (rows floats).
  *   dh     gradient that reaches h by the residual path, or NULL.
  *   dx     may be dy, h or dh itself (same pointer and ld).
- *   dweight  cols floats, or NULL; overwritten.  Its order: with G =
- *          min(rows, 304) (152 where cols > 4096), partial g adds rows g,
- *          g + G, .. in order; 32 sums add the partials k, k + 32, .. in
+ *   dweight  cols floats, or NULL; overwritten.  Its order: with t = 32 *
+ *          ceil(cols / 256), at most 1024, and G = min(rows, 152 *
+ *          floor(1024 / t), max(152, ceil(rows / 4))), partial g adds rows
+ *          g, g + G, .. in order; 32 sums add the partials k, k + 32, .. in
  *          order; those fold as the row sums' lanes do.  No atomics: the
  *          bits depend on the inputs, rows and cols only.
- * Takes G * cols floats of pool scratch (and rows more for cols > 16384).
+ * Takes G * cols floats of pool scratch (and rows more for cols > 8192).
  * rows == 0 writes dweight = +0.0.
  */
 typedef struct {
@@ -563,8 +568,9 @@ TCR_API tcr_status tcr_rmsnorm_backward(const tcr_norm_back_args *args, void *st
 
 /*
  * tcr_quantize_rows_i8 -- codes and scale of every row of y = x, or, with a
- * gate (NULL: none), of y = (gate / (1 + exp(-gate))) * x, each step rounded
- * to binary32 (exp as the CUDA library computes it).  q: rows x cols codes;
+ * gate (NULL: none), of y = (gate / (1 + exp(-gate))) * x, in binary32 with
+ * CUDA's fast exponential and quotient: y's relative error is below
+ * (8 + 1.2 max(0, -gate)) 2^-23, and y is 0 for gate < -87.  q: rows x cols codes;
  * scale: rows floats.  Weights are quantised the same way, a row being an
  * output channel.
  *

@@ -40,7 +40,8 @@ def codes(y):
     tiny = scale < 2.0 ** -126
     per = torch.tensor(127.0) / amax
     per = torch.where(bad | tiny, torch.zeros(()), per)
-    q = torch.where((bad | tiny)[:, None], torch.zeros(()), torch.round(y * per[:, None])).to(torch.int8)
+    # the product is exact in binary64: one rounding, to the code
+    q = torch.where((bad | tiny)[:, None], torch.zeros(()).double(), torch.round(y.double() * per.double()[:, None])).to(torch.int8)
     scale = torch.where(tiny, torch.zeros(()), scale)
     return q, torch.where(bad, torch.tensor(float("nan")), scale)
 
@@ -63,6 +64,12 @@ def norm64(x, r, w, eps):
     return h, y * w.double() if w is not None else y
 
 
+def groups(rows, cols):
+    """The partial sums of the weight's gradient."""
+    team = min(1024, (-(-cols // 8) + 31) // 32 * 32)
+    return min(rows, 152 * (1024 // team), max(152, -(-rows // 4)))
+
+
 def back(dy, h, w, rstd, dh):
     """(dx before rounding, dw) in binary32, in the declared orders."""
     rows, cols = h.shape
@@ -74,7 +81,7 @@ def back(dy, h, w, rstd, dh):
     if dh is not None:
         dx = dx + dh.float()
     e = dyf * xh
-    G = min(rows, 304 if cols <= 4096 else 152)
+    G = groups(rows, cols)
     part = torch.zeros(G, cols)
     for r in range(rows):
         part[r % G] = part[r % G] + e[r]

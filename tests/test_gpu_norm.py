@@ -202,10 +202,14 @@ def test_gated_quantiser(rows, cols, dt):
     y = gate.double() * torch.sigmoid(gate.double()) * up.double()
     b = both.cuda()
     q, s = tcr.tcr_quantize_rows_i8(b[:, cols:], gate=b[:, :cols])
-    want = y.abs().amax(1) / 127
-    # exp within 2 ulp (2^-22), then four roundings: within 2^-20 of y
-    assert ((s.cpu().double() - want).abs() <= 2.0 ** -19 * want).all()
-    assert ((q.cpu().double() - y / want[:, None]).abs() <= 0.5 + 127 * 2.0 ** -18).all()
+    want = y.abs().amax(1, keepdim=True) / 127
+    # CUDA's fast exponential is within 2 + 1.173 |g| ulp and counts where it
+    # is not small beside 1 (g < 0), its quotient within 2; three roundings;
+    # below exp(-87) the quotient gives 0
+    err = (8 + 1.2 * (-gate.double()).clamp(min=0)) * 2.0 ** -23 * y.abs() + 1e-30
+    serr = err.amax(1, keepdim=True) / 127 + 2.0 ** -22 * want
+    assert ((s.cpu().double()[:, None] - want).abs() <= serr).all()
+    assert ((q.cpu().double() - y / want).abs() <= 0.5 + (err + 127 * serr) / want).all()
     q, s = tcr.tcr_quantize_rows_i8(both.cuda())
     qc, sc = spec.codes(both.float())
     assert same(q, qc) and same(s, sc)
