@@ -88,12 +88,12 @@ __device__ __forceinline__ void apply_norm(const RawVec<DT> &wr, bool has_w, flo
     }
 }
 
-// Rows of at most 8 T columns, one vector a thread: teams of T threads
-// (T = 32: eight to a CTA; else the CTA, of 32 ceil(vectors / 32) <= T
-// threads) walk the rows, each loading its next row before it finishes the
-// current one, so that loads stay in flight across the row's barriers.
-template <int DT, int OP, int OUT, int T>
-__global__ void __launch_bounds__(T == 32 ? 256 : T, T == 32 ? 4 : 1024 / T)
+// Rows of at most 8 T NV columns, NV vectors a thread: teams of T threads
+// (T = 32: eight to a CTA; else the CTA) walk the rows, each loading its next
+// row before it finishes the current one, so that loads stay in flight
+// across the row's barriers.  MINB: the CTAs per SM that the registers allow.
+template <int DT, int OP, int OUT, int T, int NV, int MINB>
+__global__ void __launch_bounds__(T == 32 ? 256 : T, MINB)
 row_stream_kernel(const RowArgs a)
 {
     pdl_launch_dependents();
@@ -102,40 +102,60 @@ row_stream_kernel(const RowArgs a)
     __shared__ uint32_t redm[2][32];
     using E = typename Elem<DT>::T;
     constexpr size_t y_bytes = OUT == kOutI8 ? 1 : sizeof(E);
-    const uint32_t v = T == 32 ? threadIdx.x & 31 : threadIdx.x, cols = (uint32_t)a.cols;
+    const uint32_t t = T == 32 ? threadIdx.x & 31 : threadIdx.x, cols = (uint32_t)a.cols;
     const uint32_t threads = T == 32 ? 32 : blockDim.x;
     const size_t team = T == 32 ? (size_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
     const size_t teams = T == 32 ? (size_t)gridDim.x * 8 : gridDim.x;
     const bool has_r = a.r != nullptr, has_w = a.w != nullptr;
-    const RawVec<DT> w = OP == kRowNorm ? load_weight<DT>(a, cols, v) : RawVec<DT>();
-    RawVec<DT> x = {}, b = {};
+    RawVec<DT> x[NV], b[NV], w[NV];
     auto load = [&](size_t r) {
-        x = load_raw<DT>((const E *)a.x + r * a.ldx, cols, v, a.al_x);
-        if (has_r) b = load_raw<DT>((const E *)a.r + r * a.ldr, cols, v, a.al_r);
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            x[i] = load_raw<DT>((const E *)a.x + r * a.ldx, cols, t + i * T, a.al_x);
+            b[i] = has_r ? load_raw<DT>((const E *)a.r + r * a.ldr, cols, t + i * T, a.al_r) : RawVec<DT>();
+        }
     };
+#pragma unroll
+    for (int i = 0; i < NV; i++) w[i] = OP == kRowNorm ? load_weight<DT>(a, cols, t + i * T) : RawVec<DT>();
     if (team < a.rows) load(team);
     int buf = 0;
     for (size_t r = team; r < a.rows; r += teams, buf ^= 1) {
-        float y[kRv];
-        row_value<DT, OP>(x, b, has_r, y);
+        float y[NV][kRv];
+#pragma unroll
+        for (int i = 0; i < NV; i++) row_value<DT, OP>(x[i], b[i], has_r, y[i]);
         if (r + teams < a.rows) load(r + teams);
         // two buffers each: a thread reaches the next row's write of one only
         // after every thread has passed a barrier of the row between
+        float m = 0.0f;
         if constexpr (OP == kRowNorm) {
-            const float rstd = rstd_of(team_sum<T>(squares8(y), red[buf], threads), cols, a.eps);
-            if (a.rstd && v == 0) a.rstd[r] = rstd;
-            if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, cols, v, a.al_h, y);
-            apply_norm<DT>(w, has_w, rstd, y);
+            float s[NV];
+#pragma unroll
+            for (int i = 0; i < NV; i++) s[i] = squares8(y[i]);
+            const float rstd = rstd_of(team_sum<T>(halving<NV>(s), red[buf], threads), cols, a.eps);
+            if (a.rstd && t == 0) a.rstd[r] = rstd;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                if (kRv * ((t & ~31u) + i * T) >= cols) continue;         // whole warps: stores are warp-wide
+                if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, cols, t + i * T, a.al_h, y[i]);
+                apply_norm<DT>(w[i], has_w, rstd, y[i]);
+            }
         }
         char *out = (char *)a.y + r * a.ldy * y_bytes;
-        if constexpr (OUT == kOutSame) {
-            store_vec<DT>((E *)out, cols, v, a.al_y, y);
-        } else {
-            float scale, per;
-            const float m = kRv * v < cols ? amax8(y, 0.0f) : 0.0f;
+        float scale, per = 0.0f;
+        if constexpr (OUT == kOutI8) {
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (kRv * (t + i * T) < cols) m = amax8(y[i], m);
             i8_scale(team_max<T>(__float_as_uint(m), redm[buf], threads), scale, per);
-            if (v == 0) a.scale[r] = scale;
-            store_codes((int8_t *)out, cols, v, a.al_y, y, per);
+            if (t == 0) a.scale[r] = scale;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if (kRv * ((t & ~31u) + i * T) >= cols) continue;
+            if constexpr (OUT == kOutSame)
+                store_vec<DT>((E *)out, cols, t + i * T, a.al_y, y[i]);
+            else
+                store_codes((int8_t *)out, cols, t + i * T, a.al_y, y[i], per);
         }
     }
 }
@@ -322,31 +342,64 @@ dequant_kernel(const int8_t *q, size_t ldq, const float *scale, typename Elem<DT
 
 namespace {
 
-// One vector a thread up to 1024 vectors, as many teams as fill 152 SMs with
-// 1024 threads each (fewer rows: one team a row); then four vectors a
-// thread, one CTA a row; then the row is read once per step.
+// A launch of row_stream_kernel: as many CTAs as 152 SMs hold (or one team
+// a row).
+template <int DT, int OP, int OUT, int T, int NV, int MINB>
+const void *stream_of(size_t nvec, size_t rows, int &threads, size_t &grid)
+{
+    threads = T == 32 ? 256 : NV == 1 ? (int)((nvec + 31) / 32 * 32) : T;
+    const size_t need = T == 32 ? (rows + 7) / 8 : rows;
+    const size_t full = (size_t)152 * (size_t)(T == 32 ? MINB : MINB * T / threads);
+    grid = need < full ? need : full;
+    return (const void *)row_stream_kernel<DT, OP, OUT, T, NV, MINB>;
+}
+
+// Which shape serves a row length: the fastest of those measured at it, on
+// aligned rows.  A CTA an SM holds too few rows across the barriers, and a
+// thread's registers (its vectors, the next row's, the weight's) decide how
+// many CTAs fit: 65536 x 4096 binary16 with codes takes 277 us with 256
+// threads of 2 vectors and 3 CTAs an SM, 410 with 512 x 1 and 2, 314 with
+// 256 x 2 and 4 (spills), 303 with 128 x 4 and 4; 16384 x 8192 bfloat16 150
+// with 256 x 4 and 2, 189 with 1024 x 1.  The gate needs no weight and one
+// barrier, so one CTA more fits.
 template <int DT, int OP, int OUT>
 const void *pick(size_t nvec, size_t rows, int &threads, size_t &grid)
 {
-    if (nvec <= 1024) {
-        size_t teams_per_cta = 1, ctas;
-        if (nvec <= 32) {
-            threads = 256;
-            teams_per_cta = 8;
-            ctas = 152 * 4;
-        } else {
-            threads = (int)((nvec + 31) / 32 * 32);
-            ctas = 152 * (size_t)(1024 / threads);
+#define TCR_STREAM(T_, NV_, MINB_) return stream_of<DT, OP, OUT, T_, NV_, MINB_>(nvec, rows, threads, grid)
+    constexpr bool quant = OP == kRowQuant;
+    if constexpr (DT == kF32) {
+        if (nvec <= 32) TCR_STREAM(32, 1, 3);
+        if (nvec <= 64) TCR_STREAM(32, 2, 2);
+        if (nvec <= 128) TCR_STREAM(128, 1, 8);
+        if (nvec <= 256) TCR_STREAM(256, 1, 4);
+        if (nvec <= 512) TCR_STREAM(512, 1, 2);
+        if (nvec <= 1024) TCR_STREAM(512, 2, 1);
+    } else {
+        if (nvec <= 32) TCR_STREAM(32, 1, 4);
+        if (nvec <= 64) TCR_STREAM(32, 2, 3);
+        if (nvec <= 128) {
+            if constexpr (OUT == kOutI8)
+                TCR_STREAM(32, 4, 2);
+            else
+                TCR_STREAM(64, 2, 12);
         }
-        const size_t need = (rows + teams_per_cta - 1) / teams_per_cta;
-        grid = need < ctas ? need : ctas;
-        return nvec <= 32    ? (const void *)row_stream_kernel<DT, OP, OUT, 32>
-               : nvec <= 64  ? (const void *)row_stream_kernel<DT, OP, OUT, 64>
-               : nvec <= 128 ? (const void *)row_stream_kernel<DT, OP, OUT, 128>
-               : nvec <= 256 ? (const void *)row_stream_kernel<DT, OP, OUT, 256>
-               : nvec <= 512 ? (const void *)row_stream_kernel<DT, OP, OUT, 512>
-                             : (const void *)row_stream_kernel<DT, OP, OUT, 1024>;
+        if (nvec <= 256) TCR_STREAM(128, 2, 6);
+        if (nvec <= 512) TCR_STREAM(256, 2, (quant ? 4 : 3));
+        if (nvec <= 768) TCR_STREAM(256, 3, (quant ? 3 : 2));
+        if (nvec <= 1024) {
+            if constexpr (quant)
+                TCR_STREAM(512, 2, 2);
+            else
+                TCR_STREAM(256, 4, 2);
+        }
+        if (nvec <= 2048) {
+            if constexpr (quant)
+                TCR_STREAM(1024, 2, 1);
+            else
+                TCR_STREAM(512, 4, 1);
+        }
     }
+#undef TCR_STREAM
     grid = rows;
     if (nvec <= 2048) {
         threads = 512;

@@ -68,18 +68,27 @@ struct RawVec {
     uint4 q[DT == kF32 ? 2 : 1];
 };
 
-// Bytes sh .. sh + 4 N - 1 of the words w[0 .. N + 3] (0 <= sh < 16; the
-// same sh in every lane that runs together, so the selects are uniform).
+// Bytes sh .. sh + 4 N - 1 of the words w[0 .. N + 3] (0 <= sh < 16), sh the
+// same in every lane that runs together: one branch on its words, then a
+// funnel shift a word by the rest.  (Selecting words by predicates instead
+// cost rows of 5001 bfloat16 a third more time.)
+template <int N, int S>
+__device__ __forceinline__ void shift_by(const uint32_t (&w)[N + 4], uint32_t bits, uint32_t (&o)[N])
+{
+#pragma unroll
+    for (int k = 0; k < N; k++) o[k] = __funnelshift_r(w[k + S], w[k + S + (S < 4 ? 1 : 0)], bits);
+}
+
 template <int N>
 __device__ __forceinline__ void shift_words(const uint32_t (&w)[N + 4], uint32_t sh, uint32_t (&o)[N])
 {
-    uint32_t a[N + 2], b[N + 1];
-#pragma unroll
-    for (int k = 0; k < N + 2; k++) a[k] = (sh & 8u) ? w[k + 2] : w[k];
-#pragma unroll
-    for (int k = 0; k < N + 1; k++) b[k] = (sh & 4u) ? a[k + 1] : a[k];
-#pragma unroll
-    for (int k = 0; k < N; k++) o[k] = __funnelshift_r(b[k], b[k + 1], 8u * (sh & 3u));
+    const uint32_t bits = 8u * (sh & 3u);
+    switch (sh >> 2) {
+    case 0: shift_by<N, 0>(w, bits, o); break;
+    case 1: shift_by<N, 1>(w, bits, o); break;
+    case 2: shift_by<N, 2>(w, bits, o); break;
+    default: shift_by<N, 3>(w, bits, o); break;
+    }
 }
 
 // The elements of vector v that the row has.
@@ -152,68 +161,72 @@ __device__ __forceinline__ void unpack(const RawVec<DT> &r, float (&f)[kRv])
     }
 }
 
+template <int B>
+__device__ __forceinline__ void store_piece(char *p, const uint32_t *w)
+{
+    if constexpr (B == 16)
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (B == 8)
+        *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (B == 4)
+        *reinterpret_cast<uint32_t *>(p) = w[0];
+    else if constexpr (B == 2)
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)w[0];
+    else
+        *reinterpret_cast<uint8_t *>(p) = (uint8_t)w[0];
+}
+
 // Store a vector of NW words (the elements es bytes each, `left` of them, 0
 // for a lane without a vector) where rows are not aligned: the lanes of a
-// warp hold consecutive vectors, and between them cover whole 16-byte
-// granules, so a lane stores the granules that begin in the vector before
-// its own (taken over by a shuffle) or in its own.  What has no partner (a
-// warp's first and last vectors, a row's last) goes element by element.
-// Every lane of the warp calls this.
+// warp hold consecutive vectors, and between them cover whole granules (16
+// bytes, or 8 for codes), so a lane stores the granules that begin in the
+// vector before its own (taken over by a shuffle) or in its own.  What has
+// no partner (a warp's first and last vectors, a row's last) goes element by
+// element.  Every lane of the warp calls this.
 template <int NW, int es>
 __device__ __forceinline__ void store_shifted(char *p, uint32_t left, const uint32_t (&o)[NW])
 {
     constexpr uint32_t bytes = 4 * NW;                  // of a vector
     constexpr uint32_t G = bytes < 16 ? bytes : 16;     // granule
+    constexpr int GW = G / 4;
     constexpr uint32_t n = bytes / es;
     const uint32_t m = (uint32_t)(uintptr_t)p & (G - 1);
-    const int lane = threadIdx.x & 31;
-    uint32_t prev[G / 4];                               // the last granule of the vector before
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t w[NW + 4];
 #pragma unroll
-    for (uint32_t k = 0; k < G / 4; k++) prev[k] = __shfl_up_sync(kFull, o[NW - G / 4 + k], 1);
-    const bool joins = left == n && lane > 0 && m != 0u;        // (the vector before a vector is whole)
-    const bool next_joins = __shfl_down_sync(kFull, (int)joins, 1) && lane < 31;
-    if (left == n && m == 0u) {
+    for (int k = 0; k < GW; k++) w[k] = __shfl_up_sync(kFull, o[NW - GW + k], 1);
+    const uint32_t after = __shfl_down_sync(kFull, left, 1);
+    const bool whole = left == n;
+    const bool joins = whole && lane > 0;               // (the vector before a vector is whole)
+    const bool next_joins = after == n && lane < 31;
+    if (m == 0u) {
 #pragma unroll
-        for (uint32_t k = 0; k < bytes / G; k++)
-            if constexpr (G == 16)
-                *reinterpret_cast<uint4 *>(p + 16 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            else
-                *reinterpret_cast<uint2 *>(p) = make_uint2(o[0], o[1]);
-        return;
+        for (int k = 0; k < NW / GW; k++)
+            if (whole) store_piece<G>(p + G * k, o + GW * k);
+        if (whole || left == 0u) return;
     }
-    uint32_t w[NW + 4 + (G < 16 ? 2 : 0)], g[NW];
+    uint32_t from = 0, to = left;                       // own elements that no granule covers
+    if (m != 0u) {
 #pragma unroll
-    for (uint32_t k = 0; k < sizeof w / 4; k++) w[k] = 0u;
+        for (int k = 0; k < NW; k++) w[GW + k] = o[k];
 #pragma unroll
-    for (uint32_t k = 0; k < G / 4; k++) w[k] = prev[k];
+        for (int k = GW + NW; k < NW + 4; k++) w[k] = 0u;
+        uint32_t g[NW];
+        shift_words<NW>(w, G - m, g);                   // from p - m on
+        if (joins) {
 #pragma unroll
-    for (uint32_t k = 0; k < NW; k++) w[G / 4 + k] = o[k];
-    uint32_t ww[NW + 4];
-#pragma unroll
-    for (int k = 0; k < NW + 4; k++) ww[k] = w[k];
-    shift_words<NW>(ww, G - m, g);                      // granules from p - m on
-    uint32_t from = 0, to = left;                       // own elements not covered by granules
-    if (joins) {
-#pragma unroll
-        for (uint32_t k = 0; k < bytes / G; k++)
-            if constexpr (G == 16)
-                *reinterpret_cast<uint4 *>(p - m + 16 * k) =
-                    make_uint4(g[4 * k], g[4 * k + 1], g[4 * k + 2], g[4 * k + 3]);
-            else
-                *reinterpret_cast<uint2 *>(p - m) = make_uint2(g[0], g[1]);
-        from = (bytes - m) / es;
+            for (int k = 0; k < NW / GW; k++) store_piece<G>(p - m + G * k, g + GW * k);
+            from = (bytes - m) / es;
+        }
+        if (next_joins) to = (bytes - m) / es;
     }
-    if (next_joins) to = min(to, (bytes - m) / es);
+    if (from >= to) return;
 #pragma unroll
-    for (uint32_t k = 0; k < n; k++) {
-        if (k < from || k >= to) continue;
-        if constexpr (es == 4)
-            *reinterpret_cast<uint32_t *>(p + 4 * k) = o[k];
-        else if constexpr (es == 2)
-            *reinterpret_cast<uint16_t *>(p + 2 * k) = (uint16_t)(o[k / 2] >> (16 * (k % 2)));
-        else
-            *reinterpret_cast<uint8_t *>(p + k) = (uint8_t)(o[k / 4] >> (8 * (k % 4)));
-    }
+    for (uint32_t k = 0; k < n; k++)
+        if (k >= from && k < to) {
+            const uint32_t x = o[es * k / 4] >> (8 * (es * k & 3u));
+            store_piece<es>(p + es * k, &x);
+        }
 }
 
 // Vector v of a row, rounded to the type.  `aligned` (uniform): the rows are
@@ -254,10 +267,14 @@ __device__ __forceinline__ float tree8(const float (&e)[kRv])
                      __fadd_rn(__fadd_rn(e[4], e[5]), __fadd_rn(e[6], e[7])));
 }
 
-// a[0] after the halving fold of n (a power of two) values.
+// The halving fold of N values, absent ones up to a power of two +0.0 (a
+// sum of non-negative values or of a row's products: x + 0.0 is x but for
+// the sign of a zero).
 template <int N>
 __device__ __forceinline__ float halving(float (&a)[N])
 {
+    if constexpr (N == 3) return __fadd_rn(__fadd_rn(a[0], a[2]), __fadd_rn(a[1], 0.0f));
+    static_assert(N == 3 || (N & (N - 1)) == 0, "a power of two, or 3");
 #pragma unroll
     for (int h = N / 2; h >= 1; h /= 2)
 #pragma unroll
