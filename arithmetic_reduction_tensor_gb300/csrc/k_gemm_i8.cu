@@ -30,124 +30,43 @@
 // by a short kernel before (i8_prepare_kernel) into 16-bit scratch that TMA
 // boxes feed to the MMA as the B operand, half of the tile's tokens per SM.
 //
-// With few tiles K is also split over CTA pairs: integer additions commute,
-// so the splits add into a zeroed 32-bit scratch with atomics and the last
-// to arrive scales the tile -- the same bits in any order.
+// Whole tiles go round the CTA pairs; the tiles left over after whole rounds
+// (all of them, where tiles are few) are dealt out by steps, evenly, so that
+// the pairs end together: integer additions commute, so the pieces of a tile
+// go to slabs of 32-bit scratch and the CTA that completes the tile adds and
+// scales them -- the same bits in any order.
 //
 // CTA roles (768 threads, one persistent CTA per SM, clusters of two):
-//   warp 0        TMA producer: 128 weight rows x 128 codes, and 2 boxes of
-//                 64 columns x tile/2 tokens, into a 7-stage ring
+//   warps 0, 2    TMA copies into a 6-stage ring: 128 weight rows x 128
+//                 codes; 2 blocks of 64 columns x tile/2 tokens
 //   warp 1        TMEM allocation; the leader's issues the MMAs
-//   warps 4..15   conversion, four TMEM stages of 128 k ahead of the MMA
-//   warps 16..23  epilogue: two 128-column accumulators, so a chunk's
+//   warps 4..15   conversion, three TMEM stages of 128 k ahead of the MMA
+//   warps 16..23  epilogue: two 160-column accumulators, so a chunk's
 //                 readout runs beside the next chunk's MMAs
 // Every wait gives up after about a second as in the split-K GEMM.
 #include <cstring>
+#include <type_traits>
 
 #include "kernels.cuh"
-#include "rowvec.cuh"
+#include "codes.cuh"
 #include "tc05.cuh"
 
 namespace tcr {
 
 __device__ unsigned int g_gemm_i8_fault;
 
-__device__ __forceinline__ void store_out(void *C, int dtype, size_t i, int acc, float sa, float sw)
-{
-    if (dtype == kOutI32) {
-        ((int *)C)[i] = acc;
-        return;
-    }
-    const float v = __fmul_rn(__fmul_rn((float)acc, sa), sw);
-    if (dtype == kF16)
-        ((uint16_t *)C)[i] = float_to_elem<kF16>(v);
-    else if (dtype == kBF16)
-        ((uint16_t *)C)[i] = float_to_elem<kBF16>(v);
-    else
-        ((float *)C)[i] = v;
-}
-
-// ---------------------------------------------------------------- few tokens
-
-// 16 codes at p, `left` of them inside the row (the rest read as 0).
-__device__ __forceinline__ uint4 ld_codes(const int8_t *p, size_t left, bool aligned)
-{
-    if (aligned && left >= 16) return ld16(p);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 16; k++)
-        if ((size_t)k < left) w[k / 4] |= (uint32_t)(uint8_t)p[k] << (8 * (k % 4));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-constexpr int kGvR = 2;             // channels per warp
-
-// Lane l of a channel's warp takes the codes 16 l + 512 i.
-template <int MT>
-__global__ void __launch_bounds__(128) gemv_i8_kernel(const I8Args a)
-{
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    const size_t n0 = ((size_t)blockIdx.x * 4 + (threadIdx.x >> 5)) * kGvR;
-    const int lane = threadIdx.x & 31;
-    if (n0 >= a.N) return;
-    int acc[MT][kGvR];
-#pragma unroll
-    for (int m = 0; m < MT; m++)
-#pragma unroll
-        for (int r = 0; r < kGvR; r++) acc[m][r] = 0;
-#pragma unroll 4
-    for (size_t k = (size_t)lane * 16; k < a.K; k += 512) {
-        uint4 w[kGvR];
-#pragma unroll
-        for (int r = 0; r < kGvR; r++)
-            w[r] = n0 + r < a.N ? ld_codes(a.W + (n0 + r) * a.ldw + k, a.K - k, a.al_w)
-                                : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int m = 0; m < MT; m++) {
-            if (m >= (int)a.M) break;
-            const uint4 x = ld_codes(a.A + (size_t)m * a.lda + k, a.K - k, a.al_a);
-#pragma unroll
-            for (int r = 0; r < kGvR; r++) {
-                acc[m][r] = __dp4a((int)x.x, (int)w[r].x, acc[m][r]);
-                acc[m][r] = __dp4a((int)x.y, (int)w[r].y, acc[m][r]);
-                acc[m][r] = __dp4a((int)x.z, (int)w[r].z, acc[m][r]);
-                acc[m][r] = __dp4a((int)x.w, (int)w[r].w, acc[m][r]);
-            }
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < MT; m++)
-#pragma unroll
-        for (int r = 0; r < kGvR; r++) {
-            const int s = __reduce_add_sync(kFull, acc[m][r]);
-            if (lane == m * kGvR + r && m < (int)a.M && n0 + r < a.N)
-                store_out(a.C, a.c_dtype, (size_t)m * a.ldc + n0 + r, s, a.sa ? a.sa[m] : 1.0f,
-                          a.sw ? a.sw[n0 + r] : 1.0f);
-        }
-}
-
 // ---------------------------------------------------------------- the operands' preparation
-
-// Four codes of a word as two words of two binary16 values each.  A code
-// with its sign bit flipped is q + 128; as the low byte under 0x64 it reads
-// 1024 + q + 128, and subtracting 1152 leaves q, exactly.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    const uint32_t u = w ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-}
 
 // Blocks [0, blocks_a): the tokens' codes as binary16, rows of ldf values,
 // zero past K.  Blocks up to blocks_a + blocks_w: the weights' codes in rows
 // of ldp bytes (only when their own pitch or base does not fit TMA).  The
-// rest zero the integer scratch.  A team of 2^team_log2 threads to a row.
+// last one zeroes the counters of the split tiles.  A team of 2^team_log2 threads to a row.
 __global__ void __launch_bounds__(256) i8_prepare_kernel(const I8Prepare p)
 {
-    pdl_launch_dependents();
+    // in this order: the product's kernel may read the weights as soon as it
+    // runs, so it must not start while a kernel that writes them still runs
     pdl_wait_primary();
+    pdl_launch_dependents();
     unsigned b = blockIdx.x;
     const int team = 1 << p.team_log2;
     const int in_team = threadIdx.x & (team - 1);
@@ -156,7 +75,7 @@ __global__ void __launch_bounds__(256) i8_prepare_kernel(const I8Prepare p)
         const size_t r = b * rows_per_block + (threadIdx.x >> p.team_log2);
         if (r >= p.M) return;
         for (size_t c = (size_t)in_team * 16; c < p.ldf; c += (size_t)team * 16) {
-            const uint4 q = ld_codes(p.A + r * p.lda + c, p.K > c ? p.K - c : 0, p.al_a);
+            const uint4 q = ld_codes(p.A + r * p.lda + c, p.K > c ? (uint32_t)(p.K - c) : 0u, p.al_a);
             const uint32_t w[4] = {q.x, q.y, q.z, q.w};
             uint32_t o[8];
 #pragma unroll
@@ -173,12 +92,10 @@ __global__ void __launch_bounds__(256) i8_prepare_kernel(const I8Prepare p)
         if (r >= p.N) return;
         for (size_t c = (size_t)in_team * 16; c < p.ldp; c += (size_t)team * 16)
             *reinterpret_cast<uint4 *>(p.Wp + r * p.ldp + c) =
-                ld_codes(p.W + r * p.ldw + c, p.K > c ? p.K - c : 0, false);
+                ld_codes(p.W + r * p.ldw + c, p.K > c ? (uint32_t)(p.K - c) : 0u, false);
         return;
     }
-    b -= p.blocks_w;
-    const unsigned nz = gridDim.x - p.blocks_a - p.blocks_w;
-    for (size_t i = (size_t)b * 256 + threadIdx.x; i < p.zero_words; i += (size_t)nz * 256) p.zero[i] = 0;
+    for (size_t i = threadIdx.x; i < p.zero_words; i += 256) p.zero[i] = 0;
 }
 
 // ---------------------------------------------------------------- the tensor-core kernel
@@ -200,7 +117,7 @@ constexpr int kI8EpiWarp0 = 4 + 4 * kI8ConvGroups;
 constexpr int kI8Threads = 32 * (kI8EpiWarp0 + kI8EpiWarps);
 // Registers a thread by role (setmaxnreg); their sum over the warpgroups is
 // within what the launch holds: 768 threads of 80.
-constexpr int kI8RegsLaunch = 80, kI8RegsIssue = 48, kI8RegsConv = 64, kI8RegsEpi = 120;
+constexpr int kI8RegsLaunch = 80, kI8RegsIssue = 40, kI8RegsConv = 56, kI8RegsEpi = 136;
 static_assert(kI8RegsIssue + kI8ConvGroups * kI8RegsConv + kI8EpiWarps / 4 * kI8RegsEpi <=
                   kI8Threads / 128 * kI8RegsLaunch,
               "registers of the launch");
@@ -212,6 +129,26 @@ constexpr int kI8OffMisc = kI8OffBars + 8 * kI8NumBars;
 constexpr int kI8SmemBytes = kI8OffMisc + 64 + 1024;
 static_assert(kI8SmemBytes <= 232448, "one SM's 227 KiB");
 static_assert(kI8ACol + kI8AStages * 64 <= 512, "tensor memory columns");
+
+// mbar_wait_f with its limit (2^31 cycles: 1.0 to 1.5 s) on the SM's cycle
+// counter, whose read is short beside the global timer's: the waits of a
+// small product follow one another.
+__device__ __forceinline__ bool i8_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    for (uint32_t i = 1;; i++) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 15u) == 0u) {
+            if (*abort) return false;
+            if (clock64() - t0 > (1ll << 31)) {
+                *abort = 1u;
+                atomicOr(&g_gemm_i8_fault, 1u);
+                return false;
+            }
+        }
+    }
+}
 
 __device__ __forceinline__ uint32_t i8_cluster_rank()
 {
@@ -325,26 +262,50 @@ __device__ __forceinline__ void i8_ld16(uint32_t taddr, float (&v)[16])
     for (int j = 0; j < 16; j++) v[j] = __uint_as_float(r[j]);
 }
 
-struct I8Unit {
-    int split, tc, tt;      // K split, channel tile, token tile
+// A CTA pair's work, in turn: whole tiles pair, pair + pairs, .. below
+// g.full, then at most one piece of a tile from g.full on, each of which is
+// cut into g.per pieces for as many pairs.
+struct I8Walk {
+    int tile, k0, nb, part; // the current piece: a tile's steps k0 .. k0 + nb - 1, which piece of it
+    int u, piece;
+
+    __device__ __forceinline__ I8Walk(const I8Gemm &g, int pair, int pairs)
+    {
+        u = pair;
+        piece = pair < (g.tiles - g.full) * g.per ? pair : -1;
+    }
+    __device__ __forceinline__ bool next(const I8Gemm &g, int pairs)
+    {
+        if (u < g.full) {
+            tile = u;
+            k0 = 0;
+            nb = g.steps;
+            part = 0;
+            u += pairs;
+            return true;
+        }
+        if (piece < 0) return false;
+        tile = piece / g.per;
+        part = piece - tile * g.per;
+        k0 = part * g.steps / g.per;
+        nb = (part + 1) * g.steps / g.per - k0;
+        tile += g.full;
+        piece = -1;
+        return true;
+    }
 };
 
-// Units in split-major order; within a split, groups of 8 channel tiles,
-// the channel tile fastest, so that the tiles in flight share operands in L2.
-__device__ __forceinline__ I8Unit i8_decode(const I8Gemm &g, int u)
+// A tile's channel and token tile: groups of 8 channel tiles, the channel
+// tile fastest, so that the tiles in flight share operands in L2.
+__device__ __forceinline__ void i8_tile(const I8Gemm &g, int tile, int &tc, int &tt)
 {
     constexpr int kGroup = 8;
-    const int tiles = g.tiles_c * g.tiles_t;
-    I8Unit r;
-    r.split = u / tiles;
-    const int t = u - r.split * tiles;
     const int group = kGroup * g.tiles_t;
-    const int first = t / group * kGroup;
+    const int first = tile / group * kGroup;
     const int in_group = min(g.tiles_c - first, kGroup);
-    const int q = t % group;
-    r.tc = first + q % in_group;
-    r.tt = q / in_group;
-    return r;
+    const int q = tile % group;
+    tc = first + q % in_group;
+    tt = q / in_group;
 }
 
 __global__ void __launch_bounds__(kI8Threads, 1)
@@ -370,7 +331,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     const uint32_t rank = i8_cluster_rank();
     const bool leader = rank == 0;
     const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
-    auto wait = [&](uint32_t b, uint32_t parity) { return mbar_wait_f(b, parity, abort, &g_gemm_i8_fault); };
+    auto wait = [&](uint32_t b, uint32_t parity) { return i8_wait(b, parity, abort); };
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -401,36 +362,34 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     i8_cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    pdl_wait_primary();
-
-    // the steps (128 k each) of a split
-    auto split_steps = [&](int s) { return min(g.sps, g.steps - s * g.sps); };
     const int half = g.tn / 2;
+    I8Walk walk(g, pair, pairs);
+
+    // The kernel before this one on the stream is i8_prepare_kernel, which
+    // lets this one start only once the kernels before it are done.  So only
+    // what reads its results waits for it: the tokens' copies, the integer
+    // scratch, and the weights' copies where it repacked them.
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kI8RegsIssue));
         if (warp == 0) {
-            // ---------------- producer (a converged warp, one lane issuing)
-            const uint32_t leader_full = i8_map_leader(full(0));
-            const uint32_t token_bytes = (uint32_t)(4 * 128 * half);
+            // ---------------- the weights' copies (here and below a converged
+            // warp walks, one lane issues)
+            if (g.w_prepared) pdl_wait_primary();
             int st = 0;
             uint32_t phase = 0;
             uint32_t armed = 0, armed_phase = 0;
             bool ok = true;
-            for (int u = pair; u < g.units && ok; u += pairs) {
-                const I8Unit c = i8_decode(g, u);
-                const int nb = split_steps(c.split);
-                const int s0 = c.split * g.sps;
-                const int row_w = c.tc * kI8BM + 128 * (int)rank, row_t = c.tt * g.tn + half * (int)rank;
-                for (int j = 0; j < nb; j++) {
+            while (ok && walk.next(g, pairs)) {
+                int tc, tt;
+                i8_tile(g, walk.tile, tc, tt);
+                for (int j = 0; j < walk.nb; j++) {
                     ok = __all_sync(kFull, wait(empty(st), phase ^ 1u));
                     if (!ok) break;
-                    const uint32_t dst = ring + (uint32_t)st * kI8StageBytes;
                     if (i8_elect()) {
                         mbar_arrive_expect_tx(wfull(st), kI8WBytes);
-                        tma_load_2d(dst, &map_w, (s0 + j) * kI8BK, row_w, wfull(st));
-                        if (leader) mbar_arrive_expect_tx(full(st), token_bytes);
-                        i8_load_tokens(dst + kI8WBytes, &map_t, row_t, 2 * (s0 + j), leader_full + 8u * (uint32_t)st);
+                        tma_load_2d(ring + (uint32_t)st * kI8StageBytes, &map_w, (walk.k0 + j) * kI8BK,
+                                    tc * kI8BM + 128 * (int)rank, wfull(st));
                     }
                     __syncwarp();
                     armed |= 1u << st;
@@ -441,12 +400,39 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     }
                 }
             }
-            if (*abort) {
-                // let the copies in flight land; the tokens' share a barrier
-                // with conversions that may never come, so those get the time
-                // of a whole wait
+            if (*abort)                   // let the copies in flight land
                 for (int i = 0; i < kI8Stages; i++)
                     if ((armed >> i) & 1u) (void)mbar_wait_limited(wfull(i), (armed_phase >> i) & 1u);
+        } else if (warp == 2) {
+            // ---------------- the tokens' copies
+            pdl_wait_primary();
+            const uint32_t leader_full = i8_map_leader(full(0));
+            const uint32_t token_bytes = (uint32_t)(4 * 128 * half);
+            int st = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            while (ok && walk.next(g, pairs)) {
+                int tc, tt;
+                i8_tile(g, walk.tile, tc, tt);
+                for (int j = 0; j < walk.nb; j++) {
+                    ok = __all_sync(kFull, wait(empty(st), phase ^ 1u));
+                    if (!ok) break;
+                    if (i8_elect()) {
+                        if (leader) mbar_arrive_expect_tx(full(st), token_bytes);
+                        i8_load_tokens(ring + (uint32_t)st * kI8StageBytes + kI8WBytes, &map_t,
+                                       tt * g.tn + half * (int)rank, 2 * (walk.k0 + j),
+                                       leader_full + 8u * (uint32_t)st);
+                    }
+                    __syncwarp();
+                    if (++st == kI8Stages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (*abort) {
+                // these copies share a barrier with conversions that may
+                // never come, so they get time (10 ms) to land
                 const uint64_t t0 = global_ns();
                 while (global_ns() - t0 < 10000000ull) {
                 }
@@ -460,11 +446,9 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             int st = 0, ta = 0, b = 0;
             uint32_t phase = 0, dphase = 0;
             bool ok = true, withhold = g.inject_stall != 0u;
-            for (int u = pair; u < g.units && ok; u += pairs) {
-                const I8Unit c = i8_decode(g, u);
-                const int nb = split_steps(c.split);
+            while (ok && walk.next(g, pairs)) {
                 int in_chunk = 0;
-                for (int j = 0; j < nb && ok; j++) {
+                for (int j = 0; j < walk.nb && ok; j++) {
                     bool ready = true;
                     if (in_chunk == 0) ready = !*abort && wait(dempty(b), ((dphase >> b) & 1u) ^ 1u);
                     ready = ready && wait(full(st), phase);
@@ -474,7 +458,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     const uint32_t d = tmem + (uint32_t)(b * kI8DCols);
                     const uint32_t a = tmem + (uint32_t)(kI8ACol + 64 * ta);
                     const uint64_t t_desc = t_desc0 + (uint64_t)st * (kI8StageBytes >> 4);
-                    const bool end = in_chunk == kI8ChunkSteps - 1 || j == nb - 1;
+                    const bool end = in_chunk == kI8ChunkSteps - 1 || j == walk.nb - 1;
                     if (i8_elect()) {
                         i8_mma(d, a, t_desc, idesc, in_chunk > 0 ? 1u : 0u);
 #pragma unroll
@@ -511,8 +495,8 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int m = 32 * (warp & 3) + lane;
         const uint32_t sw = (uint32_t)(m & 7);         // 128-byte swizzle of the box
-        int total = 0;                                 // steps of all units
-        for (int u = pair; u < g.units; u += pairs) total += split_steps(i8_decode(g, u).split);
+        int total = 0;                                 // steps of all pieces
+        while (walk.next(g, pairs)) total += walk.nb;
         bool ok = true;
         for (int i = (warp - 4) >> 2; i < total; i += kI8ConvGroups) {
             const int st = i % kI8Stages;
@@ -548,90 +532,182 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kI8RegsEpi));
-        // ---------------- epilogue: a thread holds one channel, half of the tile's tokens
+        // ---------------- epilogue: a thread holds one channel, half of the tile's
+        // tokens, 16 at a time
         const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
         const int m = 32 * (warp & 3) + lane;
         const int col0 = warp < kI8EpiWarp0 + 4 ? 0 : half;
         const int nblk = half / 16;
         int b = 0;
         uint32_t dphase = 0;
-        for (int u = pair; u < g.units; u += pairs) {
-            const I8Unit c = i8_decode(g, u);
-            const int nb = split_steps(c.split);
-            int acc[kI8MaxTn / 2];
-#pragma unroll
-            for (int i = 0; i < kI8MaxTn / 2; i++) acc[i] = 0;
+        pdl_wait_primary();
+        while (walk.next(g, pairs)) {
+            int tc, tt;
+            i8_tile(g, walk.tile, tc, tt);
+            const bool split = walk.nb < g.steps;
+            const uint32_t n = (uint32_t)(tc * kI8BM + 128 * (int)rank + m);
+            const uint32_t t0 = (uint32_t)(tt * g.tn + col0);
+            // the tokens of this thread that exist
+            const int nt = n >= g.N || t0 >= g.M ? 0 : (int)min((uint32_t)half, (uint32_t)g.M - t0);
+            // a split tile's slabs of sums, laid out (piece, token, channel)
+            const int rt = walk.tile - g.full;
+            auto slab = [&](int part, int q) {
+                const size_t token = ((size_t)rt * g.per + part) * g.tn + col0 + 16 * q;
+                return g.ws + token * kI8BM + 128u * rank + m;
+            };
             bool live = true;
-            for (int j = 0; j < nb; j += kI8ChunkSteps) {
-                const bool ready = live && !*abort && wait(dfull(b), (dphase >> b) & 1u);
-                live = __all_sync(kFull, ready);
-                if (live) {
-                    tc_fence_after();
+            // this thread's scales, loaded ahead of the sums: its channel's and,
+            // 32 to a register over the lanes, the tokens'
+            const float sw = g.sw && n < g.N ? g.sw[n] : 1.0f;
+            constexpr int kSa = (kI8MaxTn / 2 + 31) / 32;
+            float sa[kSa];
 #pragma unroll
-                    for (int q = 0; q < kI8MaxTn / 32; q++) {
-                        if (q < nblk) {
-                            float v[16];
-                            i8_ld16(tmem + lane_base + (uint32_t)(b * kI8DCols + col0 + 16 * q), v);
+            for (int i = 0; i < kSa; i++) {
+                const uint32_t t = t0 + 32 * i + lane;
+                sa[i] = g.sa && t < g.M && 32 * i + lane < half ? g.sa[t] : 1.0f;
+            }
+            // C's tokens 16 q .. of this thread's channel from their sums; NaN (or
+            // the least integer) where a wait gave up
+            auto store_as = [&](auto type, int q, auto &v) {
+                constexpr int kType = decltype(type)::value, kCount = sizeof v / sizeof v[0];
+                using E = typename Elem<kType == kOutI32 ? kF32 : kType>::T;
+                E *at = (E *)g.C + (size_t)(t0 + 16 * q) * g.ldc + n;
+                const int left = nt - 16 * q;
+                const float channel = live ? sw : __int_as_float(0x7fc00000);
+                float mine = sa[0];
+                if constexpr (kCount == 16) {
 #pragma unroll
-                            for (int i = 0; i < 16; i++) acc[16 * q + i] += __float2int_rn(v[i]);
-                        }
+                    for (int i = 1; i < kSa; i++) mine = q / 2 == i ? sa[i] : mine;
+                }
+#pragma unroll
+                for (int i = 0; i < kCount; i++) {
+                    E e;
+                    if constexpr (kType == kOutI32) {
+                        e = (uint32_t)v[i];
+                    } else {
+                        const float token = kCount == 16 ? __shfl_sync(kFull, mine, 16 * (q & 1) + i)
+                                                         : __shfl_sync(kFull, sa[i / 32], i % 32);
+                        e = float_to_elem<kType>(__fmul_rn(__fmul_rn((float)v[i], token), channel));
                     }
+                    if (i < left) *at = e;
+                    at += g.ldc;
+                }
+            };
+            auto store16 = [&](int q, const int (&v)[16]) {
+                switch (g.c_dtype) {
+                case kF16: store_as(std::integral_constant<int, kF16>(), q, v); break;
+                case kBF16: store_as(std::integral_constant<int, kBF16>(), q, v); break;
+                case kF32: store_as(std::integral_constant<int, kF32>(), q, v); break;
+                default: store_as(std::integral_constant<int, kOutI32>(), q, v); break;
+                }
+            };
+            // 16 sums to where they go: this piece's slab, or C
+            auto put16 = [&](int q, const int (&v)[16]) {
+                if (split) {
+                    int *own = slab(walk.part, q);
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        if (i < nt - 16 * q) __stcg(own + i * kI8BM, v[i]);
+                } else {
+                    store16(q, v);
+                }
+            };
+            auto chunk_ready = [&]() {
+                const bool ready = !*abort && wait(dfull(b), (dphase >> b) & 1u);
+                return __all_sync(kFull, ready) != 0;
+            };
+            auto chunk_done = [&](bool read) {
+                if (read) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) i8_arrive_leader(i8_map_leader(dempty(b)));
                 }
                 dphase ^= 1u << b;
                 b ^= 1;
-            }
-            const size_t n = (size_t)c.tc * kI8BM + 128u * rank + (size_t)m;
-            const size_t t0 = (size_t)c.tt * (size_t)g.tn + (size_t)col0;
-            // the tokens of this thread that exist
-            const int nt = n >= g.N || t0 >= g.M ? 0 : (int)min((size_t)half, g.M - t0);
-            bool write = true;
-            if (g.splits > 1 && live) {
-                // this split's share of the tile, then the last split scales it
-                int *ws = g.ws + t0 * g.N + n;
+            };
+            // (Loops over the blocks of 16 are kept rolled where the sums need
+            // not stay in registers: the code runs once a tile, and its length
+            // is what a small product waits for.)
+            if (walk.nb <= kI8ChunkSteps) {
+                live = chunk_ready();
+                if (live) tc_fence_after();
+#pragma unroll 1
+                for (int q = 0; q < nblk; q++) {
+                    float f[16];
+                    int v[16];
+                    if (live) i8_ld16(tmem + lane_base + (uint32_t)(b * kI8DCols + col0 + 16 * q), f);
 #pragma unroll
-                for (int i = 0; i < kI8MaxTn / 2; i++) {
-                    if (i < nt) atomicAdd(ws, acc[i]);
-                    ws += g.N;
+                    for (int i = 0; i < 16; i++) v[i] = live ? __float2int_rn(f[i]) : (int)0x80000000;
+                    if (live || !split) put16(q, v);
                 }
-                __threadfence();
-                named_sync(1, 32 * kI8EpiWarps);
-                if (threadIdx.x == 32 * kI8EpiWarp0) {
-                    uint32_t *count = g.count + 2 * (c.tt * g.tiles_c + c.tc) + rank;
-                    *last = !*abort && atomicAdd(count, 1u) == (uint32_t)(g.splits - 1);
-                }
-                named_sync(1, 32 * kI8EpiWarps);
-                write = *last != 0u;
-                if (*abort) {                 // a role of this CTA gave up: its tiles read NaN
-                    live = false;
-                    write = true;
-                } else if (write) {
-                    __threadfence();
-                    ws = g.ws + t0 * g.N + n;
+                chunk_done(live);
+            } else {
+                int acc[kI8MaxTn / 2];
 #pragma unroll
-                    for (int i = 0; i < kI8MaxTn / 2; i++) {
-                        if (i < nt) acc[i] = __ldcg(ws);
-                        ws += g.N;
+                for (int i = 0; i < kI8MaxTn / 2; i++) acc[i] = 0;
+                for (int j = 0; j < walk.nb; j += kI8ChunkSteps) {
+                    live = live && chunk_ready();
+                    if (live) {
+                        tc_fence_after();
+#pragma unroll
+                        for (int q = 0; q < kI8MaxTn / 32; q++) {
+                            if (q < nblk) {
+                                float v[16];
+                                i8_ld16(tmem + lane_base + (uint32_t)(b * kI8DCols + col0 + 16 * q), v);
+#pragma unroll
+                                for (int i = 0; i < 16; i++) acc[16 * q + i] += __float2int_rn(v[i]);
+                            }
+                        }
+                    }
+                    chunk_done(live);
+                }
+                if (!live) {
+#pragma unroll
+                    for (int i = 0; i < kI8MaxTn / 2; i++) acc[i] = (int)0x80000000;
+                }
+                if (split) {
+                    int *own = slab(walk.part, 0);
+#pragma unroll
+                    for (int i = 0; i < kI8MaxTn / 2; i++)
+                        if (i < nt) __stcg(own + i * kI8BM, acc[i]);
+                } else {
+                    switch (g.c_dtype) {
+                    case kF16: store_as(std::integral_constant<int, kF16>(), 0, acc); break;
+                    case kBF16: store_as(std::integral_constant<int, kBF16>(), 0, acc); break;
+                    case kF32: store_as(std::integral_constant<int, kF32>(), 0, acc); break;
+                    default: store_as(std::integral_constant<int, kOutI32>(), 0, acc); break;
                     }
                 }
-            } else if (g.splits > 1) {
-                named_sync(1, 32 * kI8EpiWarps);
-                if (threadIdx.x == 32 * kI8EpiWarp0) *last = 0u;
-                named_sync(1, 32 * kI8EpiWarps);
             }
-            if (write && nt > 0) {
-                // a wait that gave up leaves NaN (or the least integer)
-                const float sw = !live ? __int_as_float(0x7fc00000) : g.sw ? g.sw[n] : 1.0f;
-                size_t at = t0 * g.ldc + n;
+            if (!split) continue;
+            // the CTA that brings the tile's last steps adds the slabs
+            __threadfence();
+            named_sync(1, 32 * kI8EpiWarps);
+            if (threadIdx.x == 32 * kI8EpiWarp0)
+                *last = live && !*abort &&
+                        atomicAdd(g.count + 2 * rt + rank, (uint32_t)walk.nb) + walk.nb == (uint32_t)g.steps;
+            named_sync(1, 32 * kI8EpiWarps);
+            const bool gave_up = *abort != 0u;       // a role of this CTA did: its tiles read NaN
+            if (__any_sync(kFull, gave_up))
+                live = false;
+            else if (*last == 0u)
+                continue;
+            __threadfence();
+#pragma unroll 1
+            for (int q = 0; q < nblk; q++) {
+                int v[16];
 #pragma unroll
-                for (int i = 0; i < kI8MaxTn / 2; i++) {
-                    if (i < nt)
-                        store_out(g.C, g.c_dtype, at, live ? acc[i] : (int)0x80000000, g.sa ? g.sa[t0 + i] : 1.0f,
-                                  sw);
-                    at += g.ldc;
+                for (int i = 0; i < 16; i++) v[i] = live ? 0 : (int)0x80000000;
+                if (live && nt > 16 * q) {
+#pragma unroll 1
+                    for (int part = 0; part < g.per; part++) {
+                        // (tokens past the tile's end read the slab's own padding)
+                        const int *from = slab(part, q);
+#pragma unroll
+                        for (int i = 0; i < 16; i++) v[i] += __ldcg(from + i * kI8BM);
+                    }
                 }
+                store16(q, v);
             }
         }
     }
@@ -686,7 +762,7 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
 {
     I8Plan p;
     std::memset(&p, 0, sizeof p);
-    if (M <= (size_t)kI8GemvTokens) {
+    if (M <= (size_t)kI8FewTokens) {
         p.launches = 1;
         return p;
     }
@@ -694,28 +770,47 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
     p.launches = 2;
     p.steps = (int)((K + kI8BK - 1) / kI8BK);
     p.tiles_c = (int)((N + kI8BM - 1) / kI8BM);
-    // the token tile: the one whose waves over the pairs come out shortest
+    p.ldf = (K + 63) / 64 * 64;
+    // The token tile and the split: the least time by what a step costs, in
+    // cycles -- the conversion of its weights (about 620) or its MMAs (4 a
+    // token, and the accumulators' readout beside them) -- and a split tile's
+    // way through the scratch (a fence, a counter, the readback: 2 to 3 us).  Whole tiles go round the pairs; the steps of the tiles
+    // left over after whole rounds are split over the pairs, as many pairs to
+    // each tile, if that ends sooner.
     size_t best = SIZE_MAX;
     for (int tn = 32; tn <= kI8MaxTn; tn += 32) {
         const size_t tt = (M + (size_t)tn - 1) / (size_t)tn;
-        const size_t tiles = tt * (size_t)p.tiles_c;
-        const size_t waves = (tiles + (size_t)pairs - 1) / (size_t)pairs;
-        const size_t cost = waves * (size_t)(tn + 16);
-        if (cost <= best) {
+        const size_t tiles = tt * (size_t)p.tiles_c, steps = (size_t)p.steps;
+        const size_t step = tn * 4 + 30 > 620 ? (size_t)tn * 4 + 30 : 620;
+        size_t full = tiles / (size_t)pairs * (size_t)pairs;
+        const size_t left = tiles - full;
+        size_t per = left ? (size_t)pairs / left : 1;        // pairs a left-over tile
+        if (per > steps) per = steps;
+        size_t cost = full / (size_t)pairs * steps * step;
+        const size_t split = (steps + per - 1) / per * step + 4000 + 10 * (size_t)tn, whole = steps * step;
+        if (left > 0) cost += per > 1 && split < whole ? split : whole;
+        if (left == 0 || per < 2 || split >= whole) {
+            full = tiles;
+            per = 1;
+        }
+        if (cost < best) {
             best = cost;
             p.tn = tn;
             p.tiles_t = (int)tt;
+            p.full = (int)full;
+            p.per = (int)per;
+            p.pairs = full == 0 ? (int)(left * per) : (int)(tiles < (size_t)pairs ? tiles : (size_t)pairs);
         }
     }
-    const size_t tiles = (size_t)p.tiles_c * (size_t)p.tiles_t;
-    size_t s = (size_t)pairs / tiles;
-    if (s > (size_t)p.steps) s = (size_t)p.steps;
-    if (s < 1) s = 1;
-    p.sps = p.steps ? (p.steps + (int)s - 1) / (int)s : 1;
-    p.splits = p.steps ? (p.steps + p.sps - 1) / p.sps : 1;
-    p.units = (int)(tiles * (size_t)p.splits);
-    p.ldf = (K + 63) / 64 * 64;
     return p;
+}
+
+// 32-bit words of the split tiles' scratch: a slab a piece, and a counter a
+// CTA and tile (which start at 0).
+static size_t i8_split_words(const I8Plan &p)
+{
+    const size_t tiles = (size_t)p.tiles_c * (size_t)p.tiles_t - (size_t)p.full;
+    return tiles * ((size_t)p.per * (size_t)p.tn * kI8BM + 2);
 }
 
 // Scratch bytes of a call: the tokens as binary16, the repacked weights
@@ -726,23 +821,13 @@ size_t gemm_i8_scratch(const I8Plan &p, size_t M, size_t N, bool repack_w)
     size_t b = M * p.ldf * 2;
     if (repack_w) b += N * p.ldf;
     b = (b + 255) / 256 * 256;
-    if (p.splits > 1) b += (M * N + 2 * (size_t)p.tiles_c * (size_t)p.tiles_t) * 4;
-    return b;
+    return b + i8_split_words(p) * 4;
 }
 
 cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool repack_w, bool inject_stall,
                            cudaStream_t stream)
 {
-    if (!p.tensor) {
-        const size_t per_block = 4 * kGvR;
-        const dim3 grid((unsigned)((a.N + per_block - 1) / per_block));
-        const void *k = a.M <= 1   ? (const void *)gemv_i8_kernel<1>
-                        : a.M <= 2 ? (const void *)gemv_i8_kernel<2>
-                        : a.M <= 4 ? (const void *)gemv_i8_kernel<4>
-                                   : (const void *)gemv_i8_kernel<8>;
-        void *args[] = {(void *)&a};
-        return launch_first(k, grid, dim3(128), args, 0, stream);
-    }
+    if (!p.tensor) return launch_gemm_i8_few(a, stream);
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
     I8Prepare q;
@@ -775,13 +860,13 @@ cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool
     I8Gemm g;
     std::memset(&g, 0, sizeof g);
     unsigned blocks_z = 0;
-    if (p.splits > 1) {
-        q.zero = (int *)((char *)scratch + off);
-        q.zero_words = a.M * a.N + 2 * (size_t)p.tiles_c * (size_t)p.tiles_t;
-        const size_t nb = (q.zero_words + 1023) / 1024;
-        blocks_z = (unsigned)(nb < 304 ? nb : 304);
-        g.ws = q.zero;
-        g.count = (uint32_t *)(q.zero + a.M * a.N);
+    if (p.per > 1) {
+        const size_t tiles = (size_t)p.tiles_c * (size_t)p.tiles_t - (size_t)p.full;
+        g.ws = (int *)((char *)scratch + off);
+        q.zero = g.ws + tiles * (size_t)p.per * (size_t)p.tn * kI8BM;
+        q.zero_words = 2 * tiles;
+        blocks_z = 1;
+        g.count = (uint32_t *)q.zero;
     }
     alignas(64) CUtensorMap mw, mt;
     const cuuint32_t estride[2] = {1, 1};
@@ -800,8 +885,12 @@ cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
+    // the split of the SM's memory that the product's kernel needs, so that
+    // its CTAs can start beside the last of these
+    cudaError_t e = set_smem_once((void *)i8_prepare_kernel, 0, 100);
+    if (e != cudaSuccess) return e;
     void *args1[] = {(void *)&q};
-    cudaError_t e = launch_first((const void *)i8_prepare_kernel, dim3(q.blocks_a + q.blocks_w + blocks_z), dim3(256),
+    e = launch_first((const void *)i8_prepare_kernel, dim3(q.blocks_a + q.blocks_w + blocks_z), dim3(256),
                                  args1, 0, stream);
     if (e != cudaSuccess) return e;
     g.sa = a.sa;
@@ -815,14 +904,14 @@ cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool
     g.tiles_c = p.tiles_c;
     g.tiles_t = p.tiles_t;
     g.steps = p.steps;
-    g.sps = p.sps;
-    g.splits = p.splits;
-    g.units = p.units;
+    g.full = p.full;
+    g.tiles = p.tiles_c * p.tiles_t;
+    g.per = p.per;
+    g.w_prepared = repack_w ? 1u : 0u;
     g.inject_stall = inject_stall ? 1u : 0u;
-    const int pairs = gemm_i8_pairs();
     void *args[] = {(void *)&mw, (void *)&mt, (void *)&g};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(2 * (p.units < pairs ? p.units : pairs)));
+    cfg.gridDim = dim3((unsigned)(2 * p.pairs));
     cfg.blockDim = dim3(kI8Threads);
     cfg.dynamicSmemBytes = kI8SmemBytes;
     cfg.stream = stream;

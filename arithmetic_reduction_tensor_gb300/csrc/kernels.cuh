@@ -234,7 +234,7 @@ size_t norm_back_scratch(size_t rows, size_t cols);
 cudaError_t launch_norm_back(int dtype, const BackArgs &a, float *dw, cudaStream_t stream);
 
 // ---- matrix product in 8-bit integers with scales (k_gemm_i8.cu)
-constexpr int kI8GemvTokens = 8;     // up to so many tokens: the integer-unit kernel
+constexpr int kI8FewTokens = 8;     // up to so many tokens: the kernels of k_gemm_i8_few.cu
 constexpr int kOutI32 = 4;           // c_dtype beside kF16, kBF16, kF32: the integer sums themselves
 struct I8Args {
     const int8_t *A, *W;
@@ -262,15 +262,16 @@ struct I8Gemm {
     const float *sa, *sw;
     void *C;
     size_t ldc, M, N;
-    int c_dtype, tn, tiles_c, tiles_t, steps, sps, splits, units;
-    int *ws;
+    int c_dtype, tn, tiles_c, tiles_t, steps;
+    int tiles, full, per;            // tiles; whole ones; pieces of each of the others
+    int *ws;                         // the split tiles' sums and, per CTA, the steps in them
     uint32_t *count;
-    uint32_t inject_stall;
+    uint32_t w_prepared, inject_stall;
 };
 struct I8Plan {
-    int tensor;                      // 0: the integer-unit kernel
+    int tensor;                      // 0: launch_gemm_i8_few
     int tn, tiles_c, tiles_t;        // tokens per tile, tiles
-    int steps, sps, splits, units;   // steps of 128 k; per split; K splits; CTA-pair work units
+    int steps, full, per, pairs;     // steps of 128 k a tile; whole tiles; pieces of each other tile; CTA pairs
     size_t ldf;                      // row pitch of the prepared operands
     int launches;
 };
@@ -279,6 +280,8 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs);
 size_t gemm_i8_scratch(const I8Plan &p, size_t M, size_t N, bool repack_w);
 cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool repack_w, bool inject_stall,
                            cudaStream_t stream);
+// Few tokens, one launch, no scratch (k_gemm_i8_few.cu).
+cudaError_t launch_gemm_i8_few(const I8Args &a, cudaStream_t stream);
 cudaError_t read_gemm_i8_faults(unsigned int *flags, bool clear);
 
 // Make the driver load every variant of a kernel family now (one

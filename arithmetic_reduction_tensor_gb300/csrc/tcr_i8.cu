@@ -267,7 +267,7 @@ tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t ldw, con
     a.al_a = rows_aligned(A, lda, M, 1);
     a.al_w = rows_aligned(W, ldw, N, 1);
     int pairs = 0;
-    if (M > (size_t)kI8GemvTokens) {
+    if (M > (size_t)kI8FewTokens) {
         pairs = gemm_i8_pairs();
         if (pairs <= 0) return TCR_ERR_UNSUPPORTED;
     }

@@ -53,7 +53,7 @@ def gen():
 
 @pytest.mark.parametrize("K", [1, 16, 100, 1024, 1025, 3000])
 @pytest.mark.parametrize("N", [1, 7, 130, 256, 300])
-@pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 9, 33, 192, 200])
+@pytest.mark.parametrize("M", [1, 2, 3, 5, 8, 9, 17, 33, 49, 64, 65, 160, 161, 200])
 def test_every_small_shape(M, N, K, gen):
     check(codes(gen, M, K), codes(gen, N, K), gen)
 
@@ -65,7 +65,7 @@ def test_larger_shapes(M, N, K, gen):
     check(codes(gen, M, K), codes(gen, N, K), gen)
 
 
-@pytest.mark.parametrize("M", [1, 8, 9, 64, 300])
+@pytest.mark.parametrize("M", [1, 2, 8, 9, 30, 64, 65, 300])
 @pytest.mark.parametrize("K", [1024, 8192, 131071])
 def test_the_largest_sums(M, K, gen):
     # every product 2^14 and of one sign: a chunk's sum is the accumulator's
@@ -79,7 +79,7 @@ def test_the_largest_sums(M, K, gen):
     check(a, w, gen)
 
 
-@pytest.mark.parametrize("M", [1, 6, 20, 260])
+@pytest.mark.parametrize("M", [1, 6, 20, 40, 60, 100, 260])
 @pytest.mark.parametrize("pitch_a,off_a,pitch_w,off_w,K", [(640, 16, 656, 32, 512), (515, 3, 512, 0, 512),
                                                           (512, 0, 600, 5, 500), (1041, 1, 1043, 7, 1037)])
 def test_strides_and_alignment(M, pitch_a, off_a, pitch_w, off_w, K, gen):
@@ -163,7 +163,8 @@ def test_refusals(gen, monkeypatch):
         tcr.tcr_gemm_i8(torch.zeros(1, 131072, dtype=torch.int8, device="cuda"),
                         torch.zeros(1, 131072, dtype=torch.int8, device="cuda"))
     assert e.value.status == tcr.ERR_UNSUPPORTED
-    out = torch.full((12, 20), 5.0, device="cuda")
+    a = codes(gen, 100, 64)                               # enough tokens for scratch
+    out = torch.full((100, 20), 5.0, device="cuda")
     for what in ("alloc", "launch"):
         monkeypatch.setenv("TCR_FAULT_INJECT", what)
         with pytest.raises(tcr.TcrError):
