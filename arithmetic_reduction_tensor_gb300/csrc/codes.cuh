@@ -43,6 +43,24 @@ __device__ __forceinline__ uint4 ld_codes(const int8_t *p, uint32_t left, bool a
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// The same for 8 codes at any alignment, by 8-byte granules.
+__device__ __forceinline__ uint2 ld_codes8(const int8_t *p, uint32_t left)
+{
+    left = min(left, 8u);
+    const uint32_t m = (uint32_t)(uintptr_t)p & 7u;
+    uint2 lo = make_uint2(0u, 0u), hi = lo;
+    if (left > 0) lo = *reinterpret_cast<const uint2 *>(p - m);
+    if (m + left > 8) hi = *reinterpret_cast<const uint2 *>(p - m + 8);
+    const bool far = m & 4u;
+    const uint32_t a = far ? lo.y : lo.x, b = far ? hi.x : lo.y, c = far ? hi.y : hi.x;
+    uint2 r = make_uint2(__funnelshift_r(a, b, 8u * (m & 3u)), __funnelshift_r(b, c, 8u * (m & 3u)));
+    if (left < 4)
+        r = make_uint2(left ? r.x & (0xffffffffu >> (32 - 8 * left)) : 0u, 0u);
+    else if (left < 8)
+        r.y = left > 4 ? r.y & (0xffffffffu >> (32 - 8 * (left - 4))) : 0u;
+    return r;
+}
+
 __device__ __forceinline__ void store_out(void *C, int dtype, size_t i, int acc, float sa, float sw)
 {
     if (dtype == kOutI32) {

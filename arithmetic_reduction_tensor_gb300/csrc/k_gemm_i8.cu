@@ -59,8 +59,8 @@ __device__ unsigned int g_gemm_i8_fault;
 
 // Blocks [0, blocks_a): the tokens' codes as binary16, rows of ldf values,
 // zero past K.  Blocks up to blocks_a + blocks_w: the weights' codes in rows
-// of ldp bytes (only when their own pitch or base does not fit TMA).  The
-// last one zeroes the counters of the split tiles.  A team of 2^team_log2 threads to a row.
+// of ldf bytes (only when their own pitch or base does not fit TMA).  The
+// last one zeroes the counters of the split tiles.  8 codes a thread.
 __global__ void __launch_bounds__(256) i8_prepare_kernel(const I8Prepare p)
 {
     // in this order: the product's kernel may read the weights as soon as it
@@ -68,34 +68,28 @@ __global__ void __launch_bounds__(256) i8_prepare_kernel(const I8Prepare p)
     pdl_wait_primary();
     pdl_launch_dependents();
     unsigned b = blockIdx.x;
-    const int team = 1 << p.team_log2;
-    const int in_team = threadIdx.x & (team - 1);
-    const size_t rows_per_block = (size_t)256 >> p.team_log2;
-    if (b < p.blocks_a) {
-        const size_t r = b * rows_per_block + (threadIdx.x >> p.team_log2);
-        if (r >= p.M) return;
-        for (size_t c = (size_t)in_team * 16; c < p.ldf; c += (size_t)team * 16) {
-            const uint4 q = ld_codes(p.A + r * p.lda + c, p.K > c ? (uint32_t)(p.K - c) : 0u, p.al_a);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 4; k++) widen4(w[k], o[2 * k], o[2 * k + 1]);
-            uint4 *dst = reinterpret_cast<uint4 *>(p.Af + r * p.ldf + c);
-            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-        }
+    if (b >= p.blocks_a + p.blocks_w) {
+        for (size_t i = threadIdx.x; i < p.zero_words; i += 256) p.zero[i] = 0;
         return;
     }
-    b -= p.blocks_a;
-    if (b < p.blocks_w) {
-        const size_t r = b * rows_per_block + (threadIdx.x >> p.team_log2);
-        if (r >= p.N) return;
-        for (size_t c = (size_t)in_team * 16; c < p.ldp; c += (size_t)team * 16)
-            *reinterpret_cast<uint4 *>(p.Wp + r * p.ldp + c) =
-                ld_codes(p.W + r * p.ldw + c, p.K > c ? (uint32_t)(p.K - c) : 0u, false);
-        return;
+    const bool tokens = b < p.blocks_a;
+    if (!tokens) b -= p.blocks_a;
+    const size_t item = (size_t)b * 256 + threadIdx.x;
+    const uint32_t per_row = (uint32_t)(p.ldf / 8);
+    const size_t r = item <= 0xffffffffu ? (uint32_t)item / per_row : item / per_row;
+    const uint32_t c = 8 * (uint32_t)(item - r * per_row);
+    if (r >= (tokens ? p.M : p.N)) return;
+    const uint32_t left = p.K > c ? (uint32_t)(p.K - c) : 0u;
+    const int8_t *from = (tokens ? p.A + r * p.lda : p.W + r * p.ldw) + c;
+    const uint2 q = tokens && p.al_a && left >= 8 ? *reinterpret_cast<const uint2 *>(from) : ld_codes8(from, left);
+    if (tokens) {
+        uint4 o;
+        widen4(q.x, o.x, o.y);
+        widen4(q.y, o.z, o.w);
+        *reinterpret_cast<uint4 *>(p.Af + r * p.ldf + c) = o;
+    } else {
+        *reinterpret_cast<uint2 *>(p.Wp + r * p.ldf + c) = q;
     }
-    for (size_t i = threadIdx.x; i < p.zero_words; i += 256) p.zero[i] = 0;
 }
 
 // ---------------------------------------------------------------- the tensor-core kernel
@@ -762,10 +756,8 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
 {
     I8Plan p;
     std::memset(&p, 0, sizeof p);
-    if (M <= (size_t)kI8FewTokens) {
-        p.launches = 1;
-        return p;
-    }
+    p.launches = 1;
+    if (M <= 2 || pairs <= 0) return p;
     p.tensor = 1;
     p.launches = 2;
     p.steps = (int)((K + kI8BK - 1) / kI8BK);
@@ -801,6 +793,17 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
             p.per = (int)per;
             p.pairs = full == 0 ? (int)(left * per) : (int)(tiles < (size_t)pairs ? tiles : (size_t)pairs);
         }
+    }
+    // Against the kernels of k_gemm_i8_few.cu, whose one launch costs 5 us less
+    // than the two, the copies' and the conversion's latency and the hand-over
+    // here, but which run 40 thousand multiply-adds a cycle and stream 1900
+    // bytes of weights (64 x 2048 x 2048: 4.5 us, 10 here; 48 x 4096 x 4096:
+    // 14.8 and 16.0; 1024 x 1024 x 1024: 18.8 and 9.4).
+    const size_t macs = N * K * ((M + 7) / 8 * 8);
+    const size_t few = 3800 + (macs / 39500 > N * K / 1900 ? macs / 39500 : N * K / 1900);
+    if (M <= (size_t)kI8FewTokens && few < 14500 + best) {
+        std::memset(&p, 0, sizeof p);
+        p.launches = 1;
     }
     return p;
 }
@@ -840,9 +843,8 @@ cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool
     q.al_a = a.al_a;
     q.Af = (uint16_t *)scratch;
     q.ldf = p.ldf;
-    while (q.team_log2 < 8 && ((size_t)16 << q.team_log2) < p.ldf) q.team_log2++;
-    const size_t rpb = (size_t)256 >> q.team_log2;
-    q.blocks_a = (unsigned)((a.M + rpb - 1) / rpb);
+    auto blocks_of = [&](size_t rows) { return (unsigned)((rows * (p.ldf / 8) + 255) / 256); };
+    q.blocks_a = blocks_of(a.M);
     const int8_t *w = a.W;
     size_t ldw = a.ldw;
     size_t off = a.M * p.ldf * 2;
@@ -850,8 +852,7 @@ cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool
         q.W = a.W;
         q.ldw = a.ldw;
         q.Wp = (int8_t *)scratch + off;
-        q.ldp = p.ldf;
-        q.blocks_w = (unsigned)((a.N + rpb - 1) / rpb);
+        q.blocks_w = blocks_of(a.N);
         w = q.Wp;
         ldw = p.ldf;
         off += a.N * p.ldf;

@@ -234,7 +234,7 @@ size_t norm_back_scratch(size_t rows, size_t cols);
 cudaError_t launch_norm_back(int dtype, const BackArgs &a, float *dw, cudaStream_t stream);
 
 // ---- matrix product in 8-bit integers with scales (k_gemm_i8.cu)
-constexpr int kI8FewTokens = 8;     // up to so many tokens: the kernels of k_gemm_i8_few.cu
+constexpr int kI8FewTokens = 1024;   // beyond: never the kernels of k_gemm_i8_few.cu
 constexpr int kOutI32 = 4;           // c_dtype beside kF16, kBF16, kF32: the integer sums themselves
 struct I8Args {
     const int8_t *A, *W;
@@ -251,11 +251,9 @@ struct I8Prepare {
     uint16_t *Af;
     size_t ldf;
     int8_t *Wp;
-    size_t ldp;
     int *zero;
     size_t zero_words;
     unsigned blocks_a, blocks_w;
-    int team_log2;
     bool al_a;
 };
 struct I8Gemm {
@@ -280,7 +278,8 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs);
 size_t gemm_i8_scratch(const I8Plan &p, size_t M, size_t N, bool repack_w);
 cudaError_t launch_gemm_i8(const I8Args &a, const I8Plan &p, void *scratch, bool repack_w, bool inject_stall,
                            cudaStream_t stream);
-// Few tokens, one launch, no scratch (k_gemm_i8_few.cu).
+// Few tokens or small matrices, one launch, no scratch (k_gemm_i8_few.cu);
+// M < 2^19.
 cudaError_t launch_gemm_i8_few(const I8Args &a, cudaStream_t stream);
 cudaError_t read_gemm_i8_faults(unsigned int *flags, bool clear);
 

@@ -266,12 +266,9 @@ tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t ldw, con
     a.c_dtype = c_dtype == TCR_I32 ? kOutI32 : c_dtype;
     a.al_a = rows_aligned(A, lda, M, 1);
     a.al_w = rows_aligned(W, ldw, N, 1);
-    int pairs = 0;
-    if (M > (size_t)kI8FewTokens) {
-        pairs = gemm_i8_pairs();
-        if (pairs <= 0) return TCR_ERR_UNSUPPORTED;
-    }
-    const I8Plan p = gemm_i8_plan(M, N, K, pairs);
+    const I8Plan p = gemm_i8_plan(M, N, K, M <= 2 ? 0 : gemm_i8_pairs());
+    // without CTA pairs the one-launch kernels serve what their grid covers
+    if (!p.tensor && M >= ((size_t)1 << 19)) return TCR_ERR_UNSUPPORTED;
     const bool repack = p.tensor && !a.al_w;
     Scratch scratch(s);
     tcr_status st = scratch.take(gemm_i8_scratch(p, M, N, repack), dev);

@@ -593,12 +593,13 @@ TCR_API tcr_status tcr_dequantize_rows_i8(const void *q, size_t ldq, const float
  *            itself (the scales are not looked at).
  * M, N < 2^31, M * N, M * K, N * K < 2^40; K <= 131071 (any S then fits 32
  * bits), a larger K returns TCR_ERR_UNSUPPORTED.  K == 0 writes zeros.
- * C's bits depend on the inputs only: integer sums have no order.  Up to 8
- * tokens run on the integer units in one launch; more on tcgen05, as exact
- * binary16 MMAs over pairs of SMs, in two launches, with pool scratch of 2
- * bytes per code of A, N * K bytes more when W's rows are not 16-byte
- * aligned, and 4 bytes per output when K is split.  TCR_ERR_UNSUPPORTED where
- * the device cannot schedule a pair.  A kernel whose wait gave up leaves NaN
+ * C's bits depend on the inputs only: integer sums have no order.  Few tokens
+ * and small matrices run in one launch without scratch; the rest on tcgen05,
+ * as exact binary16 MMAs over pairs of SMs, in two launches, with pool scratch
+ * of 2 bytes per code of A, N * K bytes more when W's rows are not 16-byte
+ * aligned, and 4 bytes per output and piece where K is split.  (A device that
+ * cannot schedule a pair runs everything in one launch, and returns
+ * TCR_ERR_UNSUPPORTED for M >= 2^19.)  A kernel whose wait gave up leaves NaN
  * (TCR_I32: the least integer) and sets the word of tcr_device_faults.
  */
 TCR_API tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t ldw, const float *scale_a,
