@@ -426,8 +426,7 @@ class NormOut(NamedTuple):
     rstd: object            # 1 / sqrt(mean square + eps) of each row
 
 
-def _float_code(t) -> int:
-    import torch
+def _float_code(torch, t) -> int:
     dt = t.dtype
     if dt is torch.bfloat16:
         return BF16
@@ -474,19 +473,18 @@ def _mismatch(name, t, shape, dtype, dev):
     raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
 
 
-def _call(name, dev, stream, *args):
+def _call(torch, name, dev, stream, *args):
     """Call a C entry point on CUDA device ``dev``, its last argument the
     stream (the current one if None)."""
-    import torch
     f = getattr(_lib or c_api(), name)
     # the current stream's handle, without the Stream object around it
     s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(dev, stream)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = f(*args, s)
     else:
         with torch.cuda.device(dev):
             st = f(*args, s)
-    if st != OK:
+    if st:
         raise TcrError(st, name)
 
 
@@ -516,7 +514,7 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
     import torch
     shape, dev = _check_rows("x", x)
     rows, cols = shape
-    dt, xt = _float_code(x), x.dtype
+    dt, xt = _float_code(torch, x), x.dtype
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or xt, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -543,7 +541,7 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
     if rstd is not None:
         tp = _vector("rstd", rstd, rows, torch.float32, dev)
-    _call("tcr_rmsnorm", dev, stream,
+    _call(torch, "tcr_rmsnorm", dev, stream,
           _NORM_ARGS.pack(xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, tp, rows, cols, eps, dt, I8 if i8 else dt))
     return NormOut(out, scale, h, rstd)
 
@@ -559,7 +557,7 @@ def tcr_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
     import torch
     shape, dev = _check_rows("h", h)
     rows, cols = shape
-    dt, ht = _float_code(h), h.dtype
+    dt, ht = _float_code(torch, h), h.dtype
     gp, ldg = _matrix("dy", dy, shape, ht, dev)
     hp, ldh = _matrix("h", h, shape, ht, dev)
     tp = _vector("rstd", rstd, rows, torch.float32, dev)
@@ -575,7 +573,7 @@ def tcr_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
         dweight = torch.empty(cols, dtype=torch.float32, device=h.device)
     if dweight is not None:
         dwp = _vector("dweight", dweight, cols, torch.float32, dev)
-    _call("tcr_rmsnorm_backward", dev, stream,
+    _call(torch, "tcr_rmsnorm_backward", dev, stream,
           _NORM_BACK_ARGS.pack(gp, ldg, hp, ldh, wp, tp, dhp, lddh, dxp, lddx, dwp, rows, cols, dt))
     return dx, dweight
 
@@ -591,12 +589,12 @@ def tcr_quantize_rows_i8(x, gate=None, out=None, scale=None, stream=None):
         out = torch.empty(shape, dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    dt = _float_code(x)
+    dt = _float_code(torch, x)
     xp, ldx = _matrix("x", x, shape, x.dtype, dev)
     gp, ldg = (None, 0) if gate is None else _matrix("gate", gate, shape, x.dtype, dev)
     qp, ldq = _matrix("out", out, shape, torch.int8, dev, True)
     sp = _vector("scale", scale, rows, torch.float32, dev)
-    _call("tcr_quantize_rows_i8", dev, stream, xp, ldx, gp, ldg, qp, ldq, sp, rows, cols, dt)
+    _call(torch, "tcr_quantize_rows_i8", dev, stream, xp, ldx, gp, ldg, qp, ldq, sp, rows, cols, dt)
     return out, scale
 
 
@@ -613,7 +611,7 @@ def tcr_dequantize_rows_i8(q, scale, dtype=None, out=None, stream=None):
     qp, ldq = _matrix("q", q, shape, torch.int8, dev)
     sp = _vector("scale", scale, rows, torch.float32, dev)
     yp, ldy = _matrix("out", out, shape, out.dtype, dev, True)
-    _call("tcr_dequantize_rows_i8", dev, stream, qp, ldq, sp, yp, ldy, rows, cols, _float_code(out))
+    _call(torch, "tcr_dequantize_rows_i8", dev, stream, qp, ldq, sp, yp, ldy, rows, cols, _float_code(torch, out))
     return out
 
 
@@ -639,11 +637,11 @@ def tcr_gemm_i8(A, W, scale_a=None, scale_w=None, out_dtype=None, out=None, stre
             raise ValueError("int32 sums take no scales")
         dt = I32
     else:
-        dt = _float_code(out)
+        dt = _float_code(torch, out)
     ap, lda = _matrix("A", A, A.shape, torch.int8, dev, True)
     wp, ldw = _matrix("W", W, W.shape, torch.int8, dev, True)
     cp, ldc = _matrix("out", out, (M, N), out.dtype, dev, True)
     sa = None if scale_a is None else _vector("scale_a", scale_a, M, torch.float32, dev)
     sw = None if scale_w is None else _vector("scale_w", scale_w, N, torch.float32, dev)
-    _call("tcr_gemm_i8", dev, stream, ap, lda, wp, ldw, sa, sw, cp, ldc, M, N, K, dt)
+    _call(torch, "tcr_gemm_i8", dev, stream, ap, lda, wp, ldw, sa, sw, cp, ldc, M, N, K, dt)
     return out

@@ -91,8 +91,9 @@ __device__ __forceinline__ void apply_norm(const RawVec<DT> &wr, bool has_w, flo
 // Rows of at most 8 T NV columns, NV vectors a thread: teams of T threads
 // (T = 32: eight to a CTA; else the CTA) walk the rows, each loading its next
 // row before it finishes the current one, so that loads stay in flight
-// across the row's barriers.  MINB: the CTAs per SM that the registers allow.
-template <int DT, int OP, int OUT, int T, int NV, int MINB>
+// across the row's barriers.  GRAN: x or r is read by granules (rows that are
+// not 16-byte aligned).  MINB: the CTAs per SM that the registers allow.
+template <int DT, int OP, int OUT, bool GRAN, int T, int NV, int MINB>
 __global__ void __launch_bounds__(T == 32 ? 256 : T, MINB)
 row_stream_kernel(const RowArgs a)
 {
@@ -107,12 +108,13 @@ row_stream_kernel(const RowArgs a)
     const size_t team = T == 32 ? (size_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
     const size_t teams = T == 32 ? (size_t)gridDim.x * 8 : gridDim.x;
     const bool has_r = a.r != nullptr, has_w = a.w != nullptr;
-    RawVec<DT> x[NV], b[NV], w[NV];
+    RawVec<DT> w[NV];
+    LoadedVec<DT, GRAN> x[NV], b[NV];
     auto load = [&](size_t r) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            x[i] = load_raw<DT>((const E *)a.x + r * a.ldx, cols, t + i * T, a.al_x);
-            b[i] = has_r ? load_raw<DT>((const E *)a.r + r * a.ldr, cols, t + i * T, a.al_r) : RawVec<DT>();
+            x[i] = load_vec<DT, GRAN>((const E *)a.x + r * a.ldx, cols, t + i * T);
+            b[i] = has_r ? load_vec<DT, GRAN>((const E *)a.r + r * a.ldr, cols, t + i * T) : LoadedVec<DT, GRAN>();
         }
     };
 #pragma unroll
@@ -122,7 +124,9 @@ row_stream_kernel(const RowArgs a)
     for (size_t r = team; r < a.rows; r += teams, buf ^= 1) {
         float y[NV][kRv];
 #pragma unroll
-        for (int i = 0; i < NV; i++) row_value<DT, OP>(x[i], b[i], has_r, y[i]);
+        for (int i = 0; i < NV; i++)
+            row_value<DT, OP>(use_vec<DT, GRAN>(x[i], (const E *)a.x + r * a.ldx, cols, t + i * T),
+                              use_vec<DT, GRAN>(b[i], (const E *)a.r + r * a.ldr, cols, t + i * T), has_r, y[i]);
         if (r + teams < a.rows) load(r + teams);
         // two buffers each: a thread reaches the next row's write of one only
         // after every thread has passed a barrier of the row between
@@ -344,14 +348,14 @@ namespace {
 
 // A launch of row_stream_kernel: as many CTAs as 152 SMs hold (or one team
 // a row).
-template <int DT, int OP, int OUT, int T, int NV, int MINB>
+template <int DT, int OP, int OUT, bool GRAN, int T, int NV, int MINB>
 const void *stream_of(size_t nvec, size_t rows, int &threads, size_t &grid)
 {
     threads = T == 32 ? 256 : NV == 1 ? (int)((nvec + 31) / 32 * 32) : T;
     const size_t need = T == 32 ? (rows + 7) / 8 : rows;
     const size_t full = (size_t)152 * (size_t)(T == 32 ? MINB : MINB * T / threads);
     grid = need < full ? need : full;
-    return (const void *)row_stream_kernel<DT, OP, OUT, T, NV, MINB>;
+    return (const void *)row_stream_kernel<DT, OP, OUT, GRAN, T, NV, MINB>;
 }
 
 // Which shape serves a row length: the fastest of those measured at it, on
@@ -361,13 +365,24 @@ const void *stream_of(size_t nvec, size_t rows, int &threads, size_t &grid)
 // threads of 2 vectors and 3 CTAs an SM, 410 with 512 x 1 and 2, 314 with
 // 256 x 2 and 4 (spills), 303 with 128 x 4 and 4; 16384 x 8192 bfloat16 150
 // with 256 x 4 and 2, 189 with 1024 x 1.  The gate needs no weight and one
-// barrier, so one CTA more fits.
+// barrier, so one CTA more fits.  Granules take more registers.
 template <int DT, int OP, int OUT>
-const void *pick(size_t nvec, size_t rows, int &threads, size_t &grid)
+const void *pick(size_t nvec, size_t rows, bool gran, int &threads, size_t &grid)
 {
-#define TCR_STREAM(T_, NV_, MINB_) return stream_of<DT, OP, OUT, T_, NV_, MINB_>(nvec, rows, threads, grid)
+#define TCR_STREAM(T_, NV_, MINB_) return stream_of<DT, OP, OUT, false, T_, NV_, MINB_>(nvec, rows, threads, grid)
+#define TCR_GRAN(T_, NV_, MINB_) return stream_of<DT, OP, OUT, true, T_, NV_, MINB_>(nvec, rows, threads, grid)
     constexpr bool quant = OP == kRowQuant;
-    if constexpr (DT == kF32) {
+    if (gran) {
+        if (nvec <= 32) TCR_GRAN(32, 1, 3);
+        if (nvec <= 64) TCR_GRAN(32, 2, 2);
+        if (nvec <= 128) TCR_GRAN(128, 1, DT == kF32 ? 4 : 6);
+        if (nvec <= 256) TCR_GRAN(256, 1, DT == kF32 ? 2 : 3);
+        if (nvec <= 512) TCR_GRAN(256, 2, DT == kF32 ? 1 : 2);
+        if (nvec <= 768) TCR_GRAN(256, 3, DT == kF32 ? 1 : 2);
+        if (nvec <= 1024) TCR_GRAN(512, 2, 1);
+        if constexpr (DT != kF32)
+            if (nvec <= 2048) TCR_GRAN(512, 4, 1);
+    } else if constexpr (DT == kF32) {
         if (nvec <= 32) TCR_STREAM(32, 1, 3);
         if (nvec <= 64) TCR_STREAM(32, 2, 2);
         if (nvec <= 128) TCR_STREAM(128, 1, 8);
@@ -399,6 +414,7 @@ const void *pick(size_t nvec, size_t rows, int &threads, size_t &grid)
                 TCR_STREAM(512, 4, 1);
         }
     }
+#undef TCR_GRAN
 #undef TCR_STREAM
     grid = rows;
     if (nvec <= 2048) {
@@ -414,12 +430,12 @@ const void *pick(size_t nvec, size_t rows, int &threads, size_t &grid)
 }
 
 template <int DT>
-const void *pick_op(int op, int out_i8, size_t nvec, size_t rows, int &threads, size_t &grid)
+const void *pick_op(int op, int out_i8, size_t nvec, size_t rows, bool gran, int &threads, size_t &grid)
 {
     if (op == kRowNorm)
-        return out_i8 ? pick<DT, kRowNorm, kOutI8>(nvec, rows, threads, grid)
-                      : pick<DT, kRowNorm, kOutSame>(nvec, rows, threads, grid);
-    return pick<DT, kRowQuant, kOutI8>(nvec, rows, threads, grid);
+        return out_i8 ? pick<DT, kRowNorm, kOutI8>(nvec, rows, gran, threads, grid)
+                      : pick<DT, kRowNorm, kOutSame>(nvec, rows, gran, threads, grid);
+    return pick<DT, kRowQuant, kOutI8>(nvec, rows, gran, threads, grid);
 }
 
 }  // namespace
@@ -429,9 +445,10 @@ cudaError_t launch_rows_op(int op, int dtype, bool out_i8, const RowArgs &a, cud
     const size_t nvec = (a.cols + kRv - 1) / kRv;
     int threads = 0;
     size_t grid = 0;
-    const void *k = dtype == kF16    ? pick_op<kF16>(op, out_i8, nvec, a.rows, threads, grid)
-                    : dtype == kBF16 ? pick_op<kBF16>(op, out_i8, nvec, a.rows, threads, grid)
-                                     : pick_op<kF32>(op, out_i8, nvec, a.rows, threads, grid);
+    const bool gran = !a.al_x || (a.r && !a.al_r);
+    const void *k = dtype == kF16    ? pick_op<kF16>(op, out_i8, nvec, a.rows, gran, threads, grid)
+                    : dtype == kBF16 ? pick_op<kBF16>(op, out_i8, nvec, a.rows, gran, threads, grid)
+                                     : pick_op<kF32>(op, out_i8, nvec, a.rows, gran, threads, grid);
     void *args[] = {(void *)&a};
     return launch_first(k, dim3((unsigned)grid), dim3((unsigned)threads), args, 0, stream);
 }

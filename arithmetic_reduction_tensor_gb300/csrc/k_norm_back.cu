@@ -15,19 +15,19 @@
 
 namespace tcr {
 
-template <int DT>
+template <int DT, bool GRAN>
 struct BackRow {
-    RawVec<DT> dy, h, dh;
+    LoadedVec<DT, GRAN> dy, h, dh;
 };
 
-template <int DT>
-__device__ __forceinline__ void load_row(const BackArgs &a, size_t r, uint32_t v, BackRow<DT> &b)
+template <int DT, bool GRAN>
+__device__ __forceinline__ void load_row(const BackArgs &a, size_t r, uint32_t v, BackRow<DT, GRAN> &b)
 {
     using E = typename Elem<DT>::T;
     const uint32_t cols = (uint32_t)a.cols;
-    b.dy = load_raw<DT>((const E *)a.dy + r * a.lddy, cols, v, a.al_dy);
-    b.h = load_raw<DT>((const E *)a.h + r * a.ldh, cols, v, a.al_h);
-    if (a.dh) b.dh = load_raw<DT>((const E *)a.dh + r * a.lddh, cols, v, a.al_dh);
+    b.dy = load_vec<DT, GRAN>((const E *)a.dy + r * a.lddy, cols, v);
+    b.h = load_vec<DT, GRAN>((const E *)a.h + r * a.ldh, cols, v);
+    if (a.dh) b.dh = load_vec<DT, GRAN>((const E *)a.dh + r * a.lddh, cols, v);
 }
 
 template <int DT>
@@ -38,13 +38,16 @@ __device__ __forceinline__ RawVec<DT> load_weight(const BackArgs &a, uint32_t v)
 
 // xh and g of a vector; returns the tree over g * xh and, where `acc` is
 // given, adds dy * xh to it.
-template <int DT>
-__device__ __forceinline__ float back_products(const BackArgs &a, const BackRow<DT> &b, const RawVec<DT> &wr,
-                                               float rstd, float (&xh)[kRv], float (&g)[kRv], float *acc)
+template <int DT, bool GRAN>
+__device__ __forceinline__ float back_products(const BackArgs &a, size_t r, uint32_t v, const BackRow<DT, GRAN> &b,
+                                               const RawVec<DT> &wr, float rstd, float (&xh)[kRv], float (&g)[kRv],
+                                               float *acc)
 {
+    using E = typename Elem<DT>::T;
+    const uint32_t cols = (uint32_t)a.cols;
     float w[kRv], e[kRv];
-    unpack<DT>(b.h, xh);
-    unpack<DT>(b.dy, g);
+    unpack<DT>(use_vec<DT, GRAN>(b.h, (const E *)a.h + r * a.ldh, cols, v), xh);
+    unpack<DT>(use_vec<DT, GRAN>(b.dy, (const E *)a.dy + r * a.lddy, cols, v), g);
     if (a.w) unpack<DT>(wr, w);
 #pragma unroll
     for (int k = 0; k < kRv; k++) {
@@ -56,20 +59,22 @@ __device__ __forceinline__ float back_products(const BackArgs &a, const BackRow<
     return tree8(e);
 }
 
-template <int DT>
-__device__ __forceinline__ void store_dx(const BackArgs &a, size_t r, uint32_t v, const BackRow<DT> &b, float rstd,
-                                         float c, const float (&xh)[kRv], const float (&g)[kRv])
+template <int DT, bool GRAN>
+__device__ __forceinline__ void store_dx(const BackArgs &a, size_t r, uint32_t v, const LoadedVec<DT, GRAN> &dh,
+                                         float rstd, float c, const float (&xh)[kRv], const float (&g)[kRv])
 {
+    using E = typename Elem<DT>::T;
+    const uint32_t cols = (uint32_t)a.cols;
     float dx[kRv];
 #pragma unroll
     for (int k = 0; k < kRv; k++) dx[k] = __fmul_rn(rstd, __fsub_rn(g[k], __fmul_rn(xh[k], c)));
     if (a.dh) {
         float d[kRv];
-        unpack<DT>(b.dh, d);
+        unpack<DT>(use_vec<DT, GRAN>(dh, (const E *)a.dh + r * a.lddh, cols, v), d);
 #pragma unroll
         for (int k = 0; k < kRv; k++) dx[k] = __fadd_rn(dx[k], d[k]);
     }
-    store_vec<DT>((typename Elem<DT>::T *)a.dx + r * a.lddx, (uint32_t)a.cols, v, a.al_dx, dx);
+    store_vec<DT>((E *)a.dx + r * a.lddx, cols, v, a.al_dx, dx);
 }
 
 // partial[b * cols + j]: CTA b's sum of column j
@@ -87,45 +92,56 @@ __device__ __forceinline__ void store_partial(const BackArgs &a, uint32_t v, con
         if (k < left) p[k] = acc[k];
 }
 
-// Rows of at most 8 T vectors, one a thread; a CTA of 32 ceil(vectors / 32)
-// <= T threads.  The next row's inputs are loaded before the current row's
-// sum is waited for, so that loads stay in flight across the barrier (16384
-// rows of 4096 bfloat16: 165 us without, one vector a thread either way).
-template <int DT, int T>
-__global__ void __launch_bounds__(T, DT == kF32 ? 1 : 1024 / T)
+// Rows of at most T NV vectors, NV a thread; NV = 1: a CTA of 32 ceil(vectors
+// / 32) <= T threads.  The next row's inputs are loaded before the current
+// row's sum is waited for, so that loads stay in flight across the barrier.
+template <int DT, bool GRAN, int T, int NV, int MINB>
+__global__ void __launch_bounds__(T, MINB)
 back_kernel(const BackArgs a)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
     __shared__ float red[2][team_floats<T>()];
-    const uint32_t v = threadIdx.x;
+    const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
     // lanes past the row take part in the row's sum with zeros
-    const RawVec<DT> w = a.w ? load_weight<DT>(a, v) : RawVec<DT>();
-    float acc[kRv];
+    RawVec<DT> w[NV];
+    float acc[NV][kRv];
+    BackRow<DT, GRAN> cur[NV];
 #pragma unroll
-    for (int k = 0; k < kRv; k++) acc[k] = 0.0f;
-    BackRow<DT> cur;
-    load_row<DT>(a, blockIdx.x, v, cur);
+    for (int i = 0; i < NV; i++) {
+        w[i] = a.w ? load_weight<DT>(a, t + i * T) : RawVec<DT>();
+        load_row<DT, GRAN>(a, blockIdx.x, t + i * T, cur[i]);
+#pragma unroll
+        for (int k = 0; k < kRv; k++) acc[i][k] = 0.0f;
+    }
     float rstd = a.rstd[blockIdx.x];
     int buf = 0;
     for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x, buf ^= 1) {
-        float xh[kRv], g[kRv];
-        const float s = back_products<DT>(a, cur, w, rstd, xh, g, acc);
+        float s[NV];
+        LoadedVec<DT, GRAN> dh[NV];
+        float xh[NV][kRv], g[NV][kRv];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            s[i] = back_products<DT, GRAN>(a, r, t + i * T, cur[i], w[i], rstd, xh[i], g[i], acc[i]);
+            dh[i] = cur[i].dh;
+        }
         const size_t next = r + gridDim.x;
-        BackRow<DT> ahead = {};
-        float rstd_ahead = 0.0f;
+        const float rstd_now = rstd;
         if (next < a.rows) {
-            load_row<DT>(a, next, v, ahead);
-            rstd_ahead = a.rstd[next];
+#pragma unroll
+            for (int i = 0; i < NV; i++) load_row<DT, GRAN>(a, next, t + i * T, cur[i]);
+            rstd = a.rstd[next];
         }
         // two buffers: a thread reaches the next row's write of this one only
         // after every thread has passed the barrier of the row between
-        const float c = __fdiv_rn(team_sum<T>(s, red[buf], blockDim.x), (float)a.cols);
-        store_dx<DT>(a, r, v, cur, rstd, c, xh, g);
-        cur = ahead;
-        rstd = rstd_ahead;
+        const float c = __fdiv_rn(team_sum<T>(halving<NV>(s), red[buf], blockDim.x), (float)a.cols);
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (kRv * ((t & ~31u) + i * T) < cols)           // whole warps: stores are warp-wide
+                store_dx<DT, GRAN>(a, r, t + i * T, dh[i], rstd_now, c, xh[i], g[i]);
     }
-    store_partial(a, v, acc);
+#pragma unroll
+    for (int i = 0; i < NV; i++) store_partial(a, t + i * T, acc[i]);
 }
 
 // Longer rows: the row sums first (c[r]), then blocks of 8 * 256 columns.
@@ -149,11 +165,11 @@ back_long_sum_kernel(const BackArgs a, float *c_out)
         const uint32_t v = threadIdx.x + bit_reverse(j, bits) * T;
         float s = 0.0f;
         if (v < nvec) {
-            BackRow<DT> row;
+            BackRow<DT, true> row;
             float xh[kRv], g[kRv];
-            load_row<DT>(b, r, v, row);
+            load_row<DT, true>(b, r, v, row);
             const RawVec<DT> w = a.w ? load_weight<DT>(a, v) : RawVec<DT>();
-            s = back_products<DT>(a, row, w, rstd, xh, g, nullptr);
+            s = back_products<DT, true>(a, r, v, row, w, rstd, xh, g, nullptr);
         }
         tc.push(s);
     }
@@ -174,11 +190,11 @@ back_long_kernel(const BackArgs a, const float *c_in)
     for (int k = 0; k < kRv; k++) acc[k] = 0.0f;
     for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const float rstd = a.rstd[r];
-        BackRow<DT> row;
+        BackRow<DT, true> row;
         float xh[kRv], g[kRv];
-        load_row<DT>(a, r, v, row);
-        (void)back_products<DT>(a, row, w, rstd, xh, g, acc);
-        store_dx<DT>(a, r, v, row, rstd, c_in[r], xh, g);
+        load_row<DT, true>(a, r, v, row);
+        (void)back_products<DT, true>(a, r, v, row, w, rstd, xh, g, acc);
+        store_dx<DT, true>(a, r, v, row.dh, rstd, c_in[r], xh, g);
     }
     store_partial(a, v, acc);
 }
@@ -233,18 +249,49 @@ size_t norm_back_scratch(size_t rows, size_t cols)
 
 namespace {
 
+// The fastest shapes measured: the registers of two rows decide how many
+// threads fit, so binary32 takes half as many of an SM's threads as the 16-bit
+// types, and 16-bit rows of more than 2048 columns go two vectors to a thread
+// (16384 x 4096 bfloat16 91 us, 108 with one).  Rows that are not aligned hold
+// a granule more of each input.
+template <int DT>
+const void *pick(size_t nvec, bool gran, unsigned &threads)
+{
+#define TCR_BACK(G_, T_, NV_, MINB_) \
+    return (threads = NV_ == 1 ? (unsigned)((nvec + 31) / 32 * 32) : T_, \
+            (const void *)back_kernel<DT, G_, T_, NV_, MINB_>)
+    if (gran) {
+        if (nvec <= 64) TCR_BACK(true, 64, 1, 8);
+        if (nvec <= 128) TCR_BACK(true, 128, 1, 4);
+        if (nvec <= 256) TCR_BACK(true, 256, 1, 2);
+        if (nvec <= 512) TCR_BACK(true, 512, 1, 1);
+        TCR_BACK(true, 1024, 1, 1);
+    }
+    if constexpr (DT == kF32) {
+        if (nvec <= 64) TCR_BACK(false, 64, 1, 8);
+        if (nvec <= 128) TCR_BACK(false, 128, 1, 4);
+        if (nvec <= 256) TCR_BACK(false, 256, 1, 2);
+        if (nvec <= 512) TCR_BACK(false, 512, 1, 1);
+    } else {
+        if (nvec <= 64) TCR_BACK(false, 64, 1, 16);
+        if (nvec <= 128) TCR_BACK(false, 128, 1, 8);
+        if (nvec <= 256) TCR_BACK(false, 256, 1, 4);
+        if (nvec <= 512) TCR_BACK(false, 256, 2, 2);
+    }
+    TCR_BACK(false, 512, 2, 1);
+#undef TCR_BACK
+}
+
 template <int DT>
 cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
 {
     const size_t nvec = (a.cols + kRv - 1) / kRv;
     if (nvec <= kBackMaxVecs) {
         void *args[] = {(void *)&a};
-        const void *k = nvec <= 64    ? (const void *)back_kernel<DT, 64>
-                        : nvec <= 128 ? (const void *)back_kernel<DT, 128>
-                        : nvec <= 256 ? (const void *)back_kernel<DT, 256>
-                        : nvec <= 512 ? (const void *)back_kernel<DT, 512>
-                                      : (const void *)back_kernel<DT, 1024>;
-        return launch_first(k, dim3((unsigned)G), dim3(team_of(a.cols)), args, 0, stream);
+        unsigned threads = 0;
+        const bool gran = !a.al_dy || !a.al_h || (a.dh && !a.al_dh);
+        const void *k = pick<DT>(nvec, gran, threads);
+        return launch_first(k, dim3((unsigned)G), dim3(threads), args, 0, stream);
     }
     float *c = a.partial + (size_t)G * a.cols;
     void *args[] = {(void *)&a, (void *)&c};

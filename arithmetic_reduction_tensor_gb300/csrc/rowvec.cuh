@@ -97,39 +97,63 @@ __device__ __forceinline__ uint32_t vec_left(uint32_t cols, uint32_t v)
     return kRv * v >= cols ? 0u : min(cols - kRv * v, (uint32_t)kRv);
 }
 
+// A vector as loaded: its storage, or (GRAN) the 16-byte granules that its
+// elements touch, one more than it has, to be shifted when it is used -- a
+// load issued ahead must not be waited for by its own shift.
+template <int DT, bool GRAN>
+struct LoadedVec {
+    uint4 q[(DT == kF32 ? 2 : 1) + (GRAN ? 1 : 0)];
+};
+
 // Vector v of a row at any element alignment; elements past cols read as 0.
-// A whole vector of a 16-byte aligned row is one 16-byte load (two of
-// binary32).  Otherwise the 16-byte granules that its elements touch are
-// read and shifted in registers: up to 15 bytes before the row's first or
-// after its last element, in a granule that holds one of them.  (Element by
-// element, rows of 5001 bfloat16 took 2.5 times as long.)
-template <int DT>
-__device__ __forceinline__ RawVec<DT> load_raw(const typename Elem<DT>::T *row, size_t cols, size_t v,
-                                               bool aligned)
+// GRAN = false (`aligned`: the rows are 16-byte aligned): one 16-byte load
+// (two of binary32) for whole vectors.  Granules reach up to 15 bytes before
+// the row's first or after its last element, but each holds one of the
+// row's elements.
+template <int DT, bool GRAN>
+__device__ __forceinline__ LoadedVec<DT, GRAN> load_vec(const typename Elem<DT>::T *row, uint32_t cols, uint32_t v)
+{
+    constexpr int es = DT == kF32 ? 4 : 2, NQ = es / 2;
+    LoadedVec<DT, GRAN> r;
+    const uint32_t left = vec_left(cols, v);
+    const char *p = (const char *)(row + kRv * v);
+    const uint32_t m = GRAN ? (uint32_t)(uintptr_t)p & 15u : 0u;
+    const uint32_t end = left ? m + left * es : 0u;          // bytes of the granules in use
+#pragma unroll
+    for (int k = 0; k < NQ + (GRAN ? 1 : 0); k++) {
+        r.q[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (16u * k < end) r.q[k] = ld16(p - m + 16 * k);
+    }
+    return r;
+}
+
+template <int DT, bool GRAN>
+__device__ __forceinline__ RawVec<DT> use_vec(const LoadedVec<DT, GRAN> &l, const typename Elem<DT>::T *row,
+                                              uint32_t cols, uint32_t v)
 {
     constexpr int es = DT == kF32 ? 4 : 2, NW = 2 * es;      // words of a vector
     RawVec<DT> r;
-    const char *p = (const char *)(row + kRv * v);
-    if (aligned && kRv * v + kRv <= cols) {
+    uint32_t o[NW];
+    if constexpr (GRAN) {
+        uint32_t w[NW + 4];
 #pragma unroll
-        for (int k = 0; k < NW / 4; k++) r.q[k] = ld16(p + 16 * k);
-        return r;
+        for (int k = 0; k < NW / 4 + 1; k++) {
+            w[4 * k] = l.q[k].x;
+            w[4 * k + 1] = l.q[k].y;
+            w[4 * k + 2] = l.q[k].z;
+            w[4 * k + 3] = l.q[k].w;
+        }
+        shift_words<NW>(w, (uint32_t)(uintptr_t)row & 15u, o);
+    } else {
+#pragma unroll
+        for (int k = 0; k < NW / 4; k++) {
+            o[4 * k] = l.q[k].x;
+            o[4 * k + 1] = l.q[k].y;
+            o[4 * k + 2] = l.q[k].z;
+            o[4 * k + 3] = l.q[k].w;
+        }
     }
     const uint32_t left = vec_left(cols, v);
-    const uint32_t m = (uint32_t)(uintptr_t)p & 15u;
-    const uint32_t end = left ? m + left * es : 0u;          // bytes of the granules in use
-    p -= m;
-    uint32_t w[NW + 4], o[NW];
-#pragma unroll
-    for (int k = 0; k < NW / 4 + 1; k++) {
-        uint4 g = make_uint4(0u, 0u, 0u, 0u);
-        if (16u * k < end) g = ld16(p + 16 * k);
-        w[4 * k] = g.x;
-        w[4 * k + 1] = g.y;
-        w[4 * k + 2] = g.z;
-        w[4 * k + 3] = g.w;
-    }
-    shift_words<NW>(w, m, o);
     if (left < kRv) {
 #pragma unroll
         for (int k = 0; k < NW; k++) {
@@ -142,6 +166,15 @@ __device__ __forceinline__ RawVec<DT> load_raw(const typename Elem<DT>::T *row, 
 #pragma unroll
     for (int k = 0; k < NW / 4; k++) r.q[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
     return r;
+}
+
+// The same at once, for rows that may or may not be aligned.
+template <int DT>
+__device__ __forceinline__ RawVec<DT> load_raw(const typename Elem<DT>::T *row, uint32_t cols, uint32_t v,
+                                               bool aligned)
+{
+    if (aligned) return use_vec<DT, false>(load_vec<DT, false>(row, cols, v), row, cols, v);
+    return use_vec<DT, true>(load_vec<DT, true>(row, cols, v), row, cols, v);
 }
 
 template <int DT>
