@@ -18,11 +18,10 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 from typing import NamedTuple
 
-from .build import LIB_PATH
+from .build import BIND_PATH, LIB_PATH
 
 __all__ = [
     "MMA_CHAIN", "SHUFFLE_TREE", "FIXED_ORDER", "MMA_CHAIN_TMEM", "F16", "BF16", "F32",
@@ -426,78 +425,41 @@ class NormOut(NamedTuple):
     rstd: object            # 1 / sqrt(mean square + eps) of each row
 
 
-def _float_code(torch, t) -> int:
-    dt = t.dtype
-    if dt is torch.bfloat16:
-        return BF16
-    if dt is torch.float16:
-        return F16
-    if dt is torch.float32:
-        return F32
-    raise TypeError(f"expected float16, bfloat16 or float32, got {dt}")
+_bind = None
 
 
-# A decoding step's calls are short beside what Python takes for them, so
-# these checks read as few properties of a tensor as they can.
+def _load_bind():
+    """The CPython module of these calls (``csrc/bind.c``), which checks the
+    tensors and makes the C call."""
+    global _bind
+    import importlib.machinery
+    import importlib.util
 
-def _matrix(name, t, shape, dtype, dev, out=False):
-    """(pointer, leading dimension) of a 2-D CUDA tensor with contiguous rows."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _mismatch(name, t, shape, dtype, dev)
-    rows, cols = shape
-    if t.is_contiguous():
-        return t.data_ptr(), cols
-    ld, step = t.stride()
-    if step != 1 and cols > 1:
-        raise ValueError(f"{name} must have contiguous rows (stride 1 along its columns)")
-    if rows <= 1:
-        ld = cols
-    elif ld < cols and (out or ld != 0):
-        raise ValueError(f"{name} has overlapping rows")
-    return t.data_ptr(), ld
-
-
-def _vector(name, t, n, dtype, dev):
-    if t.dtype is not dtype or t.shape != (n,) or t.get_device() != dev:
-        _mismatch(name, t, (n,), dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _mismatch(name, t, shape, dtype, dev):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    import torch
+    lib = c_api()
+    with _lock:
+        if _bind is None:
+            if not os.path.exists(BIND_PATH):
+                raise RuntimeError(
+                    f"libtcr is not built ({BIND_PATH} missing); run "
+                    "`python -m arithmetic_reduction_tensor_gb300.build` -- there is no fallback")
+            loader = importlib.machinery.ExtensionFileLoader("_tcrbind", BIND_PATH)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_tcrbind", BIND_PATH,
+                                                                                       loader=loader))
+            loader.exec_module(m)
+            entry = [ctypes.cast(f, ctypes.c_void_p).value for f in
+                     (lib.tcr_rmsnorm, lib.tcr_rmsnorm_backward, lib.tcr_quantize_rows_i8,
+                      lib.tcr_dequantize_rows_i8, lib.tcr_gemm_i8)]
+            m.setup(torch.float16, torch.bfloat16, torch.float32, torch.int8, torch.int32,
+                    torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch._C._cuda_setDevice,
+                    TcrError, *entry)
+            _bind = m
+    return _bind
 
 
-def _call(torch, name, dev, stream, *args):
-    """Call a C entry point on CUDA device ``dev``, its last argument the
-    stream (the current one if None)."""
-    f = getattr(_lib or c_api(), name)
-    # the current stream's handle, without the Stream object around it
-    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream_handle(dev, stream)
-    if torch._C._cuda_getDevice() == dev:
-        st = f(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = f(*args, s)
-    if st:
-        raise TcrError(st, name)
-
-
-def _check_rows(name, x):
-    if not x.is_cuda or x.dim() != 2:
-        raise ValueError(f"{name} must be a 2-D CUDA tensor")
-    return x.shape, x.get_device()
-
-
-# tcr_norm_args and tcr_norm_back_args packed in one step (the same layout,
-# native alignment)
-_NORM_ARGS = struct.Struct("@PNPNPPNPNPPNNfii0P")
-_NORM_BACK_ARGS = struct.Struct("@PNPNPPPNPNPNNi0P")
+def _handle(stream):
+    """None, or a stream's handle."""
+    return stream if stream is None else _stream_handle(None, stream)
 
 
 def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, h=None, out=None,
@@ -512,37 +474,19 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
     (stride 1 along the columns); x and residual may also be expanded rows.
     """
     import torch
-    shape, dev = _check_rows("x", x)
-    rows, cols = shape
-    dt, xt = _float_code(torch, x), x.dtype
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or xt, device=x.device)
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    i8 = out.dtype is torch.int8
-    xp, ldx = _matrix("x", x, shape, xt, dev)
-    yp, ldy = _matrix("out", out, shape, torch.int8 if i8 else xt, dev, True)
-    rp = ldr = wp = hp = ldh = sp = tp = 0
-    if residual is not None:
-        rp, ldr = _matrix("residual", residual, shape, xt, dev)
-        if h is None:
-            h = torch.empty(shape, dtype=xt, device=x.device)
-    if weight is not None:
-        wp = _vector("weight", weight, cols, xt, dev)
-    if h is not None:
-        hp, ldh = _matrix("h", h, shape, xt, dev, True)
-    if i8:
-        if scale is None:
-            scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-        sp = _vector("scale", scale, rows, torch.float32, dev)
-    else:
+    if residual is not None and h is None:
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.dtype is not torch.int8:
         scale = None
+    elif scale is None:
+        scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
     if rstd is None and want_rstd:
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    if rstd is not None:
-        tp = _vector("rstd", rstd, rows, torch.float32, dev)
-    _call(torch, "tcr_rmsnorm", dev, stream,
-          _NORM_ARGS.pack(xp, ldx, rp, ldr, wp, hp, ldh, yp, ldy, sp, tp, rows, cols, eps, dt, I8 if i8 else dt))
+        rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    (_bind or _load_bind()).rmsnorm(x, weight, residual, eps, h, out, scale, rstd, _handle(stream))
     return NormOut(out, scale, h, rstd)
 
 
@@ -555,26 +499,11 @@ def tcr_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
     gradient of x and of the residual; dweight (float32) is None when there is
     no weight or it is not wanted."""
     import torch
-    shape, dev = _check_rows("h", h)
-    rows, cols = shape
-    dt, ht = _float_code(torch, h), h.dtype
-    gp, ldg = _matrix("dy", dy, shape, ht, dev)
-    hp, ldh = _matrix("h", h, shape, ht, dev)
-    tp = _vector("rstd", rstd, rows, torch.float32, dev)
-    wp = dhp = lddh = dwp = 0
-    if weight is not None:
-        wp = _vector("weight", weight, cols, ht, dev)
-    if dh is not None:
-        dhp, lddh = _matrix("dh", dh, shape, ht, dev)
     if dx is None:
-        dx = torch.empty(shape, dtype=ht, device=h.device)
-    dxp, lddx = _matrix("dx", dx, shape, ht, dev, True)
+        dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
     if dweight is None and weight is not None and want_dweight:
-        dweight = torch.empty(cols, dtype=torch.float32, device=h.device)
-    if dweight is not None:
-        dwp = _vector("dweight", dweight, cols, torch.float32, dev)
-    _call(torch, "tcr_rmsnorm_backward", dev, stream,
-          _NORM_BACK_ARGS.pack(gp, ldg, hp, ldh, wp, tp, dhp, lddh, dxp, lddx, dwp, rows, cols, dt))
+        dweight = torch.empty(h.shape[1:], dtype=torch.float32, device=h.device)
+    (_bind or _load_bind()).rmsnorm_backward(dy, h, weight, rstd, dh, dx, dweight, _handle(stream))
     return dx, dweight
 
 
@@ -583,18 +512,11 @@ def tcr_quantize_rows_i8(x, gate=None, out=None, scale=None, stream=None):
     (``tcr_quantize_rows_i8``).  A weight matrix's rows are its output
     channels."""
     import torch
-    shape, dev = _check_rows("x", x)
-    rows, cols = shape
     if out is None:
-        out = torch.empty(shape, dtype=torch.int8, device=x.device)
+        out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     if scale is None:
-        scale = torch.empty(rows, dtype=torch.float32, device=x.device)
-    dt = _float_code(torch, x)
-    xp, ldx = _matrix("x", x, shape, x.dtype, dev)
-    gp, ldg = (None, 0) if gate is None else _matrix("gate", gate, shape, x.dtype, dev)
-    qp, ldq = _matrix("out", out, shape, torch.int8, dev, True)
-    sp = _vector("scale", scale, rows, torch.float32, dev)
-    _call(torch, "tcr_quantize_rows_i8", dev, stream, xp, ldx, gp, ldg, qp, ldq, sp, rows, cols, dt)
+        scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    (_bind or _load_bind()).quantize_rows(x, gate, out, scale, _handle(stream))
     return out, scale
 
 
@@ -602,16 +524,11 @@ def tcr_dequantize_rows_i8(q, scale, dtype=None, out=None, stream=None):
     """The values ``q * scale`` of rows of codes (``tcr_dequantize_rows_i8``),
     float32 unless ``dtype`` or ``out`` says otherwise."""
     import torch
-    shape, dev = _check_rows("q", q)
-    rows, cols = shape
     if out is None:
-        out = torch.empty(shape, dtype=dtype or torch.float32, device=q.device)
+        out = torch.empty(q.shape, dtype=dtype or torch.float32, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype {dtype}")
-    qp, ldq = _matrix("q", q, shape, torch.int8, dev)
-    sp = _vector("scale", scale, rows, torch.float32, dev)
-    yp, ldy = _matrix("out", out, shape, out.dtype, dev, True)
-    _call(torch, "tcr_dequantize_rows_i8", dev, stream, qp, ldq, sp, yp, ldy, rows, cols, _float_code(torch, out))
+    (_bind or _load_bind()).dequantize_rows(q, scale, out, _handle(stream))
     return out
 
 
@@ -621,27 +538,9 @@ def tcr_gemm_i8(A, W, scale_a=None, scale_w=None, out_dtype=None, out=None, stre
     (``tcr_gemm_i8``).  ``out_dtype``: float16, bfloat16 (the default),
     float32, or int32 for the sums themselves (scales are then refused)."""
     import torch
-    if not A.is_cuda or A.dim() != 2 or W.dim() != 2:
-        raise ValueError("A and W must be 2-D CUDA tensors")
-    M, K = A.shape
-    N = W.shape[0]
-    if W.shape[1] != K:
-        raise ValueError(f"inner dimensions differ: {tuple(A.shape)} vs {tuple(W.shape)}")
-    dev = A.get_device()
     if out is None:
-        out = torch.empty(M, N, dtype=out_dtype or torch.bfloat16, device=A.device)
+        out = torch.empty(A.shape[0], W.shape[0], dtype=out_dtype or torch.bfloat16, device=A.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    if out.dtype is torch.int32:
-        if scale_a is not None or scale_w is not None:
-            raise ValueError("int32 sums take no scales")
-        dt = I32
-    else:
-        dt = _float_code(torch, out)
-    ap, lda = _matrix("A", A, A.shape, torch.int8, dev, True)
-    wp, ldw = _matrix("W", W, W.shape, torch.int8, dev, True)
-    cp, ldc = _matrix("out", out, (M, N), out.dtype, dev, True)
-    sa = None if scale_a is None else _vector("scale_a", scale_a, M, torch.float32, dev)
-    sw = None if scale_w is None else _vector("scale_w", scale_w, N, torch.float32, dev)
-    _call(torch, "tcr_gemm_i8", dev, stream, ap, lda, wp, ldw, sa, sw, cp, ldc, M, N, K, dt)
+    (_bind or _load_bind()).gemm(A, W, scale_a, scale_w, out, _handle(stream))
     return out

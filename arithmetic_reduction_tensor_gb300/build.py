@@ -3,7 +3,8 @@
 ``python -m arithmetic_reduction_tensor_gb300.build`` or ``build_library()``
 compiles every ``csrc/*.cu`` in parallel with nvcc and links
 ``_lib/libtcr.so`` (CUDA runtime linked statically, only the ``tcr_*``
-symbols exported).  Nothing is installed outside the source tree.
+symbols exported), and compiles ``csrc/bind.c``, the CPython module of the
+8-bit path's calls, to ``_lib/_tcrbind.so`` with the host's C compiler.  Nothing is installed outside the source tree.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libtcr.so")
+BIND_SRC = os.path.join(CSRC, "bind.c")
+BIND_PATH = os.path.join(OUT_DIR, "_tcrbind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -47,11 +51,23 @@ def _headers():
 
 def _stamp(extra: list[str]) -> str:
     h = hashlib.sha256()
-    for p in _sources() + _headers():
+    for p in _sources() + _headers() + [BIND_SRC]:
         with open(p, "rb") as f:
             h.update(p.encode() + b"\0" + f.read())
     h.update(" ".join(ARCH + NVCC_FLAGS + extra).encode())
     return h.hexdigest()
+
+
+def _build_bind() -> None:
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        raise RuntimeError("no C compiler: set CC or put gcc on PATH")
+    tmp = f"{BIND_PATH}.{os.getpid()}.tmp"
+    cmd = [cc, "-O2", "-Wall", "-shared", "-fPIC", f"-I{sysconfig.get_paths()['include']}", BIND_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on {BIND_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BIND_PATH)
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -59,7 +75,8 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
     extra = list(extra_flags or [])
     stamp = _stamp(extra)
     stamp_file = os.path.join(OUT_DIR, "libtcr.stamp")
-    if not force and os.path.exists(LIB_PATH) and os.path.exists(stamp_file):
+    if (not force and os.path.exists(LIB_PATH) and os.path.exists(BIND_PATH)
+            and os.path.exists(stamp_file)):
         with open(stamp_file) as f:
             if f.read().strip() == stamp:
                 return LIB_PATH
@@ -77,6 +94,7 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags: list[
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
+    _build_bind()
     srcs = _sources()
     with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, srcs))

@@ -306,13 +306,16 @@ __device__ __forceinline__ float tree8(const float (&e)[kRv])
 template <int N>
 __device__ __forceinline__ float halving(float (&a)[N])
 {
-    if constexpr (N == 3) return __fadd_rn(__fadd_rn(a[0], a[2]), __fadd_rn(a[1], 0.0f));
-    static_assert(N == 3 || (N & (N - 1)) == 0, "a power of two, or 3");
+    if constexpr (N == 3) {
+        return __fadd_rn(__fadd_rn(a[0], a[2]), __fadd_rn(a[1], 0.0f));
+    } else {
+        static_assert((N & (N - 1)) == 0, "a power of two, or 3");
 #pragma unroll
-    for (int h = N / 2; h >= 1; h /= 2)
+        for (int h = N / 2; h >= 1; h /= 2)
 #pragma unroll
-        for (int i = 0; i < h; i++) a[i] = __fadd_rn(a[i], a[i + h]);
-    return a[0];
+            for (int i = 0; i < h; i++) a[i] = __fadd_rn(a[i], a[i + h]);
+        return a[0];
+    }
 }
 
 // The halving fold over the lanes of a warp; every lane gets the result
