@@ -6,22 +6,19 @@
 // with S exact in 32-bit integers, so C's bits depend on the inputs only,
 // whatever path, tile, split or order computed S.
 //
-// A few tokens: gemv_i8_kernel, dot products of four codes at a time on the
-// integer units, one warp to two channels; the weights are read once and
-// bound it.
-//
-// More tokens: the fifth-generation tensor cores.  GB300's 8-bit integer
-// MMA rate is a small fraction of its binary16 rate, and binary16 serves an
-// exact integer product: codes are exact in binary16 (|q| <= 128), products
-// (<= 2^14) and sums of up to 1024 of them (<= 2^24) are exact in the
-// binary32 accumulator.  So K is cut into chunks of 1024, each one chain of
-// tcgen05.mma.kind::f16 into a zeroed TMEM accumulator, and the epilogue adds
-// the chunks as 32-bit integers in registers.
+// Few tokens and small matrices go to k_gemm_i8_few.cu (gemm_i8_plan says
+// when); the rest run here, on the fifth-generation tensor cores.  GB300's
+// 8-bit integer MMA rate is a small fraction of its binary16 rate, and
+// binary16 serves an exact integer product: codes are exact in binary16 (|q|
+// <= 128), products (<= 2^14) and sums of up to 1024 of them (<= 2^24) are
+// exact in the binary32 accumulator.  So K is cut into chunks of 1024, each
+// one chain of tcgen05.mma.kind::f16 into a zeroed TMEM accumulator, and the
+// epilogue adds the chunks as 32-bit integers in registers.
 //
 // The output channels are the MMA's rows (M = 256 over a pair of SMs) and
 // the tokens its columns, so that the weights -- the operand that is large
 // when tokens are few -- travel to the SM as the 8-bit codes they are and
-// are converted there, once per tile: four warps read a 128 x 128 box of
+// are converted there, once per tile: a warpgroup reads a 128 x 128 box of
 // codes from shared memory, widen them in registers (bias to unsigned,
 // a byte permute under the exponent of 1024, one packed subtraction for two
 // values) and write them to tensor memory, where the MMA takes its A operand
@@ -31,10 +28,21 @@
 // boxes feed to the MMA as the B operand, half of the tile's tokens per SM.
 //
 // Whole tiles go round the CTA pairs; the tiles left over after whole rounds
-// (all of them, where tiles are few) are dealt out by steps, evenly, so that
-// the pairs end together: integer additions commute, so the pieces of a tile
-// go to slabs of 32-bit scratch and the CTA that completes the tile adds and
-// scales them -- the same bits in any order.
+// (all of them, where tiles are few) are cut along K over several pairs if
+// that ends sooner: integer additions commute, so the pieces go to slabs of
+// 32-bit scratch and the CTA that completes the tile adds and scales them --
+// the same bits in any order.
+//
+// What bounds it.  Many tokens: the tensor pipe under the power limit (8192
+// x 8192 x 8192: 600 us in a burst, 650 sustained, 1.70 to 1.83 PFLOP/s), the
+// preparation being 5% of it; a step's conversion (about 620 cycles of the
+// SM, its ALU work half of that) is shorter than the MMAs of 160 tokens (640)
+// and is hidden.  Few tokens: the weights' bytes (48 x 8192 x 8192: 11 of 24
+// us, the rest being the preparation, the pipeline's start and the split's
+// hand-over).  Measured on the way, 8192 x 8192 x 8192: release arrivals at
+// cluster scope 1470 us, relaxed ones 1060; issuing from a converged warp
+// 740; three conversion warpgroups that take whole steps in turn 660, with
+// tiles of 128 tokens; 618 with 160.
 //
 // CTA roles (768 threads, one persistent CTA per SM, clusters of two):
 //   warps 0, 2    TMA copies into a 6-stage ring: 128 weight rows x 128
