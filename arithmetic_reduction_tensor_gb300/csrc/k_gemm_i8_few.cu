@@ -30,8 +30,8 @@ constexpr int kFwWarps = 8;
 
 // Tokens blockIdx.y * MT ..; the weights of a token tile after the first come
 // from L2.
-template <int MT, int R>
-__global__ void __launch_bounds__(32 * kFwWarps, MT * R <= 16 ? 3 : 2)
+template <int MT, int R, bool GRAN>
+__global__ void __launch_bounds__(32 * kFwWarps, 3)
 gemm_i8_dot_kernel(const I8Args a)
 {
     constexpr int kCh = 4 * R;
@@ -61,41 +61,36 @@ gemm_i8_dot_kernel(const I8Args a)
         s = __dp4a((int)q.z, (int)c.z, s);
         s = __dp4a((int)q.w, (int)c.w, s);
     };
+    // the next step's weights are loaded ahead; a warp's steps are whole
+    // blocks of 128 k but for the row's last
     const uint32_t step = 128 * kFwWarps;
     uint32_t k = 128 * warp + 16 * (lane & 7);
-    if (a.al_a && a.al_w && K >= 16) {
-        // whole 16-byte words, the next step's weights loaded ahead
-        uint4 q[R];
-        const bool any = k + 16 <= K;
-        if (any) {
+    auto left = [&](uint32_t at) { return at < K ? K - at : 0u; };
+    auto whole = [&](uint32_t at) { return (at & ~127u) + 128 <= K; };
+    LoadedCodes<GRAN> q[R];
+    auto load = [&](uint32_t at) {
+        if (whole(at)) {
 #pragma unroll
-            for (int r = 0; r < R; r++) q[r] = ld_stream(w[r] + k);
+            for (int r = 0; r < R; r++) q[r] = load_codes<GRAN, true>(w[r] + at);
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; r++) q[r] = load_last_codes<GRAN>(w[r] + at, left(at));
         }
-        while (k + 16 <= K) {
-            uint4 next[R];
-            const bool more = k + step + 16 <= K;
-#pragma unroll
-            for (int r = 0; r < R; r++) next[r] = more ? ld_stream(w[r] + k + step) : q[r];
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-                const uint4 c = ld16(x0 + (m < tokens ? m : 0) * a.lda + k);
-#pragma unroll
-                for (int r = 0; r < R; r++) add(q[r], c, acc[m][r]);
-            }
-#pragma unroll
-            for (int r = 0; r < R; r++) q[r] = next[r];
-            k += step;
-        }
-    }
+    };
+    load(k);
     for (; k < K; k += step) {
-        uint4 q[R];
+        const bool all = whole(k);
+        uint4 now[R];
 #pragma unroll
-        for (int r = 0; r < R; r++) q[r] = ld_codes(w[r] + k, K - k, a.al_w);
+        for (int r = 0; r < R; r++) now[r] = use_codes<GRAN>(q[r], w[r] + k, left(k), all);
+        load(k + step);
 #pragma unroll
         for (int m = 0; m < MT; m++) {
-            const uint4 c = ld_codes(x0 + (m < tokens ? m : 0) * a.lda + k, K - k, a.al_a);
+            const int8_t *x = x0 + (m < tokens ? m : 0) * a.lda + k;
+            const LoadedCodes<GRAN> l = all ? load_codes<GRAN, false>(x) : load_last_codes<GRAN>(x, left(k));
+            const uint4 c = use_codes<GRAN>(l, x, left(k), all);
 #pragma unroll
-            for (int r = 0; r < R; r++) add(q[r], c, acc[m][r]);
+            for (int r = 0; r < R; r++) add(now[r], c, acc[m][r]);
         }
     }
     // the eight lanes of a channel, then the warps
@@ -122,7 +117,7 @@ gemm_i8_dot_kernel(const I8Args a)
 
 constexpr int kFwChunk = 16;        // blocks of 64 k per exact binary32 sum
 
-template <int NB, int MB>
+template <int NB, int MB, bool GRAN>
 __global__ void __launch_bounds__(32 * kFwWarps, NB * MB == 1 ? 3 : 2)
 gemm_i8_few_kernel(const I8Args a)
 {
@@ -142,7 +137,6 @@ gemm_i8_few_kernel(const I8Args a)
     for (int i = 0; i < 2 * MB; i++) w[i] = a.W + (n0 + 8 * i + g < a.N ? n0 + 8 * i + g : n0) * a.ldw + 16 * t;
 #pragma unroll
     for (int i = 0; i < NB; i++) x[i] = a.A + (m0 + (8 * i + (int)g < tokens ? 8 * i + g : 0)) * a.lda + 16 * t;
-    const bool fast = a.al_a && a.al_w;
     float d[MB][NB][4];
 #pragma unroll
     for (int i = 0; i < MB; i++)
@@ -161,29 +155,31 @@ gemm_i8_few_kernel(const I8Args a)
                     d[i][j][r] = 0.0f;
                 }
     };
-    uint4 q[2 * MB], c[NB];
+    LoadedCodes<GRAN> q[2 * MB], c[NB];
+    auto left = [&](uint32_t b) { return 64 * b + 16 * t < K ? K - 64 * b - 16 * t : 0u; };
+    auto whole = [&](uint32_t b) { return 64 * b + 64 <= K; };
     auto load = [&](uint32_t b) {
-        const uint32_t k = 64 * b;
-        const uint32_t left = k + 16 * t < K ? K - k - 16 * t : 0u;
-        if (fast && left >= 16) {
+        if (whole(b)) {
 #pragma unroll
-            for (int i = 0; i < 2 * MB; i++) q[i] = ld_stream(w[i] + k);
+            for (int i = 0; i < 2 * MB; i++) q[i] = load_codes<GRAN, true>(w[i] + 64 * b);
 #pragma unroll
-            for (int j = 0; j < NB; j++) c[j] = ld16(x[j] + k);
+            for (int j = 0; j < NB; j++) c[j] = load_codes<GRAN, false>(x[j] + 64 * b);
         } else {
 #pragma unroll
-            for (int i = 0; i < 2 * MB; i++) q[i] = ld_codes(w[i] + k, left, a.al_w);
+            for (int i = 0; i < 2 * MB; i++) q[i] = load_last_codes<GRAN>(w[i] + 64 * b, left(b));
 #pragma unroll
-            for (int j = 0; j < NB; j++) c[j] = ld_codes(x[j] + k, left, a.al_a);
+            for (int j = 0; j < NB; j++) c[j] = load_last_codes<GRAN>(x[j] + 64 * b, left(b));
         }
     };
     if (warp < blocks) load(warp);
     int in_sum = 0;
     for (uint32_t b = warp; b < blocks; b += kFwWarps) {
+        const bool all = whole(b);
         uint32_t f[MB][4][4], e[NB][4][2];        // the fragments of four MMAs
 #pragma unroll
         for (int i = 0; i < MB; i++) {
-            const uint4 lo = q[2 * i], hi = q[2 * i + 1];
+            const uint4 lo = use_codes<GRAN>(q[2 * i], w[2 * i] + 64 * b, left(b), all);
+            const uint4 hi = use_codes<GRAN>(q[2 * i + 1], w[2 * i + 1] + 64 * b, left(b), all);
             const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
             for (int s = 0; s < 4; s++) {
@@ -193,7 +189,8 @@ gemm_i8_few_kernel(const I8Args a)
         }
 #pragma unroll
         for (int j = 0; j < NB; j++) {
-            const uint32_t l[4] = {c[j].x, c[j].y, c[j].z, c[j].w};
+            const uint4 v = use_codes<GRAN>(c[j], x[j] + 64 * b, left(b), all);
+            const uint32_t l[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int s = 0; s < 4; s++) widen4(l[s], e[j][s][0], e[j][s][1]);
         }
@@ -231,7 +228,9 @@ cudaError_t launch_dot(const I8Args &a, cudaStream_t stream)
 {
     void *args[] = {(void *)&a};
     const dim3 grid((unsigned)((a.N + 4 * R - 1) / (4 * R)), (unsigned)((a.M + MT - 1) / MT));
-    return launch_first((const void *)gemm_i8_dot_kernel<MT, R>, grid, dim3(32 * kFwWarps), args, 0, stream);
+    const void *k = a.al_a && a.al_w ? (const void *)gemm_i8_dot_kernel<MT, R, false>
+                                     : (const void *)gemm_i8_dot_kernel<MT, R, true>;
+    return launch_first(k, grid, dim3(32 * kFwWarps), args, 0, stream);
 }
 
 template <int NB, int MB>
@@ -239,7 +238,9 @@ cudaError_t launch_few(const I8Args &a, cudaStream_t stream)
 {
     void *args[] = {(void *)&a};
     const dim3 grid((unsigned)((a.N + 16 * MB - 1) / (16 * MB)), (unsigned)((a.M + 8 * NB - 1) / (8 * NB)));
-    return launch_first((const void *)gemm_i8_few_kernel<NB, MB>, grid, dim3(32 * kFwWarps), args, 0, stream);
+    const void *k = a.al_a && a.al_w ? (const void *)gemm_i8_few_kernel<NB, MB, false>
+                                     : (const void *)gemm_i8_few_kernel<NB, MB, true>;
+    return launch_first(k, grid, dim3(32 * kFwWarps), args, 0, stream);
 }
 
 }  // namespace
