@@ -137,7 +137,7 @@ tcr_status tcr_rmsnorm(const tcr_norm_args *args, void *stream)
 }
 
 tcr_status tcr_rmsnorm_backward(const tcr_norm_back_args *args, void *stream)
-{
+try {
     if (!args) return TCR_ERR_INVALID_ARG;
     const tcr_norm_back_args &a = *args;
     if (!is_float(a.dtype) || !sizes_ok(a.rows, a.cols)) return TCR_ERR_INVALID_ARG;
@@ -184,6 +184,8 @@ tcr_status tcr_rmsnorm_backward(const tcr_norm_back_args *args, void *stream)
     cudaError_t e = launch_norm_back(a.dtype, b, a.dweight, s);
     const cudaError_t f = scratch.release();
     return of(e == cudaSuccess ? f : e);
+} catch (...) {         // the host's memory for a cache: nothing may cross the C boundary
+    return TCR_ERR_CUDA;
 }
 
 tcr_status tcr_quantize_rows_i8(const void *x, size_t ldx, const void *gate, size_t ldg, void *q, size_t ldq,
@@ -230,7 +232,7 @@ tcr_status tcr_dequantize_rows_i8(const void *q, size_t ldq, const float *scale,
 tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t ldw, const float *scale_a,
                        const float *scale_w, void *C, size_t ldc, size_t M, size_t N, size_t K, int c_dtype,
                        void *stream)
-{
+try {
     if (!is_float(c_dtype) && c_dtype != TCR_I32) return TCR_ERR_INVALID_ARG;
     if (M >= kMaxRows || N >= kMaxRows) return TCR_ERR_INVALID_ARG;
     if (K > kMaxK) return TCR_ERR_UNSUPPORTED;
@@ -277,6 +279,8 @@ tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t ldw, con
     cudaError_t e = launch_gemm_i8(a, p, scratch.p, repack, fault_injected("stall"), s);
     const cudaError_t f = scratch.release();
     return of(e == cudaSuccess ? f : e);
+} catch (...) {
+    return TCR_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -586,8 +586,9 @@ TCR_API tcr_status tcr_dequantize_rows_i8(const void *q, size_t ldq, const float
  * tcr_gemm_i8 -- C[t][n] = (float(S) * scale_a[t]) * scale_w[n], rounded to
  * c_dtype, S = sum over k of A[t][k] * W[n][k] exactly (32-bit integers).
  *   A        M x K codes (tokens), W: N x K codes (channels), row-major,
- *            leading dimensions lda, ldw >= K, any alignment.  All 256 code
- *            values are served.
+ *            leading dimensions lda, ldw >= K, any alignment (rows that are
+ *            not 16-byte aligned are read as the granules that hold their
+ *            codes).  All 256 code values are served.
  *   scale_a  M floats, scale_w N floats, or NULL (1).
  *   C        M x N, ldc >= N, TCR_F16, TCR_BF16, TCR_F32, or TCR_I32: S
  *            itself (the scales are not looked at).
