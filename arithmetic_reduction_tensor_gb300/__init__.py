@@ -1,8 +1,9 @@
 """tcr: tensor-core and fixed-order sum reduction on one GB300 GPU.
 
 A thin binding of ``libtcr.so`` (``include/tcr.h``), with the C names: ctypes,
-and for the calls of the 8-bit path a CPython module (``csrc/bind.c``).  It only marshals arguments: every step of every reduction runs in
-the library's CUDA kernels.  PyTorch supplies device memory and streams.
+and for the calls of the 8-bit path a CPython module (``csrc/bind.c``).  It
+only marshals arguments: every step of every reduction runs in the library's
+CUDA kernels.  PyTorch supplies device memory and streams.
 
     import torch
     import arithmetic_reduction_tensor_gb300 as tcr

@@ -48,8 +48,8 @@
 //   warps 0, 2    TMA copies into a 6-stage ring: 128 weight rows x 128
 //                 codes; 2 blocks of 64 columns x tile/2 tokens
 //   warp 1        TMEM allocation; the leader's issues the MMAs
-//   warps 4..15   conversion, three TMEM stages of 128 k ahead of the MMA
-//   warps 16..23  epilogue: two 160-column accumulators, so a chunk's
+//   warps 4..15   conversion, three to six TMEM stages of 128 k ahead
+//   warps 16..23  epilogue: two accumulators, so a chunk's
 //                 readout runs beside the next chunk's MMAs
 // Every wait gives up after about a second as in the split-K GEMM.
 #include <cstring>
@@ -110,9 +110,14 @@ constexpr int kI8WBytes = 128 * kI8BK;         // 16 KiB of codes
 constexpr int kI8TBoxBytes = kI8MaxTn / 2 * 128;    // 64 binary16 columns of half the tokens
 constexpr int kI8StageBytes = kI8WBytes + 2 * kI8TBoxBytes;
 constexpr int kI8Stages = 6;
-constexpr int kI8AStages = 3;                  // TMEM stages of the widened weights
-constexpr int kI8DCols = kI8MaxTn;             // accumulators at columns 0 and 160
-constexpr int kI8ACol = 2 * kI8DCols;          // 320: 64 columns per A stage
+// Tensor memory: two accumulators of a tile's tokens at columns 0 and tn, the
+// widened weights in stages of 64 columns behind them: 3 at 160 tokens, up to
+// 6 at fewer -- no more than stages of the ring, whose `empty` barriers free
+// both: a wait for step i - 6 must not meet the barrier a phase further on.
+__host__ __device__ constexpr int i8_a_stages(int tn)
+{
+    return (512 - 2 * tn) / 64 < kI8Stages ? (512 - 2 * tn) / 64 : kI8Stages;
+}
 constexpr int kI8ConvGroups = 3;               // warpgroups that take the steps in turn
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8EpiWarp0 = 4 + 4 * kI8ConvGroups;
@@ -130,7 +135,7 @@ constexpr int kI8NumBars = 3 * kI8Stages + 4 + 1;
 constexpr int kI8OffMisc = kI8OffBars + 8 * kI8NumBars;
 constexpr int kI8SmemBytes = kI8OffMisc + 64 + 1024;
 static_assert(kI8SmemBytes <= 232448, "one SM's 227 KiB");
-static_assert(kI8ACol + kI8AStages * 64 <= 512, "tensor memory columns");
+static_assert(i8_a_stages(kI8MaxTn) >= 3, "TMEM stages");
 
 // mbar_wait_f with its limit (2^31 cycles: 1.0 to 1.5 s) on the SM's cycle
 // counter, whose read is short beside the global timer's: the waits of a
@@ -364,7 +369,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
     i8_cluster_sync();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    const int half = g.tn / 2;
+    const int half = g.tn / 2, a_stages = i8_a_stages(g.tn);
     I8Walk walk(g, pair, pairs);
 
     // The kernel before this one on the stream is i8_prepare_kernel, which
@@ -457,8 +462,8 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     ok = __all_sync(kFull, ready);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem + (uint32_t)(b * kI8DCols);
-                    const uint32_t a = tmem + (uint32_t)(kI8ACol + 64 * ta);
+                    const uint32_t d = tmem + (uint32_t)(b * g.tn);
+                    const uint32_t a = tmem + (uint32_t)(2 * g.tn + 64 * ta);
                     const uint64_t t_desc = t_desc0 + (uint64_t)st * (kI8StageBytes >> 4);
                     const bool end = in_chunk == kI8ChunkSteps - 1 || j == walk.nb - 1;
                     if (i8_elect()) {
@@ -475,7 +480,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                         st = 0;
                         phase ^= 1u;
                     }
-                    ta = (ta + 1) % kI8AStages;
+                    if (++ta == a_stages) ta = 0;
                     in_chunk++;
                     if (end) {
                         withhold = false;
@@ -500,12 +505,14 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
         int total = 0;                                 // steps of all pieces
         while (walk.next(g, pairs)) total += walk.nb;
         bool ok = true;
-        for (int i = (warp - 4) >> 2; i < total; i += kI8ConvGroups) {
+        const int group = (warp - 4) >> 2;
+        int ta = group % a_stages;                     // TMEM stage of step i
+        for (int i = group; i < total; i += kI8ConvGroups) {
             const int st = i % kI8Stages;
             ok = __all_sync(kFull, wait(wfull(st), (uint32_t)(i / kI8Stages) & 1u));
             if (!ok) break;
             const uint32_t row = ring + (uint32_t)(st * kI8StageBytes + m * kI8BK);
-            const uint32_t dst = tmem + lane_base + (uint32_t)(kI8ACol + 64 * (i % kI8AStages));
+            const uint32_t dst = tmem + lane_base + (uint32_t)(2 * g.tn + 64 * ta);
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 uint32_t o[32];
@@ -517,9 +524,9 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                     widen4(w.z, o[8 * q + 4], o[8 * q + 5]);
                     widen4(w.w, o[8 * q + 6], o[8 * q + 7]);
                 }
-                if (h == 0 && i >= kI8AStages) {
+                if (h == 0 && i >= a_stages) {
                     // the MMAs that read this TMEM stage last are done
-                    const int e = i - kI8AStages;
+                    const int e = i - a_stages;
                     ok = __all_sync(kFull, wait(empty(e % kI8Stages), (uint32_t)(e / kI8Stages) & 1u));
                     if (!ok) break;
                     tc_fence_after();
@@ -531,6 +538,8 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
             tc_fence_before();
             __syncwarp();
             if (lane == 0) i8_arrive_leader(i8_map_leader(full(st)));
+            ta += kI8ConvGroups;
+            while (ta >= a_stages) ta -= a_stages;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kI8RegsEpi));
@@ -637,7 +646,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                 for (int q = 0; q < nblk; q++) {
                     float f[16];
                     int v[16];
-                    if (live) i8_ld16(tmem + lane_base + (uint32_t)(b * kI8DCols + col0 + 16 * q), f);
+                    if (live) i8_ld16(tmem + lane_base + (uint32_t)(b * g.tn + col0 + 16 * q), f);
 #pragma unroll
                     for (int i = 0; i < 16; i++) v[i] = live ? __float2int_rn(f[i]) : (int)0x80000000;
                     if (live || !split) put16(q, v);
@@ -655,7 +664,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant_
                         for (int q = 0; q < kI8MaxTn / 32; q++) {
                             if (q < nblk) {
                                 float v[16];
-                                i8_ld16(tmem + lane_base + (uint32_t)(b * kI8DCols + col0 + 16 * q), v);
+                                i8_ld16(tmem + lane_base + (uint32_t)(b * g.tn + col0 + 16 * q), v);
 #pragma unroll
                                 for (int i = 0; i < 16; i++) acc[16 * q + i] += __float2int_rn(v[i]);
                             }
