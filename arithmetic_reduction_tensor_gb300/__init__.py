@@ -458,9 +458,14 @@ def _load_bind():
     return _bind
 
 
-def _handle(stream):
-    """None, or a stream's handle."""
-    return stream if stream is None else _stream_handle(None, stream)
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
 
 
 def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None, h=None, out=None,
@@ -474,7 +479,7 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
     ``rstd``, which the gradient takes, when asked for.  Rows may be strided
     (stride 1 along the columns); x and residual may also be expanded rows.
     """
-    import torch
+    torch = _torch or _load_torch()
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
@@ -487,7 +492,7 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
         scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
     if rstd is None and want_rstd:
         rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-    (_bind or _load_bind()).rmsnorm(x, weight, residual, eps, h, out, scale, rstd, _handle(stream))
+    (_bind or _load_bind()).rmsnorm(x, weight, residual, eps, h, out, scale, rstd, stream)
     return NormOut(out, scale, h, rstd)
 
 
@@ -499,12 +504,12 @@ def tcr_rmsnorm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
     ``dh`` is the gradient that reaches h along the residual path.  dx is the
     gradient of x and of the residual; dweight (float32) is None when there is
     no weight or it is not wanted."""
-    import torch
+    torch = _torch or _load_torch()
     if dx is None:
         dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
     if dweight is None and weight is not None and want_dweight:
         dweight = torch.empty(h.shape[1:], dtype=torch.float32, device=h.device)
-    (_bind or _load_bind()).rmsnorm_backward(dy, h, weight, rstd, dh, dx, dweight, _handle(stream))
+    (_bind or _load_bind()).rmsnorm_backward(dy, h, weight, rstd, dh, dx, dweight, stream)
     return dx, dweight
 
 
@@ -512,24 +517,24 @@ def tcr_quantize_rows_i8(x, gate=None, out=None, scale=None, stream=None):
     """(codes, scale) of the rows of ``x``, or of ``silu(gate) * x``
     (``tcr_quantize_rows_i8``).  A weight matrix's rows are its output
     channels."""
-    import torch
+    torch = _torch or _load_torch()
     if out is None:
         out = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
-    (_bind or _load_bind()).quantize_rows(x, gate, out, scale, _handle(stream))
+    (_bind or _load_bind()).quantize_rows(x, gate, out, scale, stream)
     return out, scale
 
 
 def tcr_dequantize_rows_i8(q, scale, dtype=None, out=None, stream=None):
     """The values ``q * scale`` of rows of codes (``tcr_dequantize_rows_i8``),
     float32 unless ``dtype`` or ``out`` says otherwise."""
-    import torch
+    torch = _torch or _load_torch()
     if out is None:
         out = torch.empty(q.shape, dtype=dtype or torch.float32, device=q.device)
     elif dtype is not None and out.dtype != dtype:
         raise TypeError(f"out is {out.dtype}, dtype {dtype}")
-    (_bind or _load_bind()).dequantize_rows(q, scale, out, _handle(stream))
+    (_bind or _load_bind()).dequantize_rows(q, scale, out, stream)
     return out
 
 
@@ -538,10 +543,10 @@ def tcr_gemm_i8(A, W, scale_a=None, scale_w=None, out_dtype=None, out=None, stre
     (tokens x K) and W (channels x K), the products summed exactly
     (``tcr_gemm_i8``).  ``out_dtype``: float16, bfloat16 (the default),
     float32, or int32 for the sums themselves (scales are then refused)."""
-    import torch
+    torch = _torch or _load_torch()
     if out is None:
         out = torch.empty(A.shape[0], W.shape[0], dtype=out_dtype or torch.bfloat16, device=A.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
-    (_bind or _load_bind()).gemm(A, W, scale_a, scale_w, out, _handle(stream))
+    (_bind or _load_bind()).gemm(A, W, scale_a, scale_w, out, stream)
     return out

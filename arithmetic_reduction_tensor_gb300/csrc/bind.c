@@ -6,7 +6,7 @@
  * shape, type, device, strides -- and makes the C call on the given or the
  * current stream.  It knows tensors only by their Python attributes, so it
  * is compiled without torch.  (The same checks in Python and ctypes took 5.5
- * to 7.4 us a call, launch included; these take 3.3 to 4.8.)
+ * to 7.4 us a call, launch included; these take 3.2 to 4.7.)
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -14,7 +14,7 @@
 
 #include "../../include/tcr.h"
 
-static PyObject *s_shape, *s_dtype, *s_stride, *s_data_ptr, *s_get_device;
+static PyObject *s_shape, *s_dtype, *s_stride, *s_data_ptr, *s_get_device, *s_cuda_stream;
 /* set by setup() */
 static PyObject *t_f16, *t_bf16, *t_f32, *t_i8, *t_i32, *raw_stream, *get_device, *set_device, *error_class;
 static tcr_status (*f_rmsnorm)(const tcr_norm_args *, void *);
@@ -92,8 +92,19 @@ static int float_type(PyObject *t, PyObject **dtype)
     return code;
 }
 
-/* Type, device and address, common to matrices and vectors. */
-static int common(const char *name, PyObject *t, PyObject *dtype, const Call *c, const void **p)
+static int on_device(const char *name, PyObject *t, const Call *c)
+{
+    const long dev = device_of(t);
+    if (PyErr_Occurred()) return -1;
+    if (dev != c->dev) {
+        PyErr_Format(PyExc_ValueError, "%s must be on cuda:%ld", name, c->dev);
+        return -1;
+    }
+    return 0;
+}
+
+/* Type and address. */
+static int typed(const char *name, PyObject *t, PyObject *dtype, const void **p)
 {
     PyObject *d = PyObject_GetAttr(t, s_dtype);
     if (!d) return -1;
@@ -103,12 +114,6 @@ static int common(const char *name, PyObject *t, PyObject *dtype, const Call *c,
         return -1;
     }
     Py_DECREF(d);
-    const long dev = device_of(t);
-    if (PyErr_Occurred()) return -1;
-    if (dev != c->dev) {
-        PyErr_Format(PyExc_ValueError, "%s must be on cuda:%ld", name, c->dev);
-        return -1;
-    }
     PyObject *a = PyObject_CallMethodNoArgs(t, s_data_ptr);
     if (!a) return -1;
     *p = PyLong_AsVoidPtr(a);
@@ -116,19 +121,12 @@ static int common(const char *name, PyObject *t, PyObject *dtype, const Call *c,
     return PyErr_Occurred() ? -1 : 0;
 }
 
-/* A rows x cols matrix with contiguous rows; input: its rows may be one row
- * for all (leading dimension 0). */
-static int matrix(const char *name, PyObject *t, Py_ssize_t rows, Py_ssize_t cols, PyObject *dtype, int input,
-                  const Call *c, const void **p, size_t *ld)
+/* A rows x cols matrix with contiguous rows, its shape and device known;
+ * input: its rows may be one row for all (leading dimension 0). */
+static int rows_of(const char *name, PyObject *t, Py_ssize_t rows, Py_ssize_t cols, PyObject *dtype, int input,
+                   const void **p, size_t *ld)
 {
-    PyObject *shape;
-    Py_ssize_t n = tuple_of(t, s_shape, 0, &shape);
-    if (n < 0) return -1;
-    const int same = n == 2 && PyLong_AsSsize_t(PyTuple_GET_ITEM(shape, 0)) == rows &&
-                     PyLong_AsSsize_t(PyTuple_GET_ITEM(shape, 1)) == cols;
-    if (!same) PyErr_Format(PyExc_ValueError, "%s must have shape (%zd, %zd), got %S", name, rows, cols, shape);
-    Py_DECREF(shape);
-    if (!same || common(name, t, dtype, c, p)) return -1;
+    if (typed(name, t, dtype, p)) return -1;
     PyObject *stride;
     if (tuple_of(t, s_stride, 1, &stride) < 0) return -1;
     const Py_ssize_t l = PyLong_AsSsize_t(PyTuple_GET_ITEM(stride, 0)),
@@ -144,6 +142,21 @@ static int matrix(const char *name, PyObject *t, Py_ssize_t rows, Py_ssize_t col
         return -1;
     }
     return 0;
+}
+
+/* The same with its shape and device to be checked. */
+static int matrix(const char *name, PyObject *t, Py_ssize_t rows, Py_ssize_t cols, PyObject *dtype, int input,
+                  const Call *c, const void **p, size_t *ld)
+{
+    PyObject *shape;
+    Py_ssize_t n = tuple_of(t, s_shape, 0, &shape);
+    if (n < 0) return -1;
+    const int same = n == 2 && PyLong_AsSsize_t(PyTuple_GET_ITEM(shape, 0)) == rows &&
+                     PyLong_AsSsize_t(PyTuple_GET_ITEM(shape, 1)) == cols;
+    if (!same) PyErr_Format(PyExc_ValueError, "%s must have shape (%zd, %zd), got %S", name, rows, cols, shape);
+    Py_DECREF(shape);
+    if (!same || on_device(name, t, c)) return -1;
+    return rows_of(name, t, rows, cols, dtype, input, p, ld);
 }
 
 static int vector(const char *name, PyObject *t, Py_ssize_t n, PyObject *dtype, const Call *c, const void **p)
@@ -164,10 +177,11 @@ static int vector(const char *name, PyObject *t, Py_ssize_t n, PyObject *dtype, 
             return -1;
         }
     }
-    return common(name, t, dtype, c, p);
+    return on_device(name, t, c) ? -1 : typed(name, t, dtype, p);
 }
 
-/* The handle of the call's stream (None: the device's current one). */
+/* The handle of the call's stream: a stream object's, a number, or (None) the
+ * device's current one's. */
 static int stream_of(PyObject *stream, const Call *c, void **s)
 {
     PyObject *v;
@@ -176,8 +190,10 @@ static int stream_of(PyObject *stream, const Call *c, void **s)
         if (!dev) return -1;
         v = PyObject_CallOneArg(raw_stream, dev);
         Py_DECREF(dev);
-    } else {
+    } else if (PyLong_Check(stream)) {
         v = Py_NewRef(stream);
+    } else {
+        v = PyObject_GetAttr(stream, s_cuda_stream);
     }
     if (!v) return -1;
     *s = PyLong_AsVoidPtr(v);
@@ -248,7 +264,7 @@ static PyObject *rmsnorm(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     const double eps = PyFloat_AsDouble(a[3]);
     if (eps == -1.0 && PyErr_Occurred()) return NULL;
     n.eps = (float)eps;
-    if (matrix("x", a[0], c.rows, c.cols, dt, 1, &c, &n.x, &n.ldx) ||
+    if (rows_of("x", a[0], c.rows, c.cols, dt, 1, &n.x, &n.ldx) ||
         matrix("out", a[5], c.rows, c.cols, i8 ? t_i8 : dt, 0, &c, (const void **)&n.y, &n.ldy) ||
         (a[1] != Py_None && vector("weight", a[1], c.cols, dt, &c, &n.weight)) ||
         (a[2] != Py_None && matrix("residual", a[2], c.rows, c.cols, dt, 1, &c, &n.residual, &n.ldr)) ||
@@ -274,7 +290,7 @@ static PyObject *rmsnorm_backward(PyObject *self, PyObject *const *a, Py_ssize_t
     n.rows = (size_t)c.rows;
     n.cols = (size_t)c.cols;
     if (matrix("dy", a[0], c.rows, c.cols, dt, 1, &c, &n.dy, &n.lddy) ||
-        matrix("h", a[1], c.rows, c.cols, dt, 1, &c, &n.h, &n.ldh) ||
+        rows_of("h", a[1], c.rows, c.cols, dt, 1, &n.h, &n.ldh) ||
         (a[2] != Py_None && vector("weight", a[2], c.cols, dt, &c, &n.weight)) ||
         vector("rstd", a[3], c.rows, t_f32, &c, (const void **)&n.rstd) ||
         (a[4] != Py_None && matrix("dh", a[4], c.rows, c.cols, dt, 1, &c, &n.dh, &n.lddh)) ||
@@ -298,7 +314,7 @@ static PyObject *quantize_rows(PyObject *self, PyObject *const *a, Py_ssize_t na
     const void *x, *g = NULL, *q, *sc;
     size_t ldx, ldg = 0, ldq;
     if (first("x", a[0], &c) || (code = float_type(a[0], &dt)) < 0 ||
-        matrix("x", a[0], c.rows, c.cols, dt, 1, &c, &x, &ldx) ||
+        rows_of("x", a[0], c.rows, c.cols, dt, 1, &x, &ldx) ||
         (a[1] != Py_None && matrix("gate", a[1], c.rows, c.cols, dt, 1, &c, &g, &ldg)) ||
         matrix("out", a[2], c.rows, c.cols, t_i8, 0, &c, &q, &ldq) ||
         vector("scale", a[3], c.rows, t_f32, &c, &sc))
@@ -322,7 +338,7 @@ static PyObject *dequantize_rows(PyObject *self, PyObject *const *a, Py_ssize_t 
     const void *q, *sc, *y;
     size_t ldq, ldy;
     if (first("q", a[0], &c) || (code = float_type(a[2], &dt)) < 0 ||
-        matrix("q", a[0], c.rows, c.cols, t_i8, 1, &c, &q, &ldq) || vector("scale", a[1], c.rows, t_f32, &c, &sc) ||
+        rows_of("q", a[0], c.rows, c.cols, t_i8, 1, &q, &ldq) || vector("scale", a[1], c.rows, t_f32, &c, &sc) ||
         matrix("out", a[2], c.rows, c.cols, dt, 0, &c, &y, &ldy))
         return NULL;
     void *s;
@@ -340,6 +356,10 @@ static PyObject *gemm(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     WANT_ARGS(6);
     Call c, w;
     if (first("A", a[0], &c) || first("W", a[1], &w)) return NULL;
+    if (w.dev != c.dev) {
+        PyErr_Format(PyExc_ValueError, "W must be on cuda:%ld", c.dev);
+        return NULL;
+    }
     if (w.cols != c.cols) {
         PyErr_Format(PyExc_ValueError, "inner dimensions differ: (%zd, %zd) vs (%zd, %zd)", c.rows, c.cols, w.rows,
                      w.cols);
@@ -357,8 +377,8 @@ static PyObject *gemm(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     }
     const void *pa, *pw, *pc, *sa = NULL, *sw = NULL;
     size_t lda, ldw, ldc;
-    if (matrix("A", a[0], c.rows, c.cols, t_i8, 0, &c, &pa, &lda) ||
-        matrix("W", a[1], w.rows, w.cols, t_i8, 0, &c, &pw, &ldw) ||
+    if (rows_of("A", a[0], c.rows, c.cols, t_i8, 0, &pa, &lda) ||
+        rows_of("W", a[1], w.rows, w.cols, t_i8, 0, &pw, &ldw) ||
         matrix("out", a[4], c.rows, w.rows, ot, 0, &c, &pc, &ldc) ||
         (a[2] != Py_None && vector("scale_a", a[2], c.rows, t_f32, &c, &sa)) ||
         (a[3] != Py_None && vector("scale_w", a[3], w.rows, t_f32, &c, &sw)))
@@ -410,6 +430,7 @@ PyMODINIT_FUNC PyInit__tcrbind(void)
     s_stride = PyUnicode_InternFromString("stride");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_get_device = PyUnicode_InternFromString("get_device");
-    if (!s_shape || !s_dtype || !s_stride || !s_data_ptr || !s_get_device) return NULL;
+    s_cuda_stream = PyUnicode_InternFromString("cuda_stream");
+    if (!s_shape || !s_dtype || !s_stride || !s_data_ptr || !s_get_device || !s_cuda_stream) return NULL;
     return PyModule_Create(&module);
 }
