@@ -773,10 +773,8 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
 {
     I8Plan p;
     std::memset(&p, 0, sizeof p);
-    p.launches = 1;
     if (M <= 2 || pairs <= 0) return p;
     p.tensor = 1;
-    p.launches = 2;
     p.steps = (int)((K + kI8BK - 1) / kI8BK);
     p.tiles_c = (int)((N + kI8BM - 1) / kI8BM);
     p.ldf = (K + 63) / 64 * 64;
@@ -818,10 +816,7 @@ I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs)
     // 14.8 and 16.0; 1024 x 1024 x 1024: 18.8 and 9.4).
     const size_t macs = N * K * ((M + 7) / 8 * 8);
     const size_t few = 3800 + (macs / 39500 > N * K / 1900 ? macs / 39500 : N * K / 1900);
-    if (M <= (size_t)kI8FewTokens && few < 14500 + best) {
-        std::memset(&p, 0, sizeof p);
-        p.launches = 1;
-    }
+    if (M <= (size_t)kI8FewTokens && few < 14500 + best) std::memset(&p, 0, sizeof p);
     return p;
 }
 

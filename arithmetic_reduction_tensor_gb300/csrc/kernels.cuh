@@ -194,8 +194,8 @@ cudaError_t launch_combine(const float *partials, size_t segments, size_t count,
 // ---- row operators with an 8-bit output (k_norm.cu): one team of threads
 // per row, the row in registers (rowvec.cuh holds the declared order of
 // their sums).  Leading dimensions in elements; an input's may be 0 (one
-// row for all).  Columns of rows longer than kRowLongT * 32 are read once
-// per step.
+// row for all).  Rows of more than 32768 columns are read once per step, by
+// CTAs of kRowLongT threads.
 constexpr int kRowNorm = 0;      // y = (x + r) * rstd * w; r, w, h, rstd may be null
 constexpr int kRowQuant = 1;     // y = x, or silu(r) * x where r is given
 constexpr int kRowLongT = 512;
@@ -271,7 +271,6 @@ struct I8Plan {
     int tn, tiles_c, tiles_t;        // tokens per tile, tiles
     int steps, full, per, pairs;     // steps of 128 k a tile; whole tiles; pieces of each other tile; CTA pairs
     size_t ldf;                      // row pitch of the prepared operands
-    int launches;
 };
 int gemm_i8_pairs();
 I8Plan gemm_i8_plan(size_t M, size_t N, size_t K, int pairs);

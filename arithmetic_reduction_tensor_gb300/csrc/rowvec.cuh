@@ -19,17 +19,6 @@ namespace tcr {
 
 constexpr int kRv = 8;                 // values per vector
 
-template <int DT>
-__device__ __forceinline__ float elem_to_float(typename Elem<DT>::T e)
-{
-    if constexpr (DT == kF16)
-        return __half2float(__ushort_as_half(e));
-    else if constexpr (DT == kBF16)
-        return __uint_as_float((uint32_t)e << 16);
-    else
-        return __uint_as_float(e);
-}
-
 // Round to the type, to nearest even (bfloat16: NaN stays NaN).
 template <int DT>
 __device__ __forceinline__ typename Elem<DT>::T float_to_elem(float f)
