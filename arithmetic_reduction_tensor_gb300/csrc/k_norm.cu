@@ -13,7 +13,8 @@
 // bit for bit by the inputs.  The work is bound by memory traffic: 65536 x
 // 4096 binary16 279 us to codes, 325 to binary16, 221 for gated codes, 130
 // for reading codes back (6.1 to 6.7 TB/s); rows that are not 16-byte aligned
-// run at half to two thirds of that, bound by shifts.
+// run at that rate in binary32, at half to three quarters of it in 16 bits,
+// bound by instructions.
 #include "kernels.cuh"
 #include "rowvec.cuh"
 
@@ -94,9 +95,9 @@ __device__ __forceinline__ void apply_norm(const RawVec<DT> &wr, bool has_w, flo
 // Rows of at most 8 T NV columns, NV vectors a thread: teams of T threads
 // (T = 32: eight to a CTA; else the CTA) walk the rows, each loading its next
 // row before it finishes the current one, so that loads stay in flight
-// across the row's barriers.  GRAN: x or r is read by granules (rows that are
-// not 16-byte aligned).  MINB: the CTAs per SM that the registers allow.
-template <int DT, int OP, int OUT, bool GRAN, int T, int NV, int MINB>
+// across the row's barriers.  Rows are 16-byte aligned (codes 8-byte).  MINB:
+// the CTAs per SM that the registers allow.
+template <int DT, int OP, int OUT, int T, int NV, int MINB>
 __global__ void __launch_bounds__(T == 32 ? 256 : T, MINB)
 row_stream_kernel(const RowArgs a)
 {
@@ -112,12 +113,12 @@ row_stream_kernel(const RowArgs a)
     const size_t teams = T == 32 ? (size_t)gridDim.x * 8 : gridDim.x;
     const bool has_r = a.r != nullptr, has_w = a.w != nullptr;
     RawVec<DT> w[NV];
-    LoadedVec<DT, GRAN> x[NV], b[NV];
+    LoadedVec<DT, false> x[NV], b[NV];
     auto load = [&](size_t r) {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            x[i] = load_vec<DT, GRAN>((const E *)a.x + r * a.ldx, cols, t + i * T);
-            b[i] = has_r ? load_vec<DT, GRAN>((const E *)a.r + r * a.ldr, cols, t + i * T) : LoadedVec<DT, GRAN>();
+            x[i] = load_vec<DT, false>((const E *)a.x + r * a.ldx, cols, t + i * T);
+            b[i] = has_r ? load_vec<DT, false>((const E *)a.r + r * a.ldr, cols, t + i * T) : LoadedVec<DT, false>();
         }
     };
 #pragma unroll
@@ -128,8 +129,8 @@ row_stream_kernel(const RowArgs a)
         float y[NV][kRv];
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            row_value<DT, OP>(use_vec<DT, GRAN>(x[i], (const E *)a.x + r * a.ldx, cols, t + i * T),
-                              use_vec<DT, GRAN>(b[i], (const E *)a.r + r * a.ldr, cols, t + i * T), has_r, y[i]);
+            row_value<DT, OP>(use_vec<DT, false>(x[i], (const E *)a.x + r * a.ldx, cols, t + i * T),
+                              use_vec<DT, false>(b[i], (const E *)a.r + r * a.ldr, cols, t + i * T), has_r, y[i]);
         if (r + teams < a.rows) load(r + teams);
         // two buffers each: a thread reaches the next row's write of one only
         // after every thread has passed a barrier of the row between
@@ -143,7 +144,7 @@ row_stream_kernel(const RowArgs a)
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 if (kRv * ((t & ~31u) + i * T) >= cols) continue;         // whole warps: stores are warp-wide
-                if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, cols, t + i * T, a.al_h, y[i]);
+                if (a.h) store_vec<DT>((E *)a.h + r * a.ldh, cols, t + i * T, true, y[i]);
                 apply_norm<DT>(w[i], has_w, rstd, y[i]);
             }
         }
@@ -160,9 +161,137 @@ row_stream_kernel(const RowArgs a)
         for (int i = 0; i < NV; i++) {
             if (kRv * ((t & ~31u) + i * T) >= cols) continue;
             if constexpr (OUT == kOutSame)
-                store_vec<DT>((E *)out, cols, t + i * T, a.al_y, y[i]);
+                store_vec<DT>((E *)out, cols, t + i * T, true, y[i]);
             else
-                store_codes((int8_t *)out, cols, t + i * T, a.al_y, y[i], per);
+                store_codes((int8_t *)out, cols, t + i * T, true, y[i], per);
+        }
+    }
+}
+
+// The same for rows at any alignment, element by element: lane l of a team's
+// warp w holds elements 8 T i + 256 w + 32 j + l, so every access is of
+// consecutive elements, 32 a warp, whatever the alignment; the sums are those
+// of the vectors all the same (tree8_lanes).  Bound by instructions at 16 bits
+// (two bytes a lane and access), by memory at 32: norm to codes 100000 x 1001
+// binary16 165 us (0.62 of the copy rate), 20000 x 5001 bfloat16 206 (0.50),
+// 20000 x 2001 binary32 81 (0.94).  Shifting 16-byte granules in registers and
+// joining lanes' vectors for the stores took 272, 246 and 167.
+template <int DT, int OP, int OUT, int T, int NV, int MINB>
+__global__ void __launch_bounds__(T == 32 ? 256 : T, MINB)
+row_elem_kernel(const RowArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    __shared__ float red[2][team_floats<T>()];
+    __shared__ uint32_t redm[2][32];
+    using E = typename Elem<DT>::T;
+    const uint32_t t = T == 32 ? threadIdx.x & 31 : threadIdx.x, cols = (uint32_t)a.cols;
+    const uint32_t threads = T == 32 ? 32 : blockDim.x;
+    const uint32_t e0 = 8 * (t & ~31u) + (t & 31);           // the thread's first element
+    const size_t team = T == 32 ? (size_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
+    const size_t teams = T == 32 ? (size_t)gridDim.x * 8 : gridDim.x;
+    const bool has_r = a.r != nullptr, has_w = OP == kRowNorm && a.w != nullptr;
+    // whether all 256 elements of a warp's stretch i exist
+    auto whole = [&](int i) { return 8 * ((t & ~31u) + (uint32_t)(i * T)) + 256 <= cols; };
+    auto load8 = [&](const E *row, int i, E (&v)[kRv]) {
+        const uint32_t e = e0 + (uint32_t)(8 * T * i);
+        if (whole(i)) {
+#pragma unroll
+            for (int j = 0; j < kRv; j++) v[j] = row[e + 32 * j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRv; j++) v[j] = e + 32 * j < cols ? row[e + 32 * j] : (E)0;
+        }
+    };
+    E x[NV][kRv], b[NV][kRv], w[NV][kRv];
+    auto load = [&](size_t r) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            load8((const E *)a.x + r * a.ldx, i, x[i]);
+            if (has_r) load8((const E *)a.r + r * a.ldr, i, b[i]);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+#pragma unroll
+        for (int j = 0; j < kRv; j++) w[i][j] = (E)0;
+        if (has_w) load8((const E *)a.w, i, w[i]);
+    }
+    if (team < a.rows) load(team);
+    int buf = 0;
+    for (size_t r = team; r < a.rows; r += teams, buf ^= 1) {
+        float y[NV][kRv];
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int j = 0; j < kRv; j++) {
+                y[i][j] = elem_to_float<DT>(x[i][j]);
+                if (has_r) {
+                    const float g = elem_to_float<DT>(b[i][j]);
+                    y[i][j] = OP == kRowNorm ? __fadd_rn(y[i][j], g)
+                                             : __fmul_rn(__fdividef(g, __fadd_rn(1.0f, __expf(-g))), y[i][j]);
+                }
+            }
+        if (r + teams < a.rows) load(r + teams);
+        // (two buffers, as in row_stream_kernel)
+        if constexpr (OP == kRowNorm) {
+            float s[NV];
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                float e[kRv];
+#pragma unroll
+                for (int j = 0; j < kRv; j++) e[j] = __fmul_rn(y[i][j], y[i][j]);
+                s[i] = tree8_lanes(e);
+            }
+            const float rstd = rstd_of(team_sum<T, true>(halving<NV>(s), red[buf], threads), cols, a.eps);
+            if (a.rstd && t == 0) a.rstd[r] = rstd;
+            E *h = a.h ? (E *)a.h + r * a.ldh : nullptr;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const uint32_t e = e0 + (uint32_t)(8 * T * i);
+                const bool all = whole(i);
+#pragma unroll
+                for (int j = 0; j < kRv; j++) {
+                    if (h && (all || e + 32 * j < cols)) h[e + 32 * j] = float_to_elem<DT>(y[i][j]);
+                    y[i][j] = __fmul_rn(y[i][j], rstd);
+                    if (has_w) y[i][j] = __fmul_rn(y[i][j], elem_to_float<DT>(w[i][j]));
+                }
+            }
+        }
+        if constexpr (OUT == kOutSame) {
+            E *out = (E *)a.y + r * a.ldy;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const uint32_t e = e0 + (uint32_t)(8 * T * i);
+                const bool all = whole(i);
+#pragma unroll
+                for (int j = 0; j < kRv; j++)
+                    if (all || e + 32 * j < cols) out[e + 32 * j] = float_to_elem<DT>(y[i][j]);
+            }
+        } else {
+            float m = 0.0f, scale, per;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const uint32_t e = e0 + (uint32_t)(8 * T * i);
+                if (!whole(i)) {
+                    // absent elements are 0 times a possibly infinite rstd
+#pragma unroll
+                    for (int j = 0; j < kRv; j++)
+                        if (e + 32 * j >= cols) y[i][j] = 0.0f;
+                }
+                m = amax8(y[i], m);
+            }
+            i8_scale(team_max<T>(__float_as_uint(m), redm[buf], threads), scale, per);
+            if (t == 0) a.scale[r] = scale;
+            int8_t *out = (int8_t *)a.y + r * a.ldy;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const uint32_t e = e0 + (uint32_t)(8 * T * i);
+                const bool all = whole(i);
+#pragma unroll
+                for (int j = 0; j < kRv; j++)
+                    if (all || e + 32 * j < cols) out[e + 32 * j] = (int8_t)i8_code(y[i][j], per);
+            }
         }
     }
 }
@@ -351,14 +480,17 @@ namespace {
 
 // A launch of row_stream_kernel: as many CTAs as 152 SMs hold (or one team
 // a row).
-template <int DT, int OP, int OUT, bool GRAN, int T, int NV, int MINB>
+template <int DT, int OP, int OUT, bool ELEM, int T, int NV, int MINB>
 const void *stream_of(size_t nvec, size_t rows, int &threads, size_t &grid)
 {
     threads = T == 32 ? 256 : NV == 1 ? (int)((nvec + 31) / 32 * 32) : T;
     const size_t need = T == 32 ? (rows + 7) / 8 : rows;
     const size_t full = (size_t)152 * (size_t)(T == 32 ? MINB : MINB * T / threads);
     grid = need < full ? need : full;
-    return (const void *)row_stream_kernel<DT, OP, OUT, GRAN, T, NV, MINB>;
+    if constexpr (ELEM)
+        return (const void *)row_elem_kernel<DT, OP, OUT, T, NV, MINB>;
+    else
+        return (const void *)row_stream_kernel<DT, OP, OUT, T, NV, MINB>;
 }
 
 // Which shape serves a row length: the fastest of those measured at it, on
@@ -368,23 +500,29 @@ const void *stream_of(size_t nvec, size_t rows, int &threads, size_t &grid)
 // threads of 2 vectors and 3 CTAs an SM, 410 with 512 x 1 and 2, 314 with
 // 256 x 2 and 4 (spills), 303 with 128 x 4 and 4; 16384 x 8192 bfloat16 150
 // with 256 x 4 and 2, 189 with 1024 x 1.  The gate needs no weight and one
-// barrier, so one CTA more fits.  Granules take more registers.
+// barrier, so one CTA more fits.  By elements: norm 20000 x 5001 bfloat16 206
+// us with 256 x 3, 232 with 1024 x 1; 6000 x 12001 232 with 1024 x 2 (some
+// spills; binary32 234), 319 with row_kernel (binary32 227); the gate 133 with 1024 x 1 against 138, and
+// 164 with 1024 x 2 against 139.
 template <int DT, int OP, int OUT>
-const void *pick(size_t nvec, size_t rows, bool gran, int &threads, size_t &grid)
+const void *pick(size_t nvec, size_t rows, bool elem, int &threads, size_t &grid)
 {
 #define TCR_STREAM(T_, NV_, MINB_) return stream_of<DT, OP, OUT, false, T_, NV_, MINB_>(nvec, rows, threads, grid)
-#define TCR_GRAN(T_, NV_, MINB_) return stream_of<DT, OP, OUT, true, T_, NV_, MINB_>(nvec, rows, threads, grid)
+#define TCR_ELEM(T_, NV_, MINB_) return stream_of<DT, OP, OUT, true, T_, NV_, MINB_>(nvec, rows, threads, grid)
     constexpr bool quant = OP == kRowQuant;
-    if (gran) {
-        if (nvec <= 32) TCR_GRAN(32, 1, 3);
-        if (nvec <= 64) TCR_GRAN(32, 2, 2);
-        if (nvec <= 128) TCR_GRAN(128, 1, DT == kF32 ? 4 : 6);
-        if (nvec <= 256) TCR_GRAN(256, 1, DT == kF32 ? 2 : 3);
-        if (nvec <= 512) TCR_GRAN(256, 2, DT == kF32 ? 1 : 2);
-        if (nvec <= 768) TCR_GRAN(256, 3, DT == kF32 ? 1 : 2);
-        if (nvec <= 1024) TCR_GRAN(512, 2, 1);
-        if constexpr (DT != kF32)
-            if (nvec <= 2048) TCR_GRAN(512, 4, 1);
+    if (elem) {
+        if (nvec <= 32) TCR_ELEM(32, 1, 4);
+        if (nvec <= 64) TCR_ELEM(32, 2, 2);
+        if (nvec <= 128) TCR_ELEM(128, 1, 8);
+        if (nvec <= 256) TCR_ELEM(256, 1, 4);
+        if (nvec <= 512) TCR_ELEM(256, 2, 2);
+        if constexpr (quant) {
+            if (nvec <= 1024) TCR_ELEM(1024, 1, 1);
+        } else {
+            if (nvec <= 768) TCR_ELEM(256, 3, 2);
+            if (nvec <= 1024) TCR_ELEM(512, 2, 1);
+            if (nvec <= 2048) TCR_ELEM(1024, 2, 1);
+        }
     } else if constexpr (DT == kF32) {
         if (nvec <= 32) TCR_STREAM(32, 1, 3);
         if (nvec <= 64) TCR_STREAM(32, 2, 2);
@@ -417,7 +555,7 @@ const void *pick(size_t nvec, size_t rows, bool gran, int &threads, size_t &grid
                 TCR_STREAM(512, 4, 1);
         }
     }
-#undef TCR_GRAN
+#undef TCR_ELEM
 #undef TCR_STREAM
     grid = rows;
     if (nvec <= 2048) {
@@ -433,12 +571,12 @@ const void *pick(size_t nvec, size_t rows, bool gran, int &threads, size_t &grid
 }
 
 template <int DT>
-const void *pick_op(int op, int out_i8, size_t nvec, size_t rows, bool gran, int &threads, size_t &grid)
+const void *pick_op(int op, int out_i8, size_t nvec, size_t rows, bool elem, int &threads, size_t &grid)
 {
     if (op == kRowNorm)
-        return out_i8 ? pick<DT, kRowNorm, kOutI8>(nvec, rows, gran, threads, grid)
-                      : pick<DT, kRowNorm, kOutSame>(nvec, rows, gran, threads, grid);
-    return pick<DT, kRowQuant, kOutI8>(nvec, rows, gran, threads, grid);
+        return out_i8 ? pick<DT, kRowNorm, kOutI8>(nvec, rows, elem, threads, grid)
+                      : pick<DT, kRowNorm, kOutSame>(nvec, rows, elem, threads, grid);
+    return pick<DT, kRowQuant, kOutI8>(nvec, rows, elem, threads, grid);
 }
 
 }  // namespace
@@ -448,10 +586,10 @@ cudaError_t launch_rows_op(int op, int dtype, bool out_i8, const RowArgs &a, cud
     const size_t nvec = (a.cols + kRv - 1) / kRv;
     int threads = 0;
     size_t grid = 0;
-    const bool gran = !a.al_x || (a.r && !a.al_r);
-    const void *k = dtype == kF16    ? pick_op<kF16>(op, out_i8, nvec, a.rows, gran, threads, grid)
-                    : dtype == kBF16 ? pick_op<kBF16>(op, out_i8, nvec, a.rows, gran, threads, grid)
-                                     : pick_op<kF32>(op, out_i8, nvec, a.rows, gran, threads, grid);
+    const bool elem = !a.al_x || (a.r && !a.al_r) || (a.h && !a.al_h) || !a.al_y;
+    const void *k = dtype == kF16    ? pick_op<kF16>(op, out_i8, nvec, a.rows, elem, threads, grid)
+                    : dtype == kBF16 ? pick_op<kBF16>(op, out_i8, nvec, a.rows, elem, threads, grid)
+                                     : pick_op<kF32>(op, out_i8, nvec, a.rows, elem, threads, grid);
     void *args[] = {(void *)&a};
     return launch_first(k, dim3((unsigned)grid), dim3((unsigned)threads), args, 0, stream);
 }

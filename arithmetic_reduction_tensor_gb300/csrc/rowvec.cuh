@@ -19,6 +19,17 @@ namespace tcr {
 
 constexpr int kRv = 8;                 // values per vector
 
+template <int DT>
+__device__ __forceinline__ float elem_to_float(typename Elem<DT>::T e)
+{
+    if constexpr (DT == kF16)
+        return __half2float(__ushort_as_half(e));
+    else if constexpr (DT == kBF16)
+        return __uint_as_float((uint32_t)e << 16);
+    else
+        return __uint_as_float(e);
+}
+
 // Round to the type, to nearest even (bfloat16: NaN stays NaN).
 template <int DT>
 __device__ __forceinline__ typename Elem<DT>::T float_to_elem(float f)
@@ -316,6 +327,44 @@ __device__ __forceinline__ float halving_lanes(float v)
     return v;
 }
 
+// Rows read element by element: lane l of a warp holds elements 32 j + l, j =
+// 0 .. 7, of a stretch of 256, so that accesses of rows at any alignment are
+// consecutive over the lanes.  From its eight values the value of one of the
+// stretch's 32 vectors (tree8 of elements 8v .. 8v + 7, which lie in eight
+// lanes): three exchanges that each halve what a lane still carries.  Lane l
+// ends with vector 4 j + l / 8, j = l % 8.
+__device__ __forceinline__ float tree8_lanes(const float (&e)[kRv])
+{
+    const uint32_t lane = threadIdx.x & 31;
+    float a[4], b[2];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const bool odd = lane & 1u;
+        const float keep = odd ? e[2 * k + 1] : e[2 * k], give = odd ? e[2 * k] : e[2 * k + 1];
+        a[k] = __fadd_rn(keep, __shfl_xor_sync(kFull, give, 1));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const bool odd = lane & 2u;
+        const float keep = odd ? a[2 * k + 1] : a[2 * k], give = odd ? a[2 * k] : a[2 * k + 1];
+        b[k] = __fadd_rn(keep, __shfl_xor_sync(kFull, give, 2));
+    }
+    const bool odd = lane & 4u;
+    return __fadd_rn(odd ? b[1] : b[0], __shfl_xor_sync(kFull, odd ? b[0] : b[1], 4));
+}
+
+// The halving fold over those lanes: vector bits 4, 3, 2, 1, 0 are lane bits
+// 2, 1, 0, 4, 3.
+__device__ __forceinline__ float halving_lanes_elem(float v)
+{
+#pragma unroll
+    for (int k = 0; k < 5; k++) {
+        constexpr int order[5] = {4, 2, 1, 16, 8};
+        v = __fadd_rn(v, __shfl_xor_sync(kFull, v, order[k]));
+    }
+    return v;
+}
+
 // The fold over a team of T threads (a warp, or the whole CTA) of values
 // already folded within each thread; every thread gets the result.  `red`:
 // team_floats<T>() floats of shared memory, not in use by an earlier call
@@ -330,7 +379,8 @@ __host__ __device__ constexpr int team_floats()
     return T <= 32 ? 1 : T < 512 ? T : T / 32 * 33 + 32;
 }
 
-template <int T>
+// ELEM: lanes hold the vectors of tree8_lanes.
+template <int T, bool ELEM = false>
 __device__ __forceinline__ float team_sum(float v, float *red, uint32_t threads = T)
 {
     const uint32_t lane = threadIdx.x & 31;
@@ -353,7 +403,7 @@ __device__ __forceinline__ float team_sum(float v, float *red, uint32_t threads 
         for (int w = 0; w < T / 32; w++) a[w] = 32u * w < threads ? red[32 * w + lane] : 0.0f;
         v = halving<T / 32>(a);
     }
-    return halving_lanes(v);
+    return ELEM ? halving_lanes_elem(v) : halving_lanes(v);
 }
 
 // The largest of the team's values, each given as the bits of a
@@ -391,11 +441,17 @@ __device__ __forceinline__ void i8_scale(uint32_t amax_bits, float &scale, float
         per = __fdiv_rn(127.0f, amax);
 }
 
-// The codes of a vector: rint(y * per), ties to even, the product not
+// A code, in the low byte: rint(y * per), ties to even, the product not
 // rounded; 0 where per is 0 (y may then be NaN or infinite).  Adding
 // 1.5 * 2^23 in the same operation leaves the integer in the low bits (a
-// conversion instruction per value runs at an eighth of the rate).  Called
-// like store_vec; `aligned8`: the rows are 8-byte aligned.
+// conversion instruction per value runs at an eighth of the rate).
+__device__ __forceinline__ uint32_t i8_code(float y, float per)
+{
+    return per == 0.0f ? 0u : __float_as_uint(__fmaf_rn(y, per, 12582912.0f));
+}
+
+// The codes of a vector.  Called like store_vec; `aligned8`: the rows are
+// 8-byte aligned.
 __device__ __forceinline__ void store_codes(int8_t *row, uint32_t cols, uint32_t v, bool aligned8,
                                             const float (&y)[kRv], float per)
 {
@@ -405,7 +461,7 @@ __device__ __forceinline__ void store_codes(int8_t *row, uint32_t cols, uint32_t
         for (int k = 0; k < 2; k++) {
             uint32_t c[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) c[i] = __float_as_uint(__fmaf_rn(y[4 * k + i], per, 12582912.0f));
+            for (int i = 0; i < 4; i++) c[i] = i8_code(y[4 * k + i], per);
             o[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         }
     }
