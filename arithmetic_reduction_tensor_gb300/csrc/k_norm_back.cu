@@ -97,7 +97,8 @@ __device__ __forceinline__ void store_partial(const BackArgs &a, uint32_t v, con
 // Rows of at most T NV vectors, NV a thread; NV = 1: a CTA of 32 ceil(vectors
 // / 32) <= T threads.  The next row's inputs are loaded before the current
 // row's sum is waited for, so that loads stay in flight across the barrier.
-template <int DT, bool GRAN, int T, int NV, int MINB>
+// Rows are 16-byte aligned.
+template <int DT, int T, int NV, int MINB>
 __global__ void __launch_bounds__(T, MINB)
 back_kernel(const BackArgs a)
 {
@@ -108,11 +109,11 @@ back_kernel(const BackArgs a)
     // lanes past the row take part in the row's sum with zeros
     RawVec<DT> w[NV];
     float acc[NV][kRv];
-    BackRow<DT, GRAN> cur[NV];
+    BackRow<DT, false> cur[NV];
 #pragma unroll
     for (int i = 0; i < NV; i++) {
         w[i] = a.w ? load_weight<DT>(a, t + i * T) : RawVec<DT>();
-        load_row<DT, GRAN>(a, blockIdx.x, t + i * T, cur[i]);
+        load_row<DT, false>(a, blockIdx.x, t + i * T, cur[i]);
 #pragma unroll
         for (int k = 0; k < kRv; k++) acc[i][k] = 0.0f;
     }
@@ -120,18 +121,18 @@ back_kernel(const BackArgs a)
     int buf = 0;
     for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x, buf ^= 1) {
         float s[NV];
-        LoadedVec<DT, GRAN> dh[NV];
+        LoadedVec<DT, false> dh[NV];
         float xh[NV][kRv], g[NV][kRv];
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            s[i] = back_products<DT, GRAN>(a, r, t + i * T, cur[i], w[i], rstd, xh[i], g[i], acc[i]);
+            s[i] = back_products<DT, false>(a, r, t + i * T, cur[i], w[i], rstd, xh[i], g[i], acc[i]);
             dh[i] = cur[i].dh;
         }
         const size_t next = r + gridDim.x;
         const float rstd_now = rstd;
         if (next < a.rows) {
 #pragma unroll
-            for (int i = 0; i < NV; i++) load_row<DT, GRAN>(a, next, t + i * T, cur[i]);
+            for (int i = 0; i < NV; i++) load_row<DT, false>(a, next, t + i * T, cur[i]);
             rstd = a.rstd[next];
         }
         // two buffers: a thread reaches the next row's write of this one only
@@ -140,10 +141,85 @@ back_kernel(const BackArgs a)
 #pragma unroll
         for (int i = 0; i < NV; i++)
             if (kRv * ((t & ~31u) + i * T) < cols)           // whole warps: stores are warp-wide
-                store_dx<DT, GRAN>(a, r, t + i * T, dh[i], rstd_now, c, xh[i], g[i]);
+                store_dx<DT, false>(a, r, t + i * T, dh[i], rstd_now, c, xh[i], g[i]);
     }
 #pragma unroll
     for (int i = 0; i < NV; i++) store_partial(a, t + i * T, acc[i]);
+}
+
+// The same for rows at any alignment, one vector's worth a thread, in the
+// layout of tree8_lanes: lane l of warp w holds elements 256 w + 32 j + l.
+// 16384 x 4090 binary16 144 us, 20000 x 2001 binary32 105, 6000 x 8003
+// binary32 139; with granules shifted in registers 189, 122 and 295.
+template <int DT, int T, int MINB>
+__global__ void __launch_bounds__(T, MINB)
+back_elem_kernel(const BackArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    __shared__ float red[2][team_floats<T>()];
+    using E = typename Elem<DT>::T;
+    const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
+    const uint32_t e0 = 8 * (t & ~31u) + (t & 31);
+    const bool whole = 8 * (t & ~31u) + 256 <= cols;         // the warp's 256 elements all exist
+    auto load8 = [&](const void *base, size_t at, E (&v)[kRv]) {
+        const E *row = (const E *)base + at;
+        if (whole) {
+#pragma unroll
+            for (int j = 0; j < kRv; j++) v[j] = row[e0 + 32 * j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < kRv; j++) v[j] = e0 + 32 * j < cols ? row[e0 + 32 * j] : (E)0;
+        }
+    };
+    E dy[kRv], h[kRv], dh[kRv], w[kRv];
+    float acc[kRv];
+    auto load = [&](size_t r) {
+        load8(a.dy, r * a.lddy, dy);
+        load8(a.h, r * a.ldh, h);
+        if (a.dh) load8(a.dh, r * a.lddh, dh);
+    };
+#pragma unroll
+    for (int j = 0; j < kRv; j++) {
+        w[j] = dh[j] = (E)0;
+        acc[j] = 0.0f;
+    }
+    if (a.w) load8(a.w, 0, w);
+    load(blockIdx.x);
+    float rstd = a.rstd[blockIdx.x];
+    int buf = 0;
+    for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x, buf ^= 1) {
+        float xh[kRv], g[kRv], d[kRv], e[kRv];
+#pragma unroll
+        for (int j = 0; j < kRv; j++) {
+            xh[j] = __fmul_rn(elem_to_float<DT>(h[j]), rstd);
+            g[j] = elem_to_float<DT>(dy[j]);
+            d[j] = elem_to_float<DT>(dh[j]);
+            acc[j] = __fadd_rn(acc[j], __fmul_rn(g[j], xh[j]));
+            if (a.w) g[j] = __fmul_rn(g[j], elem_to_float<DT>(w[j]));
+            e[j] = __fmul_rn(g[j], xh[j]);
+        }
+        const float s = tree8_lanes(e);
+        const size_t next = r + gridDim.x;
+        const float rstd_now = rstd;
+        if (next < a.rows) {
+            load(next);
+            rstd = a.rstd[next];
+        }
+        // (two buffers, as in back_kernel)
+        const float c = __fdiv_rn(team_sum<T, true>(s, red[buf], blockDim.x), (float)a.cols);
+        E *dx = (E *)a.dx + r * a.lddx;
+#pragma unroll
+        for (int j = 0; j < kRv; j++) {
+            float v = __fmul_rn(rstd_now, __fsub_rn(g[j], __fmul_rn(xh[j], c)));
+            if (a.dh) v = __fadd_rn(v, d[j]);
+            if (whole || e0 + 32 * j < cols) dx[e0 + 32 * j] = float_to_elem<DT>(v);
+        }
+    }
+    float *p = a.partial + (size_t)blockIdx.x * a.cols;
+#pragma unroll
+    for (int j = 0; j < kRv; j++)
+        if (e0 + 32 * j < cols) p[e0 + 32 * j] = acc[j];
 }
 
 // Longer rows: the row sums first (c[r]), then blocks of 8 * 256 columns.
@@ -254,33 +330,36 @@ namespace {
 // The fastest shapes measured: the registers of two rows decide how many
 // threads fit, so binary32 takes half as many of an SM's threads as the 16-bit
 // types, and 16-bit rows of more than 2048 columns go two vectors to a thread
-// (16384 x 4096 bfloat16 91 us, 108 with one).  Rows that are not aligned hold
-// a granule more of each input.
+// (16384 x 4096 bfloat16 91 us, 108 with one).
 template <int DT>
-const void *pick(size_t nvec, bool gran, unsigned &threads)
+const void *pick(size_t nvec, bool elem, unsigned &threads)
 {
-#define TCR_BACK(G_, T_, NV_, MINB_) \
+#define TCR_BACK(T_, NV_, MINB_) \
     return (threads = NV_ == 1 ? (unsigned)((nvec + 31) / 32 * 32) : T_, \
-            (const void *)back_kernel<DT, G_, T_, NV_, MINB_>)
-    if (gran) {
-        if (nvec <= 64) TCR_BACK(true, 64, 1, 8);
-        if (nvec <= 128) TCR_BACK(true, 128, 1, 4);
-        if (nvec <= 256) TCR_BACK(true, 256, 1, 2);
-        if (nvec <= 512) TCR_BACK(true, 512, 1, 1);
-        TCR_BACK(true, 1024, 1, 1);
+            (const void *)back_kernel<DT, T_, NV_, MINB_>)
+#define TCR_ELEM(T_, MINB_) \
+    return (threads = (unsigned)((nvec + 31) / 32 * 32), (const void *)back_elem_kernel<DT, T_, MINB_>)
+    if (elem) {
+        if (nvec <= 64) TCR_ELEM(64, 8);
+        if (nvec <= 128) TCR_ELEM(128, 4);
+        if (nvec <= 256) TCR_ELEM(256, 2);
+        if (nvec <= 512) TCR_ELEM(512, 1);
+        if (nvec <= 768) TCR_ELEM(768, 1);
+        TCR_ELEM(1024, 1);
     }
     if constexpr (DT == kF32) {
-        if (nvec <= 64) TCR_BACK(false, 64, 1, 8);
-        if (nvec <= 128) TCR_BACK(false, 128, 1, 4);
-        if (nvec <= 256) TCR_BACK(false, 256, 1, 2);
-        if (nvec <= 512) TCR_BACK(false, 512, 1, 1);
+        if (nvec <= 64) TCR_BACK(64, 1, 8);
+        if (nvec <= 128) TCR_BACK(128, 1, 4);
+        if (nvec <= 256) TCR_BACK(256, 1, 2);
+        if (nvec <= 512) TCR_BACK(512, 1, 1);
     } else {
-        if (nvec <= 64) TCR_BACK(false, 64, 1, 16);
-        if (nvec <= 128) TCR_BACK(false, 128, 1, 8);
-        if (nvec <= 256) TCR_BACK(false, 256, 1, 4);
-        if (nvec <= 512) TCR_BACK(false, 256, 2, 2);
+        if (nvec <= 64) TCR_BACK(64, 1, 16);
+        if (nvec <= 128) TCR_BACK(128, 1, 8);
+        if (nvec <= 256) TCR_BACK(256, 1, 4);
+        if (nvec <= 512) TCR_BACK(256, 2, 2);
     }
-    TCR_BACK(false, 512, 2, 1);
+    TCR_BACK(512, 2, 1);
+#undef TCR_ELEM
 #undef TCR_BACK
 }
 
@@ -291,8 +370,8 @@ cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
     if (nvec <= kBackMaxVecs) {
         void *args[] = {(void *)&a};
         unsigned threads = 0;
-        const bool gran = !a.al_dy || !a.al_h || (a.dh && !a.al_dh);
-        const void *k = pick<DT>(nvec, gran, threads);
+        const bool elem = !a.al_dy || !a.al_h || (a.dh && !a.al_dh) || !a.al_dx;
+        const void *k = pick<DT>(nvec, elem, threads);
         return launch_first(k, dim3((unsigned)G), dim3(threads), args, 0, stream);
     }
     float *c = a.partial + (size_t)G * a.cols;
