@@ -11,10 +11,10 @@
 // in the declared order of rowvec.cuh.  Every step outside the gate is one
 // binary32 operation rounded to nearest, so the norm's results are pinned
 // bit for bit by the inputs.  The work is bound by memory traffic: 65536 x
-// 4096 binary16 279 us to codes, 325 to binary16, 221 for gated codes, 130
+// 4096 binary16 279 us to codes, 325 to binary16, 219 for gated codes, 127
 // for reading codes back (6.1 to 6.7 TB/s); rows that are not 16-byte aligned
 // run at that rate in binary32, at half to three quarters of it in 16 bits,
-// bound by instructions.
+// bound by latency (row_elem_kernel).
 #include "kernels.cuh"
 #include "rowvec.cuh"
 
@@ -171,8 +171,9 @@ row_stream_kernel(const RowArgs a)
 // The same for rows at any alignment, element by element: lane l of a team's
 // warp w holds elements 8 T i + 256 w + 32 j + l, so every access is of
 // consecutive elements, 32 a warp, whatever the alignment; the sums are those
-// of the vectors all the same (tree8_lanes).  Bound by instructions at 16 bits
-// (two bytes a lane and access), by memory at 32: norm to codes 100000 x 1001
+// of the vectors all the same (tree8_lanes).  At 16 bits (two bytes a lane and
+// access) bound by the latency of exchanges and barriers with 16 warps an SM,
+// issuing on 54% of cycles; at 32 by memory.  Norm to codes 100000 x 1001
 // binary16 165 us (0.62 of the copy rate), 20000 x 5001 bfloat16 206 (0.50),
 // 20000 x 2001 binary32 81 (0.94).  Shifting 16-byte granules in registers and
 // joining lanes' vectors for the stores took 272, 246 and 167.
@@ -501,8 +502,12 @@ const void *stream_of(size_t nvec, size_t rows, int &threads, size_t &grid)
 // with 256 x 4 and 2, 189 with 1024 x 1.  The gate needs no weight and one
 // barrier, so one CTA more fits.  By elements: norm 20000 x 5001 bfloat16 206
 // us with 256 x 3, 232 with 1024 x 1; 6000 x 12001 232 with 1024 x 2 (some
-// spills; binary32 234), 319 with row_kernel (binary32 227); the gate 133 with 1024 x 1 against 138, and
-// 164 with 1024 x 2 against 139.
+// spills; binary32 234), 319 with row_kernel (binary32 227); the gate 133 with
+// 1024 x 1 against 138, and 164 with 1024 x 2 against 139.  One CTA more an SM
+// loses: norm to codes 100000 x 1001 binary16 218 against 166.  At 257 to 384 vectors two a thread leave
+// much of the CTA idle: the gate 512 x 1 43 us, 256 x 2 60 (16384 x 2304
+// bfloat16; x 3000 55 and 61), by elements 47 and 74 (x 2051; x 3001 61 and
+// 74); norm to codes by elements 84 and 95 at 2051, 109 and 96 at 3001.
 template <int DT, int OP, int OUT>
 const void *pick(size_t nvec, size_t rows, bool elem, int &threads, size_t &grid)
 {
@@ -514,6 +519,7 @@ const void *pick(size_t nvec, size_t rows, bool elem, int &threads, size_t &grid
         if (nvec <= 64) TCR_ELEM(32, 2, 2);
         if (nvec <= 128) TCR_ELEM(128, 1, 8);
         if (nvec <= 256) TCR_ELEM(256, 1, 4);
+        if (nvec <= (quant ? 384 : 320)) TCR_ELEM(512, 1, 2);
         if (nvec <= 512) TCR_ELEM(256, 2, 2);
         if constexpr (quant) {
             if (nvec <= 1024) TCR_ELEM(1024, 1, 1);
@@ -539,6 +545,8 @@ const void *pick(size_t nvec, size_t rows, bool elem, int &threads, size_t &grid
                 TCR_STREAM(64, 2, 12);
         }
         if (nvec <= 256) TCR_STREAM(128, 2, 6);
+        if constexpr (quant)
+            if (nvec <= 384) TCR_STREAM(512, 1, 3);
         if (nvec <= 512) TCR_STREAM(256, 2, (quant ? 4 : 3));
         if (nvec <= 768) TCR_STREAM(256, 3, (quant ? 3 : 2));
         if (nvec <= 1024) {

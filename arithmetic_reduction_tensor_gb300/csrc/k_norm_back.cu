@@ -330,10 +330,16 @@ namespace {
 // The fastest shapes measured: the registers of two rows decide how many
 // threads fit, so binary32 takes half as many of an SM's threads as the 16-bit
 // types, and 16-bit rows of more than 2048 columns go two vectors to a thread
-// (16384 x 4096 bfloat16 91 us, 108 with one).
+// (16384 x 4096 bfloat16 91 us, 108 with one).  At 257 to 320 vectors
+// norm_back_groups gives an SM three CTAs, which 64 registers hold at once and
+// 128 do not: 16384 x 2560 bfloat16 87 us and 94, by elements 16384 x 2051
+// bfloat16 108 and 132, binary32 117 and 136; aligned binary32 loses more by
+// spills (16384 x 2560 150 and 128).  Few rows leave two CTAs an SM: 1000 x
+// 2560 bfloat16 14.5 us with 64 registers, 10.5 with 128.
 template <int DT>
-const void *pick(size_t nvec, bool elem, unsigned &threads)
+const void *pick(size_t nvec, int G, bool elem, unsigned &threads)
 {
+    const bool three = nvec > 256 && nvec <= 320 && G > 2 * 152;
 #define TCR_BACK(T_, NV_, MINB_) \
     return (threads = NV_ == 1 ? (unsigned)((nvec + 31) / 32 * 32) : T_, \
             (const void *)back_kernel<DT, T_, NV_, MINB_>)
@@ -343,6 +349,7 @@ const void *pick(size_t nvec, bool elem, unsigned &threads)
         if (nvec <= 64) TCR_ELEM(64, 8);
         if (nvec <= 128) TCR_ELEM(128, 4);
         if (nvec <= 256) TCR_ELEM(256, 2);
+        if (three) TCR_ELEM(512, 2);
         if (nvec <= 512) TCR_ELEM(512, 1);
         if (nvec <= 768) TCR_ELEM(768, 1);
         TCR_ELEM(1024, 1);
@@ -356,6 +363,7 @@ const void *pick(size_t nvec, bool elem, unsigned &threads)
         if (nvec <= 64) TCR_BACK(64, 1, 16);
         if (nvec <= 128) TCR_BACK(128, 1, 8);
         if (nvec <= 256) TCR_BACK(256, 1, 4);
+        if (three) TCR_BACK(512, 1, 2);
         if (nvec <= 512) TCR_BACK(256, 2, 2);
     }
     TCR_BACK(512, 2, 1);
@@ -371,7 +379,7 @@ cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
         void *args[] = {(void *)&a};
         unsigned threads = 0;
         const bool elem = !a.al_dy || !a.al_h || (a.dh && !a.al_dh) || !a.al_dx;
-        const void *k = pick<DT>(nvec, elem, threads);
+        const void *k = pick<DT>(nvec, G, elem, threads);
         return launch_first(k, dim3((unsigned)G), dim3(threads), args, 0, stream);
     }
     float *c = a.partial + (size_t)G * a.cols;

@@ -126,6 +126,46 @@ def test_strides_and_alignment_do_not_change_bits(rows, cols, pitch, off, dt):
     assert same(dx, dxs) and same(dw, dws)
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("rows,cols", [(5, 1), (9, 31), (11, 255), (9, 257), (20, 500), (9, 513), (13, 1023), (7, 1999),
+                                       (5, 2049), (1300, 2051), (1300, 2560), (6, 2561), (4, 3001), (9, 4095),
+                                       (7, 4097), (5, 6145), (320, 8191), (4, 8193), (3, 12001), (3, 16383)])
+def test_unaligned_rows_have_the_bits_of_aligned_ones(rows, cols, dt):
+    gen = torch.Generator().manual_seed(rows + cols)
+    x, r, dy = (rand(gen, rows, cols, DTS[dt]) for _ in range(3))
+    x[1], r[1] = 0, 0                                    # with eps = 0: an infinite rstd
+    x[2, cols // 2] = float("inf")
+    w = (torch.rand(cols, generator=gen) + 0.5).to(DTS[dt])
+    rstd = (torch.rand(rows, generator=gen) + 0.5).cuda()
+    even = (cols + 15) // 16 * 16
+    odd = even + 1
+
+    def guarded(dtype, pitch, off):
+        g = torch.full((rows, pitch + off), 7, dtype=dtype, device="cuda")
+        return g, g[:, off:off + cols]
+
+    # (inputs, outputs) aligned, both not, and either alone
+    got = []
+    for pi, po in ((even, even), (odd, odd), (odd, even), (even, odd)):
+        oi, oo = (1 if pi == odd else 0), (1 if po == odd else 0)
+        xs, rs, dys = (strided(t, pi, oi) for t in (x, r, dy))
+        ws = strided(w[None], even, oi)[0]
+        guards, outs = zip(*(guarded(t, po, oo) for t in (DTS[dt], DTS[dt], torch.int8, DTS[dt], torch.int8, DTS[dt],
+                                                          DTS[dt])))
+        a = tcr.tcr_rmsnorm(xs, ws, residual=rs, out=outs[0], h=outs[1], want_rstd=True)
+        b = tcr.tcr_rmsnorm(xs, ws, residual=rs, eps=0.0, out=outs[2], h=outs[3])
+        q, s = tcr.tcr_quantize_rows_i8(xs, gate=rs, out=outs[4])
+        tcr.tcr_dequantize_rows_i8(strided(q.cpu(), pi, oi), s, out=outs[5])
+        _, dw = tcr.tcr_rmsnorm_backward(dys, rs, ws, rstd, dh=rs, dx=outs[6])
+        for g in guards:                                 # nothing beside the rows was written
+            pad = g.clone()
+            pad[:, oo:oo + cols] = 7
+            assert (pad == 7).all()
+        got.append([*outs, a.rstd, b.scale, s, dw])
+    for other in got[1:]:
+        assert all(same(u, v) for u, v in zip(got[0], other))
+
+
 @pytest.mark.parametrize("cols", [64, 1000, 4096, 12000])
 def test_a_row_does_not_depend_on_the_others(cols):
     gen = torch.Generator().manual_seed(1)
