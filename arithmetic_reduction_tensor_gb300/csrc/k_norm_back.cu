@@ -79,10 +79,10 @@ __device__ __forceinline__ void store_dx(const BackArgs &a, size_t r, uint32_t v
     store_vec<DT>((E *)a.dx + r * a.lddx, cols, v, a.al_dx, dx);
 }
 
-// partial[b * cols + j]: CTA b's sum of column j
-__device__ __forceinline__ void store_partial(const BackArgs &a, uint32_t v, const float (&acc)[kRv])
+// partial[b * cols + j]: the sum of column j over the rows b, b + G, ..
+__device__ __forceinline__ void store_partial(const BackArgs &a, unsigned b, uint32_t v, const float (&acc)[kRv])
 {
-    float *p = a.partial + (size_t)blockIdx.x * a.cols + kRv * v;
+    float *p = a.partial + (size_t)b * a.cols + kRv * v;
     const uint32_t left = vec_left((uint32_t)a.cols, v);
     if (left == kRv && (a.cols & 3) == 0) {
         reinterpret_cast<float4 *>(p)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -144,7 +144,7 @@ back_kernel(const BackArgs a)
                 store_dx<DT, false>(a, r, t + i * T, dh[i], rstd_now, c, xh[i], g[i]);
     }
 #pragma unroll
-    for (int i = 0; i < NV; i++) store_partial(a, t + i * T, acc[i]);
+    for (int i = 0; i < NV; i++) store_partial(a, blockIdx.x, t + i * T, acc[i]);
 }
 
 // The same for rows at any alignment, one vector's worth a thread, in the
@@ -222,7 +222,8 @@ back_elem_kernel(const BackArgs a)
         if (e0 + 32 * j < cols) p[e0 + 32 * j] = acc[j];
 }
 
-// Longer rows: the row sums first (c[r]), then blocks of 8 * 256 columns.
+// Longer rows: the row sums first (c[r]), then blocks of 8 * 256 columns, which
+// are the grid's x: 2^27 columns are 65536 of them, one more than its y holds.
 template <int DT>
 __global__ void __launch_bounds__(kRowLongT)
 back_long_sum_kernel(const BackArgs a, float *c_out)
@@ -261,12 +262,12 @@ back_long_kernel(const BackArgs a, const float *c_in)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
-    const uint32_t v = blockIdx.y * 256 + threadIdx.x;
+    const uint32_t v = blockIdx.x * 256 + threadIdx.x;
     const RawVec<DT> w = a.w ? load_weight<DT>(a, v) : RawVec<DT>();
     float acc[kRv];
 #pragma unroll
     for (int k = 0; k < kRv; k++) acc[k] = 0.0f;
-    for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x) {
+    for (size_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         const float rstd = a.rstd[r];
         BackRow<DT, true> row;
         float xh[kRv], g[kRv];
@@ -274,7 +275,7 @@ back_long_kernel(const BackArgs a, const float *c_in)
         (void)back_products<DT, true>(a, r, v, row, w, rstd, xh, g, acc);
         store_dx<DT, true>(a, r, v, row.dh, rstd, c_in[r], xh, g);
     }
-    store_partial(a, v, acc);
+    store_partial(a, blockIdx.y, v, acc);
 }
 
 // dw[j] from the G partials of column j.
@@ -387,7 +388,7 @@ cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
     cudaError_t e = launch_first((const void *)back_long_sum_kernel<DT>, dim3((unsigned)a.rows), dim3(kRowLongT),
                                  args, 0, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)G, (unsigned)((nvec + 255) / 256));
+    const dim3 grid((unsigned)((nvec + 255) / 256), (unsigned)G);
     return launch_first((const void *)back_long_kernel<DT>, grid, dim3(256), args, 0, stream);
 }
 

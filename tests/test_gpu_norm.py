@@ -398,3 +398,19 @@ def test_failed_calls_leave_outputs_alone(monkeypatch):
             tcr.tcr_rmsnorm_backward(x, x, x[0], torch.ones(4, device="cuda"), dx=out, dweight=dw)
     monkeypatch.delenv("TCR_FAULT_INJECT")
     assert (out == 5).all() and (dw == 5).all()
+
+
+def test_the_widest_rows():
+    # 2^27 columns, the documented limit: 65536 blocks of 2048 columns in the
+    # gradient, more than a grid's y or z holds
+    cols = 1 << 27
+    one = torch.ones(1, cols, dtype=torch.float16, device="cuda")
+    h = torch.zeros(1, cols, dtype=torch.float16, device="cuda")
+    h[0, ::4] = 2.0                                      # mean square 1
+    h[0, -1] = 2.0
+    o = tcr.tcr_rmsnorm(h, eps=0.0, want_rstd=True)
+    # S = 2^27 + 4, whose sums of halves are ties to 2^27: rstd 1
+    assert o.rstd.item() == 1.0 and torch.equal(o.y, h)
+    dx, dw = tcr.tcr_rmsnorm_backward(one, h, one[0], o.rstd)
+    # S' = 2^26 + 2, likewise: c = 0.5, dx = 1 - h / 2
+    assert torch.equal(dx, 1 - h / 2) and torch.equal(dw, h[0].float())
