@@ -166,6 +166,26 @@ def test_unaligned_rows_have_the_bits_of_aligned_ones(rows, cols, dt):
         assert all(same(u, v) for u, v in zip(got[0], other))
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("rows,cols", [(4, 1), (4, 100), (5, 1001), (4, 1500), (1300, 2560), (9, 2560), (4, 2561), (4, 5001),
+                                       (4, 7000), (3, 8192), (4, 8200), (4, 12289)])
+def test_gradient_of_an_infinite_rstd(rows, cols, dt):
+    # what a forward pass with eps = 0 returns where a row's squares vanish: the
+    # row's sum is of its own elements, whatever lanes and vectors stay empty
+    gen = torch.Generator().manual_seed(rows + cols)
+    h, dy = rand(gen, rows, cols, DTS[dt]), rand(gen, rows, cols, DTS[dt])
+    h[1], dy[1] = 1e-7, 1.0                              # products of one sign: the sum is infinite, not NaN
+    w = (torch.rand(cols, generator=gen) + 0.5).to(DTS[dt])
+    rstd = torch.rand(rows, generator=gen) + 0.5
+    rstd[1] = float("inf")
+    dxc, dwc = spec.back(dy, h, w, rstd, None)
+    assert (dxc[1] == -float("inf")).all() and torch.isinf(dwc).all() and torch.isfinite(dxc[[0, 2]]).all()
+    wide, ld = w.cuda(), (cols + 15) // 16 * 16
+    for pitch, off in ((ld, 0), (ld + 1, 1)):
+        dx, dw = tcr.tcr_rmsnorm_backward(strided(dy, pitch, off), strided(h, pitch, off), wide, rstd.cuda())
+        assert same(dx, dxc.to(DTS[dt])) and same(dw, dwc)
+
+
 @pytest.mark.parametrize("cols", [64, 1000, 4096, 12000])
 def test_a_row_does_not_depend_on_the_others(cols):
     gen = torch.Generator().manual_seed(1)
