@@ -91,9 +91,11 @@ __device__ __forceinline__ void store_dx(const BackArgs &a, size_t r, uint32_t v
     store_vec<DT>((E *)a.dx + r * a.lddx, cols, v, a.al_dx, dx);
 }
 
-// partial[b * cols + j]: the sum of column j over the rows b, b + G, ..
+// partial[b * cols + j]: the sum of column j over the rows b, b + G, ..; not
+// stored where the weight's gradient is not wanted.
 __device__ __forceinline__ void store_partial(const BackArgs &a, unsigned b, uint32_t v, const float (&acc)[kRv])
 {
+    if (!a.partial) return;
     float *p = a.partial + (size_t)b * a.cols + kRv * v;
     const uint32_t left = vec_left((uint32_t)a.cols, v);
     if (left == kRv && (a.cols & 3) == 0) {
@@ -241,6 +243,7 @@ back_elem_kernel(const BackArgs a)
             if (whole || e0 + 32 * j < cols) dx[e0 + 32 * j] = float_to_elem<DT>(v);
         }
     }
+    if (!a.partial) return;
     float *p = a.partial + (size_t)blockIdx.x * a.cols;
 #pragma unroll
     for (int j = 0; j < kRv; j++)
@@ -345,10 +348,16 @@ int norm_back_groups(size_t rows, size_t cols)
     return (int)(rows < g ? rows : g);
 }
 
-size_t norm_back_scratch(size_t rows, size_t cols)
+// Floats of the partials; 0 where no weight gradient is wanted.
+static size_t partial_floats(size_t rows, size_t cols, bool dweight)
+{
+    return dweight ? (size_t)norm_back_groups(rows, cols) * cols : 0;
+}
+
+size_t norm_back_scratch(size_t rows, size_t cols, bool dweight)
 {
     const size_t nvec = (cols + kRv - 1) / kRv;
-    return ((size_t)norm_back_groups(rows, cols) * cols + (nvec > kBackMaxVecs ? rows : 0)) * sizeof(float);
+    return (partial_floats(rows, cols, dweight) + (nvec > kBackMaxVecs ? rows : 0)) * sizeof(float);
 }
 
 namespace {
@@ -398,7 +407,7 @@ const void *pick(size_t nvec, int G, bool elem, unsigned &threads)
 }
 
 template <int DT>
-cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
+cudaError_t launch_back(BackArgs a, int G, float *c, cudaStream_t stream)
 {
     const size_t nvec = (a.cols + kRv - 1) / kRv;
     if (nvec <= kBackMaxVecs) {
@@ -408,7 +417,6 @@ cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
         const void *k = pick<DT>(nvec, G, elem, threads);
         return launch_first(k, dim3((unsigned)G), dim3(threads), args, 0, stream);
     }
-    float *c = a.partial + (size_t)G * a.cols;
     void *args[] = {(void *)&a, (void *)&c};
     cudaError_t e = launch_first((const void *)back_long_sum_kernel<DT>, dim3((unsigned)a.rows), dim3(kRowLongT),
                                  args, 0, stream);
@@ -419,12 +427,14 @@ cudaError_t launch_back(BackArgs a, int G, cudaStream_t stream)
 
 }  // namespace
 
-cudaError_t launch_norm_back(int dtype, const BackArgs &a, float *dw, cudaStream_t stream)
+cudaError_t launch_norm_back(int dtype, BackArgs a, float *scratch, float *dw, cudaStream_t stream)
 {
     int G = norm_back_groups(a.rows, a.cols);
-    cudaError_t e = dtype == kF16    ? launch_back<kF16>(a, G, stream)
-                    : dtype == kBF16 ? launch_back<kBF16>(a, G, stream)
-                                     : launch_back<kF32>(a, G, stream);
+    a.partial = dw ? scratch : nullptr;
+    float *c = scratch + partial_floats(a.rows, a.cols, dw != nullptr);
+    cudaError_t e = dtype == kF16    ? launch_back<kF16>(a, G, c, stream)
+                    : dtype == kBF16 ? launch_back<kBF16>(a, G, c, stream)
+                                     : launch_back<kF32>(a, G, c, stream);
     if (e != cudaSuccess || !dw) return e;
     const float *partial = a.partial;
     size_t cols = a.cols;

@@ -214,8 +214,8 @@ cudaError_t launch_rows_op(int op, int dtype, bool out_i8, const RowArgs &a, cud
 cudaError_t launch_dequant(int dtype, const int8_t *q, size_t ldq, const float *scale, void *y, size_t ldy,
                            size_t rows, size_t cols, cudaStream_t stream);
 
-// ---- the norm's gradient (k_norm_back.cu): dx per row, dw as G partials
-// (norm_back_groups) in scratch and their declared sum.  Rows of more than
+// ---- the norm's gradient (k_norm_back.cu): dx per row, dw, where it is
+// wanted, as G partials (norm_back_groups) in scratch and their declared sum.  Rows of more than
 // kBackMaxVecs vectors of 8 take one more launch and a float of scratch
 // each.
 constexpr size_t kBackMaxVecs = 1024;
@@ -225,13 +225,13 @@ struct BackArgs {
     size_t lddy, ldh, lddh;
     void *dx;
     size_t lddx;
-    float *partial;
+    float *partial;                  // null: no weight gradient
     size_t rows, cols;
     bool al_dy, al_h, al_w, al_dh, al_dx;
 };
 int norm_back_groups(size_t rows, size_t cols);
-size_t norm_back_scratch(size_t rows, size_t cols);
-cudaError_t launch_norm_back(int dtype, const BackArgs &a, float *dw, cudaStream_t stream);
+size_t norm_back_scratch(size_t rows, size_t cols, bool dweight);
+cudaError_t launch_norm_back(int dtype, BackArgs a, float *scratch, float *dw, cudaStream_t stream);
 
 // ---- matrix product in 8-bit integers with scales (k_gemm_i8.cu)
 constexpr int kI8FewTokens = 1024;   // beyond: never the kernels of k_gemm_i8_few.cu

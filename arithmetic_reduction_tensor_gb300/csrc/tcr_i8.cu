@@ -159,7 +159,7 @@ try {
     if (a.weight && !is_aligned(a.weight, eb)) return TCR_ERR_INVALID_ARG;
     if (dev < 0) return TCR_ERR_CUDA;
     Scratch scratch(s);
-    tcr_status st = scratch.take(norm_back_scratch(a.rows, a.cols), dev);
+    tcr_status st = scratch.take(norm_back_scratch(a.rows, a.cols, a.dweight != nullptr), dev);
     if (st != TCR_OK) return st;
     if (fault_injected("launch")) return TCR_ERR_CUDA;
     BackArgs b = {};
@@ -173,7 +173,6 @@ try {
     b.lddh = a.lddh;
     b.dx = a.dx;
     b.lddx = a.lddx;
-    b.partial = (float *)scratch.p;
     b.rows = a.rows;
     b.cols = a.cols;
     b.al_dy = rows_aligned(a.dy, a.lddy, a.rows, eb);
@@ -181,7 +180,7 @@ try {
     b.al_w = is_aligned(a.weight, 16);
     b.al_dh = rows_aligned(a.dh, a.lddh, a.rows, eb);
     b.al_dx = rows_aligned(a.dx, a.lddx, a.rows, eb);
-    cudaError_t e = launch_norm_back(a.dtype, b, a.dweight, s);
+    cudaError_t e = launch_norm_back(a.dtype, b, (float *)scratch.p, a.dweight, s);
     const cudaError_t f = scratch.release();
     return of(e == cudaSuccess ? f : e);
 } catch (...) {         // the host's memory for a cache: nothing may cross the C boundary

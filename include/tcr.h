@@ -546,7 +546,8 @@ TCR_API tcr_status tcr_rmsnorm(const tcr_norm_args *args, void *stream);
  *          g, g + G, .. in order; 32 sums add the partials k, k + 32, .. in
  *          order; those fold as the row sums' lanes do.  No atomics: the
  *          bits depend on the inputs, rows and cols only.
- * Takes G * cols floats of pool scratch (and rows more for cols > 8192).
+ * Takes G * cols floats of pool scratch where dweight is wanted (and, with or
+ * without it, rows more for cols > 8192).
  * rows == 0 writes dweight = +0.0.
  */
 typedef struct {

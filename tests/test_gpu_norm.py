@@ -309,6 +309,28 @@ def test_backward(rows, cols, dt):
     assert same(dx3, a.to(DTS[dt])) and same(dw3, b)
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("rows,cols", [(3, 9), (40, 500), (700, 1024), (401, 1001), (9, 4096), (160, 4099), (20, 8192),
+                                       (7, 12289)])
+def test_a_gradient_without_the_weights(rows, cols, dt, monkeypatch):
+    # a frozen or absent weight: the same dx, and no scratch but for long rows
+    gen = torch.Generator().manual_seed(rows + cols)
+    dy, h, dh = (rand(gen, rows, cols, DTS[dt]).cuda() for _ in range(3))
+    w = (torch.rand(cols, generator=gen) + 0.5).to(DTS[dt]).cuda()
+    rstd = (torch.rand(rows, generator=gen) + 0.5).cuda()
+    want, dw = tcr.tcr_rmsnorm_backward(dy, h, w, rstd, dh=dh)
+    # a gradient asked for without a weight: that of a weight of ones
+    dx1, dw1 = tcr.tcr_rmsnorm_backward(dy, h, None, rstd, dweight=torch.empty(cols, device="cuda"))
+    dx2, dw2 = tcr.tcr_rmsnorm_backward(dy, h, torch.ones_like(w), rstd)
+    assert same(dw1, dw2) and same(dw1, dw) and same(dx1, dx2)
+    if cols <= 8192:
+        monkeypatch.setenv("TCR_FAULT_INJECT", "alloc")
+    dx, none = tcr.tcr_rmsnorm_backward(dy, h, w, rstd, dh=dh, want_dweight=False)
+    assert none is None and same(dx, want)
+    dx, none = tcr.tcr_rmsnorm_backward(dy, h, None, rstd)
+    assert none is None and same(dx, dx1)
+
+
 def test_backward_against_differences():
     # central differences of L = sum(dy * y) through the forward call in
     # binary32: step d = 2^-6; the quotient is off by the forward's roundings
