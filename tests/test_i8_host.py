@@ -1,10 +1,14 @@
 """Argument checks of the 8-bit path's entry points, before any GPU work."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import pytest
 
 import arithmetic_reduction_tensor_gb300 as tcr
-from arithmetic_reduction_tensor_gb300.build import build_library
+from arithmetic_reduction_tensor_gb300.build import BIND_PATH, build_library
 
 FAKE = 0x7F0000000000      # never dereferenced: every case below fails validation
 BAD, OK = tcr.ERR_INVALID_ARG, tcr.OK
@@ -122,3 +126,67 @@ def test_product_refuses(lib, args, status):
 def test_product_of_nothing(lib):
     assert lib.tcr_gemm_i8(None, 0, None, 0, None, None, None, 0, 0, 8, 64, tcr.F32, None) == OK
     assert lib.tcr_gemm_i8(None, 0, None, 0, None, None, None, 0, 8, 0, 64, tcr.F32, None) == OK
+
+
+SLOW_C = """
+#include <time.h>
+int slow(void)                /* stands for an entry point that waits */
+{
+    struct timespec t = {0, 300000000};
+    nanosleep(&t, 0);
+    return 0;
+}
+"""
+
+# The binding knows tensors by their attributes only; its module is set up in
+# a process of its own with the waiting function for all five entry points.
+SLOW_PY = """
+import ctypes, importlib.machinery, importlib.util, sys, threading, time
+loader = importlib.machinery.ExtensionFileLoader("_tcrbind", sys.argv[1])
+m = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_tcrbind", sys.argv[1], loader=loader))
+loader.exec_module(m)
+slow = ctypes.cast(ctypes.CDLL(sys.argv[2]).slow, ctypes.c_void_p).value
+m.setup("f16", "bf16", "f32", "i8", "i32", lambda dev: 0, lambda: 0, lambda dev: None, RuntimeError, *[slow] * 5)
+
+class Tensor:
+    def __init__(self, dtype, *shape):
+        self.dtype, self.shape = dtype, shape
+    def stride(self):
+        return (self.shape[1], 1) if len(self.shape) == 2 else (1,)
+    def data_ptr(self):
+        return 256
+    def get_device(self):
+        return 0
+
+x, q, c, s, w = Tensor("bf16", 4, 8), Tensor("i8", 4, 8), Tensor("bf16", 4, 4), Tensor("f32", 4), Tensor("bf16", 8)
+ticks, stop = [], False
+
+def tick():
+    while not stop:
+        ticks.append(time.monotonic())
+        time.sleep(0.01)
+
+threading.Thread(target=tick, daemon=True).start()
+for call in (lambda: m.rmsnorm(x, w, None, 1e-6, None, x, None, s, None),
+             lambda: m.rmsnorm_backward(x, x, w, s, None, x, None, None),
+             lambda: m.quantize_rows(x, None, q, s, None),
+             lambda: m.dequantize_rows(q, s, x, None),
+             lambda: m.gemm(q, q, s, s, c, None)):
+    a = time.monotonic()
+    call()
+    b = time.monotonic()
+    assert b - a >= 0.29, b - a
+    print(sum(a + 0.05 < t < b - 0.05 for t in ticks))
+stop = True
+"""
+
+
+def test_calls_leave_the_interpreter_to_other_threads(lib, tmp_path):
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    (tmp_path / "slow.c").write_text(SLOW_C)
+    subprocess.run([cc, "-shared", "-fPIC", str(tmp_path / "slow.c"), "-o", str(tmp_path / "slow.so")], check=True)
+    r = subprocess.run([sys.executable, "-c", SLOW_PY, BIND_PATH, str(tmp_path / "slow.so")], capture_output=True,
+                       text=True, timeout=60)
+    assert r.returncode == 0, r.stderr
+    counts = [int(n) for n in r.stdout.split()]
+    assert len(counts) == 5 and min(counts) >= 1, counts
