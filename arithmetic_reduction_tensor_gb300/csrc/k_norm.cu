@@ -38,7 +38,11 @@ struct RowPtrs {
     }
 };
 
-// The values of a vector from its inputs as loaded.
+// The values of a vector from its inputs as loaded.  The gate's exponential and
+// quotient are CUDA's fast ones: their error, (8 + 1.2 max(0, -g)) 2^-23, is
+// far below a code's half step, 2^-8 of the row's largest value, and reaches
+// the scale in its last bits.  The quotient is 0 once 1 + exp(-g) passes 2^126 (g
+// below -87.34), where the factor is less than 1.1e-36.
 template <int DT, int OP>
 __device__ __forceinline__ void row_value(const RawVec<DT> &x, const RawVec<DT> &r, bool has_r, float (&y)[kRv])
 {

@@ -570,10 +570,12 @@ TCR_API tcr_status tcr_rmsnorm_backward(const tcr_norm_back_args *args, void *st
 /*
  * tcr_quantize_rows_i8 -- codes and scale of every row of y = x, or, with a
  * gate (NULL: none), of y = (gate / (1 + exp(-gate))) * x, in binary32 with
- * CUDA's fast exponential and quotient: y's relative error is below
- * (8 + 1.2 max(0, -gate)) 2^-23, and y is 0 for gate < -87.  q: rows x cols codes;
- * scale: rows floats.  Weights are quantised the same way, a row being an
- * output channel.
+ * CUDA's fast exponential and quotient: for gate >= -87.33 a normal y's
+ * relative error is below (8 + 1.2 max(0, -gate)) 2^-23; for gate <= -87.34,
+ * where 1 + exp(-gate) passes 2^126, the factor of x (less than 1.1e-36 in
+ * magnitude) is 0; between them it is either.  A row with an infinite gate has
+ * scale NaN.  q: rows x cols codes; scale: rows floats.  Weights are quantised
+ * the same way, a row being an output channel.
  *
  * tcr_dequantize_rows_i8 -- y = q * scale[row], rounded to dtype.
  */

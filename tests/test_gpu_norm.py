@@ -275,6 +275,29 @@ def test_gated_quantiser(rows, cols, dt):
     assert same(q, qc) and same(s, sc)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("cols", [1, 100, 1001, 9001, 40000])
+def test_gate_where_its_factor_vanishes(cols, dt):
+    # rows of one gate and values near the type's largest.  Down to -87.33 the
+    # declared bound holds; from -87.34 on the quotient's denominator is past
+    # 2^126 and the factor 0
+    small, zero = ([-80.0, -86.5, -87.0], [-87.5, -88.0, -89.0, -100.0]) if dt == "bf16" else \
+        ([-80.0, -87.0, -87.2, -87.33], [-87.34, -87.5, -88.5, -89.0, -200.0])
+    gen = torch.Generator().manual_seed(cols)
+    gates = torch.tensor(small + zero + [float("inf"), -float("inf")])
+    x = ((torch.rand(len(gates), cols, generator=gen) + 1) * 1e38).to(DTS[dt])
+    g = gates[:, None].expand(len(gates), cols).to(DTS[dt])
+    y = g.double() / (1 + torch.exp(-g.double())) * x.double()
+    q, s = (t.cpu() for t in tcr.tcr_quantize_rows_i8(x.cuda(), gate=g.cuda()))
+    n, m = len(small), len(small) + len(zero)
+    want = y.abs().amax(1) / 127
+    # the declared bound, and the scale's own quotient
+    err = (8 + 1.2 * -g[:n, 0].double()) * 2.0 ** -23 + 2.0 ** -23
+    assert ((s[:n].double() - want[:n]).abs() <= err * want[:n]).all() and (s[:n] > 0).all()
+    assert ((q[:n].double() - y[:n] / want[:n, None]).abs() <= 0.5 + 2 * 127 * err[:, None]).all()
+    assert (s[n:m] == 0).all() and torch.isnan(s[m:]).all() and (q[n:] == 0).all()
+
+
 @pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 9), (33, 500), (310, 513), (700, 1024), (40, 2047), (9, 4096),
                                        (160, 4100), (5, 8192), (20, 16384), (12, 16385), (310, 17001)])
