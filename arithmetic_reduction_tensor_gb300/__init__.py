@@ -473,11 +473,12 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
     """RMS norm of the rows of ``x + residual`` (``tcr_rmsnorm``).
 
     ``out_dtype`` is x's own type (the default) or ``torch.int8``: 8-bit
-    codes with ``scale``, one float32 a row; an ``out`` given sets it.  ``h``
-    (x + residual, the next layer's residual) is returned when there is a
-    residual or an ``h`` to write to (``h=residual`` updates it in place);
-    ``rstd``, which the gradient takes, when asked for.  Rows may be strided
-    (stride 1 along the columns); x and residual may also be expanded rows.
+    codes with ``scale``, one float32 a row (refused beside another type); an
+    ``out`` given sets it.  ``h`` (x + residual, the next layer's residual) is
+    returned when there is a residual or an ``h`` to write to (``h=residual``
+    updates it in place); ``rstd``, which the gradient takes, when asked for.
+    Rows may be strided (stride 1 along the columns); x and residual may also
+    be expanded rows.
     """
     torch = _torch or _load_torch()
     if out is None:
@@ -487,7 +488,8 @@ def tcr_rmsnorm(x, weight=None, residual=None, eps: float = 1e-6, out_dtype=None
     if residual is not None and h is None:
         h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     if out.dtype is not torch.int8:
-        scale = None
+        if scale is not None:
+            raise ValueError(f"scale is of int8 codes, out is {out.dtype}")
     elif scale is None:
         scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
     if rstd is None and want_rstd:

@@ -128,6 +128,14 @@ def test_product_of_nothing(lib):
     assert lib.tcr_gemm_i8(None, 0, None, 0, None, None, None, 0, 8, 0, 64, tcr.F32, None) == OK
 
 
+def test_a_scale_that_nothing_would_write_is_refused():
+    torch = pytest.importorskip("torch")
+    x, scale = torch.zeros(4, 64), torch.zeros(4)
+    for kw in (dict(), dict(out_dtype=torch.float32), dict(out=torch.zeros(4, 64))):
+        with pytest.raises(ValueError, match="scale"):
+            tcr.tcr_rmsnorm(x, scale=scale, **kw)
+
+
 SLOW_C = """
 #include <time.h>
 int slow(void)                /* stands for an entry point that waits */
