@@ -2,6 +2,7 @@
 norm's training step (examples/w8a8_mlp.py), and the product's failure path."""
 import importlib.util
 import os
+import threading
 import time
 
 import pytest
@@ -72,5 +73,41 @@ def test_a_wait_that_runs_out_reports_and_recovers(example, monkeypatch, M, N, K
     assert tcr.tcr_device_faults(clear=True) & tcr.FAULT_PIPELINE_WAIT
     assert elapsed < 20
     assert torch.equal(tcr.tcr_gemm_i8(a, w, out_dtype=torch.int32), want)
+    torch.cuda.synchronize()
+    assert tcr.tcr_device_faults() == 0
+
+
+def test_threads_on_their_own_streams(example):
+    # the calls leave the interpreter to each other: first uses, scratch and
+    # launches of several threads at once give what one thread's give
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    blocks = [example.Block(256, 640, gen) for _ in range(2)]
+    xs = [torch.randn(rows, 256, generator=gen, device="cuda").to(torch.bfloat16) for rows in (1, 7, 60, 300, 1100, 2100)]
+
+    def step(x):
+        y = example.forward(blocks, x)
+        o = tcr.tcr_rmsnorm(x, blocks[0].norm, residual=y, want_rstd=True)
+        return (y, *tcr.tcr_rmsnorm_backward(y, o.h, blocks[0].norm, o.rstd))
+    want = [step(x) for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(k):
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                for _ in range(25):
+                    got = step(xs[k])
+            stream.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want[k])):
+                wrong.append(f"thread {k}: other results")
+        except Exception as e:        # reported below
+            wrong.append(f"thread {k}: {e!r}")
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(xs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
     torch.cuda.synchronize()
     assert tcr.tcr_device_faults() == 0
