@@ -1,8 +1,9 @@
 // k_gemm_i8_few.cu -- the 8-bit product for a few tokens (a decoding step) and
 // for small matrices.
 //
-// At these sizes the weights, read once, and the fixed cost of a launch bound
-// it: one launch, no scratch, no preparation, K split only inside a CTA.
+// At these sizes the weights, read from memory once (a token tile after the
+// first finds them in L2), and the fixed cost of a launch bound it: one launch,
+// no scratch, no preparation, K split only inside a CTA.
 //
 // One or two tokens: dot products of four codes at a time on the integer
 // units (240 multiply-adds a cycle and SM).  A CTA owns 4 R channels; a warp

@@ -7,14 +7,17 @@
 //   codes     scale = max|y| / 127, q = rint(y * (127 / max|y|))
 //
 // A team of T threads (a warp for short rows, else a CTA) keeps the row in
-// registers, NV vectors a thread, so every byte is read once; S is summed
-// in the declared order of rowvec.cuh.  Every step outside the gate is one
+// registers, NV vectors a thread, so every byte is read once (rows of more than
+// 32768 columns: once a step, row_long_kernel); S is summed in the declared
+// order of rowvec.cuh.  Every step outside the gate is one
 // binary32 operation rounded to nearest, so the norm's results are pinned
 // bit for bit by the inputs.  The work is bound by memory traffic: 65536 x
-// 4096 binary16 279 us to codes, 325 to binary16, 219 for gated codes, 127
-// for reading codes back (6.1 to 6.7 TB/s); rows that are not 16-byte aligned
-// run at that rate in binary32, at half to three quarters of it in 16 bits,
-// bound by latency (row_elem_kernel).
+// 4096 binary16 279 us to codes, 325 to binary16, 219 for gated codes, 135 for
+// codes without a gate, 127 for reading codes back (6.0 to 6.7 TB/s).  Lengths
+// that leave much of a team's vectors empty run slower (16384 x 2560 bfloat16 to
+// codes 0.67 of the copy rate).  Rows that are not 16-byte aligned run at the
+// full rate in binary32, at a third (6000 x 12001 to codes) to three quarters of
+// it in 16 bits, bound by latency (row_elem_kernel).
 #include "kernels.cuh"
 #include "rowvec.cuh"
 

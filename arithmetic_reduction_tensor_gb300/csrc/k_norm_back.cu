@@ -9,9 +9,11 @@
 // registers, and a second kernel adds the G partials: 32 threads a column,
 // thread k the partials k, k + 32, .. in order, then the halving fold over
 // the 32.  G depends on rows and cols only, so the bits of dw do too; there
-// are no atomics.  One pass over dy, h and dh; bound by memory traffic
-// (65536 x 4096 binary16 348 us, 6.2 TB/s), the barrier of each row and, for
-// few rows, by the latency of two launches.
+// are no atomics.  Rows of up to 8192 columns: one pass over dy, h and dh, bound
+// by memory traffic (65536 x 4096 binary16 351 us, 6.1 TB/s), the barrier of
+// each row and, for few rows, by the latency of two launches.  Longer rows: a
+// pass over dy and h for the row sums, then one over all three (4096 x 12288
+// bfloat16 174 us, 59 at the copy rate).
 #include "kernels.cuh"
 #include "rowvec.cuh"
 
@@ -171,8 +173,8 @@ back_kernel(const BackArgs a)
 
 // The same for rows at any alignment, one vector's worth a thread, in the
 // layout of tree8_lanes: lane l of warp w holds elements 256 w + 32 j + l.
-// 16384 x 4090 binary16 144 us, 20000 x 2001 binary32 105, 6000 x 8003
-// binary32 139; with granules shifted in registers 189, 122 and 295.
+// 16384 x 4090 binary16 145 us, 20000 x 2001 binary32 105, 6000 x 8003
+// binary32 138; with granules shifted in registers 189, 122 and 295.
 template <int DT, int T, int MINB>
 __global__ void __launch_bounds__(T, MINB)
 back_elem_kernel(const BackArgs a)
@@ -367,7 +369,7 @@ namespace {
 // types, and 16-bit rows of more than 2048 columns go two vectors to a thread
 // (16384 x 4096 bfloat16 91 us, 108 with one).  At 257 to 320 vectors
 // norm_back_groups gives an SM three CTAs, which 64 registers hold at once and
-// 128 do not: 16384 x 2560 bfloat16 87 us and 94, by elements 16384 x 2051
+// 128 do not: 16384 x 2560 bfloat16 88 us and 94, by elements 16384 x 2051
 // bfloat16 108 and 132, binary32 117 and 136; aligned binary32 loses more by
 // spills (16384 x 2560 150 and 128).  Few rows leave two CTAs an SM: 1000 x
 // 2560 bfloat16 14.5 us with 64 registers, 10.5 with 128.

@@ -475,10 +475,10 @@ TCR_API tcr_status tcr_gemm_splitk(const void *A, const void *W, float *C, size_
  * row it is not looked at) and rows of any element alignment.  rows < 2^31,
  * cols <= 2^27, rows * cols < 2^40, rows * ld < 2^48.  dtype is TCR_F16,
  * TCR_BF16 or TCR_F32 and is that of every matrix of the call but the codes.
- * 16-byte aligned rows (base and ld) are the fast case; other rows are read
- * as the 16-byte granules that hold their elements, so up to 15 bytes before
- * the first or after the last element of a row, never outside a granule that
- * the row touches.
+ * 16-byte aligned rows (base and ld) are the fast case.  Rows are read by
+ * elements, or as the 16-byte granules that hold their elements: so at most up
+ * to 15 bytes before the first or after the last element of a row, never
+ * outside a granule that the row touches.
  *
  * Declared order of their row sums.  Vector v is elements 8v .. 8v+7 (absent
  * ones +0.0) and has the value ((e0+e1)+(e2+e3))+((e4+e5)+(e6+e7)); the
