@@ -1,7 +1,8 @@
 """tcr: tensor-core and fixed-order sum reduction on one GB300 GPU.
 
 A thin binding of ``libtcr.so`` (``include/tcr.h``), with the C names: ctypes,
-and for the calls of the 8-bit path a CPython module (``csrc/bind.c``).  It
+and for the calls over rows (the 8-bit path, dropout, the layer norm, the
+cross entropy) a CPython module (``csrc/bind.c``).  It
 only marshals arguments: every step of every reduction runs in the library's
 CUDA kernels.  PyTorch supplies device memory and streams.
 
@@ -36,6 +37,9 @@ __all__ = [
     "tcr_reduce_sum_noalloc", "tcr_read_probe",
     "I8", "I32", "NormOut", "tcr_norm_args", "tcr_norm_back_args", "tcr_rmsnorm",
     "tcr_rmsnorm_backward", "tcr_quantize_rows_i8", "tcr_dequantize_rows_i8", "tcr_gemm_i8",
+    "LayerOut", "LayerGrad", "XentOut", "tcr_drop", "tcr_layernorm_args", "tcr_layernorm_back_args",
+    "tcr_xent_args", "tcr_xent_back_args", "tcr_dropout", "tcr_layernorm", "tcr_layernorm_backward",
+    "tcr_cross_entropy", "tcr_cross_entropy_backward",
 ]
 
 MMA_CHAIN, SHUFFLE_TREE, FIXED_ORDER, MMA_CHAIN_TMEM = 0, 1, 2, 3
@@ -106,6 +110,52 @@ class tcr_norm_back_args(ctypes.Structure):
                 ("cols", ctypes.c_size_t), ("dtype", ctypes.c_int)]
 
 
+class tcr_drop(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_ulonglong), ("offset", ctypes.c_ulonglong),
+                ("state", ctypes.c_void_p)]
+
+
+class tcr_layernorm_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_size_t),
+                ("residual", ctypes.c_void_p), ("ldr", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_size_t),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_size_t),
+                ("scale", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t), ("eps", ctypes.c_float),
+                ("drop", ctypes.POINTER(tcr_drop)), ("dtype", ctypes.c_int), ("y_dtype", ctypes.c_int)]
+
+
+class tcr_layernorm_back_args(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("lddy", ctypes.c_size_t),
+                ("h", ctypes.c_void_p), ("ldh", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("mean", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("dh", ctypes.c_void_p), ("lddh", ctypes.c_size_t),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_size_t),
+                ("dresidual", ctypes.c_void_p), ("lddr", ctypes.c_size_t),
+                ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t),
+                ("drop", ctypes.POINTER(tcr_drop)), ("dtype", ctypes.c_int)]
+
+
+class tcr_xent_args(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("ldw", ctypes.c_size_t), ("target", ctypes.c_void_p),
+                ("loss", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("tokens", ctypes.c_size_t), ("vocab", ctypes.c_size_t), ("hidden", ctypes.c_size_t),
+                ("ignore_index", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
+class tcr_xent_back_args(ctypes.Structure):
+    _fields_ = [("dloss", ctypes.c_void_p), ("inc_dloss", ctypes.c_size_t),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_size_t),
+                ("weight", ctypes.c_void_p), ("ldw", ctypes.c_size_t), ("target", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("lddx", ctypes.c_size_t),
+                ("dweight", ctypes.c_void_p), ("lddw", ctypes.c_size_t),
+                ("tokens", ctypes.c_size_t), ("vocab", ctypes.c_size_t), ("hidden", ctypes.c_size_t),
+                ("ignore_index", ctypes.c_longlong), ("dtype", ctypes.c_int)]
+
+
 def Mode(kind: int, R: int = 0, block_threads: int = 0, dtype: int = F16,
          run_log2: int = 0) -> tcr_mode:
     """A ``tcr_mode`` (R is used by MMA_CHAIN only, 0 meaning the default;
@@ -174,6 +224,12 @@ def c_api() -> ctypes.CDLL:
             lib.tcr_dequantize_rows_i8.restype = ctypes.c_int
             lib.tcr_gemm_i8.argtypes = [vp, sz, vp, sz, vp, vp, vp, sz, sz, sz, sz, ctypes.c_int, vp]
             lib.tcr_gemm_i8.restype = ctypes.c_int
+            lib.tcr_dropout.argtypes = [vp, sz, vp, sz, vp, sz, sz, sz, vp, ctypes.c_int, vp]
+            lib.tcr_dropout.restype = ctypes.c_int
+            for name in ("tcr_layernorm", "tcr_layernorm_backward", "tcr_cross_entropy",
+                         "tcr_cross_entropy_backward"):
+                getattr(lib, name).argtypes = [vp, vp]
+                getattr(lib, name).restype = ctypes.c_int
             lib.tcr_status_string.argtypes = [ctypes.c_int]
             lib.tcr_status_string.restype = ctypes.c_char_p
             _lib = lib
@@ -454,6 +510,9 @@ def _load_bind():
             m.setup(torch.float16, torch.bfloat16, torch.float32, torch.int8, torch.int32,
                     torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice, torch._C._cuda_setDevice,
                     TcrError, *entry)
+            m.setup_training(torch.int64, *[ctypes.cast(f, ctypes.c_void_p).value for f in
+                                            (lib.tcr_dropout, lib.tcr_layernorm, lib.tcr_layernorm_backward,
+                                             lib.tcr_cross_entropy, lib.tcr_cross_entropy_backward)])
             _bind = m
     return _bind
 
@@ -552,3 +611,137 @@ def tcr_gemm_i8(A, W, scale_a=None, scale_w=None, out_dtype=None, out=None, stre
         raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
     (_bind or _load_bind()).gemm(A, W, scale_a, scale_w, out, stream)
     return out
+
+
+# ------------------------------------------------------------------ a training step's dropout, layer norm and loss
+
+def tcr_dropout(x, p: float = 0.5, seed: int = 0, offset: int = 0, state=None, residual=None, out=None, stream=None):
+    """``residual + dropout(x)`` (``tcr_dropout``), the mask formed from
+    ``seed``, ``offset``, row and column and never stored: the gradient of x is
+    the same call on the gradient of the result.
+
+    ``seed`` and ``offset`` count modulo 2^64; give every call of a step another
+    offset.  ``state``, an int64 CUDA tensor of the two, takes their place and
+    is read when the kernel runs (a captured graph's replays then draw the
+    mask that it says).  ``out`` may be x or the residual itself.  Rows may be
+    strided (stride 1 along the columns), inputs also expanded rows."""
+    torch = _torch or _load_torch()
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    (_bind or _load_bind()).dropout(x, p, seed, offset, state, residual, out, stream)
+    return out
+
+
+class LayerOut(NamedTuple):
+    """What ``tcr_layernorm`` returns; None where an output was not asked for."""
+    y: object               # the normalised rows, or their 8-bit codes
+    scale: object           # the codes' scale of each row
+    h: object               # residual + dropout(x), rounded to the inputs' type
+    mean: object            # of each row of h
+    rstd: object            # 1 / sqrt(variance + eps) of each row
+
+
+def tcr_layernorm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, p: float = 0.0, seed: int = 0,
+                  offset: int = 0, state=None, out_dtype=None, h=None, out=None, scale=None, mean=None, rstd=None,
+                  want_stats: bool = False, stream=None) -> LayerOut:
+    """Layer norm of the rows of ``residual + dropout(x)`` (``tcr_layernorm``).
+
+    ``out_dtype`` is x's own type (the default) or ``torch.int8``: 8-bit
+    codes with ``scale``, one float32 a row (refused beside another type); an
+    ``out`` given sets it.  ``h`` (the next layer's residual, and what the
+    gradient takes) is returned when there is a residual, a dropout or an ``h``
+    to write to (``h=residual`` updates it in place); ``mean`` and ``rstd``,
+    which the gradient takes, when asked for.  ``p``, ``seed``, ``offset`` and
+    ``state`` as in ``tcr_dropout``.  Rows may be strided (stride 1 along the
+    columns); x and residual may also be expanded rows.
+    """
+    torch = _torch or _load_torch()
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out is {out.dtype}, out_dtype {out_dtype}")
+    if h is None and (residual is not None or p):
+        h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if out.dtype is not torch.int8:
+        if scale is not None:
+            raise ValueError(f"scale is of int8 codes, out is {out.dtype}")
+    elif scale is None:
+        scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    if want_stats:
+        if mean is None:
+            mean = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        if rstd is None:
+            rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    (_bind or _load_bind()).layernorm(x, weight, bias, residual, eps, p, seed, offset, state, h, out, scale, mean,
+                                      rstd, stream)
+    return LayerOut(out, scale, h, mean, rstd)
+
+
+class LayerGrad(NamedTuple):
+    """What ``tcr_layernorm_backward`` returns; None where it was not wanted."""
+    dx: object              # of x, through the dropout
+    dresidual: object       # of the residual (and of h)
+    dweight: object         # float32
+    dbias: object           # float32
+
+
+def tcr_layernorm_backward(dy, h, weight, mean, rstd, dh=None, p: float = 0.0, seed: int = 0, offset: int = 0,
+                           state=None, dx=None, dresidual=None, dweight=None, dbias=None, want_dweight: bool = True,
+                           want_dbias: bool = True, want_dresidual: bool = False, stream=None) -> LayerGrad:
+    """The gradient of ``tcr_layernorm`` (``tcr_layernorm_backward``).
+
+    ``h``, ``mean`` and ``rstd`` are the forward call's (x itself where it
+    gave no h), and so are ``p``, ``seed``, ``offset`` and ``state``; ``dh`` is the
+    gradient that reaches h along the residual path.  Without dropout dx is the
+    gradient of the residual too; with it ask for ``dresidual``.  dweight (None
+    without a weight) and dbias are float32."""
+    torch = _torch or _load_torch()
+    if dx is None:
+        dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    if dresidual is None and want_dresidual:
+        dresidual = torch.empty(h.shape, dtype=h.dtype, device=h.device)
+    if dweight is None and weight is not None and want_dweight:
+        dweight = torch.empty(h.shape[1:], dtype=torch.float32, device=h.device)
+    if dbias is None and want_dbias:
+        dbias = torch.empty(h.shape[1:], dtype=torch.float32, device=h.device)
+    (_bind or _load_bind()).layernorm_backward(dy, h, weight, mean, rstd, dh, p, seed, offset, state, dx, dresidual,
+                                               dweight, dbias, stream)
+    return LayerGrad(dx, dresidual, dweight, dbias)
+
+
+class XentOut(NamedTuple):
+    """What ``tcr_cross_entropy`` returns."""
+    loss: object            # of each token; 0 where it is ignored
+    lse: object             # log of the token's sum of exponentials, or None
+
+
+def tcr_cross_entropy(x, weight, target, ignore_index: int = -100, loss=None, lse=None, want_lse: bool = False,
+                      stream=None) -> XentOut:
+    """Softmax cross entropy of the logits ``x @ weight.T`` against ``target``,
+    one int64 a token, the logits never in memory (``tcr_cross_entropy``).
+
+    x (tokens x hidden) and weight (vocabulary x hidden) are float16 or
+    bfloat16.  A token whose target is ``ignore_index`` has loss 0 and costs
+    nothing; a target outside the vocabulary gives NaN.  The gradient takes
+    ``lse``."""
+    torch = _torch or _load_torch()
+    if loss is None:
+        loss = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    if lse is None and want_lse:
+        lse = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    (_bind or _load_bind()).cross_entropy(x, weight, target, ignore_index, loss, lse, stream)
+    return XentOut(loss, lse)
+
+
+def tcr_cross_entropy_backward(dloss, x, weight, target, lse, ignore_index: int = -100, dx=None, dweight=None,
+                               want_dx: bool = True, want_dweight: bool = True, stream=None):
+    """(dx, dweight) of ``tcr_cross_entropy`` (``tcr_cross_entropy_backward``),
+    of x's type, None where not wanted.  ``dloss``: a float32 a token, or one
+    expanded over them (the mean's gradient); ``lse`` the forward call's."""
+    torch = _torch or _load_torch()
+    if dx is None and want_dx:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if dweight is None and want_dweight:
+        dweight = torch.empty(weight.shape, dtype=weight.dtype, device=weight.device)
+    (_bind or _load_bind()).cross_entropy_backward(dloss, x, weight, target, lse, ignore_index, dx, dweight, stream)
+    return dx, dweight

@@ -1,4 +1,5 @@
-/* bind.c -- the Python side of the 8-bit path's calls, as a CPython module.
+/* bind.c -- the Python side of the calls over rows (the 8-bit path, dropout, the
+ * layer norm, the cross entropy), as a CPython module.
  *
  * A decoding step's kernels run for a few microseconds, as long as an
  * interpreter takes to look at the tensors of one call.  Each function here
@@ -18,7 +19,7 @@
 
 static PyObject *s_shape, *s_dtype, *s_stride, *s_data_ptr, *s_get_device, *s_cuda_stream;
 /* set by setup() */
-static PyObject *t_f16, *t_bf16, *t_f32, *t_i8, *t_i32, *raw_stream, *get_device, *set_device, *error_class;
+static PyObject *t_f16, *t_bf16, *t_f32, *t_i8, *t_i32, *t_i64, *raw_stream, *get_device, *set_device, *error_class;
 static tcr_status (*f_rmsnorm)(const tcr_norm_args *, void *);
 static tcr_status (*f_backward)(const tcr_norm_back_args *, void *);
 static tcr_status (*f_quantize)(const void *, size_t, const void *, size_t, void *, size_t, float *, size_t, size_t,
@@ -26,6 +27,12 @@ static tcr_status (*f_quantize)(const void *, size_t, const void *, size_t, void
 static tcr_status (*f_dequantize)(const void *, size_t, const float *, void *, size_t, size_t, size_t, int, void *);
 static tcr_status (*f_gemm)(const void *, size_t, const void *, size_t, const float *, const float *, void *, size_t,
                             size_t, size_t, size_t, int, void *);
+static tcr_status (*f_dropout)(const void *, size_t, const void *, size_t, void *, size_t, size_t, size_t,
+                               const tcr_drop *, int, void *);
+static tcr_status (*f_layernorm)(const tcr_layernorm_args *, void *);
+static tcr_status (*f_layernorm_backward)(const tcr_layernorm_back_args *, void *);
+static tcr_status (*f_xent)(const tcr_xent_args *, void *);
+static tcr_status (*f_xent_backward)(const tcr_xent_back_args *, void *);
 
 /* One call's device, and the shape that its first tensor gives. */
 typedef struct {
@@ -246,6 +253,13 @@ static PyObject *leave(long before, tcr_status st, const char *name)
         Py_END_ALLOW_THREADS;   \
     } while (0)
 
+#define WANT_TRAINING(n)                                                             \
+    WANT_ARGS(n);                                                                    \
+    if (!t_i64) {                                                                    \
+        PyErr_SetString(PyExc_RuntimeError, "setup_training() has not been called"); \
+        return NULL;                                                                 \
+    }
+
 #define WANT_ARGS(n)                                                           \
     if (nargs != (n)) {                                                        \
         PyErr_Format(PyExc_TypeError, "%s takes %d arguments", __func__, (n)); \
@@ -407,6 +421,215 @@ static PyObject *gemm(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     return leave(before, st, "tcr_gemm_i8");
 }
 
+/* A call's dropout from p, seed, offset and state (an int64 tensor of two, or
+ * None); *use: 0 where p is 0 and there is none. */
+static int drop_rule(PyObject *const *a, const Call *c, tcr_drop *d, int *use)
+{
+    d->p = PyFloat_AsDouble(a[0]);
+    if (d->p == -1.0 && PyErr_Occurred()) return -1;
+    if (!(d->p >= 0.0 && d->p <= 1.0)) {
+        PyErr_SetString(PyExc_ValueError, "p must be in 0 .. 1");
+        return -1;
+    }
+    d->seed = PyLong_AsUnsignedLongLongMask(a[1]);
+    if (PyErr_Occurred()) return -1;
+    d->offset = PyLong_AsUnsignedLongLongMask(a[2]);
+    if (PyErr_Occurred()) return -1;
+    d->state = NULL;
+    *use = d->p > 0.0;
+    return a[3] == Py_None ? 0 : vector("state", a[3], 2, t_i64, c, (const void **)&d->state);
+}
+
+/* dropout(x, p, seed, offset, state, residual, out, stream) */
+static PyObject *dropout(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
+{
+    (void)self;
+    WANT_TRAINING(8);
+    Call c;
+    PyObject *dt;
+    int code, use;
+    tcr_drop d;
+    const void *x, *r = NULL, *y;
+    size_t ldx, ldr = 0, ldy;
+    if (first("x", a[0], &c) || (code = float_type(a[0], &dt)) < 0 || drop_rule(a + 1, &c, &d, &use) ||
+        rows_of("x", a[0], c.rows, c.cols, dt, 1, &x, &ldx) ||
+        (a[5] != Py_None && matrix("residual", a[5], c.rows, c.cols, dt, 1, &c, &r, &ldr)) ||
+        matrix("out", a[6], c.rows, c.cols, dt, 0, &c, &y, &ldy))
+        return NULL;
+    void *s;
+    long before;
+    if (stream_of(a[7], &c, &s) || enter_device(&c, &before)) return NULL;
+    tcr_status st;
+    UNLOCKED(st, f_dropout(x, ldx, r, ldr, (void *)y, ldy, (size_t)c.rows, (size_t)c.cols, &d, code, s));
+    return leave(before, st, "tcr_dropout");
+}
+
+/* layernorm(x, weight, bias, residual, eps, p, seed, offset, state, h, out, scale, mean, rstd, stream) */
+static PyObject *layernorm(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
+{
+    (void)self;
+    WANT_TRAINING(15);
+    Call c;
+    tcr_layernorm_args n = {0};
+    tcr_drop d;
+    int use;
+    PyObject *dt;
+    if (first("x", a[0], &c) || (n.dtype = float_type(a[0], &dt)) < 0 || drop_rule(a + 5, &c, &d, &use)) return NULL;
+    PyObject *ot = PyObject_GetAttr(a[10], s_dtype);
+    if (!ot) return NULL;
+    const int i8 = ot == t_i8;
+    Py_DECREF(ot);
+    n.y_dtype = i8 ? TCR_I8 : n.dtype;
+    n.rows = (size_t)c.rows;
+    n.cols = (size_t)c.cols;
+    n.drop = use ? &d : NULL;
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (eps == -1.0 && PyErr_Occurred()) return NULL;
+    n.eps = (float)eps;
+    if (rows_of("x", a[0], c.rows, c.cols, dt, 1, &n.x, &n.ldx) ||
+        matrix("out", a[10], c.rows, c.cols, i8 ? t_i8 : dt, 0, &c, (const void **)&n.y, &n.ldy) ||
+        (a[1] != Py_None && vector("weight", a[1], c.cols, dt, &c, &n.weight)) ||
+        (a[2] != Py_None && vector("bias", a[2], c.cols, dt, &c, &n.bias)) ||
+        (a[3] != Py_None && matrix("residual", a[3], c.rows, c.cols, dt, 1, &c, &n.residual, &n.ldr)) ||
+        (a[9] != Py_None && matrix("h", a[9], c.rows, c.cols, dt, 0, &c, (const void **)&n.h, &n.ldh)) ||
+        (a[11] != Py_None && vector("scale", a[11], c.rows, t_f32, &c, (const void **)&n.scale)) ||
+        (a[12] != Py_None && vector("mean", a[12], c.rows, t_f32, &c, (const void **)&n.mean)) ||
+        (a[13] != Py_None && vector("rstd", a[13], c.rows, t_f32, &c, (const void **)&n.rstd)))
+        return NULL;
+    void *s;
+    long before;
+    if (stream_of(a[14], &c, &s) || enter_device(&c, &before)) return NULL;
+    tcr_status st;
+    UNLOCKED(st, f_layernorm(&n, s));
+    return leave(before, st, "tcr_layernorm");
+}
+
+/* layernorm_backward(dy, h, weight, mean, rstd, dh, p, seed, offset, state, dx, dresidual, dweight, dbias, stream) */
+static PyObject *layernorm_backward(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
+{
+    (void)self;
+    WANT_TRAINING(15);
+    Call c;
+    tcr_layernorm_back_args n = {0};
+    tcr_drop d;
+    int use;
+    PyObject *dt;
+    if (first("h", a[1], &c) || (n.dtype = float_type(a[1], &dt)) < 0 || drop_rule(a + 6, &c, &d, &use)) return NULL;
+    n.rows = (size_t)c.rows;
+    n.cols = (size_t)c.cols;
+    n.drop = use ? &d : NULL;
+    if (matrix("dy", a[0], c.rows, c.cols, dt, 1, &c, &n.dy, &n.lddy) ||
+        rows_of("h", a[1], c.rows, c.cols, dt, 1, &n.h, &n.ldh) ||
+        (a[2] != Py_None && vector("weight", a[2], c.cols, dt, &c, &n.weight)) ||
+        vector("mean", a[3], c.rows, t_f32, &c, (const void **)&n.mean) ||
+        vector("rstd", a[4], c.rows, t_f32, &c, (const void **)&n.rstd) ||
+        (a[5] != Py_None && matrix("dh", a[5], c.rows, c.cols, dt, 1, &c, &n.dh, &n.lddh)) ||
+        (a[10] != Py_None && matrix("dx", a[10], c.rows, c.cols, dt, 0, &c, (const void **)&n.dx, &n.lddx)) ||
+        (a[11] != Py_None &&
+         matrix("dresidual", a[11], c.rows, c.cols, dt, 0, &c, (const void **)&n.dresidual, &n.lddr)) ||
+        (a[12] != Py_None && vector("dweight", a[12], c.cols, t_f32, &c, (const void **)&n.dweight)) ||
+        (a[13] != Py_None && vector("dbias", a[13], c.cols, t_f32, &c, (const void **)&n.dbias)))
+        return NULL;
+    void *s;
+    long before;
+    if (stream_of(a[14], &c, &s) || enter_device(&c, &before)) return NULL;
+    tcr_status st;
+    UNLOCKED(st, f_layernorm_backward(&n, s));
+    return leave(before, st, "tcr_layernorm_backward");
+}
+
+/* x and weight of the cross entropy: their device, shapes, type and rows. */
+static int xent_inputs(PyObject *x, PyObject *weight, Call *c, Call *w, int *code, PyObject **dt, const void **px,
+                       size_t *ldx, const void **pw, size_t *ldw)
+{
+    if (first("x", x, c) || first("weight", weight, w)) return -1;
+    if (w->dev != c->dev) {
+        PyErr_Format(PyExc_ValueError, "weight must be on cuda:%ld", c->dev);
+        return -1;
+    }
+    if (w->cols != c->cols) {
+        PyErr_Format(PyExc_ValueError, "inner dimensions differ: (%zd, %zd) vs (%zd, %zd)", c->rows, c->cols, w->rows,
+                     w->cols);
+        return -1;
+    }
+    if ((*code = float_type(x, dt)) < 0) return -1;
+    if (*code == TCR_F32) {
+        PyErr_Format(PyExc_TypeError, "expected float16 or bfloat16, got %S", *dt);
+        return -1;
+    }
+    return rows_of("x", x, c->rows, c->cols, *dt, 1, px, ldx) || rows_of("weight", weight, w->rows, w->cols, *dt, 0, pw, ldw)
+               ? -1
+               : 0;
+}
+
+/* cross_entropy(x, weight, target, ignore_index, loss, lse, stream) */
+static PyObject *cross_entropy(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
+{
+    (void)self;
+    WANT_TRAINING(7);
+    Call c, w;
+    tcr_xent_args n = {0};
+    PyObject *dt;
+    if (xent_inputs(a[0], a[1], &c, &w, &n.dtype, &dt, &n.x, &n.ldx, &n.weight, &n.ldw)) return NULL;
+    n.tokens = (size_t)c.rows;
+    n.hidden = (size_t)c.cols;
+    n.vocab = (size_t)w.rows;
+    n.ignore_index = PyLong_AsLongLong(a[3]);
+    if (PyErr_Occurred()) return NULL;
+    if (vector("target", a[2], c.rows, t_i64, &c, (const void **)&n.target) ||
+        vector("loss", a[4], c.rows, t_f32, &c, (const void **)&n.loss) ||
+        (a[5] != Py_None && vector("lse", a[5], c.rows, t_f32, &c, (const void **)&n.lse)))
+        return NULL;
+    void *s;
+    long before;
+    if (stream_of(a[6], &c, &s) || enter_device(&c, &before)) return NULL;
+    tcr_status st;
+    UNLOCKED(st, f_xent(&n, s));
+    return leave(before, st, "tcr_cross_entropy");
+}
+
+/* cross_entropy_backward(dloss, x, weight, target, lse, ignore_index, dx, dweight, stream) */
+static PyObject *cross_entropy_backward(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
+{
+    (void)self;
+    WANT_TRAINING(9);
+    Call c, w;
+    tcr_xent_back_args n = {0};
+    PyObject *dt, *v;
+    if (xent_inputs(a[1], a[2], &c, &w, &n.dtype, &dt, &n.x, &n.ldx, &n.weight, &n.ldw)) return NULL;
+    n.tokens = (size_t)c.rows;
+    n.hidden = (size_t)c.cols;
+    n.vocab = (size_t)w.rows;
+    n.ignore_index = PyLong_AsLongLong(a[5]);
+    if (PyErr_Occurred()) return NULL;
+    /* dloss: contiguous, or one value expanded over the tokens */
+    const Py_ssize_t dims = tuple_of(a[0], s_shape, 0, &v);
+    if (dims < 0) return NULL;
+    const int same = dims == 1 && PyLong_AsSsize_t(PyTuple_GET_ITEM(v, 0)) == c.rows;
+    if (!same) PyErr_Format(PyExc_ValueError, "dloss must have shape (%zd,), got %S", c.rows, v);
+    Py_DECREF(v);
+    if (!same || tuple_of(a[0], s_stride, 1, &v) < 0) return NULL;
+    const Py_ssize_t inc = PyLong_AsSsize_t(PyTuple_GET_ITEM(v, 0));
+    Py_DECREF(v);
+    if (c.rows > 1 && inc != 0 && inc != 1) {
+        PyErr_SetString(PyExc_ValueError, "dloss must be contiguous or expanded from one value");
+        return NULL;
+    }
+    n.inc_dloss = c.rows > 1 ? (size_t)inc : 1;
+    if (on_device("dloss", a[0], &c) || typed("dloss", a[0], t_f32, (const void **)&n.dloss) ||
+        vector("target", a[3], c.rows, t_i64, &c, (const void **)&n.target) ||
+        vector("lse", a[4], c.rows, t_f32, &c, (const void **)&n.lse) ||
+        (a[6] != Py_None && matrix("dx", a[6], c.rows, c.cols, dt, 0, &c, (const void **)&n.dx, &n.lddx)) ||
+        (a[7] != Py_None && matrix("dweight", a[7], w.rows, w.cols, dt, 0, &c, (const void **)&n.dweight, &n.lddw)))
+        return NULL;
+    void *s;
+    long before;
+    if (stream_of(a[8], &c, &s) || enter_device(&c, &before)) return NULL;
+    tcr_status st;
+    UNLOCKED(st, f_xent_backward(&n, s));
+    return leave(before, st, "tcr_cross_entropy_backward");
+}
+
 /* setup(float16, bfloat16, float32, int8, int32, raw_stream, get_device,
  *       set_device, error class, addresses of the five entry points) */
 static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
@@ -433,9 +656,32 @@ static PyObject *setup(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
     Py_RETURN_NONE;
 }
 
+/* setup_training(int64, addresses of the five entry points of dropout, the layer
+ * norm and the cross entropy): after setup() */
+static PyObject *setup_training(PyObject *self, PyObject *const *a, Py_ssize_t nargs)
+{
+    (void)self;
+    WANT_ARGS(6);
+    void *f[5];
+    for (int i = 0; i < 5; i++) {
+        f[i] = PyLong_AsVoidPtr(a[1 + i]);
+        if (PyErr_Occurred()) return NULL;
+    }
+    Py_XSETREF(t_i64, Py_NewRef(a[0]));
+    f_dropout = (tcr_status(*)(const void *, size_t, const void *, size_t, void *, size_t, size_t, size_t,
+                               const tcr_drop *, int, void *))f[0];
+    f_layernorm = (tcr_status(*)(const tcr_layernorm_args *, void *))f[1];
+    f_layernorm_backward = (tcr_status(*)(const tcr_layernorm_back_args *, void *))f[2];
+    f_xent = (tcr_status(*)(const tcr_xent_args *, void *))f[3];
+    f_xent_backward = (tcr_status(*)(const tcr_xent_back_args *, void *))f[4];
+    Py_RETURN_NONE;
+}
+
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {FAST(setup),         FAST(rmsnorm),         FAST(rmsnorm_backward),
                                 FAST(quantize_rows), FAST(dequantize_rows), FAST(gemm),
+                                FAST(dropout),       FAST(layernorm),       FAST(layernorm_backward),
+                                FAST(cross_entropy), FAST(cross_entropy_backward), FAST(setup_training),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tcrbind", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

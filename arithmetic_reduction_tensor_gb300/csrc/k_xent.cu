@@ -1,0 +1,629 @@
+// k_xent.cu -- the matrix products of the softmax cross entropy over a
+// vocabulary, on pairs of SMs (tcgen05.mma.cta_group::2, 256 x 256 tiles).
+//
+// With l = X W^T the logits of n tokens over V entries (never in memory):
+//   forward   a tile's epilogue leaves, of each of its rows, the largest logit
+//             and the sum of 2^(log2(e) (l - largest)) over its 256 columns, and
+//             the target's logit: 8 bytes for 256 logits.
+//   gradient  over a piece of the vocabulary at a time: the logits' tiles again,
+//             their epilogue writing P = (exp(l - lse) - [target]) g in 16 bits;
+//             then one launch forms dX += P W (units of 256 tokens x 256 columns
+//             of X, K along the piece, fp32 sums across the pieces) and the
+//             piece's rows of dW = P^T X (K along the tokens).
+// P is the only thing rounded on the way: to the inputs' type, half a step of
+// each of its elements, as large an error as the rounding of the results;
+// the products' sums are 32 bits.
+//
+// X is the compact, aligned copy of the tokens that count (k_xent_rows.cu), W is
+// V x H, P is n x the piece.  Only the logits have both operands K-major as they
+// lie in memory.  The gradient's products take W, P and X as they are, MN-major:
+// a 64 x 64 box of a row-major matrix lands in shared memory as 64 rows of 128
+// swizzled bytes, which is a K-major operand of 64 rows or an MN-major one of
+// 64 k, as the descriptor and the instruction say; so no matrix is transposed.
+//
+// Roles, barriers, time limits as in gemm_splitk_pair_kernel (k_gemm.cu): a
+// producer thread, an MMA thread, four epilogue warps, two accumulators.
+#include "pair.cuh"
+#include "rowvec.cuh"
+#include "xent.h"
+
+namespace tcr {
+
+constexpr int kXBox = 64;                          // rows and columns of a box
+constexpr int kXBoxBytes = kXBox * kXBox * 2;      // 8 KiB
+constexpr int kXHalf = 128;                        // rows of an operand per CTA
+constexpr int kXHalfBytes = 2 * kXBoxBytes;
+constexpr int kXStageBytes = 2 * kXHalfBytes;      // 32 KiB: both operands
+constexpr int kXStages = 7;
+constexpr int kXDBuffers = 2;
+constexpr uint32_t kXTmemCols = kXDBuffers * kXentTile;
+constexpr int kXThreads = 192;
+constexpr int kXEpilogueThreads = 128;
+constexpr int kXGroup = 8;                         // tile rows per raster group (L2 reuse)
+constexpr int kXOffBars = kXStages * kXStageBytes;
+// barriers: full[S] (leader's: both CTAs' copies), empty[S], dfull[D], dempty[D] (leader's), drain
+constexpr int kXNumBars = 2 * kXStages + 2 * kXDBuffers + 1;
+constexpr int kXOffMisc = kXOffBars + 8 * kXNumBars;
+constexpr int kXSmemBytes = kXOffMisc + 64 + 1024;
+static_assert(kXSmemBytes <= 232448, "one SM's 227 KiB");
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ unsigned int g_xent_fault;
+
+__device__ __forceinline__ bool x_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort)
+{
+    return mbar_wait_f(bar, parity, abort, &g_xent_fault);
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// The operand of 128 rows (or MN elements) at `addr`, two boxes: K-major (8-row
+// groups 1024 bytes apart; a k-slice of 16 is 32 bytes further) or MN-major
+// (64-element blocks a box apart, groups of 8 k 1024 bytes apart; a slice
+// is 16 rows of 128 bytes further).  128-byte swizzle.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn)
+{
+    const uint64_t lbo = mn ? (uint64_t)(kXBoxBytes >> 4) : 1u;
+    return (uint64_t)((addr >> 4) & 0x3fffu) | (lbo << 16) | ((uint64_t)(1024u >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// kind::f16, M = N = 256, fp32 sums; bits 15 and 16: A and B MN-major.
+template <int DT>
+__device__ __forceinline__ uint32_t operand_instr(bool a_mn, bool b_mn)
+{
+    constexpr uint32_t ab = DT == kF16 ? 0u : 1u;
+    return (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(kXentTile >> 3) << 17) | ((uint32_t)(kXentTile >> 4) << 24);
+}
+
+// One tile's work: 64-boxes [k0, k0 + nk) of K.
+struct XUnit {
+    bool x;                // dX (else dW, or the logits)
+    int tm, tn, split, k0, nk;
+};
+
+// The units of one launch, of which pair p of `pairs` runs the i-th of its own.
+struct XUnits {
+    int mode, pairs, pair;
+    int tm, tn, nk;                    // the logits, or dW: tiles, boxes of K
+    int xm, xn, xnk, xkps, xsplits;    // dX: tiles, boxes of K, boxes a split
+    int nx, nd, lead, rem;
+
+    __device__ __forceinline__ XUnits(const XentGemm &g, int n, int mode_) : mode(mode_)
+    {
+        pairs = (int)(gridDim.x >> 1);
+        pair = (int)(blockIdx.x >> 1);
+        const int rows = (n + kXentTile - 1) / kXentTile, cols = (g.vn + kXentTile - 1) / kXentTile;
+        nx = 0;
+        lead = rem = 0;
+        xm = xn = xnk = xkps = xsplits = 0;
+        if (mode != kXentBack) {
+            tm = rows;
+            tn = cols;
+            nk = (g.H + kXBox - 1) / kXBox;
+            nd = tm * tn;
+            return;
+        }
+        const int hcols = (g.H + kXentTile - 1) / kXentTile;
+        tm = cols;
+        tn = hcols;
+        nk = (n + kXBox - 1) / kXBox;
+        nd = g.dw ? tm * tn : 0;
+        if (g.ws) {
+            xm = rows;
+            xn = hcols;
+            xnk = (g.vn + kXBox - 1) / kXBox;
+            xkps = (xnk + g.splits - 1) / g.splits;
+            xsplits = g.splits;
+            nx = xm * xn * xsplits;
+            // the long units first, one more on some pairs than on others: those
+            // take fewer of the short ones
+            rem = nx % pairs;
+            lead = rem && nk ? (xkps + nk / 2) / nk : 0;
+            if (lead > nd / (pairs - rem)) lead = nd / (pairs - rem);
+        }
+    }
+    __device__ __forceinline__ static void raster(int u, int tiles_m, int tiles_n, int &m, int &n)
+    {
+        const int group = kXGroup * tiles_n, first = u / group * kXGroup;
+        const int in_group = min(tiles_m - first, kXGroup), r = u % group;
+        m = first + r % in_group;
+        n = r / in_group;
+    }
+    __device__ __forceinline__ bool get(int i, XUnit &u) const
+    {
+        const int mine = nx ? (nx - pair + pairs - 1) / pairs : 0;       // its dX units
+        if (i < mine) {
+            const int v = pair + i * pairs, tiles = xm * xn;
+            u.x = true;
+            u.split = v / tiles;
+            raster(v % tiles, xm, xn, u.tm, u.tn);
+            u.k0 = u.split * xkps;
+            u.nk = max(0, min(xkps, xnk - u.k0));
+            return true;
+        }
+        i -= mine;
+        int d;
+        const int free_pairs = pairs - rem;
+        if (pair >= rem && i < lead) {
+            d = pair - rem + i * free_pairs;
+        } else {
+            if (pair >= rem) i -= lead;
+            d = lead * free_pairs + pair + i * pairs;
+        }
+        if (d >= nd) return false;
+        u.x = false;
+        u.split = 0;
+        raster(d, tm, tn, u.tm, u.tn);
+        u.k0 = 0;
+        u.nk = nk;
+        return true;
+    }
+};
+
+// ---------------------------------------------------------------- epilogues
+//
+// Thread m of CTA r has row 128 r + m of the tile; `ld(c, v)` gives columns
+// 32 c .. 32 c + 31 of it.
+
+// The largest logit of the row in this tile and the sum about it.
+template <class Ld>
+__device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int tn, Ld ld)
+{
+    const int col0 = tn * kXentTile;
+    const int at = g.lab[row] - col0;
+    float mx = -INFINITY, s = 0.0f, hit = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < kXentTile / 32; c++) {
+        const int left = g.V - (col0 + 32 * c);
+        float v[32];
+        ld(c, v);
+        if (left <= 0) continue;
+        if (left < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+                if (j >= left) v[j] = -INFINITY;
+        }
+        float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+        for (int j = 4; j < 32; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
+        const float now = fmaxf(mx, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+        const float about = now == -INFINITY ? 0.0f : -__fmul_rn(now, kLog2e);
+        float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 32; j++) e[j & 3] = __fadd_rn(e[j & 3], ex2(__fmaf_rn(v[j], kLog2e, about)));
+        s = __fmaf_rn(s, ex2(__fmaf_rn(mx, kLog2e, about)),
+                      __fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])));
+        mx = now;
+        if (at >= 32 * c && at < 32 * c + 32) {
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+                if (at == 32 * c + j) hit = v[j];
+        }
+    }
+    g.part[(size_t)tn * g.tpad + row] = make_float2(mx, s);
+    if (at >= 0 && at < kXentTile) g.hit[row] = hit;
+}
+
+// P of the row: (exp(l - lse) - [target]) * g, in units of the largest |g| so
+// that the target's -1 times a common g is exact (binary16: times 2^15 on top,
+// which keeps probabilities of 2^-29 normal).
+template <int DT, class Ld>
+__device__ __forceinline__ void epilogue_gradient(const XentGemm &g, size_t row, int n, int tn, Ld ld)
+{
+    const int col0 = tn * kXentTile;                     // within the piece
+    float about = 0.0f, gq = 0.0f;
+    int at = -1;
+    const bool live = row < (size_t)n;
+    if (live) {
+        const int tok = g.tok[row], lab = g.lab[row];
+        const float gmax = __uint_as_float(g.head[1]);
+        about = -__fmul_rn(g.lse[tok], kLog2e);
+        gq = g.dloss[(size_t)tok * g.inc_dloss];
+        if (gmax > 0.0f) gq = __fdiv_rn(gq, gmax);       // (gmax is that of the finite ones)
+        if (DT == kF16) gq = __fmul_rn(gq, kXentF16Scale);
+        if (lab < 0) gq = __int_as_float(0x7fc00000);    // no such entry
+        at = lab - g.v0 - col0;
+    }
+    uint16_t *out = g.P + row * g.ldp + col0;
+#pragma unroll 1
+    for (int c = 0; c < kXentTile / 32; c++) {
+        float v[32];
+        ld(c, v);
+        const int left = g.vn - (col0 + 32 * c);
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 32; j++) {
+            float p = ex2(__fmaf_rn(v[j], kLog2e, about));
+            if (at == 32 * c + j) p = __fsub_rn(p, 1.0f);
+            v[j] = gq == 0.0f || j >= left ? 0.0f : __fmul_rn(p, gq);
+        }
+#pragma unroll
+        for (int j = 0; j < 16; j++) o[j] = float2_to_word<DT>(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            *reinterpret_cast<uint4 *>(out + 32 * c + 8 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    }
+}
+
+// A split's sums of dX, added to those of the pieces before.
+template <class Ld>
+__device__ __forceinline__ void epilogue_dx(const XentGemm &g, size_t row, int split, int tn, Ld ld)
+{
+    const size_t col0 = (size_t)tn * kXentTile;
+    float *out = g.ws + (size_t)split * g.tpad * g.ldws + row * g.ldws + col0;
+#pragma unroll 1
+    for (int c = 0; c < kXentTile / 32; c++) {
+        if (col0 + 32 * c >= g.ldws) {
+            float v[32];
+            ld(c, v);
+            continue;
+        }
+        float4 before[8];
+        if (!g.first) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) before[j] = *reinterpret_cast<const float4 *>(out + 32 * c + 4 * j);
+        }
+        float v[32];
+        ld(c, v);
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            float4 f = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (!g.first)
+                f = make_float4(__fadd_rn(before[j].x, f.x), __fadd_rn(before[j].y, f.y), __fadd_rn(before[j].z, f.z),
+                                __fadd_rn(before[j].w, f.w));
+            *reinterpret_cast<float4 *>(out + 32 * c + 4 * j) = f;
+        }
+    }
+}
+
+// A row of dW, rounded.
+template <int DT, class Ld>
+__device__ __forceinline__ void epilogue_dw(const XentGemm &g, int vrow, int tn, Ld ld)
+{
+    const int col0 = tn * kXentTile;
+    float scale = __uint_as_float(g.head[1]);
+    if (DT == kF16) scale = __fmul_rn(scale, 1.0f / kXentF16Scale);
+    const bool live = vrow < g.vn;
+    uint16_t *out = (uint16_t *)g.dw + (size_t)(g.v0 + vrow) * g.lddw + col0;
+#pragma unroll 1
+    for (int c = 0; c < kXentTile / 32; c++) {
+        float v[32];
+        ld(c, v);
+        const int left = g.H - (col0 + 32 * c);
+        if (!live || left <= 0) continue;
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 16; j++) o[j] = float2_to_word<DT>(__fmul_rn(v[2 * j], scale), __fmul_rn(v[2 * j + 1], scale));
+        if (left >= 32 && g.al_dw) {
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                *reinterpret_cast<uint4 *>(out + 32 * c + 8 * j) =
+                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; j++)
+                if (j < left) out[32 * c + j] = (uint16_t)(o[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int DT, int MODE>
+__global__ void __launch_bounds__(kXThreads, 1)
+xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+            const __grid_constant__ CUtensorMap map_p, const XentGemm g)
+{
+    pdl_launch_dependents();
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t ring = smem_addr(smem);
+    const uint32_t bars = ring + kXOffBars;
+    auto full_bar = [&](int s) { return bars + 8u * (uint32_t)s; };
+    auto empty_bar = [&](int s) { return bars + 8u * (uint32_t)(kXStages + s); };
+    auto dfull_bar = [&](int b) { return bars + 8u * (uint32_t)(2 * kXStages + b); };
+    auto dempty_bar = [&](int b) { return bars + 8u * (uint32_t)(2 * kXStages + kXDBuffers + b); };
+    const uint32_t drain_bar = bars + 8u * (uint32_t)(2 * kXStages + 2 * kXDBuffers);
+    uint32_t *misc = (uint32_t *)(smem + kXOffMisc);
+    volatile uint32_t *tmem_holder = misc;
+    volatile uint32_t *abort = misc + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kXStages; s++) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        for (int b = 0; b < kXDBuffers; b++) {
+            mbar_init(dfull_bar(b), 1);
+            mbar_init(dempty_bar(b), 2 * kXEpilogueThreads);      // both CTAs' epilogues
+        }
+        mbar_init(drain_bar, 1);
+        *abort = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_x) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_w) : "memory");
+        if (MODE == kXentBack) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_p) : "memory");
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (warp == 1) {
+        // together with the peer CTA's warp 1
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr((const void *)tmem_holder)), "r"(kXTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    cluster_sync_all();        // both CTAs' barriers and allocation are in place
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    pdl_wait_primary();
+    const int n = (int)g.head[0];
+    const XUnits units(g, n, MODE);
+
+    if (warp == 0) {
+        // ---------------- producer: this CTA's halves; completion on the leader's full barrier
+        if (lane == 0) {
+            int st = 0;
+            uint32_t phase = 0;
+            bool armed[kXStages];
+            uint32_t armed_phase[kXStages];
+            for (int i = 0; i < kXStages; i++) {
+                armed[i] = false;
+                armed_phase[i] = 0;
+            }
+            XUnit u;
+            for (int i = 0; !*abort && units.get(i, u); i++) {
+                const int m0 = u.tm * kXentTile + kXHalf * (int)rank, n0 = u.tn * kXentTile + kXHalf * (int)rank;
+                const CUtensorMap *ma = MODE == kXentBack ? &map_p : &map_x;
+                const CUtensorMap *mb = MODE != kXentBack || u.x ? &map_w : &map_x;
+                const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
+                // the vocabulary's coordinate counts from the piece's first entry in P only
+                const int b_row = MODE == kXentBack ? (u.x ? g.v0 : 0) : n0 + g.v0;
+                bool ok = true;
+                for (int j = 0; j < u.nk; j++) {
+                    if (!x_wait(empty_bar(st), phase ^ 1u, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t dst = ring + (uint32_t)st * kXStageBytes;
+                    const int kc = (u.k0 + j) * kXBox;
+                    const uint32_t fb = map_to_rank(full_bar(st), 0u);
+                    if (leader) mbar_arrive_expect_tx(full_bar(st), (uint32_t)(2 * kXStageBytes));
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (a_mn)
+                            tma_load_2d_pair(dst + h * kXBoxBytes, ma, m0 + h * kXBox, kc, fb);
+                        else
+                            tma_load_2d_pair(dst + h * kXBoxBytes, ma, kc, m0 + h * kXBox, fb);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (b_mn)
+                            tma_load_2d_pair(dst + kXHalfBytes + h * kXBoxBytes, mb, n0 + h * kXBox, b_row + kc, fb);
+                        else
+                            tma_load_2d_pair(dst + kXHalfBytes + h * kXBoxBytes, mb, kc, b_row + h * kXBox, fb);
+                    }
+                    armed[st] = true;
+                    armed_phase[st] = phase;
+                    if (++st == kXStages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+            }
+            if (*abort && leader) {
+                // the full barriers count both CTAs' copies: let them land
+                for (int i = 0; i < kXStages; i++)
+                    if (armed[i]) (void)mbar_wait_limited(full_bar(i), armed_phase[i]);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------- MMA issuer (the leader's lane 0)
+        if (leader && lane == 0) {
+            int st = 0, b = 0;
+            uint32_t phase = 0, dphase = 0;       // bit b: uses of accumulator b so far, mod 2
+            bool withhold = g.inject_stall != 0u;
+            XUnit u;
+            for (int i = 0; !*abort && units.get(i, u); i++) {
+                const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
+                const uint32_t idesc = operand_instr<DT>(a_mn, b_mn);
+                const uint64_t a_ring = operand_desc(ring, a_mn), b_ring = operand_desc(ring + kXHalfBytes, b_mn);
+                const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
+                // both epilogues have read accumulator b
+                if (!x_wait(dempty_bar(b), ((dphase >> b) & 1u) ^ 1u, abort)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(b * kXentTile);
+                bool ok = true;
+                for (int j = 0; j < u.nk; j++) {
+                    if (!x_wait(full_bar(st), phase, abort)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t at = (uint64_t)st * (uint64_t)(kXStageBytes >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        tc_mma_pair(d, a_ring + at + (uint64_t)k * a_step, b_ring + at + (uint64_t)k * b_step, idesc,
+                                    (j > 0 || k > 0) ? 1u : 0u);
+                    tc_commit_pair(empty_bar(st));               // both CTAs' stage is free
+                    if (++st == kXStages) {
+                        st = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                if (withhold)
+                    withhold = false;
+                else
+                    tc_commit_pair(dfull_bar(b));                // the tile is in both CTAs' TMEM
+                dphase ^= 1u << b;
+                b ^= 1;
+            }
+            tc_commit_pair_local(drain_bar);
+            (void)mbar_wait_limited(drain_bar, 0u);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue: thread m takes row 128 rank + m of the tile
+        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+        const int m = kXHalf * (int)rank + 32 * (warp & 3) + lane;
+        int b = 0;
+        uint32_t dphase = 0;
+        XUnit u;
+        for (int i = 0; units.get(i, u); i++) {
+            const bool ready = !*abort && x_wait(dfull_bar(b), (dphase >> b) & 1u, abort);
+            const bool live = __all_sync(kFull, ready);
+            if (live) tc_fence_after();
+            // without an MMA (K of nothing) the accumulator holds another tile's sums
+            const float fill = live ? 0.0f : __int_as_float(0x7fc00000);
+            const bool read = live && u.nk > 0;
+            auto ld = [&](int c, float (&v)[32]) {
+                __syncwarp();
+                if (read) {
+                    tc_ld_row32(tmem + lane_base + (uint32_t)(b * kXentTile + 32 * c), v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j++) v[j] = fill;
+                }
+            };
+            const size_t row = (size_t)u.tm * kXentTile + (size_t)m;
+            if constexpr (MODE == kXentForward)
+                epilogue_forward(g, row, u.tn, ld);
+            else if constexpr (MODE == kXentGradient)
+                epilogue_gradient<DT>(g, row, n, u.tn, ld);
+            else if (u.x)
+                epilogue_dx(g, row, u.split, u.tn, ld);
+            else
+                epilogue_dw<DT>(g, (int)row, u.tn, ld);
+            if (live) {
+                tc_fence_before();
+                mbar_arrive_cluster(map_to_rank(dempty_bar(b), 0u));
+            }
+            dphase ^= 1u << b;
+            b ^= 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    // the leader's MMAs read the peer's shared memory and write its tensor
+    // memory: neither CTA leaves or frees before both are done
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == 1) {
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kXTmemCols)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+namespace {
+
+const void *xent_pick(int dtype, int mode)
+{
+    if (dtype == kF16)
+        return mode == kXentForward    ? (const void *)xent_kernel<kF16, kXentForward>
+               : mode == kXentGradient ? (const void *)xent_kernel<kF16, kXentGradient>
+                                       : (const void *)xent_kernel<kF16, kXentBack>;
+    return mode == kXentForward    ? (const void *)xent_kernel<kBF16, kXentForward>
+           : mode == kXentGradient ? (const void *)xent_kernel<kBF16, kXentGradient>
+                                   : (const void *)xent_kernel<kBF16, kXentBack>;
+}
+
+cudaLaunchConfig_t pair_config(int pairs, cudaLaunchAttribute (&attr)[2], cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(kXThreads);
+    cfg.dynamicSmemBytes = kXSmemBytes;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+}  // namespace
+
+// The pairs that can be resident at once on the current device, cached.
+int xent_pairs()
+{
+    static std::mutex mu;
+    static std::vector<std::pair<int, int>> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        for (auto &c : cache)
+            if (c.first == dev) return c.second;
+    }
+    int n = 0, sms = 0;
+    bool ok = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+    for (int dt : {kF16, kBF16})
+        for (int mode : {kXentForward, kXentGradient, kXentBack})
+            ok = ok && set_smem_once((void *)xent_pick(dt, mode), kXSmemBytes) == cudaSuccess;
+    if (ok) {
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = pair_config(sms / 2, attr, nullptr);
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack), &cfg) != cudaSuccess) n = 0;
+    }
+    (void)cudaGetLastError();
+    std::lock_guard<std::mutex> lk(mu);
+    cache.emplace_back(dev, n);
+    return n;
+}
+
+cudaError_t xent_map(void *map, const void *base, size_t cols, size_t rows, size_t ld)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const cuuint32_t box[2] = {kXBox, kXBox}, step[2] = {1, 1};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)ld * 2};
+    return encode((CUtensorMap *)map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (void *)base, dims, pitch, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+               ? cudaSuccess
+               : cudaErrorInvalidValue;
+}
+
+cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
+                        cudaStream_t stream)
+{
+    void *args[] = {(void *)&maps.x, (void *)&maps.w, (void *)&maps.p, (void *)&g};
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = pair_config((int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);
+    return cudaLaunchKernelExC(&cfg, xent_pick(dtype, mode), args);
+}
+
+cudaError_t read_xent_faults(unsigned int *flags, bool clear)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_xent_fault, sizeof(unsigned int));
+    if (e != cudaSuccess || !clear) return e;
+    const unsigned int zero = 0u;
+    return cudaMemcpyToSymbol(g_xent_fault, &zero, sizeof(unsigned int));
+}
+
+}  // namespace tcr

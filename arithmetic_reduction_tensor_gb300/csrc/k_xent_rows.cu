@@ -1,0 +1,249 @@
+// k_xent_rows.cu -- the passes over tokens around the products of the softmax
+// cross entropy: the compact copy of the tokens that count, the loss from the
+// tiles' parts, dX from its sums.
+//
+// Copying the tokens costs 4 bytes an element of X where the products cost 2 V
+// operations or more; for it, ignored tokens cost nothing afterwards and what
+// they hold (NaN included) reaches no sum, and X may have any pitch and
+// alignment.  All are bound by memory traffic, or, for few tokens, by latency.
+#include "kernels.cuh"
+#include "rowvec.cuh"
+#include "xent.h"
+
+namespace tcr {
+
+constexpr int kTokThreads = 256, kTokWarps = kTokThreads / 32;
+constexpr int kTokTail = 8;            // CTAs that count all tokens, and zero the rows behind the last
+
+// The live tokens among [0, n).
+__device__ __forceinline__ int count_live(const XentTokens &a, size_t n, int *red)
+{
+    int c = 0;
+#pragma unroll 8
+    for (size_t i = threadIdx.x; i < n; i += kTokThreads) c += a.target[i] != a.ignore;
+    c = __reduce_add_sync(kFull, c);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = c;
+    __syncthreads();
+    int s = 0;
+#pragma unroll
+    for (int w = 0; w < kTokWarps; w++) s += red[w];
+    __syncthreads();
+    return s;
+}
+
+// One row by a warp, 16-byte vectors where the source is aligned; H elements.
+__device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst, size_t H, bool aligned)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    if (aligned) {
+        const size_t nv = H / 8;
+#pragma unroll 4
+        for (size_t v = lane; v < nv; v += 32) reinterpret_cast<uint4 *>(dst)[v] = ld_stream(src + 8 * v);
+        for (size_t j = 8 * nv + lane; j < H; j += 32) dst[j] = src[j];
+    } else {
+#pragma unroll 8
+        for (size_t j = lane; j < H; j += 32) dst[j] = src[j];
+    }
+}
+
+// CTA b takes tokens [b chunk, (b + 1) chunk): their rows in the copy follow
+// from the count of those before, which each CTA takes itself (a scan would
+// be a launch more).
+__global__ void __launch_bounds__(kTokThreads) xent_tokens_kernel(const XentTokens a, size_t chunk, unsigned blocks)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    __shared__ int red[kTokWarps];
+    __shared__ int ranks[kTokThreads];
+    const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x >= blocks) {
+        const unsigned part = blockIdx.x - blocks;
+        const int n = count_live(a, a.tokens, red);
+        const size_t end = ((size_t)n + 63) / 64 * 64;
+        for (size_t r = (size_t)n + part * kTokWarps + warp; r < end; r += kTokTail * kTokWarps)
+            for (size_t v = lane; v < a.ldX / 8; v += 32)
+                reinterpret_cast<uint4 *>(a.X + r * a.ldX)[v] = make_uint4(0u, 0u, 0u, 0u);
+        if (part != 0) return;
+        unsigned int m = 0;
+        if (a.dloss) {
+#pragma unroll 8
+            for (size_t i = threadIdx.x; i < a.tokens; i += kTokThreads)
+                if (a.target[i] != a.ignore) {
+                    const unsigned int b = __float_as_uint(a.dloss[i * a.inc_dloss]) & 0x7fffffffu;
+                    if (b < 0x7f800000u) m = max(m, b);
+                }
+            m = __reduce_max_sync(kFull, m);
+            if (lane == 0) red[warp] = (int)m;
+            __syncthreads();
+            for (int w = 0; w < kTokWarps; w++) m = max(m, (unsigned int)red[w]);
+        }
+        if (threadIdx.x == 0) {
+            a.head[0] = (unsigned int)n;
+            a.head[1] = m;
+        }
+        return;
+    }
+    const size_t first = (size_t)blockIdx.x * chunk, last = min(first + chunk, a.tokens);
+    int base = count_live(a, first, red);
+    for (size_t t0 = first; t0 < last; t0 += kTokThreads) {          // kTokThreads tokens at a time
+        const size_t t = t0 + threadIdx.x;
+        const long long y = t < last ? a.target[t] : a.ignore;
+        const bool live = t < last && y != a.ignore;
+        const unsigned mask = __ballot_sync(kFull, live);
+        if (lane == 0) red[warp] = __popc(mask);
+        __syncthreads();
+        int r = base, all = 0;
+#pragma unroll
+        for (int w = 0; w < kTokWarps; w++) {
+            if (w < (int)warp) r += red[w];
+            all += red[w];
+        }
+        r += __popc(mask & ((1u << lane) - 1u));
+        ranks[threadIdx.x] = live ? r : -1;
+        if (t < last) a.rank[t] = live ? r : -1;
+        if (live) {
+            a.lab[r] = y >= 0 && y < (long long)a.V ? (int)y : -1;
+            a.tok[r] = (int)t;
+        }
+        __syncthreads();
+        const int here = (int)min(last - t0, (size_t)kTokThreads);
+        for (int i = (int)warp; i < here; i += kTokWarps) {
+            const int to = ranks[i];
+            if (to >= 0)
+                copy_row((const uint16_t *)a.x + (t0 + i) * a.ldx, a.X + (size_t)to * a.ldX, a.H, a.al_x);
+        }
+        base += all;
+        __syncthreads();
+    }
+}
+
+__global__ void __launch_bounds__(kTokThreads)
+xent_repack_kernel(const uint16_t *w, size_t ldw, size_t V, size_t H, uint16_t *W, size_t ldW)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    for (size_t r = (size_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5); r < V; r += (size_t)gridDim.x * kTokWarps)
+        copy_row(w + r * ldw, W + r * ldW, H, false);
+}
+
+// 32 tokens a CTA, one a lane; the warps share the tiles.  lse = log of the
+// parts' sums about the largest logit, in powers of two as they were formed.
+constexpr int kLossWarps = 16;
+__global__ void __launch_bounds__(32 * kLossWarps) xent_loss_kernel(const XentLoss a)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    constexpr float log2e = 1.44269504088896340736f, ln2 = 0.69314718055994530942f;
+    __shared__ float sm[kLossWarps][32], ss[kLossWarps][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t t = (size_t)blockIdx.x * 32 + lane;
+    const int r = t < a.tokens ? a.rank[t] : -1;
+    float m = -INFINITY, s = 0.0f;
+    if (r >= 0) {
+        // two passes over the parts (8 bytes for 256 logits): the largest, then the sum about it
+#pragma unroll 4
+        for (int j = (int)warp; j < a.tiles; j += kLossWarps) m = fmaxf(m, a.part[(size_t)j * a.tpad + r].x);
+    }
+    sm[warp][lane] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kLossWarps; w++) m = fmaxf(m, sm[w][lane]);
+    const float about = m == -INFINITY ? 0.0f : __fmul_rn(m, log2e);
+    if (r >= 0) {
+#pragma unroll 4
+        for (int j = (int)warp; j < a.tiles; j += kLossWarps) {
+            const float2 p = a.part[(size_t)j * a.tpad + r];
+            // the part's own unit is fl(p.x * log2e), as its sum was formed (a part
+            // of nothing but -infinity is 0 in any unit)
+            const float unit = p.x == -INFINITY ? about : __fmul_rn(p.x, log2e);
+            s = __fmaf_rn(p.y, exp2f(__fsub_rn(unit, about)), s);
+        }
+    }
+    ss[warp][lane] = s;
+    __syncthreads();
+    if (warp != 0 || t >= a.tokens) return;
+    float loss = 0.0f, lse = 0.0f;
+    if (r >= 0) {
+        s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kLossWarps; w++) s = __fadd_rn(s, ss[w][lane]);
+        lse = __fmul_rn(__fadd_rn(about, log2f(s)), ln2);
+        loss = a.lab[r] < 0 ? __int_as_float(0x7fc00000) : __fsub_rn(lse, a.hit[r]);
+    }
+    a.loss[t] = loss;
+    if (a.lse) a.lse[t] = lse;
+}
+
+// A CTA takes 1024 columns of a token, four a thread.
+template <int DT>
+__global__ void __launch_bounds__(256) xent_dx_kernel(const XentDx a)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const size_t j = (size_t)blockIdx.y * 1024 + 4 * threadIdx.x;
+    if (j >= a.H) return;
+    float scale = __uint_as_float(a.head[1]);
+    if (DT == kF16) scale = __fmul_rn(scale, 1.0f / kXentF16Scale);
+    for (size_t t = blockIdx.x; t < a.tokens; t += gridDim.x) {
+        const int r = a.rank[t];
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (r >= 0) {
+            const float *p = a.ws + (size_t)r * a.ldws + j;
+#pragma unroll 4
+            for (int k = 0; k < a.splits; k++) {
+                const float4 f = *reinterpret_cast<const float4 *>(p + (size_t)k * a.tpad * a.ldws);
+                s = make_float4(__fadd_rn(s.x, f.x), __fadd_rn(s.y, f.y), __fadd_rn(s.z, f.z), __fadd_rn(s.w, f.w));
+            }
+            s = make_float4(__fmul_rn(s.x, scale), __fmul_rn(s.y, scale), __fmul_rn(s.z, scale), __fmul_rn(s.w, scale));
+        }
+        const uint32_t lo = float2_to_word<DT>(s.x, s.y), hi = float2_to_word<DT>(s.z, s.w);
+        uint16_t *out = (uint16_t *)a.dx + t * a.lddx + j;
+        if (a.al_dx && j + 4 <= a.H) {
+            *reinterpret_cast<uint2 *>(out) = make_uint2(lo, hi);
+        } else {
+            out[0] = (uint16_t)lo;
+            if (j + 1 < a.H) out[1] = (uint16_t)(lo >> 16);
+            if (j + 2 < a.H) out[2] = (uint16_t)hi;
+            if (j + 3 < a.H) out[3] = (uint16_t)(hi >> 16);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+cudaError_t launch_xent_tokens(const XentTokens &a, cudaStream_t stream)
+{
+    // about a thousand CTAs at most: each reads the targets before its own
+    size_t chunk = (a.tokens + 1023) / 1024;
+    if (chunk < kTokWarps) chunk = kTokWarps;
+    unsigned blocks = (unsigned)((a.tokens + chunk - 1) / chunk);
+    void *args[] = {(void *)&a, (void *)&chunk, (void *)&blocks};
+    return launch_first((const void *)xent_tokens_kernel, dim3(blocks + kTokTail), dim3(kTokThreads), args, 0, stream);
+}
+
+cudaError_t launch_xent_repack(const void *w, size_t ldw, size_t V, size_t H, uint16_t *W, size_t ldW,
+                               cudaStream_t stream)
+{
+    const size_t need = (V + kTokWarps - 1) / kTokWarps;
+    void *args[] = {(void *)&w, (void *)&ldw, (void *)&V, (void *)&H, (void *)&W, (void *)&ldW};
+    return launch_first((const void *)xent_repack_kernel, dim3((unsigned)(need < 152 * 8 ? need : 152 * 8)),
+                        dim3(kTokThreads), args, 0, stream);
+}
+
+cudaError_t launch_xent_loss(const XentLoss &a, cudaStream_t stream)
+{
+    void *args[] = {(void *)&a};
+    return launch_first((const void *)xent_loss_kernel, dim3((unsigned)((a.tokens + 31) / 32)), dim3(32 * kLossWarps),
+                        args, 0, stream);
+}
+
+cudaError_t launch_xent_dx(int dtype, const XentDx &a, cudaStream_t stream)
+{
+    void *args[] = {(void *)&a};
+    const size_t gy = (a.H + 1023) / 1024, most = (size_t)152 * 32;
+    const dim3 grid((unsigned)(a.tokens < most ? a.tokens : most), (unsigned)gy);
+    return launch_first(dtype == kF16 ? (const void *)xent_dx_kernel<kF16> : (const void *)xent_dx_kernel<kBF16>, grid,
+                        dim3(256), args, 0, stream);
+}
+
+}  // namespace tcr

@@ -233,6 +233,44 @@ int norm_back_groups(size_t rows, size_t cols);
 size_t norm_back_scratch(size_t rows, size_t cols, bool dweight);
 cudaError_t launch_norm_back(int dtype, BackArgs a, float *scratch, float *dw, cudaStream_t stream);
 
+// ---- dropout and the layer norm with it (k_layer.cu), and its gradient
+// (k_layer_back.cu): as the row operators above, rows of more than
+// kBackMaxVecs vectors of 8 in the gradient with one more launch and two
+// floats of scratch each.
+struct DropArgs {
+    uint32_t t;                        // kept where 16 bits are at least t; 0: everything, 65536: nothing
+    float s;                           // 65536 / (65536 - t), rounded; 0 at t = 65536
+    uint32_t k0, k1, c2, c3;           // seed and offset, where state is null
+    const unsigned long long *state;   // seed and offset on the device
+};
+struct LayerArgs {
+    const void *x, *r, *w, *b;       // r, w, b may be null
+    size_t ldx, ldr;
+    void *h, *y;                     // h may be null; y: the input type, or 8-bit codes with scale
+    size_t ldh, ldy;
+    float *scale, *mean, *rstd;      // mean, rstd may be null
+    float eps;
+    size_t rows, cols;
+    bool al_x, al_r, al_w, al_b, al_h, al_y;   // 16-byte aligned rows (codes: 8-byte)
+    DropArgs drop;
+};
+cudaError_t launch_layer(int dtype, bool out_i8, const LayerArgs &a, cudaStream_t stream);
+// y = r + dropout(x); cols > 0.
+cudaError_t launch_dropout(int dtype, const LayerArgs &a, cudaStream_t stream);
+struct LayerBackArgs {
+    const void *dy, *h, *w, *dh;     // w, dh may be null
+    const float *mean, *rstd;
+    size_t lddy, ldh, lddh;
+    void *dx, *dr;                   // either may be null
+    size_t lddx, lddr;
+    float *partial_w, *partial_b;    // null: not wanted
+    size_t rows, cols;
+    bool al_dy, al_h, al_w, al_dh, al_dx, al_dr;
+    DropArgs drop;
+};
+size_t layer_back_scratch(size_t rows, size_t cols, bool dweight, bool dbias);
+cudaError_t launch_layer_back(int dtype, LayerBackArgs a, float *scratch, float *dw, float *db, cudaStream_t stream);
+
 // ---- matrix product in 8-bit integers with scales (k_gemm_i8.cu)
 constexpr int kI8FewTokens = 1024;   // beyond: never the kernels of k_gemm_i8_few.cu
 constexpr int kOutI32 = 4;           // c_dtype beside kF16, kBF16, kF32: the integer sums themselves

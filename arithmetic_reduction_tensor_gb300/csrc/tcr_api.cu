@@ -16,6 +16,7 @@
 #include "../../include/tcr.h"
 #include "kernels.cuh"
 #include "plan.h"
+#include "xent.h"
 
 namespace tcr {
 namespace plan {
@@ -956,11 +957,11 @@ tcr_status tcr_device_faults(unsigned int *flags, int clear)
 {
     if (!flags) return TCR_ERR_INVALID_ARG;
     if (current_device() < 0) return TCR_ERR_CUDA;
-    unsigned int a = 0, g = 0, i = 0;
+    unsigned int a = 0, g = 0, i = 0, x = 0;
     if (read_device_faults(&a, clear != 0) != cudaSuccess || read_gemm_faults(&g, clear != 0) != cudaSuccess ||
-        read_gemm_i8_faults(&i, clear != 0) != cudaSuccess)
+        read_gemm_i8_faults(&i, clear != 0) != cudaSuccess || read_xent_faults(&x, clear != 0) != cudaSuccess)
         return TCR_ERR_CUDA;
-    *flags = a | g | i;
+    *flags = a | g | i | x;
     return TCR_OK;
 }
 

@@ -1,0 +1,98 @@
+// xent.h -- the softmax cross entropy over a vocabulary: what its products
+// (k_xent.cu), its passes over tokens (k_xent_rows.cu) and its entry points
+// (tcr_train.cu) share.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace tcr {
+
+constexpr int kXentTile = 256;             // tokens and vocabulary entries (or columns) of a tile
+constexpr int kXentForward = 0, kXentGradient = 1, kXentBack = 2;
+constexpr float kXentF16Scale = 32768.0f;  // of P in binary16
+
+// The tokens that count, in their order: n of them, then at least zeros up to
+// a multiple of 64 rows of X.
+struct XentTokens {
+    const void *x;
+    size_t ldx;
+    const long long *target;
+    size_t tokens, H, V;
+    long long ignore;
+    bool al_x;
+    const float *dloss;        // null in the forward pass
+    size_t inc_dloss;
+    // outputs
+    uint16_t *X;               // the compact copy, ldX elements a row
+    size_t ldX;
+    int *lab, *tok, *rank;     // by compact row: label (-1: no entry of the vocabulary), token; by token: its row or -1
+    unsigned int *head;        // n, and the bits of those tokens' largest finite |dloss|
+};
+cudaError_t launch_xent_tokens(const XentTokens &a, cudaStream_t stream);
+
+// W copied to rows of ldW elements (16-byte aligned).
+cudaError_t launch_xent_repack(const void *w, size_t ldw, size_t V, size_t H, uint16_t *W, size_t ldW,
+                               cudaStream_t stream);
+
+struct XentGemm {
+    const unsigned int *head;
+    const int *lab, *tok;
+    size_t tpad;               // rows of X, P, part and ws
+    int V, H;
+    int v0, vn;                // the piece of the vocabulary (the forward pass: all of it)
+    // forward
+    float2 *part;              // [tile of the vocabulary][row]: largest logit, sum about it
+    float *hit;                // the target's logit
+    // gradient
+    const float *lse, *dloss;
+    size_t inc_dloss;
+    uint16_t *P;
+    size_t ldp;
+    // back
+    float *ws;                 // [split][row][ldws]; null: dX not wanted
+    size_t ldws;
+    int splits, first;
+    void *dw;                  // null: not wanted
+    size_t lddw;
+    bool al_dw;
+    uint32_t inject_stall;     // withhold the first tile's publication (tests of the failure path)
+};
+struct alignas(64) XentMaps {
+    CUtensorMap x, w, p;
+};
+int xent_pairs();
+cudaError_t xent_map(void *map, const void *base, size_t cols, size_t rows, size_t ld);
+cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
+                        cudaStream_t stream);
+
+// loss and lse of every token from its tiles' parts.
+struct XentLoss {
+    const float2 *part;
+    const float *hit;
+    const int *rank, *lab;
+    size_t tpad, tokens;
+    int tiles;
+    float *loss, *lse;         // lse may be null
+};
+cudaError_t launch_xent_loss(const XentLoss &a, cudaStream_t stream);
+
+// dX of every token from the splits' sums; tokens that do not count 0.
+struct XentDx {
+    const float *ws;
+    size_t tpad, ldws;
+    int splits;
+    const int *rank;
+    const unsigned int *head;
+    size_t tokens, H;
+    void *dx;
+    size_t lddx;
+    bool al_dx;
+};
+cudaError_t launch_xent_dx(int dtype, const XentDx &a, cudaStream_t stream);
+
+cudaError_t read_xent_faults(unsigned int *flags, bool clear);
+
+}  // namespace tcr

@@ -611,9 +611,184 @@ TCR_API tcr_status tcr_gemm_i8(const void *A, size_t lda, const void *W, size_t 
                                int c_dtype, void *stream);
 
 /*
+ * ---- A training step's dropout, layer norm and loss ----
+ *
+ * Dropout's mask comes from a counter-based generator and is never stored:
+ * element (r, j) takes 16 bits of the Philox4x32-10 block with counter (j / 8,
+ * r, low word of offset, high word) and key (low word of seed, high word): half
+ * j % 2 (0 the low one) of word (j % 8) / 2.  With t = rint(65536 p), ties to
+ * even, it is kept where those bits are at least t, and then multiplied by
+ * 65536 / (65536 - t) (rounded to binary32); dropped elements are +0.0,
+ * whatever they hold.  The mask depends on seed, offset, row and column only,
+ * so a gradient that is given the same four forms the same mask.
+ *   p       0 .. 1 (met to 2^-17).
+ *   state   NULL, or two 64-bit words on the device, seed and offset, read by the
+ *           kernels when they run in place of the two fields: a captured
+ *           graph draws new masks when they are changed between its replays.
+ */
+typedef struct {
+    double p;
+    unsigned long long seed, offset;
+    const unsigned long long *state;
+} tcr_drop;
+
+/*
+ * tcr_dropout -- y = residual + dropout(x), each addition and multiplication
+ * rounded to binary32, the result to dtype.  residual may be NULL.  Rows as in
+ * the 8-bit path; y may be x or the residual itself (same pointer and ld).
+ * The gradient of x is the same call on dy without a residual.
+ */
+TCR_API tcr_status tcr_dropout(const void *x, size_t ldx, const void *residual, size_t ldr, void *y, size_t ldy,
+                               size_t rows, size_t cols, const tcr_drop *drop, int dtype, void *stream);
+
+/*
+ * tcr_layernorm -- for every row
+ *   h_j = residual_j + dropout(x)_j   (without a residual: dropout(x)_j),
+ *   mean = S1 / cols, S1 the declared sum of h_j (see the 8-bit path),
+ *   rstd = 1 / sqrt(S2 / cols + eps), S2 the declared sum of fl((h_j - mean)^2),
+ *   y_j = ((h_j - mean) * rstd) * weight_j + bias_j   (each where given),
+ * every step one binary32 operation.  h is used as the binary32 sum; the stored
+ * copy is rounded to dtype.
+ *   drop               NULL: none.
+ *   residual, weight, bias, h, mean, rstd   may be NULL.  h may be x or the
+ *                      residual itself (same pointer and ld); y may be too when
+ *                      it has their type and h is NULL or elsewhere.  No other
+ *                      overlap.
+ *   y, y_dtype, scale, eps   as in tcr_rmsnorm, 8-bit codes included.
+ * cols == 0: scale 0, mean and rstd NaN.
+ */
+typedef struct {
+    const void *x;
+    size_t ldx;
+    const void *residual;
+    size_t ldr;
+    const void *weight, *bias;
+    void *h;
+    size_t ldh;
+    void *y;
+    size_t ldy;
+    float *scale, *mean, *rstd;
+    size_t rows, cols;
+    float eps;
+    const tcr_drop *drop;
+    int dtype, y_dtype;
+} tcr_layernorm_args;
+TCR_API tcr_status tcr_layernorm(const tcr_layernorm_args *args, void *stream);
+
+/*
+ * tcr_layernorm_backward -- the gradient of tcr_layernorm.  With xh = (h - mean)
+ * * rstd, g = dy * weight, a = S1 / cols and c = S2 / cols, S1 and S2 the
+ * declared row sums of g and of fl(g * xh):
+ *   dresidual = rstd * ((g - a) - xh * c) + dh,   (the gradient of h, too)
+ *   dx = dropout(dresidual)   (before its rounding; of x),
+ *   dweight_j = sum over rows of fl(dy * xh),  dbias_j = sum over rows of dy.
+ *   h, mean, rstd   the forward call's (h: its stored h; x itself where that
+ *          is h).
+ *   dh     gradient that reaches h by the residual path, or NULL.
+ *   drop   that of the forward call.
+ *   dx, dresidual, dweight, dbias   NULL where not wanted (without dropout dx
+ *          and dresidual are the same).  dx or dresidual may be dy, h or dh
+ *          itself (same pointer and ld), not each other.  dweight, dbias: cols
+ *          floats; overwritten.  Their order is that of tcr_rmsnorm_backward's
+ *          dweight: no atomics.
+ * Takes G * cols floats of pool scratch (G as there) for each of dweight and
+ * dbias that is wanted, and 2 rows more for cols > 8192.
+ * rows == 0 writes dweight = dbias = +0.0.
+ */
+typedef struct {
+    const void *dy;
+    size_t lddy;
+    const void *h;
+    size_t ldh;
+    const void *weight;
+    const float *mean, *rstd;
+    const void *dh;
+    size_t lddh;
+    void *dx;
+    size_t lddx;
+    void *dresidual;
+    size_t lddr;
+    float *dweight, *dbias;
+    size_t rows, cols;
+    const tcr_drop *drop;
+    int dtype;
+} tcr_layernorm_back_args;
+TCR_API tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, void *stream);
+
+/*
+ * tcr_cross_entropy -- the softmax cross entropy of the logits l = x weight^T
+ * over a vocabulary, without the logits in memory: for every token t
+ *   lse[t] = log(sum over v of exp(l_tv)),  loss[t] = lse[t] - l_t,target[t],
+ * in binary32; both 0 where target[t] is ignore_index.
+ *   x        tokens x hidden, weight: vocab x hidden, row-major TCR_F16 or
+ *            TCR_BF16 (dtype, both alike) of any alignment, ldx and ldw as in the
+ *            8-bit path (ldx may be 0, ldw not).
+ *   target   tokens 64-bit integers.  One that is neither ignore_index nor in
+ *            0 .. vocab - 1 gives that token's loss NaN (and NaN in its gradient).
+ *   loss, lse  tokens floats; lse may be NULL.
+ * Logits are summed by the tensor cores in binary32, within 2^-22 * ceil(hidden
+ * / 16) * sum_h |x_th weight_vh|; a row with a NaN or a logit of +infinity has
+ * lse and loss NaN.  What tokens that are ignored hold is not looked at.
+ * tokens < 2^24, vocab < 2^27, hidden < 2^20 (else TCR_ERR_UNSUPPORTED), vocab and hidden not 0,
+ * tokens * vocab and vocab * hidden < 2^40.  Takes pool scratch of 2 bytes per
+ * element of x, 8 per token and 256 entries of the vocabulary, and, where
+ * weight's rows are not 16-byte aligned, 2 per element of weight.  No atomics: the bits
+ * depend on the inputs only.
+ */
+typedef struct {
+    const void *x;
+    size_t ldx;
+    const void *weight;
+    size_t ldw;
+    const long long *target;
+    float *loss, *lse;
+    size_t tokens, vocab, hidden;
+    long long ignore_index;
+    int dtype;
+} tcr_xent_args;
+TCR_API tcr_status tcr_cross_entropy(const tcr_xent_args *args, void *stream);
+
+/*
+ * tcr_cross_entropy_backward -- the gradient of sum over t of dloss[t] * loss[t]:
+ *   P_tv = (exp(l_tv - lse[t]) - [v = target[t]]) * dloss[t],
+ *   dx = P weight,  dweight = P^T x,
+ * P 0 for tokens that are ignored.  The logits are formed again, over pieces of
+ * the vocabulary; P is rounded to dtype (in units of the largest finite |dloss|;
+ * TCR_F16: of 2^-15 of it), the products summed in binary32.
+ *   dloss    tokens floats (inc_dloss = 1), or one for all (0).
+ *   lse      the forward call's.
+ *   dx, dweight  of dtype, overwritten; NULL where not wanted.  dx may be x
+ *            itself (same pointer and ld); no other overlap.
+ * tokens == 0 writes dweight = +0.0.  The rest as in tcr_cross_entropy.  Pool
+ * scratch: 2 bytes per token and entry of a piece (as many entries as 512 MiB
+ * hold, 1024 at least; tokens counted up to a multiple of 256) and 4 per element of dx (for few tokens up to 32
+ * times that), beside the copies named there.  A kernel whose wait gave up
+ * leaves NaN and sets the word of tcr_device_faults (the forward pass, too);
+ * TCR_ERR_UNSUPPORTED on a device that cannot schedule a CTA pair.
+ */
+typedef struct {
+    const float *dloss;
+    size_t inc_dloss;
+    const void *x;
+    size_t ldx;
+    const void *weight;
+    size_t ldw;
+    const long long *target;
+    const float *lse;
+    void *dx;
+    size_t lddx;
+    void *dweight;
+    size_t lddw;
+    size_t tokens, vocab, hidden;
+    long long ignore_index;
+    int dtype;
+} tcr_xent_back_args;
+TCR_API tcr_status tcr_cross_entropy_backward(const tcr_xent_back_args *args, void *stream);
+
+/*
  * tcr_device_faults -- the fault word of the current device: bit 0
  * (TCR_FAULT_PIPELINE_WAIT) is set when a wait inside a TCR_MMA_CHAIN_TMEM,
- * split-K GEMM or 8-bit GEMM kernel gave up after its limit of about one second (the kernel then
+ * split-K GEMM, 8-bit GEMM or cross entropy kernel gave up after its limit of about one second (the kernel then
  * drained its own copies and tensor-core work, freed its tensor memory and
  * wrote NaN partials, so that call's result is NaN).  The word stays set
  * until cleared: clear != 0 resets it after reading.  Synchronous with
