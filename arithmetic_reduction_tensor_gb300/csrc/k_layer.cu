@@ -22,110 +22,140 @@ __device__ __forceinline__ float rstd_of(float s, uint32_t cols, float eps)
     return __frsqrt_rn(__fadd_rn(__fdiv_rn(s, (float)cols), eps));
 }
 
-// Rows of at most 8 T NV columns, NV pieces a thread: teams of T threads (T =
-// 32: eight to a CTA; else the CTA) walk the rows, each loading its next row
-// before it finishes the current one.  The sums' two buffers and the largest
-// magnitude's are each written again only after a barrier that every reader
-// of the last values has passed.
-template <int DT, int OUT, bool ELEM, int T, int NV, int MINB>
-__global__ void __launch_bounds__(T == 32 ? 256 : T, MINB)
-layer_kernel(const LayerArgs a)
+// One row, NV pieces a thread, of which the first LEAD are whole.
+template <int DT, int OUT, bool ELEM, int T, int NV, int LEAD>
+__device__ __forceinline__ void layer_row(const LayerArgs &a, const Drop &drop, size_t r, uint32_t t, float *red,
+                                          uint32_t *redm)
+{
+    using E = typename Elem<DT>::T;
+    constexpr int L = layout_of<DT, ELEM>();
+    constexpr uint32_t kStep = kRv * T;                  // elements between a thread's pieces
+    const uint32_t cols = (uint32_t)a.cols;
+    const bool has_r = a.r != nullptr;
+    const uint32_t at = piece_offset<L>(t);
+    auto count = [&](int i) { return piece_count<L, T, LEAD>(cols, at, i); };
+    float y[NV][kRv], s[NV];
+    {
+        const E *px = (const E *)a.x + r * a.ldx + at, *pr = (const E *)a.r + r * a.ldr + at;
+        Piece<DT> x[NV], res[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++) load_piece<DT, L>(px + i * kStep, count(i), x[i], by_words(px));
+        if (has_r) {
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                load_piece<DT, L>(pr + i * kStep, count(i), res[i], by_words(pr));
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            piece_values<DT>(x[i], y[i]);
+            drop_values<L>(drop, t + i * T, r, y[i]);
+        }
+        if (has_r) {
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                float g[kRv];
+                piece_values<DT>(res[i], g);
+                add8(y[i], g, y[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        zero_absent(count(i), y[i]);
+        s[i] = piece_tree<L>(y[i]);
+    }
+    float sum[1] = {halving<NV>(s)};
+    team_sums<T, L>(sum, red);
+    const float mean = __fdiv_rn(sum[0], (float)cols);
+    if (a.h) {
+        E *ph = (E *)a.h + r * a.ldh + at;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            store_piece<DT, L>(ph + i * kStep, count(i), y[i], by_words(ph));
+    }
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        float e[kRv];
+        add8(y[i], y[i], -mean);
+        zero_absent(count(i), y[i]);
+        mul8(e, y[i], y[i]);
+        s[i] = piece_tree<L>(e);
+    }
+    sum[0] = halving<NV>(s);
+    team_sums<T, L>(sum, red + team_sums_floats<T, 1>());
+    const float rstd = rstd_of(sum[0], cols, a.eps);
+    if (t == 0) {
+        if (a.mean) a.mean[r] = mean;
+        if (a.rstd) a.rstd[r] = rstd;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; i++) mul8(y[i], y[i], rstd);
+    if (a.w) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            float f[kRv];
+            Piece<DT> w;
+            load_piece<DT, L>((const E *)a.w + at + i * kStep, count(i), w, by_words(a.w));
+            piece_values<DT>(w, f);
+            mul8(y[i], y[i], f);
+        }
+    }
+    if (a.b) {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            float f[kRv];
+            Piece<DT> b;
+            load_piece<DT, L>((const E *)a.b + at + i * kStep, count(i), b, by_words(a.b));
+            piece_values<DT>(b, f);
+            add8(y[i], y[i], f);
+        }
+    }
+    if constexpr (OUT == kOutSame) {
+        E *py = (E *)a.y + r * a.ldy + at;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            store_piece<DT, L>(py + i * kStep, count(i), y[i], by_words(py));
+    } else {
+        float m = 0.0f, scale, per;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            zero_absent(count(i), y[i]);      // 0 times a possibly infinite rstd
+            m = amax8(y[i], m);
+        }
+        i8_scale(team_most<T>(__float_as_uint(m), redm), scale, per);
+        if (t == 0) a.scale[r] = scale;
+        int8_t *py = (int8_t *)a.y + r * a.ldy + at;
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            store_piece_codes<L>(py + i * kStep, count(i), y[i], per);
+    }
+}
+
+// Rows of at most 8 T NV columns, NV pieces a thread, a team of T threads a row
+// (T = 32: four to a CTA; else the CTA); the first LEAD pieces are whole in
+// every warp, and warps whose last is whole, too, run code without masks (most
+// of a row's warps; masks everywhere cost 16384 x 4096 bfloat16 rows a third).  No
+// team walks rows and none loads ahead: weight and bias come from L1 or L2 row
+// by row, so that registers hold one row alone and up to 1024 threads' rows
+// are in flight on an SM, at different steps.  That takes 16384 x 4096 bfloat16
+// 79 us (the copy rate), where teams that walk rows, with the weight in
+// registers and the next row's loads in flight, took 93.
+template <int DT, int OUT, bool ELEM, int T, int NV, int LEAD, int MINB>
+__global__ void __launch_bounds__(T == 32 ? 128 : T, MINB)
+layer_kernel(const __grid_constant__ LayerArgs a)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
-    __shared__ float red[2][team_floats<T>()];
+    __shared__ float red[2 * team_sums_floats<T, 1>()];
     __shared__ uint32_t redm[32];
-    using E = typename Elem<DT>::T;
-    const uint32_t t = T == 32 ? threadIdx.x & 31 : threadIdx.x, cols = (uint32_t)a.cols;
-    const uint32_t threads = T == 32 ? 32 : blockDim.x;
-    const size_t team = T == 32 ? (size_t)blockIdx.x * 8 + (threadIdx.x >> 5) : blockIdx.x;
-    const size_t teams = T == 32 ? (size_t)gridDim.x * 8 : gridDim.x;
-    const bool has_r = a.r != nullptr, has_w = a.w != nullptr, has_b = a.b != nullptr;
-    const DropArgs drop = drop_resolve(a.drop);
-    Piece<DT, ELEM> x[NV], res[NV], w[NV], b[NV];
-    auto load = [&](size_t r) {
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            load_piece<DT, ELEM>((const E *)a.x + r * a.ldx, cols, t + i * T, x[i]);
-            if (has_r) load_piece<DT, ELEM>((const E *)a.r + r * a.ldr, cols, t + i * T, res[i]);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        if (has_w) load_weight_piece<DT, ELEM>((const E *)a.w, cols, t + i * T, a.al_w, w[i]);
-        if (has_b) load_weight_piece<DT, ELEM>((const E *)a.b, cols, t + i * T, a.al_b, b[i]);
-    }
-    if (team < a.rows) load(team);
-    for (size_t r = team; r < a.rows; r += teams) {
-        float y[NV][kRv], s[NV];
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const uint32_t v = t + i * T;
-            piece_values<DT, ELEM>(x[i], (const E *)a.x + r * a.ldx, cols, v, y[i]);
-            drop_values<ELEM>(drop, v, r, y[i]);
-            if (has_r) {
-                float g[kRv];
-                piece_values<DT, ELEM>(res[i], (const E *)a.r + r * a.ldr, cols, v, g);
-#pragma unroll
-                for (int k = 0; k < kRv; k++) y[i][k] = __fadd_rn(g[k], y[i][k]);
-            }
-            s[i] = piece_tree<ELEM>(y[i]);
-        }
-        if (r + teams < a.rows) load(r + teams);
-        const float mean = __fdiv_rn(team_sum<T, ELEM>(halving<NV>(s), red[0], threads), (float)cols);
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const uint32_t v = t + i * T;
-            if (a.h && kRv * (v & ~31u) < cols)              // whole warps: stores are warp-wide
-                store_piece_values<DT, ELEM>((E *)a.h + r * a.ldh, cols, v, y[i]);
-            centre(y[i], mean);
-            zero_absent<ELEM>(cols, v, y[i]);
-            float e[kRv];
-#pragma unroll
-            for (int k = 0; k < kRv; k++) e[k] = __fmul_rn(y[i][k], y[i][k]);
-            s[i] = piece_tree<ELEM>(e);
-        }
-        const float rstd = rstd_of(team_sum<T, ELEM>(halving<NV>(s), red[1], threads), cols, a.eps);
-        if (t == 0) {
-            if (a.mean) a.mean[r] = mean;
-            if (a.rstd) a.rstd[r] = rstd;
-        }
-        float m = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const uint32_t v = t + i * T;
-            if (kRv * (v & ~31u) >= cols) continue;
-#pragma unroll
-            for (int k = 0; k < kRv; k++) y[i][k] = __fmul_rn(y[i][k], rstd);
-            float f[kRv];
-            if (has_w) {
-                piece_values<DT, ELEM>(w[i], (const E *)a.w, cols, v, f);
-#pragma unroll
-                for (int k = 0; k < kRv; k++) y[i][k] = __fmul_rn(y[i][k], f[k]);
-            }
-            if (has_b) {
-                piece_values<DT, ELEM>(b[i], (const E *)a.b, cols, v, f);
-#pragma unroll
-                for (int k = 0; k < kRv; k++) y[i][k] = __fadd_rn(y[i][k], f[k]);
-            }
-            if constexpr (OUT == kOutSame) {
-                store_piece_values<DT, ELEM>((E *)a.y + r * a.ldy, cols, v, y[i]);
-            } else {
-                zero_absent<ELEM>(cols, v, y[i]);            // 0 times a possibly infinite rstd
-                m = amax8(y[i], m);
-            }
-        }
-        if constexpr (OUT == kOutI8) {
-            float scale, per;
-            i8_scale(team_max<T>(__float_as_uint(m), redm, threads), scale, per);
-            if (t == 0) a.scale[r] = scale;
-#pragma unroll
-            for (int i = 0; i < NV; i++) {
-                const uint32_t v = t + i * T;
-                if (kRv * (v & ~31u) < cols) store_piece_codes<ELEM>((int8_t *)a.y + r * a.ldy, cols, v, y[i], per);
-            }
-        }
-    }
+    const uint32_t t = T == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const size_t r = T == 32 ? (size_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
+    if (T == 32 && r >= a.rows) return;
+    const Drop drop(a.drop);
+    if (warp_whole<T, NV>((uint32_t)a.cols, t))
+        layer_row<DT, OUT, ELEM, T, NV, NV>(a, drop, r, t, red, redm);
+    else
+        layer_row<DT, OUT, ELEM, T, NV, LEAD>(a, drop, r, t, red, redm);
 }
 
 // Rows at any alignment and length, read once a step (mean, variance, the
@@ -134,13 +164,13 @@ template <int DT>
 struct LayerRow {
     using E = typename Elem<DT>::T;
     const LayerArgs &a;
-    const DropArgs &drop;
+    const Drop &drop;
     size_t r;
     uint32_t cols;
     __device__ __forceinline__ void h(uint32_t v, float (&y)[kRv]) const
     {
         unpack<DT>(load_raw<DT>((const E *)a.x + r * a.ldx, cols, v, a.al_x), y);
-        drop_values<false>(drop, v, r, y);
+        drop_values<kVectors>(drop, v, r, y);
         if (!a.r) return;
         float g[kRv];
         unpack<DT>(load_raw<DT>((const E *)a.r + r * a.ldr, cols, v, a.al_r), g);
@@ -150,9 +180,8 @@ struct LayerRow {
     __device__ __forceinline__ void norm(uint32_t v, float mean, float rstd, float (&y)[kRv]) const
     {
         float f[kRv];
-        centre(y, mean);
-#pragma unroll
-        for (int k = 0; k < kRv; k++) y[k] = __fmul_rn(y[k], rstd);
+        add8(y, y, -mean);
+        mul8(y, y, rstd);
         if (a.w) {
             unpack<DT>(load_raw<DT>((const E *)a.w, cols, v, a.al_w), f);
 #pragma unroll
@@ -163,13 +192,13 @@ struct LayerRow {
 #pragma unroll
             for (int k = 0; k < kRv; k++) y[k] = __fadd_rn(y[k], f[k]);
         }
-        zero_absent<false>(cols, v, y);
+        zero_absent(vec_left(cols, v), y);
     }
 };
 
 template <int DT, int OUT>
 __global__ void __launch_bounds__(kRowLongT)
-layer_long_kernel(const LayerArgs a)
+layer_long_kernel(const __grid_constant__ LayerArgs a)
 {
     constexpr uint32_t T = kRowLongT;
     pdl_launch_dependents();
@@ -178,7 +207,7 @@ layer_long_kernel(const LayerArgs a)
     __shared__ uint32_t redm[32];
     using E = typename Elem<DT>::T;
     const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
-    const DropArgs drop = drop_resolve(a.drop);
+    const Drop drop(a.drop);
     const LayerRow<DT> row{a, drop, blockIdx.x, cols};
     const size_t r = blockIdx.x;
     const uint32_t nvec = (cols + kRv - 1) / kRv, steps = (nvec + T - 1) / T;
@@ -193,12 +222,12 @@ layer_long_kernel(const LayerArgs a)
             if (v < nvec) {
                 row.h(v, y);
                 if (pass == 1) {
-                    centre(y, mean);
-                    zero_absent<false>(cols, v, y);
+                    add8(y, y, -mean);
+                    zero_absent(vec_left(cols, v), y);
 #pragma unroll
                     for (int k = 0; k < kRv; k++) y[k] = __fmul_rn(y[k], y[k]);
                 } else {
-                    zero_absent<false>(cols, v, y);
+                    zero_absent(vec_left(cols, v), y);
                 }
                 s = tree8(y);
             }
@@ -246,7 +275,7 @@ layer_long_kernel(const LayerArgs a)
 constexpr int kDropRows = 4;
 template <int DT, bool ELEM>
 __global__ void __launch_bounds__(256)
-dropout_kernel(const LayerArgs a, int wr)
+dropout_kernel(const __grid_constant__ LayerArgs a, int wr)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
@@ -254,32 +283,35 @@ dropout_kernel(const LayerArgs a, int wr)
     const uint32_t cols = (uint32_t)a.cols, warp = threadIdx.x >> 5;
     const uint32_t v = 32u * ((blockIdx.x << wr) + (warp & ((1u << wr) - 1))) + (threadIdx.x & 31);
     if (kRv * (v & ~31u) >= cols) return;
-    const DropArgs drop = drop_resolve(a.drop);
+    const Drop drop(a.drop);
+    constexpr int L = layout_of<DT, ELEM>();
+    const uint32_t at = piece_offset<L>(v), n = piece_count<L>(cols, at);
     const size_t step = (size_t)gridDim.y << (3 - wr);       // rows of one step of the grid
     const bool has_r = a.r != nullptr;
     for (size_t r0 = ((size_t)blockIdx.y << (3 - wr)) + (warp >> wr); r0 < a.rows; r0 += kDropRows * step) {
-        Piece<DT, ELEM> x[kDropRows], res[kDropRows];
+        Piece<DT> x[kDropRows], res[kDropRows];
 #pragma unroll
         for (int i = 0; i < kDropRows; i++) {
             const size_t r = r0 + i * step;
             if (r >= a.rows) break;
-            load_piece<DT, ELEM>((const E *)a.x + r * a.ldx, cols, v, x[i]);
-            if (has_r) load_piece<DT, ELEM>((const E *)a.r + r * a.ldr, cols, v, res[i]);
+            const E *px = (const E *)a.x + r * a.ldx + at, *pr = (const E *)a.r + r * a.ldr + at;
+            load_piece<DT, L>(px, n, x[i], by_words(px));
+            if (has_r) load_piece<DT, L>(pr, n, res[i], by_words(pr));
         }
 #pragma unroll
         for (int i = 0; i < kDropRows; i++) {
             const size_t r = r0 + i * step;
             if (r >= a.rows) break;
             float y[kRv];
-            piece_values<DT, ELEM>(x[i], (const E *)a.x + r * a.ldx, cols, v, y);
-            drop_values<ELEM>(drop, v, r, y);
+            piece_values<DT>(x[i], y);
+            drop_values<L>(drop, v, r, y);
             if (has_r) {
                 float g[kRv];
-                piece_values<DT, ELEM>(res[i], (const E *)a.r + r * a.ldr, cols, v, g);
-#pragma unroll
-                for (int k = 0; k < kRv; k++) y[k] = __fadd_rn(g[k], y[k]);
+                piece_values<DT>(res[i], g);
+                add8(y, g, y);
             }
-            store_piece_values<DT, ELEM>((E *)a.y + r * a.ldy, cols, v, y);
+            E *py = (E *)a.y + r * a.ldy + at;
+            store_piece<DT, L>(py, n, y, by_words(py));
         }
     }
 }
@@ -288,42 +320,37 @@ dropout_kernel(const LayerArgs a, int wr)
 
 namespace {
 
-template <int DT, int OUT, bool ELEM, int T, int NV, int MINB>
-const void *shape_of(size_t nvec, size_t rows, int &threads, size_t &grid)
+template <int DT, int OUT, bool ELEM, int T, int NV, int LEAD, int MINB>
+const void *shape_of(size_t rows, int &threads, size_t &grid)
 {
-    threads = T == 32 ? 256 : NV == 1 ? (int)((nvec + 31) / 32 * 32) : T;
-    const size_t need = T == 32 ? (rows + 7) / 8 : rows;
-    const size_t full = (size_t)152 * (size_t)(T == 32 ? MINB : MINB * T / threads);
-    grid = need < full ? need : full;
-    return (const void *)layer_kernel<DT, OUT, ELEM, T, NV, MINB>;
+    threads = T == 32 ? 128 : T;
+    grid = T == 32 ? (rows + 3) / 4 : rows;
+    return (const void *)layer_kernel<DT, OUT, ELEM, T, NV, LEAD, MINB>;
 }
 
-template <int DT, int OUT>
-const void *pick(size_t nvec, size_t rows, bool elem, int &threads, size_t &grid)
+template <int DT, int OUT, bool ELEM>
+const void *pick(size_t nvec, size_t rows, int &threads, size_t &grid)
 {
-#define TCR_SHAPE(ELEM_, T_, NV_, MINB_) return shape_of<DT, OUT, ELEM_, T_, NV_, MINB_>(nvec, rows, threads, grid)
-    if (elem) {
-        if (nvec <= 32) TCR_SHAPE(true, 32, 1, 4);
-        if (nvec <= 64) TCR_SHAPE(true, 32, 2, 2);
-        if (nvec <= 128) TCR_SHAPE(true, 128, 1, 8);
-        if (nvec <= 256) TCR_SHAPE(true, 256, 1, 4);
-        if (nvec <= 512) TCR_SHAPE(true, 256, 2, 2);
-        if (nvec <= 1024) TCR_SHAPE(true, 512, 2, 1);
-    } else if constexpr (DT == kF32) {
-        if (nvec <= 32) TCR_SHAPE(false, 32, 1, 3);
-        if (nvec <= 64) TCR_SHAPE(false, 32, 2, 2);
-        if (nvec <= 128) TCR_SHAPE(false, 128, 1, 8);
-        if (nvec <= 256) TCR_SHAPE(false, 256, 1, 4);
-        if (nvec <= 512) TCR_SHAPE(false, 512, 1, 2);
-        if (nvec <= 1024) TCR_SHAPE(false, 512, 2, 1);
+// (by elements a thread's 16-bit inputs take twice the registers)
+#define TCR_SHAPE(T_, NV_, LEAD_, MINB_) \
+    return shape_of<DT, OUT, ELEM, T_, NV_, LEAD_, (ELEM && MINB_ > 1 ? MINB_ * 3 / 4 : MINB_)>(rows, threads, grid)
+    if constexpr (DT == kF32) {
+        if (nvec <= 64) TCR_SHAPE(32, 2, 0, 6);
+        if (nvec <= 128) TCR_SHAPE(64, 2, 1, 12);
+        if (nvec <= 256) TCR_SHAPE(128, 2, 1, 6);
+        if (nvec <= 512) TCR_SHAPE(256, 2, 1, 3);
+        if (nvec <= 1024) TCR_SHAPE(512, 2, 1, 1);
+        if (nvec <= 2048) TCR_SHAPE(1024, 2, 1, 1);
     } else {
-        if (nvec <= 32) TCR_SHAPE(false, 32, 1, 4);
-        if (nvec <= 64) TCR_SHAPE(false, 32, 2, 3);
-        if (nvec <= 128) TCR_SHAPE(false, 64, 2, 12);
-        if (nvec <= 256) TCR_SHAPE(false, 128, 2, 6);
-        if (nvec <= 512) TCR_SHAPE(false, 256, 2, 3);
-        if (nvec <= 1024) TCR_SHAPE(false, 256, 4, 2);
-        if (nvec <= 2048) TCR_SHAPE(false, 512, 4, 1);
+        if (nvec <= 64) TCR_SHAPE(32, 2, 0, 8);
+        if (nvec <= 128) TCR_SHAPE(32, 4, 2, 8);
+        if (nvec <= 256) TCR_SHAPE(64, 4, 2, 16);
+        if (nvec <= 384) TCR_SHAPE(128, 3, 2, 8);
+        if (nvec <= 512) TCR_SHAPE(128, 4, 3, 8);
+        if (nvec <= 768) TCR_SHAPE(256, 3, 2, 4);
+        if (nvec <= 1024) TCR_SHAPE(256, 4, 3, 4);
+        if (nvec <= 2048) TCR_SHAPE(512, 4, 2, 2);
+        if (nvec <= 4096) TCR_SHAPE(1024, 4, 2, 1);
     }
 #undef TCR_SHAPE
     grid = rows;
@@ -334,8 +361,11 @@ const void *pick(size_t nvec, size_t rows, bool elem, int &threads, size_t &grid
 template <int DT>
 const void *pick_out(bool out_i8, size_t nvec, size_t rows, bool elem, int &threads, size_t &grid)
 {
-    return out_i8 ? pick<DT, kOutI8>(nvec, rows, elem, threads, grid)
-                  : pick<DT, kOutSame>(nvec, rows, elem, threads, grid);
+    if (elem)
+        return out_i8 ? pick<DT, kOutI8, true>(nvec, rows, threads, grid)
+                      : pick<DT, kOutSame, true>(nvec, rows, threads, grid);
+    return out_i8 ? pick<DT, kOutI8, false>(nvec, rows, threads, grid)
+                  : pick<DT, kOutSame, false>(nvec, rows, threads, grid);
 }
 
 }  // namespace
@@ -345,7 +375,7 @@ cudaError_t launch_layer(int dtype, bool out_i8, const LayerArgs &a, cudaStream_
     const size_t nvec = (a.cols + kRv - 1) / kRv;
     int threads = 0;
     size_t grid = 0;
-    const bool elem = !a.al_x || (a.r && !a.al_r) || (a.h && !a.al_h) || !a.al_y;
+    const bool elem = !a.al_x || (a.r && !a.al_r) || (a.w && !a.al_w) || (a.b && !a.al_b) || (a.h && !a.al_h) || !a.al_y;
     const void *k = dtype == kF16    ? pick_out<kF16>(out_i8, nvec, a.rows, elem, threads, grid)
                     : dtype == kBF16 ? pick_out<kBF16>(out_i8, nvec, a.rows, elem, threads, grid)
                                      : pick_out<kF32>(out_i8, nvec, a.rows, elem, threads, grid);

@@ -7,175 +7,183 @@
 //   dw_j = sum over rows of dy * xh,  db_j = sum over rows of dy
 //
 // Both row sums fold in one exchange, in the declared order of rowvec.cuh.
-// dw and db: CTA b of G adds its rows b, b + G, .. in order, each thread holding
-// its columns' sums in registers, and a second kernel adds the G partials: 32
+// dw and db: CTA b of G adds its rows b, b + G, .. in order, and a second kernel adds the G partials: 32
 // threads a column, thread k the partials k, k + 32, .. in order, then the
-// halving fold over the 32.  G depends on rows and cols only
-// (norm_back_groups); there are no atomics.
+// halving fold over the 32.  G depends on rows, cols and the type only
+// (layer_back_groups); there are no atomics.
 #include "kernels.cuh"
 #include "piece.cuh"
+#include "tc05.cuh"
 
 namespace tcr {
 
-// team_sum of two values at once.
-template <int T, bool ELEM>
-__device__ __forceinline__ void team_sum2(float &a, float &b, float *red, uint32_t threads)
+// A thread's column sums, at any alignment of binary32.
+template <int L>
+__device__ __forceinline__ void store_sums(float *p, uint32_t n, const float (&acc)[kRv])
 {
-    const uint32_t lane = threadIdx.x & 31;
-    float *ra = red, *rb = red + team_floats<T>();
-    if constexpr (T >= 512) {
-        float *ta = ra + T / 32 * 33, *tb = rb + T / 32 * 33;
-        const uint32_t warp = threadIdx.x >> 5, warps = threads >> 5;
-        ra[warp * 33 + lane] = a;
-        rb[warp * 33 + lane] = b;
-        __syncthreads();
-        for (uint32_t c = warp; c < 64; c += warps) {
-            const float *r = c < 32 ? ra : rb;
-            const float s = halving_lanes(lane < warps ? r[lane * 33 + (c & 31u)] : 0.0f);
-            if (lane == 0) (c < 32 ? ta : tb)[c & 31u] = s;
-        }
-        __syncthreads();
-        a = ta[lane];
-        b = tb[lane];
-    } else if constexpr (T > 32) {
-        ra[threadIdx.x] = a;
-        rb[threadIdx.x] = b;
-        __syncthreads();
-        float fa[T / 32], fb[T / 32];
-#pragma unroll
-        for (int w = 0; w < T / 32; w++) {
-            fa[w] = 32u * w < threads ? ra[32 * w + lane] : 0.0f;
-            fb[w] = 32u * w < threads ? rb[32 * w + lane] : 0.0f;
-        }
-        a = halving<T / 32>(fa);
-        b = halving<T / 32>(fb);
+    if (L == kVectors && ((uintptr_t)p & 15u) == 0) {
+        store_piece<kF32, kVectors>((uint32_t *)p, n, acc);
+        return;
     }
-    a = ELEM ? halving_lanes_elem(a) : halving_lanes(a);
-    b = ELEM ? halving_lanes_elem(b) : halving_lanes(b);
+#pragma unroll
+    for (uint32_t k = 0; k < kRv; k++)
+        if (k < n) p[value_at<L>(k)] = acc[k];
 }
 
-// g and xh of a thread's values and the trees over g and g * xh; adds dy * xh
-// and dy to the column sums.
-template <int DT, bool ELEM>
-__device__ __forceinline__ void back_values(const float *w, float mean, float rstd, uint32_t cols, uint32_t v,
-                                            float (&xh)[kRv], float (&g)[kRv], float *accw, float *accb, float &sa,
-                                            float &sc)
+// xh from h.
+__device__ __forceinline__ void normalise(float mean, float rstd, float (&xh)[kRv])
 {
-#pragma unroll
-    for (int k = 0; k < kRv; k++) xh[k] = __fmul_rn(__fsub_rn(xh[k], mean), rstd);
-    zero_absent<ELEM>(cols, v, xh);
+    add8(xh, xh, -mean);
+    mul8(xh, xh, rstd);
+}
+
+// The trees over g and g * xh of n values: absent ones count as 0 whatever was
+// read in their place and whatever mean and rstd are.
+template <int L>
+__device__ __forceinline__ void row_trees(uint32_t n, float (&xh)[kRv], float (&g)[kRv], float &sa, float &sc)
+{
+    zero_absent(n, xh);
+    zero_absent(n, g);
     float e[kRv];
-#pragma unroll
-    for (int k = 0; k < kRv; k++) {
-        if (accw) {
-            accw[k] = __fadd_rn(accw[k], __fmul_rn(g[k], xh[k]));
-            accb[k] = __fadd_rn(accb[k], g[k]);
-        }
-        if (w) g[k] = __fmul_rn(g[k], w[k]);
-        e[k] = __fmul_rn(g[k], xh[k]);
-    }
-    sa = piece_tree<ELEM>(g);
-    sc = piece_tree<ELEM>(e);
+    mul8(e, g, xh);
+    sa = piece_tree<L>(g);
+    sc = piece_tree<L>(e);
 }
 
-__device__ __forceinline__ void back_dr(float rstd, float a, float c, const float (&xh)[kRv], float (&g)[kRv])
+// rstd * ((g - a) - xh * c), over g; xh is lost.
+__device__ __forceinline__ void back_dr(float rstd, float a, float c, float (&xh)[kRv], float (&g)[kRv])
 {
-#pragma unroll
-    for (int k = 0; k < kRv; k++) g[k] = __fmul_rn(rstd, __fsub_rn(__fsub_rn(g[k], a), __fmul_rn(xh[k], c)));
+    add8(g, g, -a);
+    mul8(xh, xh, -c);
+    add8(g, g, xh);
+    mul8(g, g, rstd);
 }
 
-// partial[b * cols + j]: the sum of column j over the rows b, b + G, ..
-template <bool ELEM>
-__device__ __forceinline__ void store_sums(float *partial, size_t b, uint32_t cols, uint32_t v, const float (&acc)[kRv])
+// The thread's sums of eight columns in shared memory, `step` float4 apart.
+__device__ __forceinline__ void add_sums(float4 *p, uint32_t step, const float (&e)[kRv])
 {
-    if (!partial) return;
-    store_piece_values_any<ELEM>(partial + b * cols, cols, v, acc);
+    const float4 u = p[0], v = p[step];
+    float f[kRv] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+    add8(f, f, e);
+    p[0] = make_float4(f[0], f[1], f[2], f[3]);
+    p[step] = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Rows of at most T NV vectors, NV pieces a thread; NV = 1: a CTA of 32
-// ceil(vectors / 32) <= T threads.  The next row's inputs are loaded before
-// the current row's sums are waited for.
-template <int DT, bool ELEM, int T, int NV, int MINB>
-__global__ void __launch_bounds__(T, MINB)
-layer_back_kernel(const LayerBackArgs a)
+// The rows of one CTA, NV pieces a thread, of which the first LEAD are whole;
+// ALL: there are a weight and a dh.
+template <int DT, bool ELEM, int T, int NV, int LEAD, bool ALL>
+__device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Drop &drop, float4 *sums, float *red)
 {
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    __shared__ float red[2][2 * team_floats<T>()];
     using E = typename Elem<DT>::T;
+    constexpr int L = layout_of<DT, ELEM>();
+    constexpr uint32_t kStep = kRv * T;
     const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
-    const bool has_w = a.w != nullptr, has_dh = a.dh != nullptr;
-    const DropArgs drop = drop_resolve(a.drop);
-    Piece<DT, ELEM> dy[NV], h[NV], dh[NV], w[NV];
-    float accw[NV][kRv], accb[NV][kRv];
-    auto load = [&](size_t r) {
-#pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const uint32_t v = t + i * T;
-            load_piece<DT, ELEM>((const E *)a.dy + r * a.lddy, cols, v, dy[i]);
-            load_piece<DT, ELEM>((const E *)a.h + r * a.ldh, cols, v, h[i]);
-            if (has_dh) load_piece<DT, ELEM>((const E *)a.dh + r * a.lddh, cols, v, dh[i]);
-        }
-    };
-#pragma unroll
-    for (int i = 0; i < NV; i++) {
-        if (has_w) load_weight_piece<DT, ELEM>((const E *)a.w, cols, t + i * T, a.al_w, w[i]);
-#pragma unroll
-        for (int k = 0; k < kRv; k++) accw[i][k] = accb[i][k] = 0.0f;
-    }
-    load(blockIdx.x);
-    float mean = a.mean[blockIdx.x], rstd = a.rstd[blockIdx.x];
+    const bool has_w = ALL || a.w != nullptr, has_dh = ALL || a.dh != nullptr;
+    const uint32_t at = piece_offset<L>(t);
+    auto count = [&](int i) { return piece_count<L, T, LEAD>(cols, at, i); };
     int buf = 0;
     for (size_t r = blockIdx.x; r < a.rows; r += gridDim.x, buf ^= 1) {
-        float sa[NV], sc[NV], xh[NV][kRv], g[NV][kRv];
-        Piece<DT, ELEM> dh_now[NV];
+        Piece<DT> dy[NV], h[NV], dh[NV];
+        const E *pdy = (const E *)a.dy + r * a.lddy + at, *ph = (const E *)a.h + r * a.ldh + at;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const uint32_t v = t + i * T;
-            float f[kRv];
-            piece_values<DT, ELEM>(h[i], (const E *)a.h + r * a.ldh, cols, v, xh[i]);
-            piece_values<DT, ELEM>(dy[i], (const E *)a.dy + r * a.lddy, cols, v, g[i]);
-            if (has_w) piece_values<DT, ELEM>(w[i], (const E *)a.w, cols, v, f);
-            back_values<DT, ELEM>(has_w ? f : nullptr, mean, rstd, cols, v, xh[i], g[i], accw[i], accb[i], sa[i],
-                                  sc[i]);
-            dh_now[i] = dh[i];
+            const uint32_t n = count(i);
+            load_piece<DT, L>(pdy + i * kStep, n, dy[i], by_words(pdy));
+            load_piece<DT, L>(ph + i * kStep, n, h[i], by_words(ph));
         }
-        const size_t next = r + gridDim.x;
-        const float rstd_now = rstd;
-        if (next < a.rows) {
-            load(next);
-            mean = a.mean[next];
-            rstd = a.rstd[next];
+        if (has_dh) {
+            const E *pdh = (const E *)a.dh + r * a.lddh + at;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                load_piece<DT, L>(pdh + i * kStep, count(i), dh[i], by_words(pdh));
+        }
+        const float mean = a.mean[r], rstd = a.rstd[r];
+        float sa[NV], sc[NV];
+        auto weigh = [&](int i, float (&g)[kRv]) {
+            Piece<DT> w;
+            float f[kRv];
+            load_piece<DT, L>((const E *)a.w + at + i * kStep, count(i), w, by_words(a.w));
+            piece_values<DT>(w, f);
+            mul8(g, g, f);
+        };
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            float xh[kRv], g[kRv];
+            piece_values<DT>(h[i], xh);
+            piece_values<DT>(dy[i], g);
+            normalise(mean, rstd, xh);
+            float e[kRv];
+            mul8(e, g, xh);
+            add_sums(sums + 4 * i * T + t, T, e);
+            add_sums(sums + (4 * i + 2) * T + t, T, g);
+            if (has_w) weigh(i, g);
+            row_trees<L>(count(i), xh, g, sa[i], sc[i]);
         }
         // two buffers: a thread reaches the next row's write of this one only
         // after every thread has passed the barrier of the row between
-        float ma = halving<NV>(sa), mc = halving<NV>(sc);
-        team_sum2<T, ELEM>(ma, mc, red[buf], blockDim.x);
-        ma = __fdiv_rn(ma, (float)cols);
-        mc = __fdiv_rn(mc, (float)cols);
+        float m[2] = {halving<NV>(sa), halving<NV>(sc)};
+        team_sums<T, L>(m, red + buf * 2 * T);
+        const float ma = __fdiv_rn(m[0], (float)cols), mc = __fdiv_rn(m[1], (float)cols);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const uint32_t v = t + i * T;
-            if (kRv * (v & ~31u) >= cols) continue;          // whole warps: stores are warp-wide
-            back_dr(rstd_now, ma, mc, xh[i], g[i]);
+            const uint32_t n = count(i);
+            float xh[kRv], g[kRv];
+            piece_values<DT>(h[i], xh);
+            piece_values<DT>(dy[i], g);
+            normalise(mean, rstd, xh);
+            if (has_w) weigh(i, g);
+            back_dr(rstd, ma, mc, xh, g);
             if (has_dh) {
                 float d[kRv];
-                piece_values<DT, ELEM>(dh_now[i], (const E *)a.dh + r * a.lddh, cols, v, d);
-#pragma unroll
-                for (int k = 0; k < kRv; k++) g[i][k] = __fadd_rn(g[i][k], d[k]);
+                piece_values<DT>(dh[i], d);
+                add8(g, g, d);
             }
-            if (a.dr) store_piece_values<DT, ELEM>((E *)a.dr + r * a.lddr, cols, v, g[i]);
+            if (a.dr) {
+                E *p = (E *)a.dr + r * a.lddr + at + i * kStep;
+                store_piece<DT, L>(p, n, g, by_words(p));
+            }
             if (a.dx) {
-                drop_values<ELEM>(drop, v, r, g[i]);
-                store_piece_values<DT, ELEM>((E *)a.dx + r * a.lddx, cols, v, g[i]);
+                E *p = (E *)a.dx + r * a.lddx + at + i * kStep;
+                drop_values<L>(drop, t + i * T, r, g);
+                store_piece<DT, L>(p, n, g, by_words(p));
             }
         }
     }
+}
+
+// Rows of at most T NV vectors, NV pieces a thread.  A CTA walks the rows b, b +
+// G, .. and keeps its sums of dw and db in shared memory, thread by thread, so
+// that registers hold one row's inputs as they were read (g and xh are formed
+// again after the barrier) and 1024 threads (binary32: 768) fit an SM: their
+// rows are at different steps, and none is loaded ahead.  16384 x 4096 bfloat16
+// with dropout, both gradients and sums 118 us; with the sums in registers and
+// the next row loaded ahead, two CTAs of 256 threads an SM, 163.
+template <int DT, bool ELEM, int T, int NV, int LEAD, int MINB>
+__global__ void __launch_bounds__(T, MINB)
+layer_back_kernel(const __grid_constant__ LayerBackArgs a)
+{
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    extern __shared__ float4 sums[];                     // [4 NV][T]: a piece's dw, then its db
+    __shared__ float red[4 * T];
+    constexpr int L = layout_of<DT, ELEM>();
+    const uint32_t t = threadIdx.x, cols = (uint32_t)a.cols;
+    const Drop drop(a.drop);
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const uint32_t v = t + i * T;
-        store_sums<ELEM>(a.partial_w, blockIdx.x, cols, v, accw[i]);
-        store_sums<ELEM>(a.partial_b, blockIdx.x, cols, v, accb[i]);
+    for (int i = 0; i < 4 * NV; i++) sums[i * T + t] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (warp_whole<T, NV>(cols, t) && a.w && a.dh)
+        layer_back_rows<DT, ELEM, T, NV, NV, true>(a, drop, sums, red);
+    else
+        layer_back_rows<DT, ELEM, T, NV, LEAD, false>(a, drop, sums, red);
+    // partial[b * cols + j]: the sum of column j over the rows b, b + G, ..
+#pragma unroll
+    for (int i = 0; i < 2 * NV; i++) {
+        float *to = i % 2 ? a.partial_b : a.partial_w;
+        if (!to) continue;
+        const uint32_t first = piece_offset<L>(t) + (uint32_t)(i / 2 * kRv * T);
+        const float4 u = sums[2 * i * T + t], v = sums[(2 * i + 1) * T + t];
+        const float f[kRv] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+        store_sums<L>(to + (size_t)blockIdx.x * cols + first, piece_count<L>(cols, first), f);
     }
 }
 
@@ -194,12 +202,12 @@ __device__ __forceinline__ void load_back(const LayerBackArgs &a, size_t r, uint
 
 template <int DT>
 __global__ void __launch_bounds__(kRowLongT)
-layer_back_sums_kernel(const LayerBackArgs a, float *sums)
+layer_back_sums_kernel(const __grid_constant__ LayerBackArgs a, float *sums)
 {
     constexpr uint32_t T = kRowLongT;
     pdl_launch_dependents();
     pdl_wait_primary();
-    __shared__ float red[2 * team_floats<T>()];
+    __shared__ float red[2 * T];
     const size_t r = blockIdx.x;
     const uint32_t cols = (uint32_t)a.cols, nvec = (cols + kRv - 1) / kRv, steps = (nvec + T - 1) / T;
     const int bits = ceil_log2_sz(steps);
@@ -211,36 +219,43 @@ layer_back_sums_kernel(const LayerBackArgs a, float *sums)
         if (v < nvec) {
             float xh[kRv], g[kRv], w[kRv];
             load_back<DT>(a, r, v, xh, g, w);
-            back_values<DT, false>(a.w ? w : nullptr, mean, rstd, cols, v, xh, g, nullptr, nullptr, sa, sc);
+            normalise(mean, rstd, xh);
+            if (a.w) mul8(g, g, w);
+            row_trees<kVectors>(vec_left(cols, v), xh, g, sa, sc);
         }
         ta.push(sa);
         tc.push(sc);
     }
-    float ma = ta.finish(), mc = tc.finish();
-    team_sum2<(int)T, false>(ma, mc, red, T);
+    float m[2] = {ta.finish(), tc.finish()};
+    team_sums<(int)T, kVectors>(m, red);
     if (threadIdx.x == 0) {
-        sums[2 * r] = __fdiv_rn(ma, (float)cols);
-        sums[2 * r + 1] = __fdiv_rn(mc, (float)cols);
+        sums[2 * r] = __fdiv_rn(m[0], (float)cols);
+        sums[2 * r + 1] = __fdiv_rn(m[1], (float)cols);
     }
 }
 
 template <int DT>
 __global__ void __launch_bounds__(256)
-layer_back_long_kernel(const LayerBackArgs a, const float *sums)
+layer_back_long_kernel(const __grid_constant__ LayerBackArgs a, const float *sums)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
     using E = typename Elem<DT>::T;
     const uint32_t v = blockIdx.x * 256 + threadIdx.x, cols = (uint32_t)a.cols;
-    const DropArgs drop = drop_resolve(a.drop);
+    const Drop drop(a.drop);
+    const uint32_t left = vec_left(cols, v);
     float accw[kRv], accb[kRv];
 #pragma unroll
     for (int k = 0; k < kRv; k++) accw[k] = accb[k] = 0.0f;
     for (size_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         const float rstd = a.rstd[r];
-        float xh[kRv], g[kRv], w[kRv], sa, sc;
+        float xh[kRv], g[kRv], w[kRv], e[kRv];
         load_back<DT>(a, r, v, xh, g, w);
-        back_values<DT, false>(a.w ? w : nullptr, a.mean[r], rstd, cols, v, xh, g, accw, accb, sa, sc);
+        normalise(a.mean[r], rstd, xh);
+        mul8(e, g, xh);
+        add8(accw, accw, e);
+        add8(accb, accb, g);
+        if (a.w) mul8(g, g, w);
         back_dr(rstd, sums[2 * r], sums[2 * r + 1], xh, g);
         if (a.dh) {
             float d[kRv];
@@ -250,12 +265,13 @@ layer_back_long_kernel(const LayerBackArgs a, const float *sums)
         }
         if (a.dr) store_vec<DT>((E *)a.dr + r * a.lddr, cols, v, a.al_dr, g);
         if (a.dx) {
-            drop_values<false>(drop, v, r, g);
+            drop_values<kVectors>(drop, v, r, g);
             store_vec<DT>((E *)a.dx + r * a.lddx, cols, v, a.al_dx, g);
         }
     }
-    store_sums<false>(a.partial_w, blockIdx.y, cols, v, accw);
-    store_sums<false>(a.partial_b, blockIdx.y, cols, v, accb);
+    const size_t to = (size_t)blockIdx.y * cols + kRv * v;
+    if (a.partial_w) store_sums<kVectors>(a.partial_w + to, left, accw);
+    if (a.partial_b) store_sums<kVectors>(a.partial_b + to, left, accb);
 }
 
 // dw[j] (block y = 0) and db[j] (1) from the G partials of column j.
@@ -284,44 +300,59 @@ layer_sums_kernel(const float *partial_w, const float *partial_b, size_t cols, i
 
 // ---------------------------------------------------------------- host
 
-static size_t sums_floats(size_t rows, size_t cols)
+// CTAs an SM of layer_back_kernel at a row length: what registers and shared
+// memory hold of the shapes below.
+static int back_ctas(size_t nvec, int dtype)
 {
-    return (cols + kRv - 1) / kRv > kBackMaxVecs ? 2 * rows : 0;
+    if (dtype == kF32) return nvec <= 128 ? 12 : nvec <= 256 ? 6 : nvec <= 512 ? 3 : nvec <= 768 ? 2 : 1;
+    return nvec <= 128 ? 16 : nvec <= 256 ? 8 : nvec <= 512 ? 4 : 2;
 }
 
-size_t layer_back_scratch(size_t rows, size_t cols, bool dweight, bool dbias)
+// As many CTAs as fit the SMs, but (above one an SM) no more than half the rows: a
+// partial costs as much traffic as a row (1001 x 1537 binary32 12.4 us, with a
+// quarter of the rows 16.3, with all of them 12.3).
+int layer_back_groups(size_t rows, size_t cols, int dtype)
 {
-    const size_t part = (size_t)norm_back_groups(rows, cols) * cols;
-    return ((dweight ? part : 0) + (dbias ? part : 0) + sums_floats(rows, cols)) * sizeof(float);
+    const size_t full = (size_t)152 * back_ctas((cols + kRv - 1) / kRv, dtype);
+    const size_t half = (rows + 1) / 2 > 152 ? (rows + 1) / 2 : 152;
+    const size_t g = full < half ? full : half;
+    return (int)(rows < g ? rows : g);
+}
+
+size_t layer_back_scratch(size_t rows, size_t cols, int dtype, bool dweight, bool dbias)
+{
+    const size_t part = (size_t)layer_back_groups(rows, cols, dtype) * cols;
+    const size_t sums = (cols + kRv - 1) / kRv > kBackMaxVecs ? 2 * rows : 0;
+    return ((dweight ? part : 0) + (dbias ? part : 0) + sums) * sizeof(float);
 }
 
 namespace {
 
-template <int DT>
-const void *pick(size_t nvec, bool elem, unsigned &threads)
+template <int DT, bool ELEM>
+const void *pick(size_t nvec, unsigned &threads, size_t &smem)
 {
-#define TCR_BACK(ELEM_, T_, NV_, MINB_) \
-    return (threads = NV_ == 1 ? (unsigned)((nvec + 31) / 32 * 32) : T_, \
-            (const void *)layer_back_kernel<DT, ELEM_, T_, NV_, MINB_>)
-    if (elem) {
-        if (nvec <= 64) TCR_BACK(true, 64, 1, 8);
-        if (nvec <= 128) TCR_BACK(true, 128, 1, 4);
-        if (nvec <= 256) TCR_BACK(true, 256, 1, 2);
-        if (nvec <= 512) TCR_BACK(true, 512, 1, 1);
-        TCR_BACK(true, 1024, 1, 1);
-    }
+#define TCR_BACK(T_, NV_, MINB_)                     \
+    return (threads = T_, smem = (size_t)T_ * NV_ * 64, \
+            (const void *)layer_back_kernel<DT, ELEM, T_, NV_, NV_ - 1, MINB_>)
+    // The fastest of those measured (bfloat16, with dropout): 16384 x 4096 256 x 2
+    // in 120 us, 128 x 4 in 121; 20000 x 2560 128 x 3 with 4 CTAs an SM in 118,
+    // with 6 (spills) 134, 256 x 2 178; 10000 x 5120 256 x 3 with 2 in 121, with 3
+    // in 140; 8192 x 8192 512 x 2 in 127, 256 x 4 in 129.
     if constexpr (DT == kF32) {
-        if (nvec <= 64) TCR_BACK(false, 64, 1, 8);
-        if (nvec <= 128) TCR_BACK(false, 128, 1, 4);
-        if (nvec <= 256) TCR_BACK(false, 256, 1, 2);
-        if (nvec <= 512) TCR_BACK(false, 512, 1, 1);
-        TCR_BACK(false, 1024, 1, 1);
+        if (nvec <= 64) TCR_BACK(64, 1, 12);
+        if (nvec <= 128) TCR_BACK(64, 2, 12);
+        if (nvec <= 256) TCR_BACK(128, 2, 6);
+        if (nvec <= 512) TCR_BACK(256, 2, 3);
+        if (nvec <= 768) TCR_BACK(256, 3, 2);
+        TCR_BACK(512, 2, 1);
     } else {
-        if (nvec <= 64) TCR_BACK(false, 64, 1, 12);
-        if (nvec <= 128) TCR_BACK(false, 128, 1, 6);
-        if (nvec <= 256) TCR_BACK(false, 256, 1, 3);
-        if (nvec <= 512) TCR_BACK(false, 512, 1, 1);
-        TCR_BACK(false, 512, 2, 1);
+        if (nvec <= 64) TCR_BACK(64, 1, 16);
+        if (nvec <= 128) TCR_BACK(64, 2, 16);
+        if (nvec <= 256) TCR_BACK(128, 2, 8);
+        if (nvec <= 384) TCR_BACK(128, 3, 4);
+        if (nvec <= 512) TCR_BACK(256, 2, 4);
+        if (nvec <= 768) TCR_BACK(256, 3, 2);
+        TCR_BACK(512, 2, 2);
     }
 #undef TCR_BACK
 }
@@ -333,9 +364,19 @@ cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream
     if (nvec <= kBackMaxVecs) {
         void *args[] = {(void *)&a};
         unsigned threads = 0;
-        const bool elem = !a.al_dy || !a.al_h || (a.dh && !a.al_dh) || (a.dx && !a.al_dx) || (a.dr && !a.al_dr);
-        const void *k = pick<DT>(nvec, elem, threads);
-        return launch_first(k, dim3((unsigned)G), dim3(threads), args, 0, stream);
+        size_t smem = 0;
+        const bool elem = !a.al_dy || !a.al_h || (a.w && !a.al_w) || (a.dh && !a.al_dh) || (a.dx && !a.al_dx) || (a.dr && !a.al_dr);
+        const void *k = elem ? pick<DT, true>(nvec, threads, smem) : pick<DT, false>(nvec, threads, smem);
+        if (smem + 16 * threads > 48 * 1024) {               // beside red
+            cudaError_t e = set_smem_once((void *)k, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
+        // A grid that fills every SM is not launched while the kernel before it
+        // finishes: where that one holds little shared memory, an SM would take
+        // its first CTAs with a small share of it and the rest in a second wave
+        // (100 calls back to back, 65536 x 1024 bfloat16: 148 us, 119 this way).
+        if (G > 2 * 152) return cudaLaunchKernel(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
+        return launch_first(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
     }
     void *args[] = {(void *)&a, (void *)&sums};
     cudaError_t e = launch_first((const void *)layer_back_sums_kernel<DT>, dim3((unsigned)a.rows), dim3(kRowLongT),
@@ -349,7 +390,7 @@ cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream
 
 cudaError_t launch_layer_back(int dtype, LayerBackArgs a, float *scratch, float *dw, float *db, cudaStream_t stream)
 {
-    int G = norm_back_groups(a.rows, a.cols);
+    int G = layer_back_groups(a.rows, a.cols, dtype);
     const size_t part = (size_t)G * a.cols;
     a.partial_w = dw ? scratch : nullptr;
     a.partial_b = db ? scratch + (dw ? part : 0) : nullptr;

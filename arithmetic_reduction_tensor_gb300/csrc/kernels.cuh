@@ -237,10 +237,12 @@ cudaError_t launch_norm_back(int dtype, BackArgs a, float *scratch, float *dw, c
 // (k_layer_back.cu): as the row operators above, rows of more than
 // kBackMaxVecs vectors of 8 in the gradient with one more launch and two
 // floats of scratch each.
+// (the generator's multipliers and key increments)
+constexpr uint32_t kPhiloxM0 = 0xD2511F53u, kPhiloxM1 = 0xCD9E8D57u, kPhiloxW0 = 0x9E3779B9u, kPhiloxW1 = 0xBB67AE85u;
 struct DropArgs {
     uint32_t t;                        // kept where 16 bits are at least t; 0: everything, 65536: nothing
     float s;                           // 65536 / (65536 - t), rounded; 0 at t = 65536
-    uint32_t k0, k1, c2, c3;           // seed and offset, where state is null
+    uint32_t rk[20], c2, c3;           // the seed's round keys and the offset, where state is null
     const unsigned long long *state;   // seed and offset on the device
 };
 struct LayerArgs {
@@ -268,7 +270,8 @@ struct LayerBackArgs {
     bool al_dy, al_h, al_w, al_dh, al_dx, al_dr;
     DropArgs drop;
 };
-size_t layer_back_scratch(size_t rows, size_t cols, bool dweight, bool dbias);
+int layer_back_groups(size_t rows, size_t cols, int dtype);
+size_t layer_back_scratch(size_t rows, size_t cols, int dtype, bool dweight, bool dbias);
 cudaError_t launch_layer_back(int dtype, LayerBackArgs a, float *scratch, float *dw, float *db, cudaStream_t stream);
 
 // ---- matrix product in 8-bit integers with scales (k_gemm_i8.cu)

@@ -26,8 +26,10 @@ bool drop_of(const tcr_drop *drop, DropArgs &d)
     if (!(drop->p >= 0.0 && drop->p <= 1.0) || !is_aligned(drop->state, 8)) return false;
     d.t = (uint32_t)std::nearbyint(65536.0 * drop->p);
     d.s = d.t < 65536u ? (float)(65536.0 / (65536.0 - d.t)) : 0.0f;
-    d.k0 = (uint32_t)drop->seed;
-    d.k1 = (uint32_t)(drop->seed >> 32);
+    for (uint32_t i = 0; i < 10; i++) {
+        d.rk[2 * i] = (uint32_t)drop->seed + i * kPhiloxW0;
+        d.rk[2 * i + 1] = (uint32_t)(drop->seed >> 32) + i * kPhiloxW1;
+    }
     d.c2 = (uint32_t)drop->offset;
     d.c3 = (uint32_t)(drop->offset >> 32);
     d.state = drop->state;
@@ -224,7 +226,7 @@ try {
     if (!a.dx && !a.dresidual && !a.dweight && !a.dbias) return TCR_OK;
     if (dev < 0) return TCR_ERR_CUDA;
     Scratch scratch(s);
-    tcr_status st = scratch.take(layer_back_scratch(a.rows, a.cols, a.dweight, a.dbias), dev);
+    tcr_status st = scratch.take(layer_back_scratch(a.rows, a.cols, a.dtype, a.dweight, a.dbias), dev);
     if (st != TCR_OK) return st;
     if (fault_injected("launch")) return TCR_ERR_CUDA;
     b.dy = a.dy;

@@ -690,9 +690,12 @@ TCR_API tcr_status tcr_layernorm(const tcr_layernorm_args *args, void *stream);
  *          and dresidual are the same).  dx or dresidual may be dy, h or dh
  *          itself (same pointer and ld), not each other.  dweight, dbias: cols
  *          floats; overwritten.  Their order is that of tcr_rmsnorm_backward's
- *          dweight: no atomics.
- * Takes G * cols floats of pool scratch (G as there) for each of dweight and
- * dbias that is wanted, and 2 rows more for cols > 8192.
+ *          dweight (no atomics) with another G: min(rows, max(152, min(152 c,
+ *          ceil(rows / 2)))), where c is, for up to 1024, 2048, 4096 and more
+ *          columns, 16, 8, 4 and 2, and of binary32 12, 6, 3 and (up to 6144) 2
+ *          and 1.
+ * Takes G * cols floats of pool scratch for each of dweight and dbias that is
+ * wanted, and 2 rows more for cols > 8192.
  * rows == 0 writes dweight = dbias = +0.0.
  */
 typedef struct {

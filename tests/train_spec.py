@@ -4,7 +4,7 @@ the cross entropy in binary64."""
 import numpy as np
 import torch
 
-from tests.rows_spec import F32, groups, row_sums
+from tests.rows_spec import F32, row_sums
 
 
 def philox(c, k):
@@ -67,10 +67,18 @@ def layer(x, r, w, b, eps, drop=None):
     return h, mean, rstd, y
 
 
-def column_sums(e):
+def groups(rows, cols, dtype):
+    """The partial sums of the gradients of weight and bias."""
+    c = [(1024, 12), (2048, 6), (4096, 3), (6144, 2), (1 << 27, 1)] if dtype == torch.float32 else \
+        [(1024, 16), (2048, 8), (4096, 4), (1 << 27, 2)]
+    c = next(n for most, n in c if cols <= most)
+    return min(rows, max(152, min(152 * c, -(-rows // 2))))
+
+
+def column_sums(e, dtype):
     """The declared order of the gradients of weight and bias."""
     rows, cols = e.shape
-    G = groups(rows, cols)
+    G = groups(rows, cols, dtype)
     part = torch.zeros(G, cols)
     for r in range(rows):
         part[r % G] = part[r % G] + e[r]
@@ -94,7 +102,7 @@ def layer_back(dy, h, w, mean, rstd, dh, drop=None):
     dr = rstd[:, None] * ((g - a[:, None]) - xh * c[:, None])
     if dh is not None:
         dr = dr + dh.float()
-    return dropped(dr, drop), dr, column_sums(dyf * xh), column_sums(dyf)
+    return dropped(dr, drop), dr, column_sums(dyf * xh, dy.dtype), column_sums(dyf, dy.dtype)
 
 
 def layer64(x, r, w, b, eps, drop=None):
