@@ -22,7 +22,19 @@
 // 64 k, as the descriptor and the instruction say; so no matrix is transposed.
 //
 // Roles, barriers, time limits as in gemm_splitk_pair_kernel (k_gemm.cu): a
-// producer thread, an MMA thread, four epilogue warps, two accumulators.
+// producer thread, an MMA thread, two accumulators; eight epilogue warps, each 32
+// rows and 128 columns of the CTA's 128 x 256.
+//
+// The tensor cores' sums lose their last bits at every step, all in the same
+// direction, so the forward pass, whose results are binary32, takes K in chains
+// of 1024 and adds the chains in registers (4096 columns: the loss' error
+// against binary64 1.4e-6 in one chain, 4e-7 so; the time is the same).  P, dX
+// and dW are rounded to 16 bits anyway.
+//
+// What the gradient's tiles write (P, dX's sums, dW) leaves by tensor-map
+// stores from shared memory, dX's later pieces as additions in L2: threads that
+// store a row each keep the memory pipe from the MMAs' operands (tensor cores
+// busy 71% of the time instead of 84).
 #include "pair.cuh"
 #include "rowvec.cuh"
 #include "xent.h"
@@ -34,18 +46,27 @@ constexpr int kXBoxBytes = kXBox * kXBox * 2;      // 8 KiB
 constexpr int kXHalf = 128;                        // rows of an operand per CTA
 constexpr int kXHalfBytes = 2 * kXBoxBytes;
 constexpr int kXStageBytes = 2 * kXHalfBytes;      // 32 KiB: both operands
-constexpr int kXStages = 7;
+constexpr int kXChain = 16;                        // boxes of K the forward pass adds up in one chain
 constexpr int kXDBuffers = 2;
 constexpr uint32_t kXTmemCols = kXDBuffers * kXentTile;
-constexpr int kXThreads = 192;
-constexpr int kXEpilogueThreads = 128;
+constexpr int kXEpilogueWarps = 8;
+constexpr int kXThreads = 64 + 32 * kXEpilogueWarps;
 constexpr int kXGroup = 8;                         // tile rows per raster group (L2 reuse)
-constexpr int kXOffBars = kXStages * kXStageBytes;
-// barriers: full[S] (leader's: both CTAs' copies), empty[S], dfull[D], dempty[D] (leader's), drain
-constexpr int kXNumBars = 2 * kXStages + 2 * kXDBuffers + 1;
-constexpr int kXOffMisc = kXOffBars + 8 * kXNumBars;
-constexpr int kXSmemBytes = kXOffMisc + 64 + 1024;
-static_assert(kXSmemBytes <= 232448, "one SM's 227 KiB");
+constexpr int kXCols = kXentTile / 2;              // columns of an epilogue warp
+constexpr int kXOutBytes = 32 * 128;               // its staging: 32 rows of 128 swizzled bytes
+// The ring, the staging (not in the forward pass, whose ring is longer for it)
+// and the barriers: full[S] (leader's: both CTAs' copies), empty[S], dfull[D],
+// dempty[D] (leader's), drain.
+template <int MODE>
+struct XLayout {
+    static constexpr int kStages = MODE == kXentForward ? 7 : 6;
+    static constexpr int kOffOut = kStages * kXStageBytes;
+    static constexpr int kOffBars = kOffOut + (MODE == kXentForward ? 0 : kXEpilogueWarps * kXOutBytes);
+    static constexpr int kNumBars = 2 * kStages + 2 * kXDBuffers + 1;
+    static constexpr int kOffMisc = kOffBars + 8 * kNumBars;
+    static constexpr int kSmemBytes = kOffMisc + 64 + 1024;
+    static_assert(kSmemBytes <= 232448, "one SM's 227 KiB");
+};
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
@@ -61,6 +82,21 @@ __device__ __forceinline__ float ex2(float x)
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// 16 consecutive fp32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tc_ld_row16(uint32_t taddr, float (&v)[16])
+{
+    uint32_t r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int j = 0; j < 16; j++) v[j] = __uint_as_float(r[j]);
 }
 
 // The operand of 128 rows (or MN elements) at `addr`, two boxes: K-major (8-row
@@ -170,59 +206,83 @@ struct XUnits {
 
 // ---------------------------------------------------------------- epilogues
 //
-// Thread m of CTA r has row 128 r + m of the tile; `ld(c, v)` gives columns
-// 32 c .. 32 c + 31 of it.
+// A lane has one row of the tile and its warp's 128 columns of it; `ld(c, v)`
+// gives the columns 32 c .. 32 c + 31 of these.  Every lane of the warp calls
+// ld and the stores.
 
-// The largest logit of the row in this tile and the sum about it.
-template <class Ld>
-__device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int tn, Ld ld)
+// The largest logit of the row among the warp's columns and the sum about it.
+__device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int part, float (&v)[kXCols])
 {
-    const int col0 = tn * kXentTile;
+    const int col0 = part * kXCols, left = g.V - col0;
     const int at = g.lab[row] - col0;
-    float mx = -INFINITY, s = 0.0f, hit = 0.0f;
-#pragma unroll 1
-    for (int c = 0; c < kXentTile / 32; c++) {
-        const int left = g.V - (col0 + 32 * c);
-        float v[32];
-        ld(c, v);
-        if (left <= 0) continue;
-        if (left < 32) {
+    if (left < kXCols) {
 #pragma unroll
-            for (int j = 0; j < 32; j++)
-                if (j >= left) v[j] = -INFINITY;
-        }
-        float m[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-        for (int j = 4; j < 32; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
-        const float now = fmaxf(mx, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
-        const float about = now == -INFINITY ? 0.0f : -__fmul_rn(now, kLog2e);
-        float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < 32; j++) e[j & 3] = __fadd_rn(e[j & 3], ex2(__fmaf_rn(v[j], kLog2e, about)));
-        s = __fmaf_rn(s, ex2(__fmaf_rn(mx, kLog2e, about)),
-                      __fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])));
-        mx = now;
-        if (at >= 32 * c && at < 32 * c + 32) {
-#pragma unroll
-            for (int j = 0; j < 32; j++)
-                if (at == 32 * c + j) hit = v[j];
-        }
+        for (int j = 0; j < kXCols; j++)
+            if (j >= left) v[j] = -INFINITY;
     }
-    g.part[(size_t)tn * g.tpad + row] = make_float2(mx, s);
-    if (at >= 0 && at < kXentTile) g.hit[row] = hit;
+    float hit = 0.0f;
+    if (at >= 0 && at < kXCols) {
+#pragma unroll
+        for (int j = 0; j < kXCols; j++)
+            if (j == at) hit = v[j];
+    }
+    float m[4] = {v[0], v[1], v[2], v[3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 4; j < kXCols; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
+    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    const float about = mx == -INFINITY ? 0.0f : -__fmul_rn(mx, kLog2e);
+#pragma unroll
+    for (int j = 0; j < kXCols; j++) e[j & 3] = __fadd_rn(e[j & 3], ex2(__fmaf_rn(v[j], kLog2e, about)));
+    const float s = __fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3]));
+    g.part[(size_t)part * g.tpad + row] = make_float2(mx, s);
+    if (at >= 0 && at < kXCols) g.hit[row] = hit;
 }
+
+// A warp's staging: 32 rows of 128 bytes, 16-byte granule k of row r at granule k ^
+// (r % 8), as a tensor map with 128-byte swizzle reads them.
+struct XOut {
+    uint8_t *smem;
+    uint32_t addr;
+    __device__ __forceinline__ void ready() const        // the last store has read it
+    {
+        if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+    }
+    __device__ __forceinline__ void put(int k, uint32_t a, uint32_t b, uint32_t c, uint32_t d) const
+    {
+        const uint32_t r = threadIdx.x & 31;
+        *reinterpret_cast<uint4 *>(smem + 128 * r + 16 * ((uint32_t)k ^ (r & 7u))) = make_uint4(a, b, c, d);
+    }
+    // Store the box at column c0, row c1 of the map's matrix.
+    template <bool ADD>
+    __device__ __forceinline__ void send(const CUtensorMap *map, int c0, int c1) const
+    {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if ((threadIdx.x & 31) != 0) return;
+        if constexpr (ADD)
+            asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];"
+                         ::"l"((uint64_t)map), "r"(c0), "r"(c1), "r"(addr)
+                         : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                         ::"l"((uint64_t)map), "r"(c0), "r"(c1), "r"(addr)
+                         : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+};
 
 // P of the row: (exp(l - lse) - [target]) * g, in units of the largest |g| so
 // that the target's -1 times a common g is exact (binary16: times 2^15 on top,
 // which keeps probabilities of 2^-29 normal).
 template <int DT, class Ld>
-__device__ __forceinline__ void epilogue_gradient(const XentGemm &g, size_t row, int n, int tn, Ld ld)
+__device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
+                                                  int n, int col0, Ld ld)
 {
-    const int col0 = tn * kXentTile;                     // within the piece
+    const int row = row0 + (threadIdx.x & 31);
     float about = 0.0f, gq = 0.0f;
     int at = -1;
-    const bool live = row < (size_t)n;
-    if (live) {
+    if (row < n) {
         const int tok = g.tok[row], lab = g.lab[row];
         const float gmax = __uint_as_float(g.head[1]);
         about = -__fmul_rn(g.lse[tok], kLog2e);
@@ -232,86 +292,102 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, size_t row,
         if (lab < 0) gq = __int_as_float(0x7fc00000);    // no such entry
         at = lab - g.v0 - col0;
     }
-    uint16_t *out = g.P + row * g.ldp + col0;
+    const int left = gq == 0.0f ? 0 : g.vn - col0;
 #pragma unroll 1
-    for (int c = 0; c < kXentTile / 32; c++) {
-        float v[32];
-        ld(c, v);
-        const int left = g.vn - (col0 + 32 * c);
-        uint32_t o[16];
+    for (int c = 0; c < kXCols / 64; c++) {
+        uint32_t o[32];
 #pragma unroll
-        for (int j = 0; j < 32; j++) {
-            float p = ex2(__fmaf_rn(v[j], kLog2e, about));
-            if (at == 32 * c + j) p = __fsub_rn(p, 1.0f);
-            v[j] = gq == 0.0f || j >= left ? 0.0f : __fmul_rn(p, gq);
+        for (int h = 0; h < 2; h++) {
+            float v[32];
+            ld(2 * c + h, v);
+#pragma unroll
+            for (int j = 0; j < 32; j++) {
+                float p = ex2(__fmaf_rn(v[j], kLog2e, about));
+                if (at == 64 * c + 32 * h + j) p = __fsub_rn(p, 1.0f);
+                v[j] = 64 * c + 32 * h + j < left ? __fmul_rn(p, gq) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; j++) o[16 * h + j] = float2_to_word<DT>(v[2 * j], v[2 * j + 1]);
         }
+        out.ready();
 #pragma unroll
-        for (int j = 0; j < 16; j++) o[j] = float2_to_word<DT>(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            *reinterpret_cast<uint4 *>(out + 32 * c + 8 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        for (int k = 0; k < 8; k++) out.put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        out.send<false>(map, col0 + 64 * c, row0);
     }
 }
 
 // A split's sums of dX, added to those of the pieces before.
 template <class Ld>
-__device__ __forceinline__ void epilogue_dx(const XentGemm &g, size_t row, int split, int tn, Ld ld)
+__device__ __forceinline__ void epilogue_dx(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
+                                            int split, int col0, Ld ld)
 {
-    const size_t col0 = (size_t)tn * kXentTile;
-    float *out = g.ws + (size_t)split * g.tpad * g.ldws + row * g.ldws + col0;
 #pragma unroll 1
-    for (int c = 0; c < kXentTile / 32; c++) {
-        if (col0 + 32 * c >= g.ldws) {
-            float v[32];
-            ld(c, v);
-            continue;
-        }
-        float4 before[8];
-        if (!g.first) {
-#pragma unroll
-            for (int j = 0; j < 8; j++) before[j] = *reinterpret_cast<const float4 *>(out + 32 * c + 4 * j);
-        }
+    for (int c = 0; c < kXCols / 32; c++) {
         float v[32];
         ld(c, v);
+        if ((size_t)(col0 + 32 * c) >= g.ldws) continue;
+        out.ready();
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            float4 f = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (!g.first)
-                f = make_float4(__fadd_rn(before[j].x, f.x), __fadd_rn(before[j].y, f.y), __fadd_rn(before[j].z, f.z),
-                                __fadd_rn(before[j].w, f.w));
-            *reinterpret_cast<float4 *>(out + 32 * c + 4 * j) = f;
-        }
+        for (int k = 0; k < 8; k++)
+            out.put(k, __float_as_uint(v[4 * k]), __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                    __float_as_uint(v[4 * k + 3]));
+        const int to = split * (int)g.tpad + row0;
+        if (g.first)
+            out.send<false>(map, col0 + 32 * c, to);
+        else
+            out.send<true>(map, col0 + 32 * c, to);
     }
 }
 
-// A row of dW, rounded.
+// Rows of dW, rounded; row0 within the piece.  Rows that no tensor map takes (not
+// 16-byte aligned) are written from the staging, 64 bytes of a row at a time.
 template <int DT, class Ld>
-__device__ __forceinline__ void epilogue_dw(const XentGemm &g, int vrow, int tn, Ld ld)
+__device__ __forceinline__ void epilogue_dw(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
+                                            int col0, Ld ld)
 {
-    const int col0 = tn * kXentTile;
+    const uint32_t lane = threadIdx.x & 31;
     float scale = __uint_as_float(g.head[1]);
     if (DT == kF16) scale = __fmul_rn(scale, 1.0f / kXentF16Scale);
-    const bool live = vrow < g.vn;
-    uint16_t *out = (uint16_t *)g.dw + (size_t)(g.v0 + vrow) * g.lddw + col0;
 #pragma unroll 1
-    for (int c = 0; c < kXentTile / 32; c++) {
-        float v[32];
-        ld(c, v);
-        const int left = g.H - (col0 + 32 * c);
-        if (!live || left <= 0) continue;
-        uint32_t o[16];
+    for (int c = 0; c < kXCols / 64; c++) {
+        uint32_t o[32];
 #pragma unroll
-        for (int j = 0; j < 16; j++) o[j] = float2_to_word<DT>(__fmul_rn(v[2 * j], scale), __fmul_rn(v[2 * j + 1], scale));
-        if (left >= 32 && g.al_dw) {
+        for (int h = 0; h < 2; h++) {
+            float v[32];
+            ld(2 * c + h, v);
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                *reinterpret_cast<uint4 *>(out + 32 * c + 8 * j) =
-                    make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; j++)
-                if (j < left) out[32 * c + j] = (uint16_t)(o[j / 2] >> (16 * (j & 1)));
+            for (int j = 0; j < 16; j++)
+                o[16 * h + j] = float2_to_word<DT>(__fmul_rn(v[2 * j], scale), __fmul_rn(v[2 * j + 1], scale));
         }
+        const int col = col0 + 64 * c, left = g.H - col;
+        if (left <= 0 || row0 >= g.vn) continue;
+        out.ready();
+#pragma unroll
+        for (int k = 0; k < 8; k++) out.put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        if (g.al_dw) {
+            out.send<false>(map, col, g.v0 + row0);
+            continue;
+        }
+        __syncwarp();
+        uint16_t *to = (uint16_t *)g.dw + (size_t)(g.v0 + row0) * g.lddw + col;
+        const int rows = min(32, g.vn - row0);
+#pragma unroll 4
+        for (int r = 0; r < rows; r++, to += g.lddw) {
+            const uint8_t *from = out.smem + 128 * r;
+            if (left >= 64 && ((uintptr_t)to & 3u) == 0u) {
+                const uint32_t at = 4 * lane;
+                reinterpret_cast<uint32_t *>(to)[lane] =
+                    *reinterpret_cast<const uint32_t *>(from + (at & 15u) + 16 * ((at >> 4) ^ (r & 7u)));
+                continue;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const uint32_t at = 2 * (lane + 32 * h);
+                if ((int)(lane + 32 * h) < left)
+                    to[lane + 32 * h] = *reinterpret_cast<const uint16_t *>(from + (at & 15u) + 16 * ((at >> 4) ^ (r & 7u)));
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -319,20 +395,21 @@ __device__ __forceinline__ void epilogue_dw(const XentGemm &g, int vrow, int tn,
 
 template <int DT, int MODE>
 __global__ void __launch_bounds__(kXThreads, 1)
-xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
-            const __grid_constant__ CUtensorMap map_p, const XentGemm g)
+xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
 {
     pdl_launch_dependents();
+    using Y = XLayout<MODE>;
+    constexpr int kStages = Y::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t ring = smem_addr(smem);
-    const uint32_t bars = ring + kXOffBars;
+    const uint32_t bars = ring + Y::kOffBars;
     auto full_bar = [&](int s) { return bars + 8u * (uint32_t)s; };
-    auto empty_bar = [&](int s) { return bars + 8u * (uint32_t)(kXStages + s); };
-    auto dfull_bar = [&](int b) { return bars + 8u * (uint32_t)(2 * kXStages + b); };
-    auto dempty_bar = [&](int b) { return bars + 8u * (uint32_t)(2 * kXStages + kXDBuffers + b); };
-    const uint32_t drain_bar = bars + 8u * (uint32_t)(2 * kXStages + 2 * kXDBuffers);
-    uint32_t *misc = (uint32_t *)(smem + kXOffMisc);
+    auto empty_bar = [&](int s) { return bars + 8u * (uint32_t)(kStages + s); };
+    auto dfull_bar = [&](int b) { return bars + 8u * (uint32_t)(2 * kStages + b); };
+    auto dempty_bar = [&](int b) { return bars + 8u * (uint32_t)(2 * kStages + kXDBuffers + b); };
+    const uint32_t drain_bar = bars + 8u * (uint32_t)(2 * kStages + 2 * kXDBuffers);
+    uint32_t *misc = (uint32_t *)(smem + Y::kOffMisc);
     volatile uint32_t *tmem_holder = misc;
     volatile uint32_t *abort = misc + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -340,20 +417,20 @@ xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
     const bool leader = rank == 0;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kXStages; s++) {
+        for (int s = 0; s < kStages; s++) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
         for (int b = 0; b < kXDBuffers; b++) {
             mbar_init(dfull_bar(b), 1);
-            mbar_init(dempty_bar(b), 2 * kXEpilogueThreads);      // both CTAs' epilogues
+            mbar_init(dempty_bar(b), 2 * kXEpilogueWarps);        // both CTAs' epilogues
         }
         mbar_init(drain_bar, 1);
         *abort = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_x) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_w) : "memory");
-        if (MODE == kXentBack) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&map_p) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&maps.x) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&maps.w) : "memory");
+        if (MODE == kXentBack) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&maps.p) : "memory");
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (warp == 1) {
@@ -376,17 +453,17 @@ xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
         if (lane == 0) {
             int st = 0;
             uint32_t phase = 0;
-            bool armed[kXStages];
-            uint32_t armed_phase[kXStages];
-            for (int i = 0; i < kXStages; i++) {
+            bool armed[kStages];
+            uint32_t armed_phase[kStages];
+            for (int i = 0; i < kStages; i++) {
                 armed[i] = false;
                 armed_phase[i] = 0;
             }
             XUnit u;
             for (int i = 0; !*abort && units.get(i, u); i++) {
                 const int m0 = u.tm * kXentTile + kXHalf * (int)rank, n0 = u.tn * kXentTile + kXHalf * (int)rank;
-                const CUtensorMap *ma = MODE == kXentBack ? &map_p : &map_x;
-                const CUtensorMap *mb = MODE != kXentBack || u.x ? &map_w : &map_x;
+                const CUtensorMap *ma = MODE == kXentBack ? &maps.p : &maps.x;
+                const CUtensorMap *mb = MODE != kXentBack || u.x ? &maps.w : &maps.x;
                 const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
                 // the vocabulary's coordinate counts from the piece's first entry in P only
                 const int b_row = MODE == kXentBack ? (u.x ? g.v0 : 0) : n0 + g.v0;
@@ -416,7 +493,7 @@ xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                     }
                     armed[st] = true;
                     armed_phase[st] = phase;
-                    if (++st == kXStages) {
+                    if (++st == kStages) {
                         st = 0;
                         phase ^= 1u;
                     }
@@ -425,7 +502,7 @@ xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
             }
             if (*abort && leader) {
                 // the full barriers count both CTAs' copies: let them land
-                for (int i = 0; i < kXStages; i++)
+                for (int i = 0; i < kStages; i++)
                     if (armed[i]) (void)mbar_wait_limited(full_bar(i), armed_phase[i]);
             }
         }
@@ -442,79 +519,121 @@ xent_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ C
                 const uint32_t idesc = operand_instr<DT>(a_mn, b_mn);
                 const uint64_t a_ring = operand_desc(ring, a_mn), b_ring = operand_desc(ring + kXHalfBytes, b_mn);
                 const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
-                // both epilogues have read accumulator b
-                if (!x_wait(dempty_bar(b), ((dphase >> b) & 1u) ^ 1u, abort)) break;
-                tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)(b * kXentTile);
                 bool ok = true;
-                for (int j = 0; j < u.nk; j++) {
-                    if (!x_wait(full_bar(st), phase, abort)) {
+                for (int j0 = 0; ok && (j0 < u.nk || j0 == 0); j0 += MODE == kXentForward ? kXChain : u.nk + 1) {
+                    // both epilogues have read accumulator b
+                    if (!x_wait(dempty_bar(b), ((dphase >> b) & 1u) ^ 1u, abort)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t at = (uint64_t)st * (uint64_t)(kXStageBytes >> 4);
+                    const uint32_t d = tmem + (uint32_t)(b * kXentTile);
+                    const int end = MODE == kXentForward ? min(u.nk, j0 + kXChain) : u.nk;
+                    for (int j = j0; j < end; j++) {
+                        if (!x_wait(full_bar(st), phase, abort)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t at = (uint64_t)st * (uint64_t)(kXStageBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        tc_mma_pair(d, a_ring + at + (uint64_t)k * a_step, b_ring + at + (uint64_t)k * b_step, idesc,
-                                    (j > 0 || k > 0) ? 1u : 0u);
-                    tc_commit_pair(empty_bar(st));               // both CTAs' stage is free
-                    if (++st == kXStages) {
-                        st = 0;
-                        phase ^= 1u;
+                        for (int k = 0; k < 4; k++)
+                            tc_mma_pair(d, a_ring + at + (uint64_t)k * a_step, b_ring + at + (uint64_t)k * b_step, idesc,
+                                        (j > j0 || k > 0) ? 1u : 0u);
+                        tc_commit_pair(empty_bar(st));           // both CTAs' stage is free
+                        if (++st == kStages) {
+                            st = 0;
+                            phase ^= 1u;
+                        }
                     }
+                    if (!ok) break;
+                    if (withhold)
+                        withhold = false;
+                    else
+                        tc_commit_pair(dfull_bar(b));            // the chain is in both CTAs' TMEM
+                    dphase ^= 1u << b;
+                    b ^= 1;
                 }
                 if (!ok) break;
-                if (withhold)
-                    withhold = false;
-                else
-                    tc_commit_pair(dfull_bar(b));                // the tile is in both CTAs' TMEM
-                dphase ^= 1u << b;
-                b ^= 1;
             }
             tc_commit_pair_local(drain_bar);
             (void)mbar_wait_limited(drain_bar, 0u);
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: thread m takes row 128 rank + m of the tile
-        const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-        const int m = kXHalf * (int)rank + 32 * (warp & 3) + lane;
+        // ---------------- epilogue: a warp takes 32 rows and 128 columns of the tile
+        const int q = warp & 3, half = (warp - 2) >> 2;          // (a warp reads the lanes of its number mod 4)
+        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * kXCols);
+        const XOut out = {smem + Y::kOffOut + (warp - 2) * kXOutBytes,
+                          ring + (uint32_t)(Y::kOffOut + (warp - 2) * kXOutBytes)};
         int b = 0;
         uint32_t dphase = 0;
+        bool live = false;
+        auto begin = [&] {
+            const bool ready = !*abort && x_wait(dfull_bar(b), (dphase >> b) & 1u, abort);
+            live = __all_sync(kFull, ready);
+            if (live) tc_fence_after();
+        };
+        auto done = [&] {
+            if (live) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(dempty_bar(b), 0u));
+            }
+            dphase ^= 1u << b;
+            b ^= 1;
+        };
         XUnit u;
         for (int i = 0; units.get(i, u); i++) {
-            const bool ready = !*abort && x_wait(dfull_bar(b), (dphase >> b) & 1u, abort);
-            const bool live = __all_sync(kFull, ready);
-            if (live) tc_fence_after();
+            const int row0 = u.tm * kXentTile + kXHalf * (int)rank + 32 * q, col0 = u.tn * kXentTile + half * kXCols;
+            if constexpr (MODE == kXentForward) {
+                float v[kXCols];
+#pragma unroll
+                for (int j = 0; j < kXCols; j++) v[j] = 0.0f;
+#pragma unroll 1
+                for (int j0 = 0; j0 < u.nk; j0 += kXChain) {
+                    begin();
+#pragma unroll
+                    for (int c = 0; c < kXCols / 16; c++) {
+                        float f[16];
+                        __syncwarp();
+                        if (live) {
+                            tc_ld_row16(base + (uint32_t)(b * kXentTile + 16 * c), f);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; j++) f[j] = __int_as_float(0x7fc00000);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j++) v[16 * c + j] = __fadd_rn(v[16 * c + j], f[j]);
+                    }
+                    done();
+                }
+                epilogue_forward(g, (size_t)(row0 + lane), 2 * u.tn + half, v);
+                continue;
+            }
+            begin();
             // without an MMA (K of nothing) the accumulator holds another tile's sums
             const float fill = live ? 0.0f : __int_as_float(0x7fc00000);
             const bool read = live && u.nk > 0;
             auto ld = [&](int c, float (&v)[32]) {
                 __syncwarp();
                 if (read) {
-                    tc_ld_row32(tmem + lane_base + (uint32_t)(b * kXentTile + 32 * c), v);
+                    tc_ld_row32(base + (uint32_t)(b * kXentTile + 32 * c), v);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; j++) v[j] = fill;
                 }
             };
-            const size_t row = (size_t)u.tm * kXentTile + (size_t)m;
-            if constexpr (MODE == kXentForward)
-                epilogue_forward(g, row, u.tn, ld);
-            else if constexpr (MODE == kXentGradient)
-                epilogue_gradient<DT>(g, row, n, u.tn, ld);
+            if constexpr (MODE == kXentGradient)
+                epilogue_gradient<DT>(g, &maps.p_out, out, row0, n, col0, ld);
             else if (u.x)
-                epilogue_dx(g, row, u.split, u.tn, ld);
+                epilogue_dx(g, &maps.ws_out, out, row0, u.split, col0, ld);
             else
-                epilogue_dw<DT>(g, (int)row, u.tn, ld);
-            if (live) {
-                tc_fence_before();
-                mbar_arrive_cluster(map_to_rank(dempty_bar(b), 0u));
-            }
-            dphase ^= 1u << b;
-            b ^= 1;
+                epilogue_dw<DT>(g, &maps.dw_out, out, row0, col0, ld);
+            done();
         }
+        if (MODE != kXentForward && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
 
     tc_fence_before();
@@ -544,12 +663,17 @@ const void *xent_pick(int dtype, int mode)
                                    : (const void *)xent_kernel<kBF16, kXentBack>;
 }
 
-cudaLaunchConfig_t pair_config(int pairs, cudaLaunchAttribute (&attr)[2], cudaStream_t stream)
+int xent_smem(int mode)
+{
+    return mode == kXentForward ? XLayout<kXentForward>::kSmemBytes : XLayout<kXentBack>::kSmemBytes;
+}
+
+cudaLaunchConfig_t pair_config(int mode, int pairs, cudaLaunchAttribute (&attr)[2], cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(kXThreads);
-    cfg.dynamicSmemBytes = kXSmemBytes;
+    cfg.dynamicSmemBytes = (size_t)xent_smem(mode);
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -583,10 +707,10 @@ int xent_pairs()
     bool ok = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
     for (int dt : {kF16, kBF16})
         for (int mode : {kXentForward, kXentGradient, kXentBack})
-            ok = ok && set_smem_once((void *)xent_pick(dt, mode), kXSmemBytes) == cudaSuccess;
+            ok = ok && set_smem_once((void *)xent_pick(dt, mode), xent_smem(mode)) == cudaSuccess;
     if (ok) {
         cudaLaunchAttribute attr[2];
-        cudaLaunchConfig_t cfg = pair_config(sms / 2, attr, nullptr);
+        cudaLaunchConfig_t cfg = pair_config(kXentBack, sms / 2, attr, nullptr);
         cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack), &cfg) != cudaSuccess) n = 0;
     }
@@ -596,15 +720,17 @@ int xent_pairs()
     return n;
 }
 
-cudaError_t xent_map(void *map, const void *base, size_t cols, size_t rows, size_t ld)
+// A matrix of 16-bit values (or, `wide`, of binary32) read in boxes of 64 x 64 or
+// written in boxes of 128 bytes x 32 rows.
+cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, bool out, bool wide)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
-    const cuuint32_t box[2] = {kXBox, kXBox}, step[2] = {1, 1};
-    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)ld * 2};
-    return encode((CUtensorMap *)map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (void *)base, dims, pitch, box, step,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+    const cuuint32_t box[2] = {wide ? 32u : (cuuint32_t)kXBox, out ? 32u : (cuuint32_t)kXBox}, step[2] = {1, 1};
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)ld * (wide ? 4 : 2)};
+    return encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (void *)base, dims,
+                  pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? cudaSuccess
                : cudaErrorInvalidValue;
 }
@@ -612,9 +738,9 @@ cudaError_t xent_map(void *map, const void *base, size_t cols, size_t rows, size
 cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
                         cudaStream_t stream)
 {
-    void *args[] = {(void *)&maps.x, (void *)&maps.w, (void *)&maps.p, (void *)&g};
+    void *args[] = {(void *)&maps, (void *)&g};
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair_config((int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);
+    cudaLaunchConfig_t cfg = pair_config(mode, (int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);
     return cudaLaunchKernelExC(&cfg, xent_pick(dtype, mode), args);
 }
 

@@ -119,7 +119,7 @@ cudaError_t xent_prepare(XentTokens &k, const XentSizes &z, const XentCommon &c,
     cudaError_t e = launch_xent_tokens(k, s);
     if (e == cudaSuccess) e = xent_map(&maps.x, k.X, z.H, z.tpad, z.ldX);
     if (e == cudaSuccess) e = xent_map(&maps.w, w, z.H, z.V, ldw);
-    maps.p = maps.x;
+    maps.p = maps.p_out = maps.ws_out = maps.dw_out = maps.x;      // (those that are not used)
     return e;
 }
 
@@ -275,7 +275,7 @@ try {
     Parts parts;
     XentCommon c;
     c.place(parts, z);
-    const size_t at_part = parts.add(tiles_v * z.tpad * sizeof(float2)), at_hit = parts.add(z.tpad * 4);
+    const size_t at_part = parts.add(2 * tiles_v * z.tpad * sizeof(float2)), at_hit = parts.add(z.tpad * 4);
     Scratch scratch(s);
     if ((st = scratch.take(parts.bytes, dev)) != TCR_OK) return st;
     if (fault_injected("launch")) return TCR_ERR_CUDA;
@@ -304,7 +304,7 @@ try {
         g.inject_stall = fault_injected("stall");
         e = launch_xent(a.dtype, kXentForward, maps, g, (size_t)z.tiles_t * tiles_v, pairs, s);
         if (e == cudaSuccess) {
-            XentLoss l = {g.part, g.hit, k.rank, k.lab, z.tpad, z.T, (int)tiles_v, a.loss, a.lse};
+            XentLoss l = {g.part, g.hit, k.rank, k.lab, z.tpad, z.T, 2 * (int)tiles_v, a.loss, a.lse};
             e = launch_xent_loss(l, s);
         }
     }
@@ -370,6 +370,12 @@ try {
     XentMaps maps;
     cudaError_t e = xent_prepare(k, z, c, base, a.weight, a.ldw, maps, s);
     if (e == cudaSuccess) e = xent_map(&maps.p, base + at_P, piece, z.tpad, piece);
+    if (e == cudaSuccess) e = xent_map(&maps.p_out, base + at_P, piece, z.tpad, piece, true);
+    if (e == cudaSuccess && a.dx) e = xent_map(&maps.ws_out, base + at_ws, ldws, splits * z.tpad, ldws, true, true);
+    // a tensor-map store writes whole granules of 16 bytes, past a row's end as well
+    const bool al_dw = rows_aligned(a.dweight, a.lddw, z.V, 2) && z.H % 8 == 0;
+    if (e == cudaSuccess && a.dweight && al_dw)
+        e = xent_map(&maps.dw_out, a.dweight, z.H, z.V, z.V == 1 ? z.ldX : a.lddw, true);
     XentGemm g = {};
     g.head = k.head;
     g.lab = k.lab;
@@ -387,7 +393,7 @@ try {
     g.splits = (int)splits;
     g.dw = a.dweight;
     g.lddw = a.lddw;
-    g.al_dw = rows_aligned(a.dweight, a.lddw, z.V, 2);
+    g.al_dw = al_dw;
     g.inject_stall = fault_injected("stall");
     for (size_t v0 = 0; v0 < z.V && e == cudaSuccess; v0 += piece) {
         g.v0 = (int)v0;

@@ -44,7 +44,7 @@ struct XentGemm {
     int V, H;
     int v0, vn;                // the piece of the vocabulary (the forward pass: all of it)
     // forward
-    float2 *part;              // [tile of the vocabulary][row]: largest logit, sum about it
+    float2 *part;              // [half a tile of the vocabulary][row]: largest logit, sum about it
     float *hit;                // the target's logit
     // gradient
     const float *lse, *dloss;
@@ -60,11 +60,13 @@ struct XentGemm {
     bool al_dw;
     uint32_t inject_stall;     // withhold the first tile's publication (tests of the failure path)
 };
+// Read maps of X, W and P; write maps of P, of dX's sums (rows of all splits) and of dW.
 struct alignas(64) XentMaps {
-    CUtensorMap x, w, p;
+    CUtensorMap x, w, p, p_out, ws_out, dw_out;
 };
 int xent_pairs();
-cudaError_t xent_map(void *map, const void *base, size_t cols, size_t rows, size_t ld);
+cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, bool out = false,
+                     bool wide = false);
 cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
                         cudaStream_t stream);
 

@@ -120,6 +120,12 @@ def test_strides_and_alignment_do_not_change_bits(T, H, V, dt):
         assert all(same(a, b) for a, b in zip(want, got))
         for g in (gx, gw):
             assert (g[:, :off] == 7).all() and (g[:, off + H:] == 7).all()
+    # what lies between the rows is not looked at
+    for pitch in (H + 8 - H % 8, H + 24 - H % 8, H + 3):
+        xn = torch.full((T, pitch), float("nan"), dtype=x.dtype, device="cuda")
+        wn = torch.full((V, pitch), float("nan"), dtype=x.dtype, device="cuda")
+        xn[:, :H], wn[:, :H] = x, w
+        assert all(same(a, b) for a, b in zip(want, step(xn[:, :H], wn[:, :H], target, dloss)))
     # one row of x for all; the gradient of a mean; dx over x
     xe = x[:1].expand(T, H)
     assert same(tcr.tcr_cross_entropy(xe, w, target).loss, tcr.tcr_cross_entropy(xe.contiguous(), w, target).loss)
