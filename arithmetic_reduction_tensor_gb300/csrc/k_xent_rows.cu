@@ -31,24 +31,29 @@ __device__ __forceinline__ int count_live(const XentTokens &a, size_t n, int *re
     return s;
 }
 
-// One row by a warp, 16-byte vectors where the source is aligned; H elements.
-__device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst, size_t H, bool aligned)
+// One row by a warp, to a 16-byte aligned one of whole vectors; unaligned rows as
+// the granules that hold their elements, shifted in registers (by elements a
+// 5003 x 1001 matrix took 9.0 us instead of 5).
+template <bool GRAN>
+__device__ __forceinline__ void copy_row(const uint16_t *src, uint16_t *dst, uint32_t H)
 {
-    const uint32_t lane = threadIdx.x & 31;
-    if (aligned) {
-        const size_t nv = H / 8;
-#pragma unroll 4
-        for (size_t v = lane; v < nv; v += 32) reinterpret_cast<uint4 *>(dst)[v] = ld_stream(src + 8 * v);
-        for (size_t j = 8 * nv + lane; j < H; j += 32) dst[j] = src[j];
-    } else {
-#pragma unroll 8
-        for (size_t j = lane; j < H; j += 32) dst[j] = src[j];
+    constexpr int kAtOnce = 8;
+    const uint32_t lane = threadIdx.x & 31, nvec = (H + kRv - 1) / kRv;
+    for (uint32_t v0 = lane; v0 < nvec + lane; v0 += 32 * kAtOnce) {     // (the same steps in every lane)
+        LoadedVec<kBF16, GRAN> l[kAtOnce];
+#pragma unroll
+        for (uint32_t k = 0; k < kAtOnce; k++) l[k] = load_vec<kBF16, GRAN>(src, H, v0 + 32 * k);
+#pragma unroll
+        for (uint32_t k = 0; k < kAtOnce; k++)
+            if (v0 + 32 * k < nvec)
+                reinterpret_cast<uint4 *>(dst)[v0 + 32 * k] = use_vec<kBF16, GRAN>(l[k], src, H, v0 + 32 * k).q[0];
     }
 }
 
 // CTA b takes tokens [b chunk, (b + 1) chunk): their rows in the copy follow
 // from the count of those before, which each CTA takes itself (a scan would
-// be a launch more).
+// be a launch more).  CTAs past those and the tail copy W where it has to be
+// copied.
 __global__ void __launch_bounds__(kTokThreads) xent_tokens_kernel(const XentTokens a, size_t chunk, unsigned blocks)
 {
     pdl_launch_dependents();
@@ -56,6 +61,12 @@ __global__ void __launch_bounds__(kTokThreads) xent_tokens_kernel(const XentToke
     __shared__ int red[kTokWarps];
     __shared__ int ranks[kTokThreads];
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (blockIdx.x >= blocks + kTokTail) {
+        const size_t step = (size_t)(gridDim.x - blocks - kTokTail) * kTokWarps;
+        for (size_t r = (size_t)(blockIdx.x - blocks - kTokTail) * kTokWarps + warp; r < a.V; r += step)
+            copy_row<true>((const uint16_t *)a.w + r * a.ldw, a.W + r * a.ldX, (uint32_t)a.H);
+        return;
+    }
     if (blockIdx.x >= blocks) {
         const unsigned part = blockIdx.x - blocks;
         const int n = count_live(a, a.tokens, red);
@@ -109,49 +120,47 @@ __global__ void __launch_bounds__(kTokThreads) xent_tokens_kernel(const XentToke
         const int here = (int)min(last - t0, (size_t)kTokThreads);
         for (int i = (int)warp; i < here; i += kTokWarps) {
             const int to = ranks[i];
-            if (to >= 0)
-                copy_row((const uint16_t *)a.x + (t0 + i) * a.ldx, a.X + (size_t)to * a.ldX, a.H, a.al_x);
+            if (to < 0) continue;
+            const uint16_t *row = (const uint16_t *)a.x + (t0 + i) * a.ldx;
+            if (a.al_x)
+                copy_row<false>(row, a.X + (size_t)to * a.ldX, (uint32_t)a.H);
+            else
+                copy_row<true>(row, a.X + (size_t)to * a.ldX, (uint32_t)a.H);
         }
         base += all;
         __syncthreads();
     }
 }
 
-__global__ void __launch_bounds__(kTokThreads)
-xent_repack_kernel(const uint16_t *w, size_t ldw, size_t V, size_t H, uint16_t *W, size_t ldW)
-{
-    pdl_launch_dependents();
-    pdl_wait_primary();
-    for (size_t r = (size_t)blockIdx.x * kTokWarps + (threadIdx.x >> 5); r < V; r += (size_t)gridDim.x * kTokWarps)
-        copy_row(w + r * ldw, W + r * ldW, H, false);
-}
-
-// 32 tokens a CTA, one a lane; the warps share the tiles.  lse = log of the
-// parts' sums about the largest logit, in powers of two as they were formed.
-constexpr int kLossWarps = 16;
-__global__ void __launch_bounds__(32 * kLossWarps) xent_loss_kernel(const XentLoss a)
+// Four tokens a CTA (32 bytes of each part's row), 64 threads a token over the
+// parts.  lse = log of the parts' sums about the largest logit, in powers of
+// two as they were formed.
+constexpr int kLossTokens = 4, kLossThreads = 256, kLossSlices = kLossThreads / kLossTokens;
+__global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss a)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
     constexpr float log2e = 1.44269504088896340736f, ln2 = 0.69314718055994530942f;
-    __shared__ float sm[kLossWarps][32], ss[kLossWarps][32];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const size_t t = (size_t)blockIdx.x * 32 + lane;
-    const int r = t < a.tokens ? a.rank[t] : -1;
+    __shared__ float red[2][kLossThreads / 32][kLossTokens];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = threadIdx.x % kLossTokens;
+    const size_t t = (size_t)blockIdx.x * kLossTokens + k;
+    const int r = t < a.tokens ? a.rank[t] : -1, first = (int)threadIdx.x / kLossTokens;
     float m = -INFINITY, s = 0.0f;
     if (r >= 0) {
-        // two passes over the parts (8 bytes for 256 logits): the largest, then the sum about it
-#pragma unroll 4
-        for (int j = (int)warp; j < a.tiles; j += kLossWarps) m = fmaxf(m, a.part[(size_t)j * a.tpad + r].x);
+        // two passes over the parts (8 bytes for 128 logits): the largest, then the sum about it
+#pragma unroll 8
+        for (int j = first; j < a.parts; j += kLossSlices) m = fmaxf(m, a.part[(size_t)j * a.tpad + r].x);
     }
-    sm[warp][lane] = m;
+#pragma unroll
+    for (int h = kLossTokens; h < 32; h *= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, h));
+    if (lane < kLossTokens) red[0][warp][k] = m;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kLossWarps; w++) m = fmaxf(m, sm[w][lane]);
+    for (int w = 0; w < kLossThreads / 32; w++) m = fmaxf(m, red[0][w][k]);
     const float about = m == -INFINITY ? 0.0f : __fmul_rn(m, log2e);
     if (r >= 0) {
-#pragma unroll 4
-        for (int j = (int)warp; j < a.tiles; j += kLossWarps) {
+#pragma unroll 8
+        for (int j = first; j < a.parts; j += kLossSlices) {
             const float2 p = a.part[(size_t)j * a.tpad + r];
             // the part's own unit is fl(p.x * log2e), as its sum was formed (a part
             // of nothing but -infinity is 0 in any unit)
@@ -159,14 +168,16 @@ __global__ void __launch_bounds__(32 * kLossWarps) xent_loss_kernel(const XentLo
             s = __fmaf_rn(p.y, exp2f(__fsub_rn(unit, about)), s);
         }
     }
-    ss[warp][lane] = s;
+#pragma unroll
+    for (int h = kLossTokens; h < 32; h *= 2) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, h));
+    if (lane < kLossTokens) red[1][warp][k] = s;
     __syncthreads();
-    if (warp != 0 || t >= a.tokens) return;
+    if (threadIdx.x >= kLossTokens || t >= a.tokens) return;
     float loss = 0.0f, lse = 0.0f;
     if (r >= 0) {
         s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kLossWarps; w++) s = __fadd_rn(s, ss[w][lane]);
+        for (int w = 0; w < kLossThreads / 32; w++) s = __fadd_rn(s, red[1][w][k]);
         lse = __fmul_rn(__fadd_rn(about, log2f(s)), ln2);
         loss = a.lab[r] < 0 ? __int_as_float(0x7fc00000) : __fsub_rn(lse, a.hit[r]);
     }
@@ -217,24 +228,18 @@ cudaError_t launch_xent_tokens(const XentTokens &a, cudaStream_t stream)
     size_t chunk = (a.tokens + 1023) / 1024;
     if (chunk < kTokWarps) chunk = kTokWarps;
     unsigned blocks = (unsigned)((a.tokens + chunk - 1) / chunk);
+    const size_t need = (a.V + kTokWarps - 1) / kTokWarps, most = 152 * 8;
+    const unsigned repack = a.w ? (unsigned)(need < most ? need : most) : 0u;
     void *args[] = {(void *)&a, (void *)&chunk, (void *)&blocks};
-    return launch_first((const void *)xent_tokens_kernel, dim3(blocks + kTokTail), dim3(kTokThreads), args, 0, stream);
-}
-
-cudaError_t launch_xent_repack(const void *w, size_t ldw, size_t V, size_t H, uint16_t *W, size_t ldW,
-                               cudaStream_t stream)
-{
-    const size_t need = (V + kTokWarps - 1) / kTokWarps;
-    void *args[] = {(void *)&w, (void *)&ldw, (void *)&V, (void *)&H, (void *)&W, (void *)&ldW};
-    return launch_first((const void *)xent_repack_kernel, dim3((unsigned)(need < 152 * 8 ? need : 152 * 8)),
-                        dim3(kTokThreads), args, 0, stream);
+    return launch_first((const void *)xent_tokens_kernel, dim3(blocks + kTokTail + repack), dim3(kTokThreads), args, 0,
+                        stream);
 }
 
 cudaError_t launch_xent_loss(const XentLoss &a, cudaStream_t stream)
 {
     void *args[] = {(void *)&a};
-    return launch_first((const void *)xent_loss_kernel, dim3((unsigned)((a.tokens + 31) / 32)), dim3(32 * kLossWarps),
-                        args, 0, stream);
+    return launch_first((const void *)xent_loss_kernel, dim3((unsigned)((a.tokens + kLossTokens - 1) / kLossTokens)),
+                        dim3(kLossThreads), args, 0, stream);
 }
 
 cudaError_t launch_xent_dx(int dtype, const XentDx &a, cudaStream_t stream)

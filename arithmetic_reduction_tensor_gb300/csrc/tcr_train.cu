@@ -109,8 +109,9 @@ cudaError_t xent_prepare(XentTokens &k, const XentSizes &z, const XentCommon &c,
     k.rank = (int *)(base + c.rank);
     k.head = (unsigned int *)(base + c.head);
     if (z.repack) {
-        cudaError_t e = launch_xent_repack(w, ldw, z.V, z.H, (uint16_t *)(base + c.W), z.ldX, s);
-        if (e != cudaSuccess) return e;
+        k.w = w;
+        k.ldw = ldw;
+        k.W = (uint16_t *)(base + c.W);
         w = base + c.W;
         ldw = z.ldX;
     } else if (z.V == 1) {

@@ -28,14 +28,13 @@ struct XentTokens {
     // outputs
     uint16_t *X;               // the compact copy, ldX elements a row
     size_t ldX;
+    const void *w;             // W to be copied to rows of ldX elements at W; null: not
+    size_t ldw;
+    uint16_t *W;
     int *lab, *tok, *rank;     // by compact row: label (-1: no entry of the vocabulary), token; by token: its row or -1
     unsigned int *head;        // n, and the bits of those tokens' largest finite |dloss|
 };
 cudaError_t launch_xent_tokens(const XentTokens &a, cudaStream_t stream);
-
-// W copied to rows of ldW elements (16-byte aligned).
-cudaError_t launch_xent_repack(const void *w, size_t ldw, size_t V, size_t H, uint16_t *W, size_t ldW,
-                               cudaStream_t stream);
 
 struct XentGemm {
     const unsigned int *head;
@@ -76,7 +75,7 @@ struct XentLoss {
     const float *hit;
     const int *rank, *lab;
     size_t tpad, tokens;
-    int tiles;
+    int parts;
     float *loss, *lse;         // lse may be null
 };
 cudaError_t launch_xent_loss(const XentLoss &a, cudaStream_t stream);
