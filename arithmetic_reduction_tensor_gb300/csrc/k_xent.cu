@@ -119,20 +119,22 @@ __device__ __forceinline__ uint32_t operand_instr(bool a_mn, bool b_mn)
            ((uint32_t)(kXentTile >> 3) << 17) | ((uint32_t)(kXentTile >> 4) << 24);
 }
 
-// One tile's work: 64-boxes [k0, k0 + nk) of K.
+// One tile's work: 64-boxes [k0, k0 + nk) of K; of A's four boxes of rows the
+// first `rows` hold something that is wanted (tokens; the others are not read,
+// and what the MMAs make of their places in shared memory is not looked at).
 struct XUnit {
     bool x;                // dX (else dW, or the logits)
-    int tm, tn, split, k0, nk;
+    int tm, tn, split, k0, nk, rows;
 };
 
 // The units of one launch, of which pair p of `pairs` runs the i-th of its own.
 struct XUnits {
-    int mode, pairs, pair;
+    int mode, n, pairs, pair;
     int tm, tn, nk;                    // the logits, or dW: tiles, boxes of K
     int xm, xn, xnk, xkps, xsplits;    // dX: tiles, boxes of K, boxes a split
     int nx, nd, lead, rem;
 
-    __device__ __forceinline__ XUnits(const XentGemm &g, int n, int mode_) : mode(mode_)
+    __device__ __forceinline__ XUnits(const XentGemm &g, int n_, int mode_) : mode(mode_), n(n_)
     {
         pairs = (int)(gridDim.x >> 1);
         pair = (int)(blockIdx.x >> 1);
@@ -183,6 +185,7 @@ struct XUnits {
             raster(v % tiles, xm, xn, u.tm, u.tn);
             u.k0 = u.split * xkps;
             u.nk = max(0, min(xkps, xnk - u.k0));
+            u.rows = boxes_of_tokens(u.tm);
             return true;
         }
         i -= mine;
@@ -200,7 +203,12 @@ struct XUnits {
         raster(d, tm, tn, u.tm, u.tn);
         u.k0 = 0;
         u.nk = nk;
+        u.rows = mode == kXentBack ? 4 : boxes_of_tokens(u.tm);
         return true;
+    }
+    __device__ __forceinline__ int boxes_of_tokens(int m) const
+    {
+        return min(4, (n - m * kXentTile + kXBox - 1) / kXBox);
     }
 };
 
@@ -293,6 +301,7 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
         at = lab - g.v0 - col0;
     }
     const int left = gq == 0.0f ? 0 : g.vn - col0;
+    if (row0 >= (n + kXBox - 1) / kXBox * kXBox) return;     // not read: dW's K ends with the tokens' last box
 #pragma unroll 1
     for (int c = 0; c < kXCols / 64; c++) {
         uint32_t o[32];
@@ -319,13 +328,13 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
 // A split's sums of dX, added to those of the pieces before.
 template <class Ld>
 __device__ __forceinline__ void epilogue_dx(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
-                                            int split, int col0, Ld ld)
+                                            int n, int split, int col0, Ld ld)
 {
 #pragma unroll 1
     for (int c = 0; c < kXCols / 32; c++) {
         float v[32];
         ld(c, v);
-        if ((size_t)(col0 + 32 * c) >= g.ldws) continue;
+        if ((size_t)(col0 + 32 * c) >= g.ldws || row0 >= n) continue;
         out.ready();
 #pragma unroll
         for (int k = 0; k < 8; k++)
@@ -476,9 +485,10 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     const uint32_t dst = ring + (uint32_t)st * kXStageBytes;
                     const int kc = (u.k0 + j) * kXBox;
                     const uint32_t fb = map_to_rank(full_bar(st), 0u);
-                    if (leader) mbar_arrive_expect_tx(full_bar(st), (uint32_t)(2 * kXStageBytes));
+                    if (leader) mbar_arrive_expect_tx(full_bar(st), (uint32_t)((u.rows + 4) * kXBoxBytes));
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
+                        if (2 * (int)rank + h >= u.rows) break;
                         if (a_mn)
                             tma_load_2d_pair(dst + h * kXBoxBytes, ma, m0 + h * kXBox, kc, fb);
                         else
@@ -608,7 +618,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     }
                     done();
                 }
-                epilogue_forward(g, (size_t)(row0 + lane), 2 * u.tn + half, v);
+                if (row0 < n) epilogue_forward(g, (size_t)(row0 + lane), 2 * u.tn + half, v);
                 continue;
             }
             begin();
@@ -627,7 +637,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             if constexpr (MODE == kXentGradient)
                 epilogue_gradient<DT>(g, &maps.p_out, out, row0, n, col0, ld);
             else if (u.x)
-                epilogue_dx(g, &maps.ws_out, out, row0, u.split, col0, ld);
+                epilogue_dx(g, &maps.ws_out, out, row0, n, u.split, col0, ld);
             else
                 epilogue_dw<DT>(g, &maps.dw_out, out, row0, col0, ld);
             done();
