@@ -162,9 +162,10 @@ struct XUnits {
             xsplits = g.splits;
             nx = xm * xn * xsplits;
             // the long units first, one more on some pairs than on others: those
-            // take fewer of the short ones
+            // take fewer of the short ones (whose epilogue takes as long as 7 boxes)
+            const int cost = max(nk, 7);
             rem = nx % pairs;
-            lead = rem && nk ? (xkps + nk / 2) / nk : 0;
+            lead = rem ? (xkps + cost / 2) / cost : 0;
             if (lead > nd / (pairs - rem)) lead = nd / (pairs - rem);
         }
     }
@@ -378,23 +379,24 @@ __device__ __forceinline__ void epilogue_dw(const XentGemm &g, const CUtensorMap
             continue;
         }
         __syncwarp();
-        uint16_t *to = (uint16_t *)g.dw + (size_t)(g.v0 + row0) * g.lddw + col;
+        uint16_t *to = (uint16_t *)g.dw + (size_t)(g.v0 + row0) * g.lddw + col + lane;
         const int rows = min(32, g.vn - row0);
-#pragma unroll 4
-        for (int r = 0; r < rows; r++, to += g.lddw) {
-            const uint8_t *from = out.smem + 128 * r;
-            if (left >= 64 && ((uintptr_t)to & 3u) == 0u) {
-                const uint32_t at = 4 * lane;
-                reinterpret_cast<uint32_t *>(to)[lane] =
-                    *reinterpret_cast<const uint32_t *>(from + (at & 15u) + 16 * ((at >> 4) ^ (r & 7u)));
-                continue;
+        const bool in0 = (int)lane < left, in1 = (int)lane + 32 < left;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 8) {               // eight rows' values read ahead of their stores
+            uint16_t e[16];
+#pragma unroll
+            for (uint32_t i = 0; i < 16; i++) {              // (a row's number mod 8 is i / 2)
+                const uint32_t at = 2 * (lane + 32 * (i & 1u));
+                e[i] = *reinterpret_cast<const uint16_t *>(out.smem + 128 * (r0 + i / 2) + (at & 15u) +
+                                                           16 * ((at >> 4) ^ (i / 2)));
             }
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const uint32_t at = 2 * (lane + 32 * h);
-                if ((int)(lane + 32 * h) < left)
-                    to[lane + 32 * h] = *reinterpret_cast<const uint16_t *>(from + (at & 15u) + 16 * ((at >> 4) ^ (r & 7u)));
-            }
+            for (int i = 0; i < 8; i++, to += g.lddw)
+                if (r0 + i < rows) {
+                    if (in0) to[0] = e[2 * i];
+                    if (in1) to[32] = e[2 * i + 1];
+                }
         }
         __syncwarp();
     }
