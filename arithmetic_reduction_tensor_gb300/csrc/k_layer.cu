@@ -64,7 +64,7 @@ __device__ __forceinline__ void layer_row(const LayerArgs &a, const Drop &drop, 
         zero_absent(count(i), y[i]);
         s[i] = piece_tree<L>(y[i]);
     }
-    float sum[1] = {halving<NV>(s)};
+    float sum[1] = {fold<NV>(s)};
     team_sums<T, L>(sum, red);
     const float mean = __fdiv_rn(sum[0], (float)cols);
     if (a.h) {
@@ -81,7 +81,7 @@ __device__ __forceinline__ void layer_row(const LayerArgs &a, const Drop &drop, 
         mul8(e, y[i], y[i]);
         s[i] = piece_tree<L>(e);
     }
-    sum[0] = halving<NV>(s);
+    sum[0] = fold<NV>(s);
     team_sums<T, L>(sum, red + team_sums_floats<T, 1>());
     const float rstd = rstd_of(sum[0], cols, a.eps);
     if (t == 0) {
@@ -152,8 +152,11 @@ layer_kernel(const __grid_constant__ LayerArgs a)
     const size_t r = T == 32 ? (size_t)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     if (T == 32 && r >= a.rows) return;
     const Drop drop(a.drop);
-    if (warp_whole<T, NV>((uint32_t)a.cols, t))
+    const uint32_t cols = (uint32_t)a.cols;
+    if (warp_whole<T, NV>(cols, t))
         layer_row<DT, OUT, ELEM, T, NV, NV>(a, drop, r, t, red, redm);
+    else if (LEAD < NV - 1 && warp_whole<T, (NV > 1 ? NV - 1 : 1)>(cols, t))
+        layer_row<DT, OUT, ELEM, T, NV, (LEAD < NV - 1 ? NV - 1 : LEAD)>(a, drop, r, t, red, redm);
     else
         layer_row<DT, OUT, ELEM, T, NV, LEAD>(a, drop, r, t, red, redm);
 }

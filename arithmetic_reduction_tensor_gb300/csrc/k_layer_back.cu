@@ -7,10 +7,10 @@
 //   dw_j = sum over rows of dy * xh,  db_j = sum over rows of dy
 //
 // Both row sums fold in one exchange, in the declared order of rowvec.cuh.
-// dw and db: CTA b of G adds its rows b, b + G, .. in order, and a second kernel adds the G partials: 32
-// threads a column, thread k the partials k, k + 32, .. in order, then the
-// halving fold over the 32.  G depends on rows, cols and the type only
-// (layer_back_groups); there are no atomics.
+// dw and db: CTA b of G adds its rows b, b + G, .. in order, and a second kernel
+// adds the G partials: 32 threads a column, thread k the partials k, k + 32, .. in
+// order, then the halving fold over the 32.  G depends on rows, cols and the
+// type only (layer_back_groups); there are no atomics.
 #include "kernels.cuh"
 #include "piece.cuh"
 #include "tc05.cuh"
@@ -121,7 +121,7 @@ __device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Dr
         }
         // two buffers: a thread reaches the next row's write of this one only
         // after every thread has passed the barrier of the row between
-        float m[2] = {halving<NV>(sa), halving<NV>(sc)};
+        float m[2] = {fold<NV>(sa), fold<NV>(sc)};
         team_sums<T, L>(m, red + buf * 2 * T);
         const float ma = __fdiv_rn(m[0], (float)cols), mc = __fdiv_rn(m[1], (float)cols);
 #pragma unroll
@@ -375,7 +375,7 @@ cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream
         // finishes: where that one holds little shared memory, an SM would take
         // its first CTAs with a small share of it and the rest in a second wave
         // (100 calls back to back, 65536 x 1024 bfloat16: 148 us, 119 this way).
-        if (G > 2 * 152) return cudaLaunchKernel(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
+        if (G == 152 * back_ctas(nvec, DT)) return cudaLaunchKernel(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
         return launch_first(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
     }
     void *args[] = {(void *)&a, (void *)&sums};

@@ -59,8 +59,21 @@ __device__ __forceinline__ uint32_t piece_count(uint32_t cols, uint32_t first, i
     return i < LEAD ? (uint32_t)kRv : piece_count<L>(cols, first + (uint32_t)(i * kRv * T));
 }
 
-// Whether a warp's last piece is whole, of NV that T threads (t: the thread's
-// number among them) share; the same for the warp.
+// The halving fold (rowvec.cuh) of a thread's N values, absent ones up to a power
+// of two +0.0.
+template <int N>
+__device__ __forceinline__ float fold(const float (&s)[N])
+{
+    constexpr int P = N <= 1 ? 1 : N <= 2 ? 2 : N <= 4 ? 4 : 8;
+    static_assert(N <= 8, "");
+    float a[P];
+#pragma unroll
+    for (int i = 0; i < P; i++) a[i] = i < N ? s[i] : 0.0f;
+    return halving<P>(a);
+}
+
+// Whether the first NV pieces, which T threads (t: the thread's number among
+// them) share, are whole in this warp; the same for the warp.
 template <int T, int NV>
 __device__ __forceinline__ bool warp_whole(uint32_t cols, uint32_t t)
 {

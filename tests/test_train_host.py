@@ -1,13 +1,18 @@
 """Argument checks of dropout, the layer norm and the cross entropy, before any
 GPU work, and the generator against its published vectors."""
 import ctypes
+import os
+import shutil
+import subprocess
+import sys
 
 import numpy as np
 import pytest
 
 import arithmetic_reduction_tensor_gb300 as tcr
-from arithmetic_reduction_tensor_gb300.build import build_library
+from arithmetic_reduction_tensor_gb300.build import BIND_PATH, build_library
 from tests import train_spec as spec
+from tests.test_i8_host import SLOW_C, SLOW_PY
 
 FAKE = 0x7F0000000000      # never dereferenced: every case below fails validation
 BAD, OK, UNSUPPORTED = tcr.ERR_INVALID_ARG, tcr.OK, tcr.ERR_UNSUPPORTED
@@ -151,3 +156,40 @@ def test_cross_entropy_of_nothing(lib):
     assert lib.tcr_cross_entropy(ctypes.byref(xent_args(tokens=0, x=None, target=None)), None) == OK
     assert lib.tcr_cross_entropy_backward(ctypes.byref(xent_back_args(tokens=0, dweight=None)), None) == OK
     assert lib.tcr_cross_entropy_backward(ctypes.byref(xent_back_args(dx=None, dweight=None)), None) == OK
+
+
+def test_calls_leave_the_interpreter_to_other_threads(lib, tmp_path):
+    # as for the 8-bit path's calls, with the waiting function behind the five of these
+    setup, calls = SLOW_PY.split("class Tensor:")[0], "class Tensor:" + SLOW_PY.split("class Tensor:")[1]
+    head, tail = calls.split("for call in (")[0], calls.split("m.gemm(q, q, s, s, c, None)):")[1]
+    code = setup + """
+try:
+    m.dropout(*[None] * 8)
+except RuntimeError as e:
+    assert "setup_training" in str(e)
+m.setup_training("i64", *[slow] * 5)
+""" + head + """
+t = Tensor("i64", 4)
+for call in (lambda: m.dropout(x, 0.1, 1, 2, None, None, x, None),
+             lambda: m.layernorm(x, w, w, x, 1e-5, 0.1, 1, 2, None, x, x, None, s, s, None),
+             lambda: m.layernorm_backward(x, x, w, s, s, None, 0.0, 0, 0, None, x, None, None, None, None),
+             lambda: m.cross_entropy(x, c8, t, -100, s, s, None),
+             lambda: m.cross_entropy_backward(s, x, c8, t, s, -100, x, c8, None)):
+""".replace("t = Tensor", "c8 = Tensor(\"bf16\", 9, 8)\nt = Tensor") + tail
+    cc = os.environ.get("CC") or shutil.which("gcc") or shutil.which("cc")
+    (tmp_path / "slow.c").write_text(SLOW_C)
+    subprocess.run([cc, "-shared", "-fPIC", str(tmp_path / "slow.c"), "-o", str(tmp_path / "slow.so")], check=True)
+    r = subprocess.run([sys.executable, "-c", code, BIND_PATH, str(tmp_path / "slow.so")], capture_output=True,
+                       text=True, timeout=60)
+    assert r.returncode == 0, r.stderr
+    counts = [int(n) for n in r.stdout.split()]
+    assert len(counts) == 5 and min(counts) >= 1, counts
+
+
+@pytest.mark.parametrize("p", [0.0, 0.1, 0.25, 0.5, 0.9999, 1.0])
+def test_share_of_the_generators_bits_that_are_kept(p):
+    k = spec.keep(64, 4096, p, 0x0123456789ABCDEF, 1 << 40)
+    t = spec.threshold(p)
+    assert abs(t / 65536 - p) <= 2.0 ** -17
+    share = float(k.double().mean())
+    assert abs(share - (1 - t / 65536)) <= 5 * (max(p * (1 - p), 1e-12) / k.numel()) ** 0.5
