@@ -304,8 +304,16 @@ layer_sums_kernel(const float *partial_w, const float *partial_b, size_t cols, i
 // memory hold of the shapes below.
 static int back_ctas(size_t nvec, int dtype)
 {
-    if (dtype == kF32) return nvec <= 128 ? 12 : nvec <= 256 ? 6 : nvec <= 512 ? 3 : nvec <= 768 ? 2 : 1;
-    return nvec <= 128 ? 16 : nvec <= 256 ? 8 : nvec <= 512 ? 4 : 2;
+    if (dtype == kF32)
+        return nvec <= 128 ? 12 : nvec <= 256 ? 6 : nvec <= 384 ? 4 : nvec <= 640 ? 3 : nvec <= 768 ? 2 : 1;
+    return nvec <= 128   ? 16
+           : nvec <= 192 ? 12
+           : nvec <= 320 ? 8
+           : nvec <= 384 ? 5
+           : nvec <= 640 ? 4
+           : nvec <= 768 ? 2
+           : nvec <= 896 ? 3
+                         : 2;
 }
 
 // As many CTAs as fit the SMs, but (above one an SM) no more than half the rows: a
@@ -334,24 +342,31 @@ const void *pick(size_t nvec, unsigned &threads, size_t &smem)
 #define TCR_BACK(T_, NV_, MINB_)                     \
     return (threads = T_, smem = (size_t)T_ * NV_ * 64, \
             (const void *)layer_back_kernel<DT, ELEM, T_, NV_, NV_ - 1, MINB_>)
-    // The fastest of those measured (bfloat16, with dropout): 16384 x 4096 256 x 2
-    // in 120 us, 128 x 4 in 121; 20000 x 2560 128 x 3 with 4 CTAs an SM in 118,
-    // with 6 (spills) 134, 256 x 2 178; 10000 x 5120 256 x 3 with 2 in 121, with 3
-    // in 140; 8192 x 8192 512 x 2 in 127, 256 x 4 in 129.
+    // The fastest of those measured (with dropout and the sums; threads whose last
+    // pieces are past the row's end issue for nothing): bfloat16 16384 x 4096 256 x 2
+    // in 125 us, 128 x 4 in 128; 32768 x 1536 64 x 3 97, 128 x 2 129; 20000 x 2560
+    // 64 x 5 102, 128 x 3 123; 10000 x 5120 128 x 5 103, 256 x 3 139; 10000 x 6144
+    // 256 x 3 127, 128 x 6 130; 8000 x 7168 128 x 7 125, 512 x 2 142.
     if constexpr (DT == kF32) {
         if (nvec <= 64) TCR_BACK(64, 1, 12);
         if (nvec <= 128) TCR_BACK(64, 2, 12);
         if (nvec <= 256) TCR_BACK(128, 2, 6);
+        if (nvec <= 384) TCR_BACK(128, 3, 4);
         if (nvec <= 512) TCR_BACK(256, 2, 3);
+        if (nvec <= 640) TCR_BACK(128, 5, 3);
         if (nvec <= 768) TCR_BACK(256, 3, 2);
         TCR_BACK(512, 2, 1);
     } else {
         if (nvec <= 64) TCR_BACK(64, 1, 16);
         if (nvec <= 128) TCR_BACK(64, 2, 16);
+        if (nvec <= 192) TCR_BACK(64, 3, 12);
         if (nvec <= 256) TCR_BACK(128, 2, 8);
-        if (nvec <= 384) TCR_BACK(128, 3, 4);
+        if (nvec <= 320) TCR_BACK(64, 5, 8);
+        if (nvec <= 384) TCR_BACK(128, 3, 5);
         if (nvec <= 512) TCR_BACK(256, 2, 4);
+        if (nvec <= 640) TCR_BACK(128, 5, 4);
         if (nvec <= 768) TCR_BACK(256, 3, 2);
+        if (nvec <= 896) TCR_BACK(128, 7, 3);
         TCR_BACK(512, 2, 2);
     }
 #undef TCR_BACK

@@ -233,7 +233,7 @@ int norm_back_groups(size_t rows, size_t cols);
 size_t norm_back_scratch(size_t rows, size_t cols, bool dweight);
 cudaError_t launch_norm_back(int dtype, BackArgs a, float *scratch, float *dw, cudaStream_t stream);
 
-// ---- dropout and the layer norm with it (k_layer.cu), and its gradient
+// ---- dropout and the layer norm with it (k_layer.cu, layer.cuh), and its gradient
 // (k_layer_back.cu): as the row operators above, rows of more than
 // kBackMaxVecs vectors of 8 in the gradient with one more launch and two
 // floats of scratch each.
@@ -250,13 +250,16 @@ struct LayerArgs {
     size_t ldx, ldr;
     void *h, *y;                     // h may be null; y: the input type, or 8-bit codes with scale
     size_t ldh, ldy;
-    float *scale, *mean, *rstd;      // mean, rstd may be null
+    float *scale, *mean, *rstd;      // scale: of codes, null otherwise; mean, rstd may be null
     float eps;
     size_t rows, cols;
     bool al_x, al_r, al_w, al_b, al_h, al_y;   // 16-byte aligned rows (codes: 8-byte)
     DropArgs drop;
 };
-cudaError_t launch_layer(int dtype, bool out_i8, const LayerArgs &a, cudaStream_t stream);
+cudaError_t launch_layer(int dtype, const LayerArgs &a, cudaStream_t stream);
+const void *layer_kernel_f16(size_t nvec, bool elem, int &team);
+const void *layer_kernel_bf16(size_t nvec, bool elem, int &team);
+const void *layer_kernel_f32(size_t nvec, bool elem, int &team);
 // y = r + dropout(x); cols > 0.
 cudaError_t launch_dropout(int dtype, const LayerArgs &a, cudaStream_t stream);
 struct LayerBackArgs {

@@ -258,34 +258,42 @@ __device__ __forceinline__ void mul8(float (&r)[kRv], const float (&a)[kRv], flo
 template <int L>
 __device__ __forceinline__ float piece_tree(const float (&e)[kRv])
 {
-    if constexpr (L == kVectors) return tree8(e);
-    if constexpr (L == kSingles) return tree8_lanes(e);
-    const uint32_t lane = threadIdx.x & 31;
-    float a[4], b[2];
+    if constexpr (L == kVectors) {
+        return tree8(e);
+    } else if constexpr (L == kSingles) {
+        return tree8_lanes(e);
+    } else {
+        const uint32_t lane = threadIdx.x & 31;
+        float a[4], b[2];
 #pragma unroll
-    for (int k = 0; k < 4; k++) a[k] = __fadd_rn(e[2 * k], e[2 * k + 1]);
+        for (int k = 0; k < 4; k++) a[k] = __fadd_rn(e[2 * k], e[2 * k + 1]);
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const bool odd = lane & 1u;
-        const float keep = odd ? a[2 * k + 1] : a[2 * k], give = odd ? a[2 * k] : a[2 * k + 1];
-        b[k] = __fadd_rn(keep, __shfl_xor_sync(kFull, give, 1));
+        for (int k = 0; k < 2; k++) {
+            const bool odd = lane & 1u;
+            const float keep = odd ? a[2 * k + 1] : a[2 * k], give = odd ? a[2 * k] : a[2 * k + 1];
+            b[k] = __fadd_rn(keep, __shfl_xor_sync(kFull, give, 1));
+        }
+        const bool odd = lane & 2u;
+        return __fadd_rn(odd ? b[1] : b[0], __shfl_xor_sync(kFull, odd ? b[0] : b[1], 2));
     }
-    const bool odd = lane & 2u;
-    return __fadd_rn(odd ? b[1] : b[0], __shfl_xor_sync(kFull, odd ? b[0] : b[1], 2));
 }
 
 // The halving fold over those lanes.
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v)
 {
-    if constexpr (L == kVectors) return halving_lanes(v);
-    if constexpr (L == kSingles) return halving_lanes_elem(v);
+    if constexpr (L == kVectors) {
+        return halving_lanes(v);
+    } else if constexpr (L == kSingles) {
+        return halving_lanes_elem(v);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 5; k++) {
-        constexpr int order[5] = {2, 1, 16, 8, 4};       // vector bits 4, 3, 2, 1, 0
-        v = __fadd_rn(v, __shfl_xor_sync(kFull, v, order[k]));
+        for (int k = 0; k < 5; k++) {
+            constexpr int order[5] = {2, 1, 16, 8, 4};       // vector bits 4, 3, 2, 1, 0
+            v = __fadd_rn(v, __shfl_xor_sync(kFull, v, order[k]));
+        }
+        return v;
     }
-    return v;
 }
 
 // team_sum (rowvec.cuh) of N values at once, with a barrier that the warps of a

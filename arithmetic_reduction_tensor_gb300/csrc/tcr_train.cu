@@ -184,7 +184,7 @@ tcr_status tcr_layernorm(const tcr_layernorm_args *args, void *stream)
     r.ldh = a.ldh;
     r.y = a.y;
     r.ldy = a.ldy;
-    r.scale = a.scale;
+    r.scale = a.y_dtype == TCR_I8 ? a.scale : nullptr;
     r.mean = a.mean;
     r.rstd = a.rstd;
     r.eps = a.eps;
@@ -196,7 +196,7 @@ tcr_status tcr_layernorm(const tcr_layernorm_args *args, void *stream)
     r.al_b = is_aligned(a.bias, 16);
     r.al_h = rows_aligned(a.h, a.ldh, a.rows, eb);
     r.al_y = a.y_dtype == TCR_I8 ? rows_aligned(a.y, a.ldy, a.rows, 1, 8) : rows_aligned(a.y, a.ldy, a.rows, eb);
-    return of(launch_layer(a.dtype, a.y_dtype == TCR_I8, r, (cudaStream_t)stream));
+    return of(launch_layer(a.dtype, r, (cudaStream_t)stream));
 }
 
 tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, void *stream)

@@ -60,7 +60,7 @@ struct XentGemm {
     uint32_t inject_stall;     // withhold the first tile's publication (tests of the failure path)
 };
 // Read maps of X, W and P; write maps of P, of dX's sums (rows of all splits) and of dW.
-struct alignas(64) XentMaps {
+struct XentMaps {
     CUtensorMap x, w, p, p_out, ws_out, dw_out;
 };
 int xent_pairs();

@@ -691,8 +691,9 @@ TCR_API tcr_status tcr_layernorm(const tcr_layernorm_args *args, void *stream);
  *          itself (same pointer and ld), not each other.  dweight, dbias: cols
  *          floats; overwritten.  Their order is that of tcr_rmsnorm_backward's
  *          dweight (no atomics) with another G: min(rows, max(152, min(152 c,
- *          ceil(rows / 2)))), where c is, for up to 1024, 2048, 4096 and more
- *          columns, 16, 8, 4 and 2, and of binary32 12, 6, 3 and (up to 6144) 2
+ *          ceil(rows / 2)))), where c is, for up to 128, 192, 320, 384, 640, 768,
+ *          896 and more vectors of 8 a row, 16, 12, 8, 5, 4, 2, 3 and 2, and of
+ *          binary32, for up to 128, 256, 384, 640, 768 and more, 12, 6, 4, 3, 2
  *          and 1.
  * Takes G * cols floats of pool scratch for each of dweight and dbias that is
  * wanted, and 2 rows more for cols > 8192.

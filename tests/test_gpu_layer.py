@@ -34,8 +34,8 @@ def of(drop):
     return {} if drop is None else dict(zip(("p", "seed", "offset"), drop))
 
 
-COLS = [1, 2, 7, 8, 9, 31, 100, 255, 256, 257, 500, 512, 513, 1001, 1024, 1025, 2048, 2049, 2999, 4096, 4099,
-        8192, 8200, 16384, 16391, 32769, 40000]
+COLS = [1, 2, 7, 8, 9, 31, 100, 255, 256, 257, 500, 512, 513, 1001, 1024, 1025, 1400, 2048, 2049, 2999, 4096, 4099,
+        5120, 5121, 6000, 7168, 7170, 8192, 8200, 12000, 16384, 16391, 32769, 40000]
 
 
 @pytest.mark.parametrize("dt", DTS)
@@ -212,7 +212,8 @@ def test_strides_and_alignment_do_not_change_bits(rows, cols, dt):
 
 
 @pytest.mark.parametrize("dt", DTS)
-@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 8), (3, 100), (200, 257), (700, 513), (5, 1000), (321, 2049), (157, 2600), (9, 4100),
+@pytest.mark.parametrize("rows,cols", [(1, 1), (2, 8), (3, 100), (200, 257), (700, 513), (5, 1000), (321, 2049), (157, 2600), (9, 4100), (401, 1400), (700, 5100),
+                                       (7, 6000), (5, 7000),
                                        (4, 8192), (3, 8200), (2, 20003)])
 def test_gradient_bits(rows, cols, dt):
     gen = torch.Generator().manual_seed(rows * cols)

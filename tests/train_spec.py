@@ -69,9 +69,9 @@ def layer(x, r, w, b, eps, drop=None):
 
 def groups(rows, cols, dtype):
     """The partial sums of the gradients of weight and bias."""
-    c = [(1024, 12), (2048, 6), (4096, 3), (6144, 2), (1 << 27, 1)] if dtype == torch.float32 else \
-        [(1024, 16), (2048, 8), (4096, 4), (1 << 27, 2)]
-    c = next(n for most, n in c if cols <= most)
+    c = [(128, 12), (256, 6), (384, 4), (640, 3), (768, 2), (1 << 24, 1)] if dtype == torch.float32 else \
+        [(128, 16), (192, 12), (320, 8), (384, 5), (640, 4), (768, 2), (896, 3), (1 << 24, 2)]
+    c = next(n for most, n in c if -(-cols // 8) <= most)
     return min(rows, max(152, min(152 * c, -(-rows // 2))))
 
 
