@@ -52,7 +52,12 @@ constexpr uint32_t kXTmemCols = kXDBuffers * kXentTile;
 constexpr int kXEpilogueWarps = 8;
 constexpr int kXThreads = 64 + 32 * kXEpilogueWarps;
 constexpr int kXGroup = 8;                         // tile rows per raster group (L2 reuse)
-constexpr int kXCols = kXentTile / 2;              // columns of an epilogue warp
+// Columns of a tile that an epilogue warp takes, and the warps that a tile's columns keep busy.
+template <int TN>
+struct XTile {
+    static constexpr int kCols = TN < 128 ? TN : 128, kWarps = 4 * (TN / kCols);
+    static constexpr int kBBytes = TN / 2 * kXBox * 2;       // B's share of a stage per CTA
+};
 constexpr int kXOutBytes = 32 * 128;               // its staging: 32 rows of 128 swizzled bytes
 // The ring, the staging (not in the forward pass, whose ring is longer for it)
 // and the barriers: full[S] (leader's: both CTAs' copies), empty[S], dfull[D],
@@ -110,13 +115,13 @@ __device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn)
            (2ull << 61);
 }
 
-// kind::f16, M = N = 256, fp32 sums; bits 15 and 16: A and B MN-major.
-template <int DT>
+// kind::f16, M = 256, N = TN, fp32 sums; bits 15 and 16: A and B MN-major.
+template <int DT, int TN>
 __device__ __forceinline__ uint32_t operand_instr(bool a_mn, bool b_mn)
 {
     constexpr uint32_t ab = DT == kF16 ? 0u : 1u;
     return (1u << 4) | (ab << 7) | (ab << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-           ((uint32_t)(kXentTile >> 3) << 17) | ((uint32_t)(kXentTile >> 4) << 24);
+           ((uint32_t)(TN >> 3) << 17) | ((uint32_t)(kXentTile >> 4) << 24);
 }
 
 // One tile's work: 64-boxes [k0, k0 + nk) of K; of A's four boxes of rows the
@@ -134,11 +139,11 @@ struct XUnits {
     int xm, xn, xnk, xkps, xsplits;    // dX: tiles, boxes of K, boxes a split
     int nx, nd, lead, rem;
 
-    __device__ __forceinline__ XUnits(const XentGemm &g, int n_, int mode_) : mode(mode_), n(n_)
+    __device__ __forceinline__ XUnits(const XentGemm &g, int n_, int mode_, int tile_cols) : mode(mode_), n(n_)
     {
         pairs = (int)(gridDim.x >> 1);
         pair = (int)(blockIdx.x >> 1);
-        const int rows = (n + kXentTile - 1) / kXentTile, cols = (g.vn + kXentTile - 1) / kXentTile;
+        const int rows = (n + kXentTile - 1) / kXentTile, cols = (g.vn + tile_cols - 1) / tile_cols;
         nx = 0;
         lead = rem = 0;
         xm = xn = xnk = xkps = xsplits = 0;
@@ -220,31 +225,32 @@ struct XUnits {
 // ld and the stores.
 
 // The largest logit of the row among the warp's columns and the sum about it.
-__device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int part, float (&v)[kXCols])
+template <int COLS>
+__device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int part, float (&v)[COLS])
 {
-    const int col0 = part * kXCols, left = g.V - col0;
+    const int col0 = part * COLS, left = g.V - col0;
     const int at = g.lab[row] - col0;
-    if (left < kXCols) {
+    if (left < COLS) {
 #pragma unroll
-        for (int j = 0; j < kXCols; j++)
+        for (int j = 0; j < COLS; j++)
             if (j >= left) v[j] = -INFINITY;
     }
     float hit = 0.0f;
-    if (at >= 0 && at < kXCols) {
+    if (at >= 0 && at < COLS) {
 #pragma unroll
-        for (int j = 0; j < kXCols; j++)
+        for (int j = 0; j < COLS; j++)
             if (j == at) hit = v[j];
     }
     float m[4] = {v[0], v[1], v[2], v[3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 4; j < kXCols; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
+    for (int j = 4; j < COLS; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
     const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
     const float about = mx == -INFINITY ? 0.0f : -__fmul_rn(mx, kLog2e);
 #pragma unroll
-    for (int j = 0; j < kXCols; j++) e[j & 3] = __fadd_rn(e[j & 3], ex2(__fmaf_rn(v[j], kLog2e, about)));
+    for (int j = 0; j < COLS; j++) e[j & 3] = __fadd_rn(e[j & 3], ex2(__fmaf_rn(v[j], kLog2e, about)));
     const float s = __fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3]));
     g.part[(size_t)part * g.tpad + row] = make_float2(mx, s);
-    if (at >= 0 && at < kXCols) g.hit[row] = hit;
+    if (at >= 0 && at < COLS) g.hit[row] = hit;
 }
 
 // A warp's staging: 32 rows of 128 bytes, 16-byte granule k of row r at granule k ^
@@ -284,7 +290,7 @@ struct XOut {
 // P of the row: (exp(l - lse) - [target]) * g, in units of the largest |g| so
 // that the target's -1 times a common g is exact (binary16: times 2^15 on top,
 // which keeps probabilities of 2^-29 normal).
-template <int DT, class Ld>
+template <int DT, int COLS, class Ld>
 __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
                                                   int n, int col0, Ld ld)
 {
@@ -304,7 +310,7 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
     const int left = gq == 0.0f ? 0 : g.vn - col0;
     if (row0 >= (n + kXBox - 1) / kXBox * kXBox) return;     // not read: dW's K ends with the tokens' last box
 #pragma unroll 1
-    for (int c = 0; c < kXCols / 64; c++) {
+    for (int c = 0; c < COLS / 64; c++) {
         uint32_t o[32];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -332,7 +338,7 @@ __device__ __forceinline__ void epilogue_dx(const XentGemm &g, const CUtensorMap
                                             int n, int split, int col0, Ld ld)
 {
 #pragma unroll 1
-    for (int c = 0; c < kXCols / 32; c++) {
+    for (int c = 0; c < XTile<kXentTile>::kCols / 32; c++) {
         float v[32];
         ld(c, v);
         if ((size_t)(col0 + 32 * c) >= g.ldws || row0 >= n) continue;
@@ -359,7 +365,7 @@ __device__ __forceinline__ void epilogue_dw(const XentGemm &g, const CUtensorMap
     float scale = __uint_as_float(g.head[1]);
     if (DT == kF16) scale = __fmul_rn(scale, 1.0f / kXentF16Scale);
 #pragma unroll 1
-    for (int c = 0; c < kXCols / 64; c++) {
+    for (int c = 0; c < XTile<kXentTile>::kCols / 64; c++) {
         uint32_t o[32];
 #pragma unroll
         for (int h = 0; h < 2; h++) {
@@ -404,12 +410,15 @@ __device__ __forceinline__ void epilogue_dw(const XentGemm &g, const CUtensorMap
 
 // ---------------------------------------------------------------- the kernel
 
-template <int DT, int MODE>
+// TN: columns of a tile, 256; of the logits also 64, where 256 would leave most of
+// the SMs without a tile (64 tokens x 2048 over 1000: TODOA us, with 256 16.8).
+template <int DT, int MODE, int TN>
 __global__ void __launch_bounds__(kXThreads, 1)
 xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
 {
     pdl_launch_dependents();
     using Y = XLayout<MODE>;
+    using N = XTile<TN>;
     constexpr int kStages = Y::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -434,14 +443,15 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
         }
         for (int b = 0; b < kXDBuffers; b++) {
             mbar_init(dfull_bar(b), 1);
-            mbar_init(dempty_bar(b), 2 * kXEpilogueWarps);        // both CTAs' epilogues
+            mbar_init(dempty_bar(b), 2 * N::kWarps);              // both CTAs' epilogues
         }
         mbar_init(drain_bar, 1);
         *abort = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&maps.x) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&maps.w) : "memory");
-        if (MODE == kXentBack) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&maps.p) : "memory");
+        auto fetch = [](const CUtensorMap *m) { asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory"); };
+        fetch(&maps.x);
+        fetch(MODE == kXentBack ? &maps.p : &maps.x128);
+        fetch(MODE == kXentBack ? &maps.w : TN == 64 ? &maps.w32 : &maps.w128);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (warp == 1) {
@@ -457,25 +467,29 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
     const uint32_t tmem = *tmem_holder;
     pdl_wait_primary();
     const int n = (int)g.head[0];
-    const XUnits units(g, n, MODE);
+    const XUnits units(g, n, MODE, TN);
 
     if (warp == 0) {
         // ---------------- producer: this CTA's halves; completion on the leader's full barrier
         if (lane == 0) {
             int st = 0;
-            uint32_t phase = 0;
-            bool armed[kStages];
-            uint32_t armed_phase[kStages];
-            for (int i = 0; i < kStages; i++) {
-                armed[i] = false;
-                armed_phase[i] = 0;
-            }
+            uint32_t phase = 0, armed = 0;                   // stages armed so far, in turn
+            const uint32_t full0 = map_to_rank(full_bar(0), 0u);
             XUnit u;
             for (int i = 0; !*abort && units.get(i, u); i++) {
-                const int m0 = u.tm * kXentTile + kXHalf * (int)rank, n0 = u.tn * kXentTile + kXHalf * (int)rank;
-                const CUtensorMap *ma = MODE == kXentBack ? &maps.p : &maps.x;
-                const CUtensorMap *mb = MODE != kXentBack || u.x ? &maps.w : &maps.x;
+                const int m0 = u.tm * kXentTile + kXHalf * (int)rank, n0 = u.tn * TN + TN / 2 * (int)rank;
                 const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
+                // K-major operands come in boxes of all their rows, 128 (A: or 64) or 32; MN-major
+                // ones in two of 64 x 64
+                const int a_boxes = min(2, max(0, u.rows - 2 * (int)rank));
+                const bool a_whole = !a_mn && a_boxes == 2;
+                const CUtensorMap *ma = MODE == kXentBack ? (a_whole ? &maps.p128 : &maps.p)
+                                                          : (a_whole ? &maps.x128 : &maps.x);
+                const CUtensorMap *mb = TN == 64            ? &maps.w32
+                                        : MODE != kXentBack ? &maps.w128
+                                        : u.x               ? &maps.w
+                                                            : &maps.x;
+                const uint32_t bytes = (uint32_t)(u.rows * kXBoxBytes + 2 * N::kBBytes);
                 // the vocabulary's coordinate counts from the piece's first entry in P only
                 const int b_row = MODE == kXentBack ? (u.x ? g.v0 : 0) : n0 + g.v0;
                 bool ok = true;
@@ -484,27 +498,22 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = ring + (uint32_t)st * kXStageBytes;
+                    const uint32_t dst = ring + (uint32_t)st * kXStageBytes, fb = full0 + 8u * (uint32_t)st;
                     const int kc = (u.k0 + j) * kXBox;
-                    const uint32_t fb = map_to_rank(full_bar(st), 0u);
-                    if (leader) mbar_arrive_expect_tx(full_bar(st), (uint32_t)((u.rows + 4) * kXBoxBytes));
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (2 * (int)rank + h >= u.rows) break;
-                        if (a_mn)
-                            tma_load_2d_pair(dst + h * kXBoxBytes, ma, m0 + h * kXBox, kc, fb);
-                        else
-                            tma_load_2d_pair(dst + h * kXBoxBytes, ma, kc, m0 + h * kXBox, fb);
+                    if (leader) mbar_arrive_expect_tx(full_bar(st), bytes);
+                    if (a_mn) {
+                        tma_load_2d_pair(dst, ma, m0, kc, fb);
+                        tma_load_2d_pair(dst + kXBoxBytes, ma, m0 + kXBox, kc, fb);
+                    } else if (a_boxes > 0) {
+                        tma_load_2d_pair(dst, ma, kc, m0, fb);
                     }
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (b_mn)
-                            tma_load_2d_pair(dst + kXHalfBytes + h * kXBoxBytes, mb, n0 + h * kXBox, b_row + kc, fb);
-                        else
-                            tma_load_2d_pair(dst + kXHalfBytes + h * kXBoxBytes, mb, kc, b_row + h * kXBox, fb);
+                    if (b_mn) {
+                        tma_load_2d_pair(dst + kXHalfBytes, mb, n0, b_row + kc, fb);
+                        tma_load_2d_pair(dst + kXHalfBytes + kXBoxBytes, mb, n0 + kXBox, b_row + kc, fb);
+                    } else {
+                        tma_load_2d_pair(dst + kXHalfBytes, mb, kc, b_row, fb);
                     }
-                    armed[st] = true;
-                    armed_phase[st] = phase;
+                    armed++;
                     if (++st == kStages) {
                         st = 0;
                         phase ^= 1u;
@@ -514,8 +523,8 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             }
             if (*abort && leader) {
                 // the full barriers count both CTAs' copies: let them land
-                for (int i = 0; i < kStages; i++)
-                    if (armed[i]) (void)mbar_wait_limited(full_bar(i), armed_phase[i]);
+                for (uint32_t i = armed < (uint32_t)kStages ? 0u : armed - kStages; i < armed; i++)
+                    (void)mbar_wait_limited(full_bar((int)(i % kStages)), (i / kStages) & 1u);
             }
         }
         __syncwarp();
@@ -528,7 +537,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             XUnit u;
             for (int i = 0; !*abort && units.get(i, u); i++) {
                 const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
-                const uint32_t idesc = operand_instr<DT>(a_mn, b_mn);
+                const uint32_t idesc = operand_instr<DT, TN>(a_mn, b_mn);
                 const uint64_t a_ring = operand_desc(ring, a_mn), b_ring = operand_desc(ring + kXHalfBytes, b_mn);
                 const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
                 bool ok = true;
@@ -575,7 +584,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
     } else {
         // ---------------- epilogue: a warp takes 32 rows and 128 columns of the tile
         const int q = warp & 3, half = (warp - 2) >> 2;          // (a warp reads the lanes of its number mod 4)
-        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * kXCols);
+        const uint32_t base = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(half * N::kCols);
         const XOut out = {smem + Y::kOffOut + (warp - 2) * kXOutBytes,
                           ring + (uint32_t)(Y::kOffOut + (warp - 2) * kXOutBytes)};
         int b = 0;
@@ -596,17 +605,17 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             b ^= 1;
         };
         XUnit u;
-        for (int i = 0; units.get(i, u); i++) {
-            const int row0 = u.tm * kXentTile + kXHalf * (int)rank + 32 * q, col0 = u.tn * kXentTile + half * kXCols;
+        for (int i = 0; warp - 2 < N::kWarps && units.get(i, u); i++) {
+            const int row0 = u.tm * kXentTile + kXHalf * (int)rank + 32 * q, col0 = u.tn * TN + half * N::kCols;
             if constexpr (MODE == kXentForward) {
-                float v[kXCols];
+                float v[N::kCols];
 #pragma unroll
-                for (int j = 0; j < kXCols; j++) v[j] = 0.0f;
+                for (int j = 0; j < N::kCols; j++) v[j] = 0.0f;
 #pragma unroll 1
                 for (int j0 = 0; j0 < u.nk; j0 += kXChain) {
                     begin();
 #pragma unroll
-                    for (int c = 0; c < kXCols / 16; c++) {
+                    for (int c = 0; c < N::kCols / 16; c++) {
                         float f[16];
                         __syncwarp();
                         if (live) {
@@ -620,7 +629,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     }
                     done();
                 }
-                if (row0 < n) epilogue_forward(g, (size_t)(row0 + lane), 2 * u.tn + half, v);
+                if (row0 < n) epilogue_forward<N::kCols>(g, (size_t)(row0 + lane), u.tn * (TN / N::kCols) + half, v);
                 continue;
             }
             begin();
@@ -637,7 +646,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                 }
             };
             if constexpr (MODE == kXentGradient)
-                epilogue_gradient<DT>(g, &maps.p_out, out, row0, n, col0, ld);
+                epilogue_gradient<DT, N::kCols>(g, &maps.p_out, out, row0, n, col0, ld);
             else if (u.x)
                 epilogue_dx(g, &maps.ws_out, out, row0, n, u.split, col0, ld);
             else
@@ -664,15 +673,20 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
 
 namespace {
 
-const void *xent_pick(int dtype, int mode)
+template <int DT>
+const void *xent_pick(int mode, bool narrow)
 {
-    if (dtype == kF16)
-        return mode == kXentForward    ? (const void *)xent_kernel<kF16, kXentForward>
-               : mode == kXentGradient ? (const void *)xent_kernel<kF16, kXentGradient>
-                                       : (const void *)xent_kernel<kF16, kXentBack>;
-    return mode == kXentForward    ? (const void *)xent_kernel<kBF16, kXentForward>
-           : mode == kXentGradient ? (const void *)xent_kernel<kBF16, kXentGradient>
-                                   : (const void *)xent_kernel<kBF16, kXentBack>;
+    if (mode == kXentForward)
+        return narrow ? (const void *)xent_kernel<DT, kXentForward, 64> : (const void *)xent_kernel<DT, kXentForward, 256>;
+    if (mode == kXentGradient)
+        return narrow ? (const void *)xent_kernel<DT, kXentGradient, 64>
+                      : (const void *)xent_kernel<DT, kXentGradient, 256>;
+    return (const void *)xent_kernel<DT, kXentBack, 256>;
+}
+
+const void *xent_pick(int dtype, int mode, bool narrow)
+{
+    return dtype == kF16 ? xent_pick<kF16>(mode, narrow) : xent_pick<kBF16>(mode, narrow);
 }
 
 int xent_smem(int mode)
@@ -719,12 +733,13 @@ int xent_pairs()
     bool ok = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
     for (int dt : {kF16, kBF16})
         for (int mode : {kXentForward, kXentGradient, kXentBack})
-            ok = ok && set_smem_once((void *)xent_pick(dt, mode), xent_smem(mode)) == cudaSuccess;
+            for (bool narrow : {false, true})
+                ok = ok && set_smem_once((void *)xent_pick(dt, mode, narrow), xent_smem(mode)) == cudaSuccess;
     if (ok) {
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = pair_config(kXentBack, sms / 2, attr, nullptr);
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack), &cfg) != cudaSuccess) n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack, false), &cfg) != cudaSuccess) n = 0;
     }
     (void)cudaGetLastError();
     std::lock_guard<std::mutex> lk(mu);
@@ -732,13 +747,13 @@ int xent_pairs()
     return n;
 }
 
-// A matrix of 16-bit values (or, `wide`, of binary32) read in boxes of 64 x 64 or
-// written in boxes of 128 bytes x 32 rows.
-cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, bool out, bool wide)
+// A matrix of 16-bit values (or, `wide`, of binary32) in boxes of 128 bytes x 64 or
+// 32 rows.
+cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, int box_rows, bool wide)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (!encode) return cudaErrorNotSupported;
-    const cuuint32_t box[2] = {wide ? 32u : (cuuint32_t)kXBox, out ? 32u : (cuuint32_t)kXBox}, step[2] = {1, 1};
+    const cuuint32_t box[2] = {wide ? 32u : (cuuint32_t)kXBox, (cuuint32_t)box_rows}, step[2] = {1, 1};
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, pitch[1] = {(cuuint64_t)ld * (wide ? 4 : 2)};
     return encode(map, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, (void *)base, dims,
                   pitch, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -747,13 +762,19 @@ cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t row
                : cudaErrorInvalidValue;
 }
 
+int xent_tile_cols(size_t tokens, size_t vn, int pairs)
+{
+    const size_t tiles = ((tokens + kXentTile - 1) / kXentTile) * ((vn + kXentTile - 1) / kXentTile);
+    return 2 * tiles <= (size_t)pairs ? 64 : kXentTile;
+}
+
 cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
-                        cudaStream_t stream)
+                        int tile_cols, cudaStream_t stream)
 {
     void *args[] = {(void *)&maps, (void *)&g};
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = pair_config(mode, (int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);
-    return cudaLaunchKernelExC(&cfg, xent_pick(dtype, mode), args);
+    return cudaLaunchKernelExC(&cfg, xent_pick(dtype, mode, tile_cols == 64), args);
 }
 
 cudaError_t read_xent_faults(unsigned int *flags, bool clear)

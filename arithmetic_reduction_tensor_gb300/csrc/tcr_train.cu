@@ -118,9 +118,12 @@ cudaError_t xent_prepare(XentTokens &k, const XentSizes &z, const XentCommon &c,
         ldw = z.ldX;            // not looked at by the caller; the map wants a pitch
     }
     cudaError_t e = launch_xent_tokens(k, s);
-    if (e == cudaSuccess) e = xent_map(&maps.x, k.X, z.H, z.tpad, z.ldX);
-    if (e == cudaSuccess) e = xent_map(&maps.w, w, z.H, z.V, ldw);
-    maps.p = maps.p_out = maps.ws_out = maps.dw_out = maps.x;      // (those that are not used)
+    if (e == cudaSuccess) e = xent_map(&maps.x, k.X, z.H, z.tpad, z.ldX, 64);
+    if (e == cudaSuccess) e = xent_map(&maps.w, w, z.H, z.V, ldw, 64);
+    if (e == cudaSuccess) e = xent_map(&maps.x128, k.X, z.H, z.tpad, z.ldX, 128);
+    if (e == cudaSuccess) e = xent_map(&maps.w128, w, z.H, z.V, ldw, 128);
+    if (e == cudaSuccess) e = xent_map(&maps.w32, w, z.H, z.V, ldw, 32);
+    maps.p = maps.p128 = maps.p_out = maps.ws_out = maps.dw_out = maps.x;      // (those that are not used)
     return e;
 }
 
@@ -272,11 +275,13 @@ try {
     if (pairs < 1) return TCR_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     const XentSizes z = xent_sizes(a.weight, a.ldw, a.tokens, a.vocab, a.hidden);
-    const size_t tiles_v = (z.V + kXentTile - 1) / kXentTile;
+    const int tile = xent_tile_cols(z.T, z.V, pairs);
+    const size_t tiles_v = (z.V + (size_t)tile - 1) / (size_t)tile;
+    const size_t n_parts = tiles_v * (size_t)(tile / xent_part_cols(tile));
     Parts parts;
     XentCommon c;
     c.place(parts, z);
-    const size_t at_part = parts.add(2 * tiles_v * z.tpad * sizeof(float2)), at_hit = parts.add(z.tpad * 4);
+    const size_t at_part = parts.add(n_parts * z.tpad * sizeof(float2)), at_hit = parts.add(z.tpad * 4);
     Scratch scratch(s);
     if ((st = scratch.take(parts.bytes, dev)) != TCR_OK) return st;
     if (fault_injected("launch")) return TCR_ERR_CUDA;
@@ -303,9 +308,9 @@ try {
         g.part = (float2 *)(base + at_part);
         g.hit = (float *)(base + at_hit);
         g.inject_stall = fault_injected("stall");
-        e = launch_xent(a.dtype, kXentForward, maps, g, (size_t)z.tiles_t * tiles_v, pairs, s);
+        e = launch_xent(a.dtype, kXentForward, maps, g, (size_t)z.tiles_t * tiles_v, pairs, tile, s);
         if (e == cudaSuccess) {
-            XentLoss l = {g.part, g.hit, k.rank, k.lab, z.tpad, z.T, 2 * (int)tiles_v, a.loss, a.lse};
+            XentLoss l = {g.part, g.hit, k.rank, k.lab, z.tpad, z.T, (int)n_parts, a.loss, a.lse};
             e = launch_xent_loss(l, s);
         }
     }
@@ -370,13 +375,14 @@ try {
     k.inc_dloss = a.inc_dloss;
     XentMaps maps;
     cudaError_t e = xent_prepare(k, z, c, base, a.weight, a.ldw, maps, s);
-    if (e == cudaSuccess) e = xent_map(&maps.p, base + at_P, piece, z.tpad, piece);
-    if (e == cudaSuccess) e = xent_map(&maps.p_out, base + at_P, piece, z.tpad, piece, true);
-    if (e == cudaSuccess && a.dx) e = xent_map(&maps.ws_out, base + at_ws, ldws, splits * z.tpad, ldws, true, true);
+    if (e == cudaSuccess) e = xent_map(&maps.p, base + at_P, piece, z.tpad, piece, 64);
+    if (e == cudaSuccess) e = xent_map(&maps.p128, base + at_P, piece, z.tpad, piece, 128);
+    if (e == cudaSuccess) e = xent_map(&maps.p_out, base + at_P, piece, z.tpad, piece, 32);
+    if (e == cudaSuccess && a.dx) e = xent_map(&maps.ws_out, base + at_ws, ldws, splits * z.tpad, ldws, 32, true);
     // a tensor-map store writes whole granules of 16 bytes, past a row's end as well
     const bool al_dw = rows_aligned(a.dweight, a.lddw, z.V, 2) && z.H % 8 == 0;
     if (e == cudaSuccess && a.dweight && al_dw)
-        e = xent_map(&maps.dw_out, a.dweight, z.H, z.V, z.V == 1 ? z.ldX : a.lddw, true);
+        e = xent_map(&maps.dw_out, a.dweight, z.H, z.V, z.V == 1 ? z.ldX : a.lddw, 32);
     XentGemm g = {};
     g.head = k.head;
     g.lab = k.lab;
@@ -401,9 +407,11 @@ try {
         g.vn = (int)(z.V - v0 < piece ? z.V - v0 : piece);
         g.first = v0 == 0;
         const size_t tiles_v = ((size_t)g.vn + kXentTile - 1) / kXentTile;
-        e = launch_xent(a.dtype, kXentGradient, maps, g, (size_t)z.tiles_t * tiles_v, pairs, s);
+        const int tile = xent_tile_cols(z.T, (size_t)g.vn, pairs);
+        const size_t logits = (size_t)z.tiles_t * (((size_t)g.vn + (size_t)tile - 1) / (size_t)tile);
+        e = launch_xent(a.dtype, kXentGradient, maps, g, logits, pairs, tile, s);
         const size_t units = (g.ws ? tiles_x * splits : 0) + (g.dw ? tiles_v * tiles_h : 0);
-        if (e == cudaSuccess) e = launch_xent(a.dtype, kXentBack, maps, g, units, pairs, s);
+        if (e == cudaSuccess) e = launch_xent(a.dtype, kXentBack, maps, g, units, pairs, kXentTile, s);
     }
     if (e == cudaSuccess && a.dx) {
         XentDx d = {g.ws, z.tpad, ldws, (int)splits, k.rank, k.head, z.T, z.H, a.dx, a.lddx,

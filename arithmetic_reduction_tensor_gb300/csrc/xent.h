@@ -43,7 +43,7 @@ struct XentGemm {
     int V, H;
     int v0, vn;                // the piece of the vocabulary (the forward pass: all of it)
     // forward
-    float2 *part;              // [half a tile of the vocabulary][row]: largest logit, sum about it
+    float2 *part;              // [part of the vocabulary][row]: largest logit, sum about it
     float *hit;                // the target's logit
     // gradient
     const float *lse, *dloss;
@@ -59,15 +59,18 @@ struct XentGemm {
     bool al_dw;
     uint32_t inject_stall;     // withhold the first tile's publication (tests of the failure path)
 };
-// Read maps of X, W and P; write maps of P, of dX's sums (rows of all splits) and of dW.
+// Read maps of X, W and P, in boxes of 64 rows or of the number named; write maps of P, of dX's sums (rows of all splits) and of dW.
 struct XentMaps {
-    CUtensorMap x, w, p, p_out, ws_out, dw_out;
+    CUtensorMap x, x128, w, w128, w32, p, p128, p_out, ws_out, dw_out;
 };
 int xent_pairs();
-cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, bool out = false,
+cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, int box_rows,
                      bool wide = false);
+// Columns of the logits' tiles over vn entries of the vocabulary, 256 or 64, and of a part.
+int xent_tile_cols(size_t tokens, size_t vn, int pairs);
+inline int xent_part_cols(int tile_cols) { return tile_cols < 128 ? tile_cols : 128; }
 cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
-                        cudaStream_t stream);
+                        int tile_cols, cudaStream_t stream);
 
 // loss and lse of every token from its tiles' parts.
 struct XentLoss {

@@ -735,7 +735,7 @@ TCR_API tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, v
  * lse and loss NaN.  What tokens that are ignored hold is not looked at.
  * tokens < 2^24, vocab < 2^27, hidden < 2^20 (else TCR_ERR_UNSUPPORTED), vocab and hidden not 0,
  * tokens * vocab and vocab * hidden < 2^40.  Takes pool scratch of 2 bytes per
- * element of x, 8 per token and 128 entries of the vocabulary, and, where
+ * element of x, 8 per token and 128 entries of the vocabulary (64 where these are few), and, where
  * weight's rows are not 16-byte aligned, 2 per element of weight.  No atomics: the bits
  * depend on the inputs only.
  */
