@@ -45,7 +45,6 @@ constexpr int kXBox = 64;                          // rows and columns of a box
 constexpr int kXBoxBytes = kXBox * kXBox * 2;      // 8 KiB
 constexpr int kXHalf = 128;                        // rows of an operand per CTA
 constexpr int kXHalfBytes = 2 * kXBoxBytes;
-constexpr int kXStageBytes = 2 * kXHalfBytes;      // 32 KiB: both operands
 constexpr int kXChain = 16;                        // boxes of K the forward pass adds up in one chain
 constexpr int kXDBuffers = 2;
 constexpr uint32_t kXTmemCols = kXDBuffers * kXentTile;
@@ -57,15 +56,16 @@ template <int TN>
 struct XTile {
     static constexpr int kCols = TN < 128 ? TN : 128, kWarps = 4 * (TN / kCols);
     static constexpr int kBBytes = TN / 2 * kXBox * 2;       // B's share of a stage per CTA
+    static constexpr int kStageBytes = kXHalfBytes + kBBytes;
 };
 constexpr int kXOutBytes = 32 * 128;               // its staging: 32 rows of 128 swizzled bytes
 // The ring, the staging (not in the forward pass, whose ring is longer for it)
 // and the barriers: full[S] (leader's: both CTAs' copies), empty[S], dfull[D],
 // dempty[D] (leader's), drain.
-template <int MODE>
+template <int MODE, int TN>
 struct XLayout {
-    static constexpr int kStages = MODE == kXentForward ? 7 : 6;
-    static constexpr int kOffOut = kStages * kXStageBytes;
+    static constexpr int kStages = (MODE == kXentForward ? 224 : 192) * 1024 / XTile<TN>::kStageBytes;
+    static constexpr int kOffOut = kStages * XTile<TN>::kStageBytes;
     static constexpr int kOffBars = kOffOut + (MODE == kXentForward ? 0 : kXEpilogueWarps * kXOutBytes);
     static constexpr int kNumBars = 2 * kStages + 2 * kXDBuffers + 1;
     static constexpr int kOffMisc = kOffBars + 8 * kNumBars;
@@ -410,14 +410,17 @@ __device__ __forceinline__ void epilogue_dw(const XentGemm &g, const CUtensorMap
 
 // ---------------------------------------------------------------- the kernel
 
-// TN: columns of a tile, 256; of the logits also 64, where 256 would leave most of
-// the SMs without a tile (64 tokens x 2048 over 1000: TODOA us, with 256 16.8).
+// TN: columns of a tile, 256; of the logits also 64, where every such tile has a
+// pair to itself.  A box of K takes the MMAs as long either way (their A, 128 rows
+// an SM, comes from shared memory at 128 cycles a slice of 16), so a narrow tile
+// saves its epilogue's time alone: 64 tokens x 2048 over 1000 15.2 us, 16.8 with
+// 256 columns.
 template <int DT, int MODE, int TN>
 __global__ void __launch_bounds__(kXThreads, 1)
 xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
 {
     pdl_launch_dependents();
-    using Y = XLayout<MODE>;
+    using Y = XLayout<MODE, TN>;
     using N = XTile<TN>;
     constexpr int kStages = Y::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -498,7 +501,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = ring + (uint32_t)st * kXStageBytes, fb = full0 + 8u * (uint32_t)st;
+                    const uint32_t dst = ring + (uint32_t)st * N::kStageBytes, fb = full0 + 8u * (uint32_t)st;
                     const int kc = (u.k0 + j) * kXBox;
                     if (leader) mbar_arrive_expect_tx(full_bar(st), bytes);
                     if (a_mn) {
@@ -556,7 +559,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t at = (uint64_t)st * (uint64_t)(kXStageBytes >> 4);
+                        const uint64_t at = (uint64_t)st * (uint64_t)(N::kStageBytes >> 4);
 #pragma unroll
                         for (int k = 0; k < 4; k++)
                             tc_mma_pair(d, a_ring + at + (uint64_t)k * a_step, b_ring + at + (uint64_t)k * b_step, idesc,
@@ -689,17 +692,20 @@ const void *xent_pick(int dtype, int mode, bool narrow)
     return dtype == kF16 ? xent_pick<kF16>(mode, narrow) : xent_pick<kBF16>(mode, narrow);
 }
 
-int xent_smem(int mode)
+int xent_smem(int mode, bool narrow)
 {
-    return mode == kXentForward ? XLayout<kXentForward>::kSmemBytes : XLayout<kXentBack>::kSmemBytes;
+    if (mode == kXentForward)
+        return narrow ? XLayout<kXentForward, 64>::kSmemBytes : XLayout<kXentForward, 256>::kSmemBytes;
+    if (mode == kXentGradient && narrow) return XLayout<kXentGradient, 64>::kSmemBytes;
+    return XLayout<kXentBack, 256>::kSmemBytes;
 }
 
-cudaLaunchConfig_t pair_config(int mode, int pairs, cudaLaunchAttribute (&attr)[2], cudaStream_t stream)
+cudaLaunchConfig_t pair_config(int mode, bool narrow, int pairs, cudaLaunchAttribute (&attr)[2], cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
     cfg.blockDim = dim3(kXThreads);
-    cfg.dynamicSmemBytes = (size_t)xent_smem(mode);
+    cfg.dynamicSmemBytes = (size_t)xent_smem(mode, narrow);
     cfg.stream = stream;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -734,10 +740,10 @@ int xent_pairs()
     for (int dt : {kF16, kBF16})
         for (int mode : {kXentForward, kXentGradient, kXentBack})
             for (bool narrow : {false, true})
-                ok = ok && set_smem_once((void *)xent_pick(dt, mode, narrow), xent_smem(mode)) == cudaSuccess;
+                ok = ok && set_smem_once((void *)xent_pick(dt, mode, narrow), xent_smem(mode, narrow)) == cudaSuccess;
     if (ok) {
         cudaLaunchAttribute attr[2];
-        cudaLaunchConfig_t cfg = pair_config(kXentBack, sms / 2, attr, nullptr);
+        cudaLaunchConfig_t cfg = pair_config(kXentBack, false, sms / 2, attr, nullptr);
         cfg.numAttrs = 1;
         if (cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack, false), &cfg) != cudaSuccess) n = 0;
     }
@@ -764,8 +770,8 @@ cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t row
 
 int xent_tile_cols(size_t tokens, size_t vn, int pairs)
 {
-    const size_t tiles = ((tokens + kXentTile - 1) / kXentTile) * ((vn + kXentTile - 1) / kXentTile);
-    return 2 * tiles <= (size_t)pairs ? 64 : kXentTile;
+    const size_t narrow = ((tokens + kXentTile - 1) / kXentTile) * ((vn + 63) / 64);
+    return narrow <= (size_t)pairs ? 64 : kXentTile;
 }
 
 cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
@@ -773,7 +779,7 @@ cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGem
 {
     void *args[] = {(void *)&maps, (void *)&g};
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = pair_config(mode, (int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);
+    cudaLaunchConfig_t cfg = pair_config(mode, tile_cols == 64, (int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);
     return cudaLaunchKernelExC(&cfg, xent_pick(dtype, mode, tile_cols == 64), args);
 }
 
