@@ -229,7 +229,8 @@ template <int COLS>
 __device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int part, float (&v)[COLS])
 {
     const int col0 = part * COLS, left = g.V - col0;
-    const int at = g.lab[row] - col0;
+    const int lab = g.head ? g.lab[row] : row < (size_t)g.n ? xent_label(g.target[row], (size_t)g.V) : -1;
+    const int at = lab - col0;
     if (left < COLS) {
 #pragma unroll
         for (int j = 0; j < COLS; j++)
@@ -469,7 +470,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     pdl_wait_primary();
-    const int n = (int)g.head[0];
+    const int n = g.head ? (int)g.head[0] : g.n;
     const XUnits units(g, n, MODE, TN);
 
     if (warp == 0) {

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kTokThreads) xent_tokens_kernel(const XentToke
         ranks[threadIdx.x] = live ? r : -1;
         if (t < last) a.rank[t] = live ? r : -1;
         if (live) {
-            a.lab[r] = y >= 0 && y < (long long)a.V ? (int)y : -1;
+            a.lab[r] = xent_label(y, a.V);
             a.tok[r] = (int)t;
         }
         __syncthreads();
@@ -144,7 +144,18 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
     __shared__ float red[2][kLossThreads / 32][kLossTokens];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = threadIdx.x % kLossTokens;
     const size_t t = (size_t)blockIdx.x * kLossTokens + k;
-    const int r = t < a.tokens ? a.rank[t] : -1, first = (int)threadIdx.x / kLossTokens;
+    const int first = (int)threadIdx.x / kLossTokens;
+    int r = -1, lab = -1;
+    if (t < a.tokens) {
+        if (a.rank) {
+            r = a.rank[t];
+            if (r >= 0) lab = a.lab[r];
+        } else {
+            const long long y = a.target[t];
+            if (y != a.ignore) r = (int)t;
+            lab = xent_label(y, a.V);
+        }
+    }
     float m = -INFINITY, s = 0.0f;
     if (r >= 0) {
         // two passes over the parts (8 bytes for 128 logits): the largest, then the sum about it
@@ -179,7 +190,7 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
 #pragma unroll
         for (int w = 0; w < kLossThreads / 32; w++) s = __fadd_rn(s, red[1][w][k]);
         lse = __fmul_rn(__fadd_rn(about, log2f(s)), ln2);
-        loss = a.lab[r] < 0 ? __int_as_float(0x7fc00000) : __fsub_rn(lse, a.hit[r]);
+        loss = lab < 0 ? __int_as_float(0x7fc00000) : __fsub_rn(lse, a.hit[r]);
     }
     a.loss[t] = loss;
     if (a.lse) a.lse[t] = lse;

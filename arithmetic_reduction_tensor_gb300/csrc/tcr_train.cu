@@ -98,6 +98,19 @@ struct XentCommon {
     }
 };
 
+// The maps of X (rows of ldx elements) and W; those of the gradient are not used.
+cudaError_t xent_read_maps(XentMaps &maps, const void *x, size_t ldx, size_t rows, const void *w, size_t ldw,
+                           const XentSizes &z)
+{
+    cudaError_t e = xent_map(&maps.x, x, z.H, rows, ldx, 64);
+    if (e == cudaSuccess) e = xent_map(&maps.x128, x, z.H, rows, ldx, 128);
+    if (e == cudaSuccess) e = xent_map(&maps.w, w, z.H, z.V, ldw, 64);
+    if (e == cudaSuccess) e = xent_map(&maps.w128, w, z.H, z.V, ldw, 128);
+    if (e == cudaSuccess) e = xent_map(&maps.w32, w, z.H, z.V, ldw, 32);
+    maps.p = maps.p128 = maps.p_out = maps.ws_out = maps.dw_out = maps.x;
+    return e;
+}
+
 // The tokens' compact copy, W where it has to be copied, and the tensor maps.
 cudaError_t xent_prepare(XentTokens &k, const XentSizes &z, const XentCommon &c, char *base, const void *w, size_t ldw,
                          XentMaps &maps, cudaStream_t s)
@@ -118,13 +131,7 @@ cudaError_t xent_prepare(XentTokens &k, const XentSizes &z, const XentCommon &c,
         ldw = z.ldX;            // not looked at by the caller; the map wants a pitch
     }
     cudaError_t e = launch_xent_tokens(k, s);
-    if (e == cudaSuccess) e = xent_map(&maps.x, k.X, z.H, z.tpad, z.ldX, 64);
-    if (e == cudaSuccess) e = xent_map(&maps.w, w, z.H, z.V, ldw, 64);
-    if (e == cudaSuccess) e = xent_map(&maps.x128, k.X, z.H, z.tpad, z.ldX, 128);
-    if (e == cudaSuccess) e = xent_map(&maps.w128, w, z.H, z.V, ldw, 128);
-    if (e == cudaSuccess) e = xent_map(&maps.w32, w, z.H, z.V, ldw, 32);
-    maps.p = maps.p128 = maps.p_out = maps.ws_out = maps.dw_out = maps.x;      // (those that are not used)
-    return e;
+    return e == cudaSuccess ? xent_read_maps(maps, k.X, z.ldX, z.tpad, w, ldw, z) : e;
 }
 
 }  // namespace
@@ -278,28 +285,40 @@ try {
     const int tile = xent_tile_cols(z.T, z.V, pairs);
     const size_t tiles_v = (z.V + (size_t)tile - 1) / (size_t)tile;
     const size_t n_parts = tiles_v * (size_t)(tile / xent_part_cols(tile));
+    // One tile of tokens, aligned: X is read where it lies, ignored tokens or not
+    // (nothing of theirs reaches another token's row), and the launch that copies
+    // is saved (64 tokens x 64 over 1000 10.7 -> 8.6 us, x 1024 14.0 -> 11.2).
+    const bool al_x = rows_aligned(a.x, a.ldx, z.T, 2);
+    const bool direct = z.T <= (size_t)kXentTile && !z.repack && al_x && (z.T == 1 || a.ldx >= z.H);
     Parts parts;
     XentCommon c;
-    c.place(parts, z);
+    if (!direct) c.place(parts, z);
     const size_t at_part = parts.add(n_parts * z.tpad * sizeof(float2)), at_hit = parts.add(z.tpad * 4);
     Scratch scratch(s);
     if ((st = scratch.take(parts.bytes, dev)) != TCR_OK) return st;
     if (fault_injected("launch")) return TCR_ERR_CUDA;
     char *base = (char *)scratch.p;
     XentTokens k = {};
-    k.x = a.x;
-    k.ldx = a.ldx;
-    k.target = a.target;
-    k.tokens = z.T;
-    k.H = z.H;
-    k.V = z.V;
-    k.ignore = a.ignore_index;
-    k.al_x = rows_aligned(a.x, a.ldx, z.T, 2);
     XentMaps maps;
-    cudaError_t e = xent_prepare(k, z, c, base, a.weight, a.ldw, maps, s);
+    cudaError_t e;
+    if (direct) {
+        e = xent_read_maps(maps, a.x, z.T == 1 ? z.ldX : a.ldx, z.T, a.weight, z.V == 1 ? z.ldX : a.ldw, z);
+    } else {
+        k.x = a.x;
+        k.ldx = a.ldx;
+        k.target = a.target;
+        k.tokens = z.T;
+        k.H = z.H;
+        k.V = z.V;
+        k.ignore = a.ignore_index;
+        k.al_x = al_x;
+        e = xent_prepare(k, z, c, base, a.weight, a.ldw, maps, s);
+    }
     if (e == cudaSuccess) {
         XentGemm g = {};
         g.head = k.head;
+        g.n = (int)z.T;
+        g.target = a.target;
         g.lab = k.lab;
         g.tok = k.tok;
         g.tpad = z.tpad;
@@ -310,7 +329,8 @@ try {
         g.inject_stall = fault_injected("stall");
         e = launch_xent(a.dtype, kXentForward, maps, g, (size_t)z.tiles_t * tiles_v, pairs, tile, s);
         if (e == cudaSuccess) {
-            XentLoss l = {g.part, g.hit, k.rank, k.lab, z.tpad, z.T, (int)n_parts, a.loss, a.lse};
+            XentLoss l = {g.part, g.hit,  k.rank, k.lab,        a.target, a.ignore_index,
+                          z.tpad, z.T, z.V,    (int)n_parts, a.loss,   a.lse};
             e = launch_xent_loss(l, s);
         }
     }

@@ -14,6 +14,12 @@ constexpr int kXentTile = 256;             // tokens and vocabulary entries (or 
 constexpr int kXentForward = 0, kXentGradient = 1, kXentBack = 2;
 constexpr float kXentF16Scale = 32768.0f;  // of P in binary16
 
+// A target as an entry of the vocabulary, -1 where there is no such entry.
+__host__ __device__ inline int xent_label(long long y, size_t V)
+{
+    return y >= 0 && y < (long long)V ? (int)y : -1;
+}
+
 // The tokens that count, in their order: n of them, then at least zeros up to
 // a multiple of 64 rows of X.
 struct XentTokens {
@@ -37,7 +43,9 @@ struct XentTokens {
 cudaError_t launch_xent_tokens(const XentTokens &a, cudaStream_t stream);
 
 struct XentGemm {
-    const unsigned int *head;
+    const unsigned int *head;  // null: all of n tokens, their labels from target (the forward pass of few)
+    int n;
+    const long long *target;
     const int *lab, *tok;
     size_t tpad;               // rows of X, P, part and ws
     int V, H;
@@ -76,8 +84,10 @@ cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGem
 struct XentLoss {
     const float2 *part;
     const float *hit;
-    const int *rank, *lab;
-    size_t tpad, tokens;
+    const int *rank, *lab;     // null: as of target
+    const long long *target;
+    long long ignore;
+    size_t tpad, tokens, V;
     int parts;
     float *loss, *lse;         // lse may be null
 };

@@ -732,7 +732,7 @@ TCR_API tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, v
  *   loss, lse  tokens floats; lse may be NULL.
  * Logits are summed by the tensor cores in binary32, within 2^-22 * ceil(hidden
  * / 16) * sum_h |x_th weight_vh|; a row with a NaN or a logit of +infinity has
- * lse and loss NaN.  What tokens that are ignored hold is not looked at.
+ * lse and loss NaN.  What tokens that are ignored hold reaches no result.
  * tokens < 2^24, vocab < 2^27, hidden < 2^20 (else TCR_ERR_UNSUPPORTED), vocab and hidden not 0,
  * tokens * vocab and vocab * hidden < 2^40.  Takes pool scratch of 2 bytes per
  * element of x, 8 per token and 128 entries of the vocabulary (64 where these are few), and, where

@@ -128,6 +128,10 @@ def test_strides_and_alignment_do_not_change_bits(T, H, V, dt):
         wn = torch.full((V, pitch), float("nan"), dtype=x.dtype, device="cuda")
         xn[:, :H], wn[:, :H] = x, w
         assert all(same(a, b) for a, b in zip(want, step(xn[:, :H], wn[:, :H], target, dloss)))
+    # few tokens, more than a tile of them and unaligned ones: the same bits of each
+    if T > 64:
+        few = tcr.tcr_cross_entropy(x[:64], w, target[:64], want_lse=True)
+        assert same(few.loss, want[0][:64]) and same(few.lse, want[1][:64])
     # one row of x for all; the gradient of a mean; dx over x
     xe = x[:1].expand(T, H)
     assert same(tcr.tcr_cross_entropy(xe, w, target).loss, tcr.tcr_cross_entropy(xe.contiguous(), w, target).loss)
@@ -140,11 +144,12 @@ def test_strides_and_alignment_do_not_change_bits(T, H, V, dt):
     assert same(dx, want[2])
 
 
-def test_ignored_tokens_count_for_nothing_whatever_they_hold():
-    x, w, target, dloss = case(700, 136, 1300, "bf16", ignored=0.4)
+@pytest.mark.parametrize("T", [200, 256, 257, 700])
+def test_ignored_tokens_count_for_nothing_whatever_they_hold(T):
+    x, w, target, dloss = case(T, 136, 1300, "bf16", ignored=0.4)
     want = step(x, w, target, dloss)
     live = target != -100
-    assert 0 < int(live.sum()) < 700
+    assert 0 < int(live.sum()) < T
     xn, dn = x.clone(), dloss.clone()
     xn[~live] = float("nan")
     dn[~live] = float("inf")
