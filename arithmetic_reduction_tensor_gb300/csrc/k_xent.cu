@@ -3,8 +3,8 @@
 //
 // With l = X W^T the logits of n tokens over V entries (never in memory):
 //   forward   a tile's epilogue leaves, of each of its rows, the largest logit
-//             and the sum of 2^(log2(e) (l - largest)) over its 256 columns, and
-//             the target's logit: 8 bytes for 256 logits.
+//             and the sum of 2^(log2(e) (l - largest)) over 128 of its columns,
+//             and the target's logit: 8 bytes for 128 logits.
 //   gradient  over a piece of the vocabulary at a time: the logits' tiles again,
 //             their epilogue writing P = (exp(l - lse) - [target]) g in 16 bits;
 //             then one launch forms dX += P W (units of 256 tokens x 256 columns
@@ -14,8 +14,8 @@
 // each of its elements, as large an error as the rounding of the results;
 // the products' sums are 32 bits.
 //
-// X is the compact, aligned copy of the tokens that count (k_xent_rows.cu), W is
-// V x H, P is n x the piece.  Only the logits have both operands K-major as they
+// X is the compact, aligned copy of the tokens that count (k_xent_rows.cu; few
+// aligned tokens in the forward pass: x itself), W is V x H, P is n x the piece.  Only the logits have both operands K-major as they
 // lie in memory.  The gradient's products take W, P and X as they are, MN-major:
 // a 64 x 64 box of a row-major matrix lands in shared memory as 64 rows of 128
 // swizzled bytes, which is a K-major operand of 64 rows or an MN-major one of
@@ -28,13 +28,20 @@
 // The tensor cores' sums lose their last bits at every step, all in the same
 // direction, so the forward pass, whose results are binary32, takes K in chains
 // of 1024 and adds the chains in registers (4096 columns: the loss' error
-// against binary64 1.4e-6 in one chain, 4e-7 so; the time is the same).  P, dX
+// against binary64 1.4e-6 in one chain, 3e-7 so, for 2% of the time).  P, dX
 // and dW are rounded to 16 bits anyway.
 //
 // What the gradient's tiles write (P, dX's sums, dW) leaves by tensor-map
 // stores from shared memory, dX's later pieces as additions in L2: threads that
-// store a row each keep the memory pipe from the MMAs' operands (tensor cores
-// busy 71% of the time instead of 84).
+// store a row each keep the memory pipe from the MMAs' operands (4096 x 2048 over
+// 9728: P's launch 104 us that way, 98 so).
+//
+// Many tokens are bound by the tensor pipe: 4096 x 4096 over 65536 forward 1.17 ms in
+// a burst, the cuBLAS rate, 1.33 under the power limit; with the gradient over
+// 32768 2.33 and 2.74 ms, 8 T V H operations at 1.89 and 1.61 PFLOP/s.  The producer
+// is one thread, and a box more a stage costs it: operands that lie K-major come
+// in one box of all their rows (two of 64 rows: 2.56 ms).  Few tokens are bound by
+// reading W: 16 x 4096 over 131072 175 us, 6.1 TB/s.
 #include "pair.cuh"
 #include "rowvec.cuh"
 #include "xent.h"
@@ -754,8 +761,8 @@ int xent_pairs()
     return n;
 }
 
-// A matrix of 16-bit values (or, `wide`, of binary32) in boxes of 128 bytes x 64 or
-// 32 rows.
+// A matrix of 16-bit values (or, `wide`, of binary32) in boxes of 128 bytes x
+// box_rows rows.
 cudaError_t xent_map(CUtensorMap *map, const void *base, size_t cols, size_t rows, size_t ld, int box_rows, bool wide)
 {
     PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();

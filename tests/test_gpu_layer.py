@@ -212,6 +212,37 @@ def test_strides_and_alignment_do_not_change_bits(rows, cols, dt):
 
 
 @pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("cols", [9, 128, 255, 1000, 1501, 2560, 5001, 9000])
+def test_every_tensor_at_an_alignment_of_its_own(cols, dt):
+    gen = torch.Generator().manual_seed(cols)
+    rnd = lambda n: int(torch.randint(0, n, (1,), generator=gen))      # noqa: E731
+    rows = 7
+    x, r, dy, dh = (rand(gen, rows, cols, DTS[dt]) for _ in range(4))
+    w = (torch.rand(cols, generator=gen) + 0.5).to(DTS[dt])
+    b = torch.randn(cols, generator=gen).to(DTS[dt])
+
+    def place(t):
+        return strided(t, cols + rnd(9), rnd(9)) if t.dim() == 2 else strided(t[None], cols, rnd(9))[0]
+
+    want = tcr.tcr_layernorm(x.cuda(), w.cuda(), b.cuda(), residual=r.cuda(), **of(DROP), want_stats=True)
+    codes = tcr.tcr_layernorm(x.cuda(), w.cuda(), b.cuda(), residual=r.cuda(), **of(DROP), out_dtype=torch.int8)
+    grad = tcr.tcr_layernorm_backward(dy.cuda(), want.h, w.cuda(), want.mean, want.rstd, dh=dh.cuda(), **of(DROP),
+                                      want_dresidual=True)
+    for _ in range(6):
+        o = tcr.tcr_layernorm(place(x), place(w), place(b), residual=place(r), **of(DROP), h=place(x), out=place(x),
+                              want_stats=True)
+        assert same(o.y, want.y) and same(o.h, want.h) and same(o.mean, want.mean) and same(o.rstd, want.rstd)
+        q = tcr.tcr_layernorm(place(x), place(w), place(b), residual=place(r), **of(DROP), h=place(x),
+                              out=place(codes.y.cpu()))
+        assert same(q.y, codes.y) and same(q.scale, codes.scale)
+        g = tcr.tcr_layernorm_backward(place(dy), place(want.h.cpu()), place(w), want.mean, want.rstd, dh=place(dh),
+                                       **of(DROP), dx=place(x), dresidual=place(x))
+        assert all(same(p, q) for p, q in zip(g, grad))
+        y = tcr.tcr_dropout(place(x), **of(DROP), residual=place(r), out=place(x))
+        assert same(y, want.h)
+
+
+@pytest.mark.parametrize("dt", DTS)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (2, 8), (3, 100), (200, 257), (700, 513), (5, 1000), (321, 2049), (157, 2600), (9, 4100), (401, 1400), (700, 5100),
                                        (7, 6000), (5, 7000),
                                        (4, 8192), (3, 8200), (2, 20003)])
