@@ -98,7 +98,7 @@ __device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Dr
                 load_piece<DT, L>(pdh + i * kStep, count(i), dh[i], by_words(pdh));
         }
         const float mean = a.mean[r], rstd = a.rstd[r];
-        float sa[NV], sc[NV];
+        float sa[NV], sc[NV], g_of[NV][kRv];
         auto weigh = [&](int i, float (&g)[kRv]) {
             Piece<DT> w;
             float f[kRv];
@@ -108,7 +108,7 @@ __device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Dr
         };
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            float xh[kRv], g[kRv];
+            float xh[kRv], (&g)[kRv] = g_of[i];
             piece_values<DT>(h[i], xh);
             piece_values<DT>(dy[i], g);
             normalise(mean, rstd, xh);
@@ -127,11 +127,9 @@ __device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Dr
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const uint32_t n = count(i);
-            float xh[kRv], g[kRv];
+            float xh[kRv], (&g)[kRv] = g_of[i];
             piece_values<DT>(h[i], xh);
-            piece_values<DT>(dy[i], g);
             normalise(mean, rstd, xh);
-            if (has_w) weigh(i, g);
             back_dr(rstd, ma, mc, xh, g);
             if (has_dh) {
                 float d[kRv];
@@ -153,11 +151,12 @@ __device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Dr
 
 // Rows of at most T NV vectors, NV pieces a thread.  A CTA walks the rows b, b +
 // G, .. and keeps its sums of dw and db in shared memory, thread by thread, so
-// that registers hold one row's inputs as they were read (g and xh are formed
-// again after the barrier) and 1024 threads (binary32: 768) fit an SM: their
-// rows are at different steps, and none is loaded ahead.  16384 x 4096 bfloat16
-// with dropout, both gradients and sums 118 us; with the sums in registers and
-// the next row loaded ahead, two CTAs of 256 threads an SM, 163.
+// that registers hold one row's g and its h and dh as they were read (xh is
+// formed again after the barrier) and 1024 threads (binary32: 768) fit an SM:
+// their rows are at different steps, and none is loaded ahead.  16384 x 4096
+// bfloat16 with dropout, both gradients and sums 119 us (issuing on 63% of
+// cycles, 83% of the copy rate without the sums' launch); with the sums in
+// registers and the next row loaded ahead, two CTAs of 256 threads an SM, 163.
 template <int DT, bool ELEM, int T, int NV, int LEAD, int MINB>
 __global__ void __launch_bounds__(T, MINB)
 layer_back_kernel(const __grid_constant__ LayerBackArgs a)
@@ -344,8 +343,8 @@ const void *pick(size_t nvec, unsigned &threads, size_t &smem)
             (const void *)layer_back_kernel<DT, ELEM, T_, NV_, NV_ - 1, MINB_>)
     // The fastest of those measured (with dropout and the sums; threads whose last
     // pieces are past the row's end issue for nothing): bfloat16 16384 x 4096 256 x 2
-    // in 125 us, 128 x 4 in 128; 32768 x 1536 64 x 3 97, 128 x 2 129; 20000 x 2560
-    // 64 x 5 102, 128 x 3 123; 10000 x 5120 128 x 5 103, 256 x 3 139; 10000 x 6144
+    // in 119 us, 128 x 4 in 124; 32768 x 1536 64 x 3 97, 128 x 2 129; 20000 x 2560
+    // 64 x 5 101, 128 x 3 123; 10000 x 5120 128 x 5 101, 256 x 3 139; 10000 x 6144
     // 256 x 3 127, 128 x 6 130; 8000 x 7168 128 x 7 125, 512 x 2 142.
     if constexpr (DT == kF32) {
         if (nvec <= 64) TCR_BACK(64, 1, 12);
