@@ -155,7 +155,7 @@ __device__ __forceinline__ void layer_back_rows(const LayerBackArgs &a, const Dr
 // formed again after the barrier) and 1024 threads (binary32: 768) fit an SM:
 // their rows are at different steps, and none is loaded ahead.  16384 x 4096
 // bfloat16 with dropout, both gradients and sums 119 us (issuing on 63% of
-// cycles, 83% of the copy rate without the sums' launch); with the sums in
+// cycles; 83% of the copy rate, 87% without the sums' launch); with the sums in
 // registers and the next row loaded ahead, two CTAs of 256 threads an SM, 163.
 template <int DT, bool ELEM, int T, int NV, int LEAD, int MINB>
 __global__ void __launch_bounds__(T, MINB)
