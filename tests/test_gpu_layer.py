@@ -405,6 +405,32 @@ def test_streams_graphs_and_threads():
     assert not wrong
 
 
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("cols", [1, 31, 256, 500, 1000, 1001, 2560, 5001, 7168, 16384, 16391, 40000])
+def test_outputs_over_the_inputs(cols, dt):
+    gen = torch.Generator().manual_seed(cols)
+    x, r = rand(gen, 9, cols, DTS[dt]), rand(gen, 9, cols, DTS[dt])
+    w = (torch.rand(cols, generator=gen) + 0.5).to(DTS[dt]).cuda()
+    b = torch.randn(cols, generator=gen).to(DTS[dt]).cuda()
+    want = tcr.tcr_layernorm(x.cuda(), w, b, residual=r.cuda(), **of(DROP), want_stats=True)
+    codes = tcr.tcr_layernorm(x.cuda(), w, b, residual=r.cuda(), **of(DROP), out_dtype=torch.int8)
+    alone = tcr.tcr_layernorm(x.cuda(), w, b)
+    for pitch, off in (((cols + 7) // 8 * 8, 0), (cols + 3, 1)):
+        def xr():
+            return strided(x, pitch, off), strided(r, pitch, off)
+
+        for over_x in (True, False):                     # h over one, y over the other
+            xs, rs = xr()
+            o = tcr.tcr_layernorm(xs, w, b, residual=rs, **of(DROP), h=xs if over_x else rs, out=rs if over_x else xs,
+                                  want_stats=True)
+            assert same(o.h, want.h) and same(o.y, want.y) and same(o.mean, want.mean) and same(o.rstd, want.rstd)
+            xs, rs = xr()
+            o = tcr.tcr_layernorm(xs, w, b, residual=rs, **of(DROP), h=xs if over_x else rs, out_dtype=torch.int8)
+            assert same(o.h, want.h) and same(o.y, codes.y) and same(o.scale, codes.scale)
+        xs, _ = xr()
+        assert same(tcr.tcr_layernorm(xs, w, b, out=xs).y, alone.y)
+
+
 def test_the_widest_rows():
     # 2^27 columns, the documented limit; every sum a power of two or exact
     cols = 1 << 27
