@@ -3,8 +3,8 @@
 //
 // With l = X W^T the logits of n tokens over V entries (never in memory):
 //   forward   a tile's epilogue leaves, of each of its rows, the largest logit
-//             and the sum of 2^(log2(e) (l - largest)) over 128 of its columns,
-//             and the target's logit: 8 bytes for 128 logits.
+//             and the sum of exp(l - largest) over the others of 128 of its
+//             columns, and the target's logit: 8 bytes for 128 logits.
 //   gradient  over a piece of the vocabulary at a time: the logits' tiles again,
 //             their epilogue writing P = (exp(l - lse) - [target]) g in 16 bits;
 //             then one launch forms dX += P W (units of 256 tokens x 256 columns
@@ -80,20 +80,11 @@ struct XLayout {
     static_assert(kSmemBytes <= 232448, "one SM's 227 KiB");
 };
 
-constexpr float kLog2e = 1.44269504088896340736f;
-
 __device__ unsigned int g_xent_fault;
 
 __device__ __forceinline__ bool x_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort)
 {
     return mbar_wait_f(bar, parity, abort, &g_xent_fault);
-}
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // 16 consecutive fp32 columns of this thread's TMEM lane.
@@ -231,7 +222,11 @@ struct XUnits {
 // gives the columns 32 c .. 32 c + 31 of these.  Every lane of the warp calls
 // ld and the stores.
 
-// The largest logit of the row among the warp's columns and the sum about it.
+// The largest logit m of the row among the warp's columns, and the sum of exp(l
+// - m) over the others: without the largest's 1, in which small sums would
+// drown, the loss of a token that is predicted well keeps its bits.  The
+// differences are taken before they are scaled, so that the logits' size costs
+// no bits and overflows nothing.
 template <int COLS>
 __device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int part, float (&v)[COLS])
 {
@@ -243,22 +238,28 @@ __device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, 
         for (int j = 0; j < COLS; j++)
             if (j >= left) v[j] = -INFINITY;
     }
-    float hit = 0.0f;
     if (at >= 0 && at < COLS) {
+        float hit = 0.0f;
 #pragma unroll
         for (int j = 0; j < COLS; j++)
             if (j == at) hit = v[j];
+        g.hit[row] = hit;
     }
     float m[4] = {v[0], v[1], v[2], v[3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 4; j < COLS; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
-    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    const float about = mx == -INFINITY ? 0.0f : -__fmul_rn(mx, kLog2e);
+    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), about = xent_about(mx);
+    int others = -1;                                         // as large as the largest
 #pragma unroll
-    for (int j = 0; j < COLS; j++) e[j & 3] = __fadd_rn(e[j & 3], ex2(__fmaf_rn(v[j], kLog2e, about)));
-    const float s = __fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3]));
+    for (int j = 0; j < COLS; j++) {
+        const float t = xent_exp(v[j], about);
+        if (v[j] == mx)
+            others++;
+        else
+            e[j & 3] = __fadd_rn(e[j & 3], t);
+    }
+    const float s = __fadd_rn(__fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])), (float)others);
     g.part[(size_t)part * g.tpad + row] = make_float2(mx, s);
-    if (at >= 0 && at < COLS) g.hit[row] = hit;
 }
 
 // A warp's staging: 32 rows of 128 bytes, 16-byte granule k of row r at granule k ^

@@ -133,15 +133,17 @@ __global__ void __launch_bounds__(kTokThreads) xent_tokens_kernel(const XentToke
 }
 
 // Four tokens a CTA (32 bytes of each part's row), 64 threads a token over the
-// parts.  lse = log of the parts' sums about the largest logit, in powers of
-// two as they were formed.
+// parts.  With M the largest logit, h the target's and A the sum of exp(l - M) over
+// the others,
+//   lse = M + log1p(A),  loss = (M - h) + log1p(A).
+// The loss is not lse - h: that difference of two numbers as large as the logits
+// would leave a token that is predicted well (A << 1, h = M) no bit of its loss.
 constexpr int kLossTokens = 4, kLossThreads = 256, kLossSlices = kLossThreads / kLossTokens;
 __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss a)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
-    constexpr float log2e = 1.44269504088896340736f, ln2 = 0.69314718055994530942f;
-    __shared__ float red[2][kLossThreads / 32][kLossTokens];
+    __shared__ float red[3][kLossThreads / 32][kLossTokens];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = threadIdx.x % kLossTokens;
     const size_t t = (size_t)blockIdx.x * kLossTokens + k;
     const int first = (int)threadIdx.x / kLossTokens;
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
             lab = xent_label(y, a.V);
         }
     }
-    float m = -INFINITY, s = 0.0f;
+    float m = -INFINITY, s = 0.0f, tops = 0.0f;
     if (r >= 0) {
         // two passes over the parts (8 bytes for 128 logits): the largest, then the sum about it
 #pragma unroll 8
@@ -168,29 +170,43 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kLossThreads / 32; w++) m = fmaxf(m, red[0][w][k]);
-    const float about = m == -INFINITY ? 0.0f : __fmul_rn(m, log2e);
+    const float about = xent_about(m);
     if (r >= 0) {
 #pragma unroll 8
         for (int j = first; j < a.parts; j += kLossSlices) {
             const float2 p = a.part[(size_t)j * a.tpad + r];
-            // the part's own unit is fl(p.x * log2e), as its sum was formed (a part
-            // of nothing but -infinity is 0 in any unit)
-            const float unit = p.x == -INFINITY ? about : __fmul_rn(p.x, log2e);
-            s = __fmaf_rn(p.y, exp2f(__fsub_rn(unit, about)), s);
+            const float w = exp2f(__fmul_rn(__fsub_rn(p.x, about), kLog2e));
+            // the part's largest counts beside its others, but for one that is M
+            if (p.x == m)
+                tops += 1.0f;
+            else
+                s = __fadd_rn(s, w);
+            s = __fmaf_rn(p.y, w, s);
         }
     }
 #pragma unroll
-    for (int h = kLossTokens; h < 32; h *= 2) s = __fadd_rn(s, __shfl_xor_sync(kFull, s, h));
-    if (lane < kLossTokens) red[1][warp][k] = s;
+    for (int h = kLossTokens; h < 32; h *= 2) {
+        s = __fadd_rn(s, __shfl_xor_sync(kFull, s, h));
+        tops = __fadd_rn(tops, __shfl_xor_sync(kFull, tops, h));
+    }
+    if (lane < kLossTokens) {
+        red[1][warp][k] = s;
+        red[2][warp][k] = tops;
+    }
     __syncthreads();
     if (threadIdx.x >= kLossTokens || t >= a.tokens) return;
     float loss = 0.0f, lse = 0.0f;
     if (r >= 0) {
         s = 0.0f;
+        tops = -1.0f;
 #pragma unroll
-        for (int w = 0; w < kLossThreads / 32; w++) s = __fadd_rn(s, red[1][w][k]);
-        lse = __fmul_rn(__fadd_rn(about, log2f(s)), ln2);
-        loss = lab < 0 ? __int_as_float(0x7fc00000) : __fsub_rn(lse, a.hit[r]);
+        for (int w = 0; w < kLossThreads / 32; w++) {
+            s = __fadd_rn(s, red[1][w][k]);
+            tops = __fadd_rn(tops, red[2][w][k]);
+        }
+        const float log_s = log1pf(__fadd_rn(s, tops));
+        lse = __fadd_rn(m, log_s);
+        loss = lab < 0 ? __int_as_float(0x7fc00000) : __fadd_rn(__fsub_rn(m, a.hit[r]), log_s);
     }
     a.loss[t] = loss;
     if (a.lse) a.lse[t] = lse;

@@ -20,6 +20,29 @@ __host__ __device__ inline int xent_label(long long y, size_t V)
     return y >= 0 && y < (long long)V ? (int)y : -1;
 }
 
+#ifdef __CUDACC__
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// What logits are taken about: their largest, m, but 0 where there is none.
+__device__ __forceinline__ float xent_about(float m)
+{
+    return m == -INFINITY ? 0.0f : m;
+}
+
+// exp(l - about).
+__device__ __forceinline__ float xent_exp(float l, float about)
+{
+    return ex2(__fmul_rn(__fsub_rn(l, about), kLog2e));
+}
+#endif
+
 // The tokens that count, in their order: n of them, then at least zeros up to
 // a multiple of 64 rows of X.
 struct XentTokens {
@@ -51,7 +74,7 @@ struct XentGemm {
     int V, H;
     int v0, vn;                // the piece of the vocabulary (the forward pass: all of it)
     // forward
-    float2 *part;              // [part of the vocabulary][row]: largest logit, sum about it
+    float2 *part;              // [part of the vocabulary][row]: largest logit, sum of the others about it
     float *hit;                // the target's logit
     // gradient
     const float *lse, *dloss;

@@ -723,7 +723,10 @@ TCR_API tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, v
  * tcr_cross_entropy -- the softmax cross entropy of the logits l = x weight^T
  * over a vocabulary, without the logits in memory: for every token t
  *   lse[t] = log(sum over v of exp(l_tv)),  loss[t] = lse[t] - l_t,target[t],
- * in binary32; both 0 where target[t] is ignore_index.
+ * in binary32; both 0 where target[t] is ignore_index.  With M_t the largest
+ * logit and A_t the sum of exp(l_tv - M_t) over the others they are M_t +
+ * log1p(A_t) and (M_t - l_t,target[t]) + log1p(A_t): beyond what the logits' own
+ * errors make of it the loss, never below 0, is off by at most 2^-14 of itself.
  *   x        tokens x hidden, weight: vocab x hidden, row-major TCR_F16 or
  *            TCR_BF16 (dtype, both alike) of any alignment, ldx and ldw as in the
  *            8-bit path (ldx may be 0, ldw not).
