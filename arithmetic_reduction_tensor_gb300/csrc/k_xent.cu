@@ -309,7 +309,7 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
     if (row < n) {
         const int tok = g.tok[row], lab = g.lab[row];
         const float gmax = __uint_as_float(g.head[1]);
-        about = -__fmul_rn(g.lse[tok], kLog2e);
+        about = g.lse[tok];
         gq = g.dloss[(size_t)tok * g.inc_dloss];
         if (gmax > 0.0f) gq = __fdiv_rn(gq, gmax);       // (gmax is that of the finite ones)
         if (DT == kF16) gq = __fmul_rn(gq, kXentF16Scale);
@@ -327,7 +327,7 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
             ld(2 * c + h, v);
 #pragma unroll
             for (int j = 0; j < 32; j++) {
-                float p = ex2(__fmaf_rn(v[j], kLog2e, about));
+                float p = xent_exp(v[j], about);                 // (no product of a logit that overflows)
                 if (at == 64 * c + 32 * h + j) p = __fsub_rn(p, 1.0f);
                 v[j] = 64 * c + 32 * h + j < left ? __fmul_rn(p, gq) : 0.0f;
             }

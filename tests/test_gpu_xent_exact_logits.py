@@ -80,3 +80,80 @@ def test_losses_of_tokens_predicted_well(T, V, base, dt):
             q = relative(logits)
             assert ((o.loss.double() - loss).abs() <= q * loss + 2.0 ** -100).all()
             assert ((o.lse.double() - lse).abs() <= q * log + U * lse.abs() + 2.0 ** -100).all()
+
+
+def probabilities(x, w, target, dloss, lse):
+    """P read back through dx: entry v alone has column H + v of the weight, x 0 there."""
+    (T, H), V = x.shape, len(w)
+    xp, wp = x.new_zeros(T, H + V), w.new_zeros(V, H + V)
+    xp[:, :H], wp[:, :H] = x, w
+    wp[:, H:] = torch.eye(V, dtype=w.dtype, device=w.device)
+    o = tcr.tcr_cross_entropy(xp, wp, target, want_lse=True)
+    assert torch.equal(o.lse, lse)
+    return tcr.tcr_cross_entropy_backward(dloss, xp, wp, target, lse, want_dweight=False)[0][:, H:]
+
+
+def check_probabilities(P, logits, target, dloss, dt):
+    """P against binary64: p = exp(d) is off by the exponential's share of `relative`
+    and by lse's own error, a rounding of U |lse| and that of its logarithm; then
+    (p - [target]) g and its rounding, in units of the largest |g| (2^15 smaller in
+    binary16), and dx's.  Every product but one of dx's sum is 0."""
+    _, lse, log = loss64(logits, target)
+    d = (logits - lse[:, None]).abs().clamp(max=90)
+    p = torch.exp(logits - lse[:, None])
+    hit = torch.zeros_like(p).scatter_(1, target[:, None], 1.0)
+    g = dloss.double()[:, None]
+    q = 2.0 ** -22 + 3 * U * d + ((U * lse.abs()) + relative(logits) * log)[:, None] + 4 * U
+    err = (p * q + 2 * U * (p + hit)) * g.abs()
+    want = (p - hit) * g
+    eps, tiny = rows_spec.EPS_OUT[DTS[dt]], rows_spec.TINY[DTS[dt]]
+    low = float(g.abs().max()) * (2.0 ** -25 * 2.0 ** -15 if dt == "f16" else 2.0 ** -126)
+    err = err + eps * (want.abs() + err) + low
+    assert ((P.double() - want).abs() <= err + eps * (want.abs() + err) + tiny).all()
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("base", [-256.0, 0.0, 30.0, 256.0])
+@pytest.mark.parametrize("T,V", [(70, 300), (300, 300), (5000, 600)])
+def test_gradients_of_tokens_predicted_well(T, V, base, dt):
+    for low, high in ((-40.0, -2.0), (-12.0, -6.0)):
+        x, w, best, logits = exact_case(T, V, dt, base, low, high)
+        target = torch.where(torch.arange(T, device="cuda") % 3 == 0, (best + 1) % V, best)
+        lse = tcr.tcr_cross_entropy(x, w, target, want_lse=True).lse
+        dloss = torch.full((T,), 0.125, device="cuda")
+        dloss[::7] = -0.01
+        check_probabilities(probabilities(x, w, target, dloss, lse), logits, target, dloss, dt)
+
+
+@pytest.mark.parametrize("T,V", SIZES)
+def test_logits_at_the_ends_of_the_types(T, V):
+    # entries that are masked by the type's lowest value, some of them whole parts of the
+    # vocabulary, in one column of the weight; the largest value in turn
+    for dt, last in (("bf16", 3.3895313892515355e38), ("f16", 65504.0)):
+        x, w, best, logits = exact_case(T, V, dt, 5.0, -9.0, -1.0)
+        masked = torch.arange(V, device="cuda") % 3 == 1
+        masked[:256] = True
+        masked[best] = False
+        w[masked], w[masked, 0] = 0, -last
+        logits[:, masked] = -last
+        loss, lse, log = loss64(logits, best)
+        o = tcr.tcr_cross_entropy(x, w, best, want_lse=True)
+        q = 2.0 ** -22 + 2 * 3 * U * 9 + 116 * U         # the others' differences are 9 or less
+        assert ((o.loss.double() - loss).abs() <= q * loss).all()
+        assert ((o.lse.double() - lse).abs() <= q * log + U * lse.abs()).all()
+        if V <= 600:
+            dloss = torch.full((T,), 1.0, device="cuda")
+            check_probabilities(probabilities(x, w, best, dloss, o.lse), logits, best, dloss, dt)
+        # a target that is masked: as far off as the type goes
+        hidden = torch.full_like(best, int(masked.nonzero()[0, 0]))
+        o = tcr.tcr_cross_entropy(x, w, hidden)
+        assert ((o.loss.double() - loss64(logits, hidden)[0]).abs() <= 2 * U * last).all()
+        # every logit at an end: the loss is that of equal ones
+        for end in (last, -last):
+            w[:], w[:, 0] = 0, end
+            o = tcr.tcr_cross_entropy(x, w, best, want_lse=True)
+            flat = torch.tensor(float(V), dtype=torch.float64).log()
+            assert ((o.loss.double() - flat).abs() <= (2.0 ** -22 + 116 * U) * flat).all()
+            assert ((o.lse.double() - (end + flat)).abs() <= U * last + 1e-5).all()
+            if V <= 600:
+                assert probabilities(x, w, best, torch.ones(T, device="cuda"), o.lse).isfinite().all()
