@@ -26,10 +26,12 @@
 // rows and 128 columns of the CTA's 128 x 256.
 //
 // The tensor cores' sums lose their last bits at every step, all in the same
-// direction, so the forward pass, whose results are binary32, takes K in chains
-// of 1024 and adds the chains in registers (4096 columns: the loss' error
-// against binary64 1.4e-6 in one chain, 3e-7 so, for 2% of the time).  P, dX
-// and dW are rounded to 16 bits anyway.
+// direction, so the logits take K in chains of 1024 and add the chains in
+// registers (4096 columns: the loss' error against binary64 1.4e-6 in one chain,
+// 3e-7 so, for 2% of the forward pass' time).  The gradient does the same, so that its
+// logits are the forward pass' bit for bit: P of a token that is predicted well is a
+// difference of l and lse, which other sums would shift by their own loss.  dX and dW
+// are rounded to 16 bits anyway.
 //
 // What the gradient's tiles write (P, dX's sums, dW) leaves by tensor-map
 // stores from shared memory, dX's later pieces as additions in L2: threads that
@@ -52,7 +54,7 @@ constexpr int kXBox = 64;                          // rows and columns of a box
 constexpr int kXBoxBytes = kXBox * kXBox * 2;      // 8 KiB
 constexpr int kXHalf = 128;                        // rows of an operand per CTA
 constexpr int kXHalfBytes = 2 * kXBoxBytes;
-constexpr int kXChain = 16;                        // boxes of K the forward pass adds up in one chain
+constexpr int kXChain = 16;                        // boxes of K that the logits add up in one chain
 constexpr int kXDBuffers = 2;
 constexpr uint32_t kXTmemCols = kXDBuffers * kXentTile;
 constexpr int kXEpilogueWarps = 8;
@@ -299,10 +301,11 @@ struct XOut {
 // P of the row: (exp(l - lse) - [target]) * g, in units of the largest |g| so
 // that the target's -1 times a common g is exact (binary16: times 2^15 on top,
 // which keeps probabilities of 2^-29 normal).
-template <int DT, int COLS, class Ld>
+template <int DT, int COLS>
 __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
-                                                  int n, int col0, Ld ld)
+                                                  int n, int col0, const float (&v)[COLS])
 {
+    if (row0 >= (n + kXBox - 1) / kXBox * kXBox) return;     // not read: dW's K ends with the tokens' last box
     const int row = row0 + (threadIdx.x & 31);
     float about = 0.0f, gq = 0.0f;
     int at = -1;
@@ -317,26 +320,26 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
         at = lab - g.v0 - col0;
     }
     const int left = gq == 0.0f ? 0 : g.vn - col0;
-    if (row0 >= (n + kXBox - 1) / kXBox * kXBox) return;     // not read: dW's K ends with the tokens' last box
-#pragma unroll 1
+#pragma unroll
     for (int c = 0; c < COLS / 64; c++) {
-        uint32_t o[32];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            float v[32];
-            ld(2 * c + h, v);
-#pragma unroll
-            for (int j = 0; j < 32; j++) {
-                float p = xent_exp(v[j], about);                 // (no product of a logit that overflows)
-                if (at == 64 * c + 32 * h + j) p = __fsub_rn(p, 1.0f);
-                v[j] = 64 * c + 32 * h + j < left ? __fmul_rn(p, gq) : 0.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < 16; j++) o[16 * h + j] = float2_to_word<DT>(v[2 * j], v[2 * j + 1]);
-        }
         out.ready();
 #pragma unroll
-        for (int k = 0; k < 8; k++) out.put(k, o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        for (int k = 0; k < 8; k++) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                float q[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int col = 64 * c + 8 * k + j + i;
+                    float p = xent_exp(v[col], about);               // (no product of a logit that overflows)
+                    if (at == col) p = __fsub_rn(p, 1.0f);
+                    q[i] = col < left ? __fmul_rn(p, gq) : 0.0f;
+                }
+                o[j / 2] = float2_to_word<DT>(q[0], q[1]);
+            }
+            out.put(k, o[0], o[1], o[2], o[3]);
+        }
         out.send<false>(map, col0 + 64 * c, row0);
     }
 }
@@ -553,7 +556,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                 const uint64_t a_ring = operand_desc(ring, a_mn), b_ring = operand_desc(ring + kXHalfBytes, b_mn);
                 const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
                 bool ok = true;
-                for (int j0 = 0; ok && (j0 < u.nk || j0 == 0); j0 += MODE == kXentForward ? kXChain : u.nk + 1) {
+                for (int j0 = 0; ok && (j0 < u.nk || j0 == 0); j0 += MODE != kXentBack ? kXChain : u.nk + 1) {
                     // both epilogues have read accumulator b
                     if (!x_wait(dempty_bar(b), ((dphase >> b) & 1u) ^ 1u, abort)) {
                         ok = false;
@@ -561,7 +564,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(b * kXentTile);
-                    const int end = MODE == kXentForward ? min(u.nk, j0 + kXChain) : u.nk;
+                    const int end = MODE != kXentBack ? min(u.nk, j0 + kXChain) : u.nk;
                     for (int j = j0; j < end; j++) {
                         if (!x_wait(full_bar(st), phase, abort)) {
                             ok = false;
@@ -619,7 +622,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
         XUnit u;
         for (int i = 0; warp - 2 < N::kWarps && units.get(i, u); i++) {
             const int row0 = u.tm * kXentTile + kXHalf * (int)rank + 32 * q, col0 = u.tn * TN + half * N::kCols;
-            if constexpr (MODE == kXentForward) {
+            if constexpr (MODE != kXentBack) {
                 float v[N::kCols];
 #pragma unroll
                 for (int j = 0; j < N::kCols; j++) v[j] = 0.0f;
@@ -641,7 +644,10 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     }
                     done();
                 }
-                if (row0 < n) epilogue_forward<N::kCols>(g, (size_t)(row0 + lane), u.tn * (TN / N::kCols) + half, v);
+                if constexpr (MODE == kXentGradient)
+                    epilogue_gradient<DT, N::kCols>(g, &maps.p_out, out, row0, n, col0, v);
+                else if (row0 < n)
+                    epilogue_forward<N::kCols>(g, (size_t)(row0 + lane), u.tn * (TN / N::kCols) + half, v);
                 continue;
             }
             begin();
@@ -657,9 +663,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     for (int j = 0; j < 32; j++) v[j] = fill;
                 }
             };
-            if constexpr (MODE == kXentGradient)
-                epilogue_gradient<DT, N::kCols>(g, &maps.p_out, out, row0, n, col0, ld);
-            else if (u.x)
+            if (u.x)
                 epilogue_dx(g, &maps.ws_out, out, row0, n, u.split, col0, ld);
             else
                 epilogue_dw<DT>(g, &maps.dw_out, out, row0, col0, ld);

@@ -157,3 +157,34 @@ def test_logits_at_the_ends_of_the_types(T, V):
             assert ((o.lse.double() - (end + flat)).abs() <= U * last + 1e-5).all()
             if V <= 600:
                 assert probabilities(x, w, best, torch.ones(T, device="cuda"), o.lse).isfinite().all()
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,H,V", [(64, 1096, 512), (64, 4096, 512), (1100, 4096, 1100), (300, 8200, 700)])
+def test_both_passes_see_the_same_logits(T, H, V, dt):
+    # positive products, whose sums lose their last bits all one way: a token's row of P
+    # adds up to 0 all the same, but for what the exponentials, lse's rounding and P's
+    # own roundings leave.  A column of ones in the weight, 0 in x, adds it up.
+    gen = torch.Generator(device="cuda").manual_seed(T + H)
+    x = torch.randn(T, H + 8, generator=gen, device="cuda").abs()
+    w = torch.randn(V, H + 8, generator=gen, device="cuda").abs() * (47.0 / H)
+    target = torch.randperm(V, generator=gen, device="cuda")[torch.arange(T, device="cuda") % V]
+    x[:, H:] = 0
+    x = x.to(DTS[dt])
+    few = min(T, V)
+    w[target[:few]] += x[:few].float() * (30.0 / (x[:few].float() ** 2).sum(1, keepdim=True))
+    w[:, H:] = 1
+    w = w.to(DTS[dt])
+    logits = x.double() @ w.double().t()
+    loss, lse, log = loss64(logits, target)
+    assert float(loss.median()) < 0.05 and float(lse.min()) > 20
+    p = torch.exp(logits - lse[:, None])
+    size = 2 * p.scatter(1, target[:, None], 0.0).sum(1)                 # sum of |P|
+    d = (logits - lse[:, None]).abs()
+    off = 2.0 ** -22 + 3 * U * (p * d).sum(1) + U * lse + relative(logits) * log + 4 * U
+    eps = rows_spec.EPS_OUT[DTS[dt]]
+    got = tcr.tcr_cross_entropy(x, w, target, want_lse=True)
+    dx, _ = tcr.tcr_cross_entropy_backward(torch.ones(T, device="cuda"), x, w, target, got.lse, want_dweight=False)
+    # (the logits' own errors, which `size` is taken without: a thousandth)
+    bound = (1.001 * size * (eps + 2.0 ** -22 * -(-V // 16)) + 2 * off) * (1 + 2 * eps) + 2.0 ** -30
+    assert (dx[:, H].double().abs() <= bound).all()
