@@ -224,11 +224,30 @@ struct XUnits {
 // gives the columns 32 c .. 32 c + 31 of these.  Every lane of the warp calls
 // ld and the stores.
 
-// The largest logit m of the row among the warp's columns, and the sum of exp(l
-// - m) over the others: without the largest's 1, in which small sums would
-// drown, the loss of a token that is predicted well keeps its bits.  The
-// differences are taken before they are scaled, so that the logits' size costs
-// no bits and overflows nothing.
+// The largest logit m of the row among 64 columns, and the sum of exp(l - m) over
+// the others: without the largest's 1, in which small sums would drown, the loss
+// of a token that is predicted well keeps its bits.  The differences are taken
+// before they are scaled, so that the logits' size costs no bits and overflows
+// nothing.
+template <int C0, int COLS>
+__device__ __forceinline__ float2 part_of(const float (&v)[COLS])
+{
+    float m[4] = {v[C0], v[C0 + 1], v[C0 + 2], v[C0 + 3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 4; j < 64; j++) m[j & 3] = fmaxf(m[j & 3], v[C0 + j]);
+    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), about = xent_about(mx);
+    int others = -1;                                         // as large as the largest
+#pragma unroll
+    for (int j = 0; j < 64; j++) {
+        const float t = xent_exp(v[C0 + j], about);
+        if (v[C0 + j] == mx)
+            others++;
+        else
+            e[j & 3] = __fadd_rn(e[j & 3], t);
+    }
+    return make_float2(mx, __fadd_rn(__fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])), (float)others));
+}
+
 template <int COLS>
 __device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, int part, float (&v)[COLS])
 {
@@ -247,21 +266,9 @@ __device__ __forceinline__ void epilogue_forward(const XentGemm &g, size_t row, 
             if (j == at) hit = v[j];
         g.hit[row] = hit;
     }
-    float m[4] = {v[0], v[1], v[2], v[3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int j = 4; j < COLS; j++) m[j & 3] = fmaxf(m[j & 3], v[j]);
-    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), about = xent_about(mx);
-    int others = -1;                                         // as large as the largest
-#pragma unroll
-    for (int j = 0; j < COLS; j++) {
-        const float t = xent_exp(v[j], about);
-        if (v[j] == mx)
-            others++;
-        else
-            e[j & 3] = __fadd_rn(e[j & 3], t);
-    }
-    const float s = __fadd_rn(__fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])), (float)others);
-    g.part[(size_t)part * g.tpad + row] = make_float2(mx, s);
+    float2 p = part_of<0>(v);
+    if constexpr (COLS == 128) p = xent_join(p, part_of<64>(v));
+    g.part[(size_t)part * g.tpad + row] = p;
 }
 
 // A warp's staging: 32 rows of 128 bytes, 16-byte granule k of row r at granule k ^

@@ -159,10 +159,17 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
         }
     }
     float m = -INFINITY, s = 0.0f, tops = 0.0f;
+    // part j of 128 entries; narrow ones, each absent one -infinity, joined as the wide tiles' are
+    const int parts = a.narrow ? (a.parts + 1) / 2 : a.parts;
+    auto part = [&](int j) {
+        if (!a.narrow) return a.part[(size_t)j * a.tpad + r];
+        const float2 p = a.part[(size_t)(2 * j) * a.tpad + r];
+        return xent_join(p, 2 * j + 1 < a.parts ? a.part[(size_t)(2 * j + 1) * a.tpad + r] : make_float2(-INFINITY, 63.0f));
+    };
     if (r >= 0) {
         // two passes over the parts (8 bytes for 128 logits): the largest, then the sum about it
 #pragma unroll 8
-        for (int j = first; j < a.parts; j += kLossSlices) m = fmaxf(m, a.part[(size_t)j * a.tpad + r].x);
+        for (int j = first; j < parts; j += kLossSlices) m = fmaxf(m, part(j).x);
     }
 #pragma unroll
     for (int h = kLossTokens; h < 32; h *= 2) m = fmaxf(m, __shfl_xor_sync(kFull, m, h));
@@ -173,8 +180,8 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
     const float about = xent_about(m);
     if (r >= 0) {
 #pragma unroll 8
-        for (int j = first; j < a.parts; j += kLossSlices) {
-            const float2 p = a.part[(size_t)j * a.tpad + r];
+        for (int j = first; j < parts; j += kLossSlices) {
+            const float2 p = part(j);
             const float w = exp2f(__fmul_rn(__fsub_rn(p.x, about), kLog2e));
             // the part's largest counts beside its others, but for one that is M
             if (p.x == m)

@@ -17,6 +17,7 @@ constexpr size_t kMaxTokens = (size_t)1 << 24;     // exclusive, as the next two
 constexpr size_t kMaxVocab = (size_t)1 << 27;
 constexpr size_t kMaxHidden = (size_t)1 << 20;
 constexpr size_t kMaxP = (size_t)512 << 20;        // bytes of P in a piece of the vocabulary
+constexpr size_t kSplitPairs = 76;                 // pairs that dX is split for: a constant, as its splits are its sums' order
 
 // The kernel's form of a call's dropout; none where drop is null.
 bool drop_of(const tcr_drop *drop, DropArgs &d)
@@ -330,7 +331,7 @@ try {
         e = launch_xent(a.dtype, kXentForward, maps, g, (size_t)z.tiles_t * tiles_v, pairs, tile, s);
         if (e == cudaSuccess) {
             XentLoss l = {g.part, g.hit,  k.rank, k.lab,        a.target, a.ignore_index,
-                          z.tpad, z.T, z.V,    (int)n_parts, a.loss,   a.lse};
+                          z.tpad, z.T, z.V,    (int)n_parts, tile == 64, a.loss, a.lse};
             e = launch_xent_loss(l, s);
         }
     }
@@ -369,7 +370,7 @@ try {
     const size_t pieces = (vpad + most - 1) / most, piece = round_up((vpad + pieces - 1) / pieces, kXentTile);
     // dX's K, the piece, in splits: enough for a unit a pair where tiles are few, of 4 boxes at least
     const size_t tiles_h = (z.H + kXentTile - 1) / kXentTile, tiles_x = (size_t)z.tiles_t * tiles_h;
-    size_t splits = (size_t)pairs / tiles_x, boxes = (z.V < piece ? z.V : piece) / 64 / 4;
+    size_t splits = kSplitPairs / tiles_x, boxes = (z.V < piece ? z.V : piece) / 64 / 4;
     if (splits > boxes) splits = boxes;
     if (splits > 32) splits = 32;
     if (splits < 1) splits = 1;

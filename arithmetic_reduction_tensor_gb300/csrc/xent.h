@@ -41,6 +41,16 @@ __device__ __forceinline__ float xent_exp(float l, float about)
 {
     return ex2(__fmul_rn(__fsub_rn(l, about), kLog2e));
 }
+
+// Two parts of the vocabulary (largest logit, sum of the others about it) as one.
+// A tile of 256 columns joins its parts of 64 in the epilogue, the parts of narrow
+// tiles are joined where they are read: the same bits.
+__device__ __forceinline__ float2 xent_join(float2 a, float2 b)
+{
+    const bool first = a.x >= b.x;
+    const float2 hi = first ? a : b, lo = first ? b : a;
+    return make_float2(hi.x, __fmaf_rn(__fadd_rn(lo.y, 1.0f), xent_exp(lo.x, xent_about(hi.x)), hi.y));
+}
 #endif
 
 // The tokens that count, in their order: n of them, then at least zeros up to
@@ -112,6 +122,7 @@ struct XentLoss {
     long long ignore;
     size_t tpad, tokens, V;
     int parts;
+    bool narrow;               // parts of 64 entries, to be joined two by two
     float *loss, *lse;         // lse may be null
 };
 cudaError_t launch_xent_loss(const XentLoss &a, cudaStream_t stream);

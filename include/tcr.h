@@ -740,7 +740,7 @@ TCR_API tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, v
  * tokens * vocab and vocab * hidden < 2^40.  Takes pool scratch of 2 bytes per
  * element of x, 8 per token and 128 entries of the vocabulary (64 where these are few), and, where
  * weight's rows are not 16-byte aligned, 2 per element of weight.  No atomics: the bits
- * depend on the inputs only.
+ * of a token's loss and lse depend on its row, its target, ignore_index and weight only.
  */
 typedef struct {
     const void *x;
@@ -767,7 +767,10 @@ TCR_API tcr_status tcr_cross_entropy(const tcr_xent_args *args, void *stream);
  *   lse      the forward call's.
  *   dx, dweight  of dtype, overwritten; NULL where not wanted.  dx may be x
  *            itself (same pointer and ld); no other overlap.
- * tokens == 0 writes dweight = +0.0.  The rest as in tcr_cross_entropy.  Pool
+ * tokens == 0 writes dweight = +0.0.  The rest as in tcr_cross_entropy, but that the
+ * bits of dx depend on the number of tokens, too (its sums over the vocabulary are
+ * split where tokens are few, and end with its pieces), and those of dweight and of all
+ * of P on the largest |dloss|.  Pool
  * scratch: 2 bytes per token and entry of a piece (as many entries as 512 MiB
  * hold, 1024 at least; tokens counted up to a multiple of 256) and 4 per element of dx (for few tokens up to 32
  * times that), beside the copies named there.  A kernel whose wait gave up

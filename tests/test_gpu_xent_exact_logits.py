@@ -188,3 +188,29 @@ def test_both_passes_see_the_same_logits(T, H, V, dt):
     # (the logits' own errors, which `size` is taken without: a thousandth)
     bound = (1.001 * size * (eps + 2.0 ** -22 * -(-V // 16)) + 2 * off) * (1 + 2 * eps) + 2.0 ** -30
     assert (dx[:, H].double().abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dt", DTS)
+@pytest.mark.parametrize("T,V", [(300, 2500), (700, 2000), (520, 1985), (600, 1700), (300, 9000)])
+def test_bits_of_a_token_do_not_depend_on_the_others(T, V, dt):
+    # on both sides of where tiles of the vocabulary become narrow
+    gen = torch.Generator(device="cuda").manual_seed(T + V)
+    x = torch.randn(T, 72, generator=gen, device="cuda").to(DTS[dt])
+    w = (torch.randn(V, 72, generator=gen, device="cuda") / 3).to(DTS[dt])
+    target = torch.randint(0, V, (T,), generator=gen, device="cuda")
+    all_of = tcr.tcr_cross_entropy(x, w, target, want_lse=True)
+    for n in (1, 64, 257, T // 2):
+        few = tcr.tcr_cross_entropy(x[:n], w, target[:n], want_lse=True)
+        assert torch.equal(few.loss, all_of.loss[:n]) and torch.equal(few.lse, all_of.lse[:n])
+    # ignored tokens: the same numbers without them, dweight's too
+    target[torch.rand(T, generator=gen, device="cuda") < 0.4] = -100
+    live = target != -100
+    dloss = torch.randn(T, generator=gen, device="cuda")
+    dloss[~live] = 0
+    a = tcr.tcr_cross_entropy(x, w, target, want_lse=True)
+    b = tcr.tcr_cross_entropy(x[live], w, target[live], want_lse=True)
+    assert torch.equal(a.loss[live], b.loss) and torch.equal(a.lse[live], b.lse)
+    assert torch.equal(b.loss, all_of.loss[live])
+    dw = [tcr.tcr_cross_entropy_backward(d, xx, w, t, o.lse, want_dx=False)[1]
+          for d, xx, t, o in ((dloss, x, target, a), (dloss[live], x[live], target[live], b))]
+    assert torch.equal(*dw)
