@@ -45,6 +45,7 @@
 // in one box of all their rows (two of 64 rows: 2.56 ms).  Few tokens are bound by
 // reading W: 16 x 4096 over 131072 175 us, 6.1 TB/s.
 #include "pair.cuh"
+#include "plan.h"
 #include "rowvec.cuh"
 #include "xent.h"
 
@@ -740,7 +741,8 @@ cudaLaunchConfig_t pair_config(int mode, bool narrow, int pairs, cudaLaunchAttri
 
 }  // namespace
 
-// The pairs that can be resident at once on the current device, cached.
+// The pairs that can be resident at once on the current device, cached; -1, not
+// cached, where the device could not be asked.
 int xent_pairs()
 {
     static std::mutex mu;
@@ -748,7 +750,7 @@ int xent_pairs()
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) {
         (void)cudaGetLastError();
-        return 0;
+        return -1;
     }
     {
         std::lock_guard<std::mutex> lk(mu);
@@ -765,9 +767,10 @@ int xent_pairs()
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = pair_config(kXentBack, false, sms / 2, attr, nullptr);
         cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack, false), &cfg) != cudaSuccess) n = 0;
+        ok = cudaOccupancyMaxActiveClusters(&n, xent_pick(kBF16, kXentBack, false), &cfg) == cudaSuccess;
     }
     (void)cudaGetLastError();
+    if (!ok || plan::fault_injected("query")) return -1;
     std::lock_guard<std::mutex> lk(mu);
     cache.emplace_back(dev, n);
     return n;

@@ -40,7 +40,8 @@ int occupancy(int dev, Family fam, bool rows, int dtype, int op, bool aligned, i
 // made.
 cudaMemPool_t pool_for(int dev);
 // Whether the environment asks for a failure of this kind (tests of the
-// error paths): TCR_FAULT_INJECT = "alloc", "launch" or "stall".
+// error paths): TCR_FAULT_INJECT = "alloc", "launch", "stall" or "query"
+// (a device that could not be asked what it can hold).
 bool fault_injected(const char *what);
 
 int log2_exact(int v);

@@ -280,7 +280,7 @@ try {
     const int dev = current_device();
     if (dev < 0) return TCR_ERR_CUDA;
     const int pairs = xent_pairs();
-    if (pairs < 1) return TCR_ERR_UNSUPPORTED;
+    if (pairs < 1) return pairs < 0 ? TCR_ERR_CUDA : TCR_ERR_UNSUPPORTED;
     cudaStream_t s = (cudaStream_t)stream;
     const XentSizes z = xent_sizes(a.weight, a.ldw, a.tokens, a.vocab, a.hidden);
     const int tile = xent_tile_cols(z.T, z.V, pairs);
@@ -361,7 +361,7 @@ try {
     const int dev = current_device();
     if (dev < 0) return TCR_ERR_CUDA;
     const int pairs = xent_pairs();
-    if (pairs < 1) return TCR_ERR_UNSUPPORTED;
+    if (pairs < 1) return pairs < 0 ? TCR_ERR_CUDA : TCR_ERR_UNSUPPORTED;
     const XentSizes z = xent_sizes(a.weight, a.ldw, a.tokens, a.vocab, a.hidden);
     // the piece of the vocabulary: equal ones, as few as kMaxP allows
     const size_t vpad = round_up(z.V, kXentTile);
