@@ -45,3 +45,26 @@ def test_a_failed_question_is_asked_again():
     r = subprocess.run([sys.executable, "-c", FIRST], cwd=root, env={**os.environ, "PYTHONPATH": root},
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,H,V,pitch", [(1030, 264, 300000, 264), (1030, 301, 300000, 307), (2000, 264, 150000, 269),
+                                         (1030, 1, 300001, 1)])
+def test_pieces_of_the_vocabulary_in_every_form(T, H, V, pitch, dt):
+    # P of these does not fit one piece: later pieces add to dX and write their rows of dW,
+    # by tensor-map stores or by threads, of a weight read where it lies or copied
+    x, w, target, dloss = case(T, H, V, dt, ignored=0.3)
+    ws = torch.full((V, pitch), float("nan"), dtype=w.dtype, device="cuda")[:, :H]
+    ws.copy_(w)
+    o = tcr.tcr_cross_entropy(x, ws, target, want_lse=True)
+    wide = torch.full((V + 2, pitch + 3), 7, dtype=w.dtype, device="cuda")
+    guarded = wide[1:V + 1, 2:2 + H]
+    dx, _ = tcr.tcr_cross_entropy_backward(dloss, x, ws, target, o.lse, dweight=guarded)
+    check(x, w, target, dloss, o.loss, o.lse, dx, guarded)
+    frame = torch.ones_like(wide, dtype=torch.bool)
+    frame[1:V + 1, 2:2 + H] = False
+    assert (wide[frame] == 7).all()
+    # the same bits where the rows are aligned (to a form that tensor maps take, if H is a multiple of 8)
+    dx2, dw2 = tcr.tcr_cross_entropy_backward(dloss, x, w, target, o.lse)
+    assert torch.equal(dx, dx2) and torch.equal(guarded, dw2)
+    assert tcr.tcr_device_faults() == 0
