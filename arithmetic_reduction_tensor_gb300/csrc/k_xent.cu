@@ -31,7 +31,10 @@
 // 3e-7 so, for 2% of the forward pass' time).  The gradient does the same, so that its
 // logits are the forward pass' bit for bit: P of a token that is predicted well is a
 // difference of l and lse, which other sums would shift by their own loss.  dX and dW
-// are rounded to 16 bits anyway.
+// are rounded to 16 bits, which chains of 16384 do not spoil (terms of one sign: 2e-5
+// low after 16384 of them in one chain, 1.6e-4 after 65536, 1.4e-3 after 262144); a
+// launch with longer ones adds them in registers (kXentBackLong), the others read
+// the accumulators as they store.
 //
 // What the gradient's tiles write (P, dX's sums, dW) leaves by tensor-map
 // stores from shared memory, dX's later pieces as additions in L2: threads that
@@ -55,7 +58,7 @@ constexpr int kXBox = 64;                          // rows and columns of a box
 constexpr int kXBoxBytes = kXBox * kXBox * 2;      // 8 KiB
 constexpr int kXHalf = 128;                        // rows of an operand per CTA
 constexpr int kXHalfBytes = 2 * kXBoxBytes;
-constexpr int kXChain = 16;                        // boxes of K that the logits add up in one chain
+constexpr int kXChain = 16, kXBackChain = kXentChain / kXBox;   // boxes of K added up in one chain: of the logits, of dX and dW
 constexpr int kXDBuffers = 2;
 constexpr uint32_t kXTmemCols = kXDBuffers * kXentTile;
 constexpr int kXEpilogueWarps = 8;
@@ -135,12 +138,13 @@ struct XUnit {
 
 // The units of one launch, of which pair p of `pairs` runs the i-th of its own.
 struct XUnits {
-    int mode, n, pairs, pair;
+    int n, pairs, pair;
+    bool back;
     int tm, tn, nk;                    // the logits, or dW: tiles, boxes of K
     int xm, xn, xnk, xkps, xsplits;    // dX: tiles, boxes of K, boxes a split
     int nx, nd, lead, rem;
 
-    __device__ __forceinline__ XUnits(const XentGemm &g, int n_, int mode_, int tile_cols) : mode(mode_), n(n_)
+    __device__ __forceinline__ XUnits(const XentGemm &g, int n_, bool back_, int tile_cols) : n(n_), back(back_)
     {
         pairs = (int)(gridDim.x >> 1);
         pair = (int)(blockIdx.x >> 1);
@@ -148,7 +152,7 @@ struct XUnits {
         nx = 0;
         lead = rem = 0;
         xm = xn = xnk = xkps = xsplits = 0;
-        if (mode != kXentBack) {
+        if (!back) {
             tm = rows;
             tn = cols;
             nk = (g.H + kXBox - 1) / kXBox;
@@ -210,7 +214,7 @@ struct XUnits {
         raster(d, tm, tn, u.tm, u.tn);
         u.k0 = 0;
         u.nk = nk;
-        u.rows = mode == kXentBack ? 4 : boxes_of_tokens(u.tm);
+        u.rows = back ? 4 : boxes_of_tokens(u.tm);
         return true;
     }
     __device__ __forceinline__ int boxes_of_tokens(int m) const
@@ -353,11 +357,11 @@ __device__ __forceinline__ void epilogue_gradient(const XentGemm &g, const CUten
 }
 
 // A split's sums of dX, added to those of the pieces before.
-template <class Ld>
+template <int UNROLL, class Ld>
 __device__ __forceinline__ void epilogue_dx(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
                                             int n, int split, int col0, Ld ld)
 {
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int c = 0; c < XTile<kXentTile>::kCols / 32; c++) {
         float v[32];
         ld(c, v);
@@ -377,14 +381,14 @@ __device__ __forceinline__ void epilogue_dx(const XentGemm &g, const CUtensorMap
 
 // Rows of dW, rounded; row0 within the piece.  Rows that no tensor map takes (not
 // 16-byte aligned) are written from the staging, 64 bytes of a row at a time.
-template <int DT, class Ld>
+template <int DT, int UNROLL, class Ld>
 __device__ __forceinline__ void epilogue_dw(const XentGemm &g, const CUtensorMap *map, const XOut &out, int row0,
                                             int col0, Ld ld)
 {
     const uint32_t lane = threadIdx.x & 31;
     float scale = __uint_as_float(g.head[1]);
     if (DT == kF16) scale = __fmul_rn(scale, 1.0f / kXentF16Scale);
-#pragma unroll 1
+#pragma unroll UNROLL
     for (int c = 0; c < XTile<kXentTile>::kCols / 64; c++) {
         uint32_t o[32];
 #pragma unroll
@@ -443,6 +447,8 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
     using Y = XLayout<MODE, TN>;
     using N = XTile<TN>;
     constexpr int kStages = Y::kStages;
+    constexpr bool kBack = MODE == kXentBack || MODE == kXentBackLong;
+    constexpr int kChain = kBack ? kXBackChain : kXChain;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t ring = smem_addr(smem);
@@ -473,8 +479,8 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         auto fetch = [](const CUtensorMap *m) { asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory"); };
         fetch(&maps.x);
-        fetch(MODE == kXentBack ? &maps.p : &maps.x128);
-        fetch(MODE == kXentBack ? &maps.w : TN == 64 ? &maps.w32 : &maps.w128);
+        fetch(kBack ? &maps.p : &maps.x128);
+        fetch(kBack ? &maps.w : TN == 64 ? &maps.w32 : &maps.w128);
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     if (warp == 1) {
@@ -490,7 +496,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
     const uint32_t tmem = *tmem_holder;
     pdl_wait_primary();
     const int n = g.head ? (int)g.head[0] : g.n;
-    const XUnits units(g, n, MODE, TN);
+    const XUnits units(g, n, kBack, TN);
 
     if (warp == 0) {
         // ---------------- producer: this CTA's halves; completion on the leader's full barrier
@@ -501,20 +507,16 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             XUnit u;
             for (int i = 0; !*abort && units.get(i, u); i++) {
                 const int m0 = u.tm * kXentTile + kXHalf * (int)rank, n0 = u.tn * TN + TN / 2 * (int)rank;
-                const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
+                const bool a_mn = kBack && !u.x, b_mn = kBack;
                 // K-major operands come in boxes of all their rows, 128 (A: or 64) or 32; MN-major
                 // ones in two of 64 x 64
                 const int a_boxes = min(2, max(0, u.rows - 2 * (int)rank));
                 const bool a_whole = !a_mn && a_boxes == 2;
-                const CUtensorMap *ma = MODE == kXentBack ? (a_whole ? &maps.p128 : &maps.p)
-                                                          : (a_whole ? &maps.x128 : &maps.x);
-                const CUtensorMap *mb = TN == 64            ? &maps.w32
-                                        : MODE != kXentBack ? &maps.w128
-                                        : u.x               ? &maps.w
-                                                            : &maps.x;
+                const CUtensorMap *ma = kBack ? (a_whole ? &maps.p128 : &maps.p) : (a_whole ? &maps.x128 : &maps.x);
+                const CUtensorMap *mb = TN == 64 ? &maps.w32 : !kBack ? &maps.w128 : u.x ? &maps.w : &maps.x;
                 const uint32_t bytes = (uint32_t)(u.rows * kXBoxBytes + 2 * N::kBBytes);
                 // the vocabulary's coordinate counts from the piece's first entry in P only
-                const int b_row = MODE == kXentBack ? (u.x ? g.v0 : 0) : n0 + g.v0;
+                const int b_row = kBack ? (u.x ? g.v0 : 0) : n0 + g.v0;
                 bool ok = true;
                 for (int j = 0; j < u.nk; j++) {
                     if (!x_wait(empty_bar(st), phase ^ 1u, abort)) {
@@ -559,12 +561,12 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             bool withhold = g.inject_stall != 0u;
             XUnit u;
             for (int i = 0; !*abort && units.get(i, u); i++) {
-                const bool a_mn = MODE == kXentBack && !u.x, b_mn = MODE == kXentBack;
+                const bool a_mn = kBack && !u.x, b_mn = kBack;
                 const uint32_t idesc = operand_instr<DT, TN>(a_mn, b_mn);
                 const uint64_t a_ring = operand_desc(ring, a_mn), b_ring = operand_desc(ring + kXHalfBytes, b_mn);
                 const uint64_t a_step = a_mn ? 2048u >> 4 : 32u >> 4, b_step = b_mn ? 2048u >> 4 : 32u >> 4;
                 bool ok = true;
-                for (int j0 = 0; ok && (j0 < u.nk || j0 == 0); j0 += MODE != kXentBack ? kXChain : u.nk + 1) {
+                for (int j0 = 0; ok && (j0 < u.nk || j0 == 0); j0 += kChain) {
                     // both epilogues have read accumulator b
                     if (!x_wait(dempty_bar(b), ((dphase >> b) & 1u) ^ 1u, abort)) {
                         ok = false;
@@ -572,7 +574,7 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
                     }
                     tc_fence_after();
                     const uint32_t d = tmem + (uint32_t)(b * kXentTile);
-                    const int end = MODE != kXentBack ? min(u.nk, j0 + kXChain) : u.nk;
+                    const int end = min(u.nk, j0 + kChain);
                     for (int j = j0; j < end; j++) {
                         if (!x_wait(full_bar(st), phase, abort)) {
                             ok = false;
@@ -630,12 +632,13 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
         XUnit u;
         for (int i = 0; warp - 2 < N::kWarps && units.get(i, u); i++) {
             const int row0 = u.tm * kXentTile + kXHalf * (int)rank + 32 * q, col0 = u.tn * TN + half * N::kCols;
-            if constexpr (MODE != kXentBack) {
+            if constexpr (MODE != kXentBack) {                   // chains, added up in registers
                 float v[N::kCols];
 #pragma unroll
-                for (int j = 0; j < N::kCols; j++) v[j] = 0.0f;
+                for (int j = 0; j < N::kCols; j++) v[j] = kBack ? -0.0f : 0.0f;
+                const bool none = u.nk == 0;
 #pragma unroll 1
-                for (int j0 = 0; j0 < u.nk; j0 += kXChain) {
+                for (int j0 = 0; j0 < u.nk || (kBack && j0 == 0); j0 += kChain) {
                     begin();
 #pragma unroll
                     for (int c = 0; c < N::kCols / 16; c++) {
@@ -647,35 +650,47 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
 #pragma unroll
                             for (int j = 0; j < 16; j++) f[j] = __int_as_float(0x7fc00000);
                         }
+                        // (without an MMA, K of nothing, the accumulator holds another tile's sums)
 #pragma unroll
-                        for (int j = 0; j < 16; j++) v[16 * c + j] = __fadd_rn(v[16 * c + j], f[j]);
+                        for (int j = 0; j < 16; j++)
+                            v[16 * c + j] = kBack && live && none ? 0.0f : __fadd_rn(v[16 * c + j], f[j]);
                     }
                     done();
                 }
-                if constexpr (MODE == kXentGradient)
+                if constexpr (MODE == kXentForward) {
+                    if (row0 < n) epilogue_forward<N::kCols>(g, (size_t)(row0 + lane), u.tn * (TN / N::kCols) + half, v);
+                } else if constexpr (MODE == kXentGradient) {
                     epilogue_gradient<DT, N::kCols>(g, &maps.p_out, out, row0, n, col0, v);
-                else if (row0 < n)
-                    epilogue_forward<N::kCols>(g, (size_t)(row0 + lane), u.tn * (TN / N::kCols) + half, v);
-                continue;
-            }
-            begin();
-            // without an MMA (K of nothing) the accumulator holds another tile's sums
-            const float fill = live ? 0.0f : __int_as_float(0x7fc00000);
-            const bool read = live && u.nk > 0;
-            auto ld = [&](int c, float (&v)[32]) {
-                __syncwarp();
-                if (read) {
-                    tc_ld_row32(base + (uint32_t)(b * kXentTile + 32 * c), v);
                 } else {
+                    auto of = [&](int c, float (&w)[32]) {
 #pragma unroll
-                    for (int j = 0; j < 32; j++) v[j] = fill;
+                        for (int j = 0; j < 32; j++) w[j] = v[32 * c + j];
+                    };
+                    if (u.x)
+                        epilogue_dx<4>(g, &maps.ws_out, out, row0, n, u.split, col0, of);
+                    else
+                        epilogue_dw<DT, 2>(g, &maps.dw_out, out, row0, col0, of);
                 }
-            };
-            if (u.x)
-                epilogue_dx(g, &maps.ws_out, out, row0, n, u.split, col0, ld);
-            else
-                epilogue_dw<DT>(g, &maps.dw_out, out, row0, col0, ld);
-            done();
+            } else {
+                begin();
+                // without an MMA (K of nothing) the accumulator holds another tile's sums
+                const float fill = live ? 0.0f : __int_as_float(0x7fc00000);
+                const bool read = live && u.nk > 0;
+                auto ld = [&](int c, float (&v)[32]) {
+                    __syncwarp();
+                    if (read) {
+                        tc_ld_row32(base + (uint32_t)(b * kXentTile + 32 * c), v);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j++) v[j] = fill;
+                    }
+                };
+                if (u.x)
+                    epilogue_dx<1>(g, &maps.ws_out, out, row0, n, u.split, col0, ld);
+                else
+                    epilogue_dw<DT, 1>(g, &maps.dw_out, out, row0, col0, ld);
+                done();
+            }
         }
         if (MODE != kXentForward && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
@@ -705,7 +720,8 @@ const void *xent_pick(int mode, bool narrow)
     if (mode == kXentGradient)
         return narrow ? (const void *)xent_kernel<DT, kXentGradient, 64>
                       : (const void *)xent_kernel<DT, kXentGradient, 256>;
-    return (const void *)xent_kernel<DT, kXentBack, 256>;
+    return mode == kXentBack ? (const void *)xent_kernel<DT, kXentBack, 256>
+                             : (const void *)xent_kernel<DT, kXentBackLong, 256>;
 }
 
 const void *xent_pick(int dtype, int mode, bool narrow)
@@ -760,7 +776,7 @@ int xent_pairs()
     int n = 0, sms = 0;
     bool ok = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
     for (int dt : {kF16, kBF16})
-        for (int mode : {kXentForward, kXentGradient, kXentBack})
+        for (int mode : {kXentForward, kXentGradient, kXentBack, kXentBackLong})
             for (bool narrow : {false, true})
                 ok = ok && set_smem_once((void *)xent_pick(dt, mode, narrow), xent_smem(mode, narrow)) == cudaSuccess;
     if (ok) {
@@ -800,6 +816,10 @@ int xent_tile_cols(size_t tokens, size_t vn, int pairs)
 cudaError_t launch_xent(int dtype, int mode, const XentMaps &maps, const XentGemm &g, size_t units, int pairs,
                         int tile_cols, cudaStream_t stream)
 {
+    // a K of more than one chain: dX's, dW's
+    if (mode == kXentBack && ((g.ws && ((g.vn + kXBox - 1) / kXBox + g.splits - 1) / g.splits > kXBackChain) ||
+                              (g.dw && g.tpad > (size_t)(kXBackChain * kXBox))))
+        mode = kXentBackLong;
     void *args[] = {(void *)&maps, (void *)&g};
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = pair_config(mode, tile_cols == 64, (int)(units < (size_t)pairs ? units : (size_t)pairs), attr, stream);

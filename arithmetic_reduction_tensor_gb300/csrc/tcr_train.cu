@@ -372,6 +372,11 @@ try {
     const size_t tiles_h = (z.H + kXentTile - 1) / kXentTile, tiles_x = (size_t)z.tiles_t * tiles_h;
     size_t splits = kSplitPairs / tiles_x, boxes = (z.V < piece ? z.V : piece) / 64 / 4;
     if (splits > boxes) splits = boxes;
+    // Few tokens: a split a chain, too, so that the launch need not add chains up in
+    // registers, which a short K of dW pays for (16 x 4096 over 131072 628 us, 685 with
+    // 4 splits; 1024 tokens 2064 and 2118, 2048 4028 and 3989).
+    const size_t chains = ((z.V < piece ? z.V : piece) + kXentChain - 1) / kXentChain;
+    if (z.T <= 1024 && splits < chains) splits = chains;
     if (splits > 32) splits = 32;
     if (splits < 1) splits = 1;
     const size_t ldws = round_up(z.H, 32);

@@ -10,8 +10,9 @@
 
 namespace tcr {
 
+constexpr int kXentChain = 16384;           // K of dX and dW that the tensor cores add up in one chain
 constexpr int kXentTile = 256;             // tokens and vocabulary entries (or columns) of a tile
-constexpr int kXentForward = 0, kXentGradient = 1, kXentBack = 2;
+constexpr int kXentForward = 0, kXentGradient = 1, kXentBack = 2, kXentBackLong = 3;
 constexpr float kXentF16Scale = 32768.0f;  // of P in binary16
 
 // A target as an entry of the vocabulary, -1 where there is no such entry.

@@ -762,7 +762,9 @@ TCR_API tcr_status tcr_cross_entropy(const tcr_xent_args *args, void *stream);
  * P 0 for tokens that are ignored.  The logits are formed again, over pieces of
  * the vocabulary; exp(l_tv - lse[t]) is off by at most 2^-15 + 2^-24 |lse[t]| of
  * itself beyond what the logits' errors make of it, P is rounded to dtype (in units of
- * the largest finite |dloss|; TCR_F16: of 2^-15 of it), the products summed in binary32.
+ * the largest finite |dloss|; TCR_F16: of 2^-15 of it).  The products are summed in binary32, in
+ * chains of 16384 terms by the tensor cores: off by at most 2^-12 of the sum of
+ * their magnitudes.
  *   dloss    tokens floats (inc_dloss = 1), or one for all (0).
  *   lse      the forward call's.
  *   dx, dweight  of dtype, overwritten; NULL where not wanted.  dx may be x

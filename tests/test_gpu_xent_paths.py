@@ -8,7 +8,8 @@ import pytest
 
 import arithmetic_reduction_tensor_gb300 as tcr
 from arithmetic_reduction_tensor_gb300.build import build_library
-from tests.test_gpu_xent import case, check
+from tests import rows_spec
+from tests.test_gpu_xent import DTS, U, case, check
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -68,3 +69,41 @@ def test_pieces_of_the_vocabulary_in_every_form(T, H, V, pitch, dt):
     dx2, dw2 = tcr.tcr_cross_entropy_backward(dloss, x, w, target, o.lse)
     assert torch.equal(dx, dx2) and torch.equal(guarded, dw2)
     assert tcr.tcr_device_faults() == 0
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("T,H", [(16384 + 64, 8), (65536, 65), (262144, 64), (1 << 21, 16)])
+def test_weight_gradients_of_many_tokens(T, H, dt):
+    # logits of 0 over 256 entries, every token's target entry 0: P is 2^-8 of the common
+    # dloss, exactly, so dW of the other entries is a sum of T terms of one sign, off
+    # by the tensor cores' 2^-22 a step of 16 over 16384 tokens, the additions of
+    # such chains (U each) and its rounding
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = (torch.rand(T, H, generator=gen, device="cuda") * 0.5 + 0.5).to(DTS[dt])
+    w = torch.zeros(256, H, dtype=x.dtype, device="cuda")
+    target = torch.zeros(T, dtype=torch.long, device="cuda")
+    lse = tcr.tcr_cross_entropy(x, w, target, want_lse=True).lse
+    g = torch.full((1,), 1 / T, device="cuda")
+    _, dw = tcr.tcr_cross_entropy_backward(g.expand(T), x, w, target, lse, want_dx=False)
+    want = x.double().sum(0) * float(g) / 256
+    eps = rows_spec.EPS_OUT[x.dtype]
+    # P: the exponential's 2^-22 and lse's rounding U log(256), then exact or one half step of a power of 2
+    off = 2.0 ** -22 * -(-min(T, 16384) // 16) + (T // 16384 + 2) * U + 2.0 ** -21 + 8 * U
+    assert ((dw[1:].double() - want).abs() <= (off + eps + eps * off) * want + rows_spec.TINY[x.dtype]).all()
+
+
+def test_input_gradients_of_a_long_piece():
+    # the same of dX: 2^19 entries in one piece, one split; the target entry's row is 0
+    T, H, V = 512, 5120, 1 << 19
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(V, H, dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1.0, generator=gen)
+    w[0] = 0
+    x = torch.zeros(T, H, dtype=w.dtype, device="cuda")
+    target = torch.zeros(T, dtype=torch.long, device="cuda")
+    lse = tcr.tcr_cross_entropy(x, w, target, want_lse=True).lse
+    one = torch.ones(1, device="cuda")
+    dx, _ = tcr.tcr_cross_entropy_backward(one.expand(T), x, w, target, lse, want_dweight=False)
+    want = sum(b.double().sum(0) for b in w.split(1 << 15)) / V
+    off = 2.0 ** -22 * 1024 + (V // 16384 + 2) * U + 2.0 ** -21 + 16 * U
+    eps = rows_spec.EPS_OUT[w.dtype]
+    assert ((dx.double() - want).abs() <= (off + eps + eps * off) * want).all()
