@@ -233,14 +233,15 @@ layer_back_sums_kernel(const __grid_constant__ LayerBackArgs a, float *sums)
     }
 }
 
+constexpr int kBackLongT = 256;
 template <int DT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kBackLongT)
 layer_back_long_kernel(const __grid_constant__ LayerBackArgs a, const float *sums)
 {
     pdl_launch_dependents();
     pdl_wait_primary();
     using E = typename Elem<DT>::T;
-    const uint32_t v = blockIdx.x * 256 + threadIdx.x, cols = (uint32_t)a.cols;
+    const uint32_t v = blockIdx.x * kBackLongT + threadIdx.x, cols = (uint32_t)a.cols;
     const Drop drop(a.drop);
     const uint32_t left = vec_left(cols, v);
     float accw[kRv], accb[kRv];
@@ -318,11 +319,25 @@ static int back_ctas(size_t nvec, int dtype)
 // As many CTAs as fit the SMs, but (above one an SM) no more than half the rows: a
 // partial costs as much traffic as a row (1001 x 1537 binary32 12.4 us, with a
 // quarter of the rows 16.3, with all of them 12.3).
+// Longer rows: as many as make, with their blocks of columns, two rounds of the
+// three CTAs that an SM holds, or one of the four in binary32.  As many as the rule
+// above counts were 64 CTAs a group here, and their partials as large as the
+// inputs: bfloat16 304 x 131072 277 us and 159 MB of partials, so 192 and 15; 152 x 2^20
+// 1491 and 921; 4096 x 16384 309 and 312, 20000 x 12288 1168 and 1164 (with four an SM 209,
+// 921, 339, 1308, with eight 199, 873, 315, 1206); binary32 152 x 2^19 with four 409,
+// three 489, six 463, 4096 x 16384 305, 318, 328, 8192 x 8200 411, 461, 447.
 int layer_back_groups(size_t rows, size_t cols, int dtype)
 {
-    const size_t full = (size_t)152 * back_ctas((cols + kRv - 1) / kRv, dtype);
-    const size_t half = (rows + 1) / 2 > 152 ? (rows + 1) / 2 : 152;
-    const size_t g = full < half ? full : half;
+    const size_t nvec = (cols + kRv - 1) / kRv;
+    size_t g;
+    if (nvec > kBackMaxVecs) {
+        g = (size_t)152 * (dtype == kF32 ? 4 : 6) / ((nvec + kBackLongT - 1) / kBackLongT);
+        if (g < 1) g = 1;
+    } else {
+        const size_t full = (size_t)152 * back_ctas(nvec, dtype);
+        const size_t half = (rows + 1) / 2 > 152 ? (rows + 1) / 2 : 152;
+        g = full < half ? full : half;
+    }
     return (int)(rows < g ? rows : g);
 }
 
@@ -396,8 +411,8 @@ cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream
     cudaError_t e = launch_first((const void *)layer_back_sums_kernel<DT>, dim3((unsigned)a.rows), dim3(kRowLongT),
                                  args, 0, stream);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)((nvec + 255) / 256), (unsigned)G);
-    return launch_first((const void *)layer_back_long_kernel<DT>, grid, dim3(256), args, 0, stream);
+    const dim3 grid((unsigned)((nvec + kBackLongT - 1) / kBackLongT), (unsigned)G);
+    return launch_first((const void *)layer_back_long_kernel<DT>, grid, dim3(kBackLongT), args, 0, stream);
 }
 
 }  // namespace

@@ -694,7 +694,8 @@ TCR_API tcr_status tcr_layernorm(const tcr_layernorm_args *args, void *stream);
  *          ceil(rows / 2)))), where c is, for up to 128, 192, 320, 384, 640, 768,
  *          896 and more vectors of 8 a row, 16, 12, 8, 5, 4, 2, 3 and 2, and of
  *          binary32, for up to 128, 256, 384, 640, 768 and more, 12, 6, 4, 3, 2
- *          and 1.
+ *          and 1; for cols > 8192 min(rows, max(1, floor(912 / ceil(cols / 2048)))),
+ *          of binary32 with 608.
  * Takes G * cols floats of pool scratch for each of dweight and dbias that is
  * wanted, and 2 rows more for cols > 8192.
  * rows == 0 writes dweight = dbias = +0.0.
