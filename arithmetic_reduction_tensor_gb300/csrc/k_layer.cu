@@ -1,6 +1,7 @@
 // k_layer.cu -- dropout, and the launch of the layer norm (layer.cuh).
 #include "kernels.cuh"
 #include "piece.cuh"
+#include "plan.h"
 
 namespace tcr {
 
@@ -74,7 +75,7 @@ cudaError_t launch_dropout(int dtype, const LayerArgs &a, cudaStream_t stream)
     const size_t steps = (a.rows + ((size_t)8 >> wr) - 1) / ((size_t)8 >> wr);
     // kDropRows steps a CTA; few rows: one, spread over the SMs
     size_t gy = (steps + kDropRows - 1) / kDropRows;
-    if (gx * gy < 4 * 152) gy = steps;
+    if (gx * gy < 4 * (size_t)plan::kRuleSMs) gy = steps;
     if (gy > 65535) gy = 65535;
     const bool elem = !a.al_x || (a.r && !a.al_r) || !a.al_y;
     const void *k;

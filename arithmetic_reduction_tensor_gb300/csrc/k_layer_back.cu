@@ -13,6 +13,7 @@
 // type only (layer_back_groups); there are no atomics.
 #include "kernels.cuh"
 #include "piece.cuh"
+#include "plan.h"
 #include "tc05.cuh"
 
 namespace tcr {
@@ -300,61 +301,15 @@ layer_sums_kernel(const float *partial_w, const float *partial_b, size_t cols, i
 
 // ---------------------------------------------------------------- host
 
-// CTAs an SM of layer_back_kernel at a row length: what registers and shared
-// memory hold of the shapes below.
-static int back_ctas(size_t nvec, int dtype)
-{
-    if (dtype == kF32)
-        return nvec <= 128 ? 12 : nvec <= 256 ? 6 : nvec <= 384 ? 4 : nvec <= 640 ? 3 : nvec <= 768 ? 2 : 1;
-    return nvec <= 128   ? 16
-           : nvec <= 192 ? 12
-           : nvec <= 320 ? 8
-           : nvec <= 384 ? 5
-           : nvec <= 640 ? 4
-           : nvec <= 768 ? 2
-           : nvec <= 896 ? 3
-                         : 2;
-}
-
-// As many CTAs as fit the SMs, but (above one an SM) no more than half the rows: a
-// partial costs as much traffic as a row (1001 x 1537 binary32 12.4 us, with a
-// quarter of the rows 16.3, with all of them 12.3).
-// Longer rows: as many as make, with their blocks of columns, two rounds of the
-// three CTAs that an SM holds, or one of the four in binary32.  As many as the rule
-// above counts were 64 CTAs a group here, and their partials as large as the
-// inputs: bfloat16 304 x 131072 277 us and 159 MB of partials, so 192 and 15; 152 x 2^20
-// 1491 and 921; 4096 x 16384 309 and 312, 20000 x 12288 1168 and 1164 (with four an SM 209,
-// 921, 339, 1308, with eight 199, 873, 315, 1206); binary32 152 x 2^19 with four 409,
-// three 489, six 463, 4096 x 16384 305, 318, 328, 8192 x 8200 411, 461, 447.
-int layer_back_groups(size_t rows, size_t cols, int dtype)
-{
-    const size_t nvec = (cols + kRv - 1) / kRv;
-    size_t g;
-    if (nvec > kBackMaxVecs) {
-        g = (size_t)152 * (dtype == kF32 ? 4 : 6) / ((nvec + kBackLongT - 1) / kBackLongT);
-        if (g < 1) g = 1;
-    } else {
-        const size_t full = (size_t)152 * back_ctas(nvec, dtype);
-        const size_t half = (rows + 1) / 2 > 152 ? (rows + 1) / 2 : 152;
-        g = full < half ? full : half;
-    }
-    return (int)(rows < g ? rows : g);
-}
-
-size_t layer_back_scratch(size_t rows, size_t cols, int dtype, bool dweight, bool dbias)
-{
-    const size_t part = (size_t)layer_back_groups(rows, cols, dtype) * cols;
-    const size_t sums = (cols + kRv - 1) / kRv > kBackMaxVecs ? 2 * rows : 0;
-    return ((dweight ? part : 0) + (dbias ? part : 0) + sums) * sizeof(float);
-}
-
 namespace {
 
+// The kernel of a row length, and the CTAs of it that an SM holds (what registers
+// and shared memory let it): they make the number of partial sums.
 template <int DT, bool ELEM>
-const void *pick(size_t nvec, unsigned &threads, size_t &smem)
+const void *pick(size_t nvec, unsigned &threads, size_t &smem, int &ctas)
 {
-#define TCR_BACK(T_, NV_, MINB_)                     \
-    return (threads = T_, smem = (size_t)T_ * NV_ * 64, \
+#define TCR_BACK(T_, NV_, MINB_)                                      \
+    return (threads = T_, smem = (size_t)T_ * NV_ * 64, ctas = MINB_, \
             (const void *)layer_back_kernel<DT, ELEM, T_, NV_, NV_ - 1, MINB_>)
     // The fastest of those measured (with dropout and the sums; threads whose last
     // pieces are past the row's end issue for nothing): bfloat16 16384 x 4096 256 x 2
@@ -386,6 +341,54 @@ const void *pick(size_t nvec, unsigned &threads, size_t &smem)
 #undef TCR_BACK
 }
 
+int back_ctas(size_t nvec, int dtype)
+{
+    unsigned threads;
+    size_t smem;
+    int ctas = 0;
+    if (dtype == kF32)
+        pick<kF32, false>(nvec, threads, smem, ctas);
+    else
+        pick<kBF16, false>(nvec, threads, smem, ctas);           // (binary16's are the same)
+    return ctas;
+}
+
+}  // namespace
+
+// As many CTAs as fit the SMs, but (above one an SM) no more than half the rows: a
+// partial costs as much traffic as a row (1001 x 1537 binary32 12.4 us, with a
+// quarter of the rows 16.3, with all of them 12.3).
+// Longer rows: as many as make, with their blocks of columns, two rounds of the
+// three CTAs that an SM holds, or one of the four in binary32.  As many as the rule
+// above counts were 64 CTAs a group here, and their partials as large as the
+// inputs: bfloat16 304 x 131072 277 us and 159 MB of partials, so 192 and 15; 152 x 2^20
+// 1491 and 921; 4096 x 16384 309 and 312, 20000 x 12288 1168 and 1164 (with four an SM 209,
+// 921, 339, 1308, with eight 199, 873, 315, 1206); binary32 152 x 2^19 with four 409,
+// three 489, six 463, 4096 x 16384 305, 318, 328, 8192 x 8200 411, 461, 447.
+int layer_back_groups(size_t rows, size_t cols, int dtype)
+{
+    const size_t nvec = (cols + kRv - 1) / kRv;
+    size_t g;
+    if (nvec > kBackMaxVecs) {
+        g = (size_t)plan::kRuleSMs * (dtype == kF32 ? 4 : 6) / ((nvec + kBackLongT - 1) / kBackLongT);
+        if (g < 1) g = 1;
+    } else {
+        const size_t full = (size_t)plan::kRuleSMs * back_ctas(nvec, dtype);
+        const size_t one = plan::kRuleSMs, half = (rows + 1) / 2 > one ? (rows + 1) / 2 : one;
+        g = full < half ? full : half;
+    }
+    return (int)(rows < g ? rows : g);
+}
+
+size_t layer_back_scratch(size_t rows, size_t cols, int dtype, bool dweight, bool dbias)
+{
+    const size_t part = (size_t)layer_back_groups(rows, cols, dtype) * cols;
+    const size_t sums = (cols + kRv - 1) / kRv > kBackMaxVecs ? 2 * rows : 0;
+    return ((dweight ? part : 0) + (dbias ? part : 0) + sums) * sizeof(float);
+}
+
+namespace {
+
 template <int DT>
 cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream)
 {
@@ -394,8 +397,9 @@ cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream
         void *args[] = {(void *)&a};
         unsigned threads = 0;
         size_t smem = 0;
+        int ctas = 0;
         const bool elem = !a.al_dy || !a.al_h || (a.w && !a.al_w) || (a.dh && !a.al_dh) || (a.dx && !a.al_dx) || (a.dr && !a.al_dr);
-        const void *k = elem ? pick<DT, true>(nvec, threads, smem) : pick<DT, false>(nvec, threads, smem);
+        const void *k = elem ? pick<DT, true>(nvec, threads, smem, ctas) : pick<DT, false>(nvec, threads, smem, ctas);
         if (smem + 16 * threads > 48 * 1024) {               // beside red
             cudaError_t e = set_smem_once((void *)k, (int)smem);
             if (e != cudaSuccess) return e;
@@ -404,7 +408,8 @@ cudaError_t launch_back(LayerBackArgs a, int G, float *sums, cudaStream_t stream
         // finishes: where that one holds little shared memory, an SM would take
         // its first CTAs with a small share of it and the rest in a second wave
         // (100 calls back to back, 65536 x 1024 bfloat16: 148 us, 119 this way).
-        if (G == 152 * back_ctas(nvec, DT)) return cudaLaunchKernel(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
+        if (G == plan::kRuleSMs * ctas)
+            return cudaLaunchKernel(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
         return launch_first(k, dim3((unsigned)G), dim3(threads), args, smem, stream);
     }
     void *args[] = {(void *)&a, (void *)&sums};

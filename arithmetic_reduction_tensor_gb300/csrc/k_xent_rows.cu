@@ -7,6 +7,7 @@
 // they hold (NaN included) reaches no sum, and X may have any pitch and
 // alignment.  All are bound by memory traffic, or, for few tokens, by latency.
 #include "kernels.cuh"
+#include "plan.h"
 #include "rowvec.cuh"
 #include "xent.h"
 
@@ -262,7 +263,7 @@ cudaError_t launch_xent_tokens(const XentTokens &a, cudaStream_t stream)
     size_t chunk = (a.tokens + 1023) / 1024;
     if (chunk < kTokWarps) chunk = kTokWarps;
     unsigned blocks = (unsigned)((a.tokens + chunk - 1) / chunk);
-    const size_t need = (a.V + kTokWarps - 1) / kTokWarps, most = 152 * 8;
+    const size_t need = (a.V + kTokWarps - 1) / kTokWarps, most = (size_t)plan::kRuleSMs * 8;
     const unsigned repack = a.w ? (unsigned)(need < most ? need : most) : 0u;
     void *args[] = {(void *)&a, (void *)&chunk, (void *)&blocks};
     return launch_first((const void *)xent_tokens_kernel, dim3(blocks + kTokTail + repack), dim3(kTokThreads), args, 0,
@@ -279,7 +280,7 @@ cudaError_t launch_xent_loss(const XentLoss &a, cudaStream_t stream)
 cudaError_t launch_xent_dx(int dtype, const XentDx &a, cudaStream_t stream)
 {
     void *args[] = {(void *)&a};
-    const size_t gy = (a.H + 1023) / 1024, most = (size_t)152 * 32;
+    const size_t gy = (a.H + 1023) / 1024, most = (size_t)plan::kRuleSMs * 32;
     const dim3 grid((unsigned)(a.tokens < most ? a.tokens : most), (unsigned)gy);
     return launch_first(dtype == kF16 ? (const void *)xent_dx_kernel<kF16> : (const void *)xent_dx_kernel<kBF16>, grid,
                         dim3(256), args, 0, stream);

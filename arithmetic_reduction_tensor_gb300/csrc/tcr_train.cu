@@ -17,7 +17,7 @@ constexpr size_t kMaxTokens = (size_t)1 << 24;     // exclusive, as the next two
 constexpr size_t kMaxVocab = (size_t)1 << 27;
 constexpr size_t kMaxHidden = (size_t)1 << 20;
 constexpr size_t kMaxP = (size_t)512 << 20;        // bytes of P in a piece of the vocabulary
-constexpr size_t kSplitPairs = 76;                 // pairs that dX is split for: a constant, as its splits are its sums' order
+constexpr size_t kSplitPairs = kRuleSMs / 2;                 // pairs that dX is split for: a constant, as its splits are its sums' order
 
 // The kernel's form of a call's dropout; none where drop is null.
 bool drop_of(const tcr_drop *drop, DropArgs &d)
