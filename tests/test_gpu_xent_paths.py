@@ -107,3 +107,25 @@ def test_input_gradients_of_a_long_piece():
     off = 2.0 ** -22 * 1024 + (V // 16384 + 2) * U + 2.0 ** -21 + 16 * U
     eps = rows_spec.EPS_OUT[w.dtype]
     assert ((dx.double() - want).abs() <= (off + eps + eps * off) * want).all()
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("live", [0, 1, 70, 17000])
+def test_few_of_many_tokens_count(live, dt):
+    # the launch is the one for long sums, the sums are not: the same bits as without the ignored
+    T, H, V = 40000, 72, 700
+    x, w, target, dloss = case(T, H, V, dt, ignored=0.0)
+    keep = torch.zeros(T, dtype=torch.bool, device="cuda")
+    keep[torch.randperm(T, device="cuda")[:live]] = True
+    target[~keep], x[~keep] = -100, float("nan")
+    o = tcr.tcr_cross_entropy(x, w, target, want_lse=True)
+    dx, dw = tcr.tcr_cross_entropy_backward(dloss, x, w, target, o.lse)
+    assert (dx[~keep] == 0).all() and (o.loss[~keep] == 0).all()
+    if live == 0:
+        assert (dw == 0).all()
+        return
+    few = tcr.tcr_cross_entropy(x[keep], w, target[keep], want_lse=True)
+    dx1, dw1 = tcr.tcr_cross_entropy_backward(dloss[keep], x[keep], w, target[keep], few.lse)
+    assert torch.equal(o.loss[keep], few.loss) and torch.equal(dw, dw1)
+    check(x[keep], w, target[keep], dloss[keep], few.loss, few.lse, dx1, dw1)
+    check(x[keep], w, target[keep], dloss[keep], None, None, dx[keep], None)
