@@ -48,6 +48,7 @@
 // in one box of all their rows (two of 64 rows: 2.56 ms).  Few tokens are bound by
 // reading W: 16 x 4096 over 131072 175 us, 6.1 TB/s.
 #include "pair.cuh"
+#include "piece.cuh"
 #include "plan.h"
 #include "rowvec.cuh"
 #include "xent.h"
@@ -106,6 +107,39 @@ __device__ __forceinline__ void tc_ld_row16(uint32_t taddr, float (&v)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int j = 0; j < 16; j++) v[j] = __uint_as_float(r[j]);
+}
+
+// COLS consecutive fp32 columns of this thread's TMEM lane, all on their way
+// before the first is waited for.
+template <int COLS>
+__device__ __forceinline__ void tc_ld_row(uint32_t taddr, float (&v)[COLS])
+{
+    uint32_t r[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+            "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+            "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+            : "=r"(r[c + 0]), "=r"(r[c + 1]), "=r"(r[c + 2]), "=r"(r[c + 3]), "=r"(r[c + 4]), "=r"(r[c + 5]),
+              "=r"(r[c + 6]), "=r"(r[c + 7]), "=r"(r[c + 8]), "=r"(r[c + 9]), "=r"(r[c + 10]),
+              "=r"(r[c + 11]), "=r"(r[c + 12]), "=r"(r[c + 13]), "=r"(r[c + 14]), "=r"(r[c + 15]),
+              "=r"(r[c + 16]), "=r"(r[c + 17]), "=r"(r[c + 18]), "=r"(r[c + 19]), "=r"(r[c + 20]),
+              "=r"(r[c + 21]), "=r"(r[c + 22]), "=r"(r[c + 23]), "=r"(r[c + 24]), "=r"(r[c + 25]),
+              "=r"(r[c + 26]), "=r"(r[c + 27]), "=r"(r[c + 28]), "=r"(r[c + 29]), "=r"(r[c + 30]),
+              "=r"(r[c + 31])
+            : "r"(taddr + (uint32_t)c)
+            : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int c = 0; c < COLS; c += 16)               // (not used before the wait)
+        asm volatile(""
+                     : "+r"(r[c + 0]), "+r"(r[c + 1]), "+r"(r[c + 2]), "+r"(r[c + 3]), "+r"(r[c + 4]),
+                       "+r"(r[c + 5]), "+r"(r[c + 6]), "+r"(r[c + 7]), "+r"(r[c + 8]), "+r"(r[c + 9]),
+                       "+r"(r[c + 10]), "+r"(r[c + 11]), "+r"(r[c + 12]), "+r"(r[c + 13]), "+r"(r[c + 14]),
+                       "+r"(r[c + 15]));
+#pragma unroll
+    for (int j = 0; j < COLS; j++) v[j] = __uint_as_float(r[j]);
 }
 
 // The operand of 128 rows (or MN elements) at `addr`, two boxes: K-major (8-row
@@ -229,28 +263,57 @@ struct XUnits {
 // gives the columns 32 c .. 32 c + 31 of these.  Every lane of the warp calls
 // ld and the stores.
 
+// exp(l - about) of two logits (an instruction for both but for the exponentials).
+__device__ __forceinline__ void exp_pair(float a, float b, uint64_t minus_about, float &x, float &y)
+{
+    uint64_t d = add_pair(pack_pair(a, b), minus_about);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(d), "l"(pack_pair(kLog2e, kLog2e)));
+    unpack_pair(d, x, y);
+    x = ex2(x);
+    y = ex2(y);
+}
+
+// The smaller, or NaN where either is (fmaxf gives the other).
+__device__ __forceinline__ float min_or_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // The largest logit m of the row among 64 columns, and the sum of exp(l - m) over
 // the others: without the largest's 1, in which small sums would drown, the loss
 // of a token that is predicted well keeps its bits.  The differences are taken
 // before they are scaled, so that the logits' size costs no bits and overflows
-// nothing.
+// nothing.  A tournament whose losers stay finds both (v is lost): comparing each with
+// the largest and counting those alike took 4096 x 1024 over 16384 100 us, 95 so, 93 with
+// the logits loaded at once (tc_ld_row).
 template <int C0, int COLS>
-__device__ __forceinline__ float2 part_of(const float (&v)[COLS])
+__device__ __forceinline__ float2 part_of(float (&v)[COLS])
 {
-    float m[4] = {v[C0], v[C0 + 1], v[C0 + 2], v[C0 + 3]}, e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 4; j < 64; j++) m[j & 3] = fmaxf(m[j & 3], v[C0 + j]);
-    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), about = xent_about(mx);
-    int others = -1;                                         // as large as the largest
+    for (int h = 32; h >= 1; h /= 2) {
 #pragma unroll
-    for (int j = 0; j < 64; j++) {
-        const float t = xent_exp(v[C0 + j], about);
-        if (v[C0 + j] == mx)
-            others++;
-        else
-            e[j & 3] = __fadd_rn(e[j & 3], t);
+        for (int j = C0; j < C0 + h; j++) {
+            const float a = v[j], b = v[j + h];
+            v[j] = fmaxf(a, b);
+            v[j + h] = min_or_nan(a, b);
+        }
     }
-    return make_float2(mx, __fadd_rn(__fadd_rn(__fadd_rn(e[0], e[1]), __fadd_rn(e[2], e[3])), (float)others));
+    const float mx = v[C0], minus = -xent_about(mx);
+    const uint64_t minus_about = pack_pair(minus, minus);
+    float e[4];
+    exp_pair(v[C0 + 1], v[C0 + 1], minus_about, e[0], e[1]);
+    e[1] = e[2] = e[3] = 0.0f;
+    uint64_t s[2] = {pack_pair(e[0], e[1]), pack_pair(e[2], e[3])};
+#pragma unroll
+    for (int j = 2; j < 64; j += 2) {
+        float x, y;
+        exp_pair(v[C0 + j], v[C0 + j + 1], minus_about, x, y);
+        s[(j >> 1) & 1] = add_pair(s[(j >> 1) & 1], pack_pair(x, y));
+    }
+    unpack_pair(add_pair(s[0], s[1]), e[0], e[1]);
+    return make_float2(mx, __fadd_rn(e[0], e[1]));
 }
 
 template <int COLS>
@@ -634,11 +697,18 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
             const int row0 = u.tm * kXentTile + kXHalf * (int)rank + 32 * q, col0 = u.tn * TN + half * N::kCols;
             if constexpr (MODE != kXentBack) {                   // chains, added up in registers
                 float v[N::kCols];
+                begin();
+                __syncwarp();
+                // (without an MMA, K of nothing, the accumulator holds another tile's sums)
+                if (live && !(kBack && u.nk == 0)) {
+                    tc_ld_row(base + (uint32_t)(b * kXentTile), v);
+                } else {
 #pragma unroll
-                for (int j = 0; j < N::kCols; j++) v[j] = kBack ? -0.0f : 0.0f;
-                const bool none = u.nk == 0;
+                    for (int j = 0; j < N::kCols; j++) v[j] = live ? 0.0f : __int_as_float(0x7fc00000);
+                }
+                done();
 #pragma unroll 1
-                for (int j0 = 0; j0 < u.nk || (kBack && j0 == 0); j0 += kChain) {
+                for (int j0 = kChain; j0 < u.nk; j0 += kChain) {
                     begin();
 #pragma unroll
                     for (int c = 0; c < N::kCols / 16; c++) {
@@ -650,10 +720,8 @@ xent_kernel(const __grid_constant__ XentMaps maps, const XentGemm g)
 #pragma unroll
                             for (int j = 0; j < 16; j++) f[j] = __int_as_float(0x7fc00000);
                         }
-                        // (without an MMA, K of nothing, the accumulator holds another tile's sums)
 #pragma unroll
-                        for (int j = 0; j < 16; j++)
-                            v[16 * c + j] = kBack && live && none ? 0.0f : __fadd_rn(v[16 * c + j], f[j]);
+                        for (int j = 0; j < 16; j++) v[16 * c + j] = __fadd_rn(v[16 * c + j], f[j]);
                     }
                     done();
                 }

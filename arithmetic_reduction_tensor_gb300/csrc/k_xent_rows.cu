@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kLossThreads) xent_loss_kernel(const XentLoss 
     auto part = [&](int j) {
         if (!a.narrow) return a.part[(size_t)j * a.tpad + r];
         const float2 p = a.part[(size_t)(2 * j) * a.tpad + r];
-        return xent_join(p, 2 * j + 1 < a.parts ? a.part[(size_t)(2 * j + 1) * a.tpad + r] : make_float2(-INFINITY, 63.0f));
+        return xent_join(p, 2 * j + 1 < a.parts ? a.part[(size_t)(2 * j + 1) * a.tpad + r] : make_float2(-INFINITY, 0.0f));
     };
     if (r >= 0) {
         // two passes over the parts (8 bytes for 128 logits): the largest, then the sum about it
