@@ -721,9 +721,9 @@ def tcr_cross_entropy(x, weight, target, ignore_index: int = -100, loss=None, ls
     one int64 a token, the logits never in memory (``tcr_cross_entropy``).
 
     x (tokens x hidden) and weight (vocabulary x hidden) are float16 or
-    bfloat16.  A token whose target is ``ignore_index`` has loss 0 and costs
-    nothing; a target outside the vocabulary gives NaN.  The gradient takes
-    ``lse``."""
+    bfloat16.  A token whose target is ``ignore_index`` has loss 0, and what it
+    holds reaches no result; beyond 256 tokens it costs nothing.  A target
+    outside the vocabulary gives NaN.  The gradient takes ``lse``."""
     torch = _torch or _load_torch()
     if loss is None:
         loss = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)

@@ -315,7 +315,11 @@ const void *pick(size_t nvec, unsigned &threads, size_t &smem, int &ctas)
     // pieces are past the row's end issue for nothing): bfloat16 16384 x 4096 256 x 2
     // in 119 us, 128 x 4 in 124; 32768 x 1536 64 x 3 97, 128 x 2 129; 20000 x 2560
     // 64 x 5 101, 128 x 3 123; 10000 x 5120 128 x 5 101, 256 x 3 139; 10000 x 6144
-    // 256 x 3 127, 128 x 6 130; 8000 x 7168 128 x 7 125, 512 x 2 142.
+    // 256 x 3 127, 128 x 6 130; 8000 x 7168 128 x 7 125, 512 x 2 142.  binary32, 2^26
+    // elements: 512 columns 64 x 1 224, 128 x 1 278; 3000 128 x 3 217, 256 x 2 241; 4096 256 x
+    // 2 236, 128 x 4 229; 6144 256 x 3 222, 128 x 6 216.  Not the fastest: 1024 64 x 2 240,
+    // 128 x 1 205; 2048 128 x 2 238, 256 x 1 219; 5120 128 x 5 227, 256 x 3 219; 8192 512 x 2 249,
+    // 128 x 8 213.  A shape's CTAs are the order of dw's and db's sums, which stays.
     if constexpr (DT == kF32) {
         if (nvec <= 64) TCR_BACK(64, 1, 12);
         if (nvec <= 128) TCR_BACK(64, 2, 12);

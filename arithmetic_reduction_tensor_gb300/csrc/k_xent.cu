@@ -41,9 +41,10 @@
 // store a row each keep the memory pipe from the MMAs' operands (4096 x 2048 over
 // 9728: P's launch 104 us that way, 98 so).
 //
-// Many tokens are bound by the tensor pipe: 4096 x 4096 over 65536 forward 1.17 ms in
-// a burst, the cuBLAS rate, 1.33 under the power limit; with the gradient over
-// 32768 2.33 and 2.74 ms, 8 T V H operations at 1.89 and 1.61 PFLOP/s.  The producer
+// Many tokens are bound by the tensor pipe: 4096 x 4096 over 65536 forward 1.18 ms in
+// a burst (the product alone by cuBLAS, logits written in 16 bits, 1.09 to 1.15), 1.27 to
+// 1.33 under the power limit (1.22 beside 1.27); with the gradient over 32768 2.37
+// and 2.56 to 2.74 ms, 8 T V H operations at 1.86 and 1.61 to 1.72 PFLOP/s.  The producer
 // is one thread, and a box more a stage costs it: operands that lie K-major come
 // in one box of all their rows (two of 64 rows: 2.56 ms).  Few tokens are bound by
 // reading W: 16 x 4096 over 131072 175 us, 6.1 TB/s.

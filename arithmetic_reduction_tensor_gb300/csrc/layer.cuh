@@ -272,8 +272,10 @@ layer_long_kernel(const __grid_constant__ LayerArgs a)
 // are past the row's end issue for nothing: 6151 x 5120 128 x 5 40 us, 256 x 3 49;
 // 4500 x 7168 128 x 7 42, 256 x 4 46; unaligned 32768 x 1500 64 x 3 114, 64 x 4 194.
 // 8192 x 8192 256 x 4 with 4 CTAs an SM 83, 4096 x 16384 512 x 4 with 2 CTAs 100,
-// with 1 146.  binary32 8192 x 4096 256 x 2 88, 128 x 4 94, 512 x 1 99.  MINB_: CTAs
-// an SM at 64 registers a thread (80 from five pieces on and in binary32).
+// with 1 146.  binary32, 2^26 elements: 512 columns 32 x 2 155, 64 x 1 154; 1024 64 x 2
+// 155, 128 x 1 153, 32 x 4 156; 2048 128 x 2 155, 256 x 1 160; 4096 256 x 2 161, 128 x 4 157, 512
+// x 1 191; 8192 512 x 2 195, 256 x 4 203, 1024 x 1 259; 16384 1024 x 2 216, 512 x 4 216.  MINB_:
+// CTAs an SM at 64 registers a thread (80 from five pieces on and in binary32).
 template <int DT, bool ELEM>
 const void *layer_shape(size_t nvec, int &team)
 {

@@ -738,10 +738,12 @@ TCR_API tcr_status tcr_layernorm_backward(const tcr_layernorm_back_args *args, v
  * / 16) * sum_h |x_th weight_vh|; a row with a NaN or a logit of +infinity has
  * lse and loss NaN.  What tokens that are ignored hold reaches no result.
  * tokens < 2^24, vocab < 2^27, hidden < 2^20 (else TCR_ERR_UNSUPPORTED), vocab and hidden not 0,
- * tokens * vocab and vocab * hidden < 2^40.  Takes pool scratch of 2 bytes per
- * element of x, 8 per token and 128 entries of the vocabulary (64 where these are few), and, where
- * weight's rows are not 16-byte aligned, 2 per element of weight.  No atomics: the bits
- * of a token's loss and lse depend on its row, its target, ignore_index and weight only.
+ * tokens * vocab and vocab * hidden < 2^40.  Takes pool scratch of 8 bytes per
+ * token and 128 entries of the vocabulary (64 where these are few), 2 per element of x
+ * (not where there are up to 256 tokens and all rows are 16-byte aligned: x is then read
+ * where it lies, ignored tokens with the rest), and, where weight's rows are not 16-byte
+ * aligned, 2 per element of weight.  No atomics: the bits of a token's loss and lse
+ * depend on its row, its target, ignore_index and weight only.
  */
 typedef struct {
     const void *x;
@@ -760,24 +762,24 @@ TCR_API tcr_status tcr_cross_entropy(const tcr_xent_args *args, void *stream);
  * tcr_cross_entropy_backward -- the gradient of sum over t of dloss[t] * loss[t]:
  *   P_tv = (exp(l_tv - lse[t]) - [v = target[t]]) * dloss[t],
  *   dx = P weight,  dweight = P^T x,
- * P 0 for tokens that are ignored.  The logits are formed again, over pieces of
- * the vocabulary; exp(l_tv - lse[t]) is off by at most 2^-15 + 2^-24 |lse[t]| of
- * itself beyond what the logits' errors make of it, P is rounded to dtype (in units of
- * the largest finite |dloss|; TCR_F16: of 2^-15 of it).  The products are summed in binary32, in
- * chains of 16384 terms by the tensor cores: off by at most 2^-12 of the sum of
- * their magnitudes.
+ * P 0 for tokens that are ignored.  The logits are formed again, bit for bit, over
+ * pieces of the vocabulary.  exp(l_tv - lse[t]) is off by at most 2^-15 + 2^-24 |lse[t]|
+ * of itself beyond what the logits' errors make of it; P is rounded to dtype (in
+ * units of the largest finite |dloss|; TCR_F16: of 2^-15 of it).  The products are
+ * summed in binary32, by the tensor cores in chains of 16384 terms: off by at most
+ * 2^-12 of the sum of their magnitudes.
  *   dloss    tokens floats (inc_dloss = 1), or one for all (0).
  *   lse      the forward call's.
  *   dx, dweight  of dtype, overwritten; NULL where not wanted.  dx may be x
  *            itself (same pointer and ld); no other overlap.
- * tokens == 0 writes dweight = +0.0.  The rest as in tcr_cross_entropy, but that the
- * bits of dx depend on the number of tokens, too (its sums over the vocabulary are
- * split where tokens are few, and end with its pieces), and those of dweight and of all
- * of P on the largest |dloss|.  Pool
- * scratch: 2 bytes per token and entry of a piece (as many entries as 512 MiB
- * hold, 1024 at least; tokens counted up to a multiple of 256) and 4 per element of dx (for few tokens up to 32
- * times that), beside the copies named there.  A kernel whose wait gave up
- * leaves NaN and sets the word of tcr_device_faults (the forward pass, too);
+ * tokens == 0 writes dweight = +0.0.  The rest as in tcr_cross_entropy, but that
+ * tokens are copied, however few, and that the bits depend on the largest |dloss|, too,
+ * and those of dx on the number of tokens (its sums over the vocabulary are split where
+ * tokens are few, and end with the pieces).
+ * Pool scratch: 2 bytes per token and entry of a piece (as many entries as 512 MiB
+ * hold, 1024 at least; tokens counted up to a multiple of 256) and 4 per element of dx
+ * (for few tokens up to 32 times that), beside the copies named there.  A kernel whose
+ * wait gave up leaves NaN and sets the word of tcr_device_faults (the forward pass, too);
  * TCR_ERR_UNSUPPORTED on a device that cannot schedule a CTA pair.
  */
 typedef struct {
