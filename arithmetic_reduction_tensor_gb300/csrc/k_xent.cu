@@ -260,7 +260,7 @@ struct XUnits {
 
 // ---------------------------------------------------------------- epilogues
 //
-// A lane has one row of the tile and its warp's 128 columns of it; `ld(c, v)`
+// A lane has one row of the tile and its warp's 128 (64) columns of it: v, or `ld(c, v)`
 // gives the columns 32 c .. 32 c + 31 of these.  Every lane of the warp calls
 // ld and the stores.
 
